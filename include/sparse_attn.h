@@ -40,7 +40,9 @@ typedef enum {
 
 typedef enum {
     SA_KV_BF16 = 0,          /* kv is bf16 [b][rows][d] */
-    SA_KV_FP8_E4M3 = 1       /* kv is e4m3 [b][rows][d] + kv_scale e8m0 [b][rows][d/32] */
+    SA_KV_FP8_E4M3 = 1,      /* kv is e4m3 [b][rows][d] + kv_scale e8m0 [b][rows][d/32] */
+    SA_KV_FP4_E2M1 = 2       /* kv is e2m1 [b][rows][d/2], two codes to a byte (the even element in
+                                the low four bits) + kv_scale e8m0 [b][rows][d/32] */
 } sa_kv_format;
 
 /* Which kernel family computes sparse_attn (sa_sparse_attn_family). */
@@ -70,10 +72,13 @@ typedef enum {
  *
  * Arguments
  *   q          bf16 [b][s][h][d]
- *   kv         bf16 [b][rows][d] (SA_KV_BF16) or e4m3 [b][rows][d] (SA_KV_FP8_E4M3)
- *   kv_scale   e8m0 [b][rows][d/32] for SA_KV_FP8_E4M3 (block 32 along d), NULL for bf16.
+ *   kv         bf16 [b][rows][d] (SA_KV_BF16), e4m3 [b][rows][d] (SA_KV_FP8_E4M3) or e2m1
+ *              [b][rows][d/2] bytes (SA_KV_FP4_E2M1)
+ *   kv_scale   e8m0 [b][rows][d/32] for the fp8 and fp4 formats (block 32 along d), NULL for bf16.
  *              An fp8 row j decodes to e4m3(kv[j][k]) * 2^(kv_scale[j][k/32] - 127), exactly
- *              the bf16 values the act_quant round trip produces.
+ *              the bf16 values the act_quant round trip produces; an fp4 row the same way from its
+ *              e2m1 codes (sa_act_quant_fp4), a scale byte above 252 counting as 252, so that an fp4
+ *              row is finite whatever its bytes are.
  *   sink       f32 [h] (may be -inf)
  *   idx        int32 [b][s][topk], each entry in [-1, rows).  An entry outside that range is
  *              treated as -1 and sets SA_ERR_INDEX in the workspace status word.

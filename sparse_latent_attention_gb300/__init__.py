@@ -8,6 +8,15 @@ streams only; all the arithmetic runs in the library's sm_103a kernels.
     o = sparse_attn(q, codes, sink, idx, scale, kv_scale=e8m0)  # fp8 e4m3 kv + e8m0 scales
     window_idxs(start_pos, seqlen, window, out=idx[..., :window])
     act_quant_fp8(x, out_rt=x)                                  # in-place block-32 round trip
+
+A cache held in 4 bits (e2m1 codes, two to a byte, and e8m0 scales), and its eviction by weight:
+
+    act_quant_fp4(x, codes=codes, scales=scales)                # or window_write_fp4
+    o = sparse_attn(q, codes, sink, idx, scale, kv_scale=scales, lse=lse)
+    row_weights(q, codes, lse, idx, scale, acc, kv_scale=scales)    # acc += each row's weight
+    kept, remap = evict_select(acc, n_keep, keep_first=window)
+    codes, scales, acc = compact_rows([codes, scales, acc], kept)
+    idx = remap_idx(idx, remap)
 """
 
 from __future__ import annotations
@@ -17,13 +26,18 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (SA_KV_BF16, SA_KV_FP8_E4M3, SA_SCORE_BF16, SA_SCORE_F32, SA_STATUS_BYTES,
-                   SparseAttnError, load, status_string)
+from ._lib import (SA_KV_BF16, SA_KV_FP4_E2M1, SA_KV_FP8_E4M3, SA_SCORE_BF16, SA_SCORE_F32,
+                   SA_STATUS_BYTES, SparseAttnError, load, status_string)
 
 __all__ = ["sparse_attn", "window_idxs", "act_quant_fp8", "window_write", "indexer_topk",
            "candidate_blocks", "hc_split_sinkhorn",
+           "act_quant_fp4", "window_write_fp4", "row_weights", "evict_select", "compact_rows",
+           "remap_idx", "WEIGHT_UNIT",
            "workspace_size", "new_workspace", "read_status", "SparseAttnError", "SA_KV_BF16",
-           "SA_KV_FP8_E4M3", "SA_SCORE_F32", "SA_SCORE_BF16", "load"]
+           "SA_KV_FP8_E4M3", "SA_KV_FP4_E2M1", "SA_SCORE_F32", "SA_SCORE_BF16", "load"]
+
+# row_weights' accumulators are int64 multiples of this: acc * WEIGHT_UNIT are the weights in f32
+WEIGHT_UNIT = 2.0 ** -32
 
 
 def _ptr(t) -> ctypes.c_void_p | None:
@@ -33,6 +47,16 @@ def _ptr(t) -> ctypes.c_void_p | None:
 def _stream(stream) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _call(name, dev, stream, *args):
+    """A library call on the device its tensors are on: with that device current, on ``stream`` or
+    the device's current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    _lib.check(getattr(load(), name)(*args, ctypes.c_void_p(s.cuda_stream)), name)
 
 
 def _need(t, name, dtype, device=None):
@@ -63,27 +87,38 @@ FAMILIES = {"auto": _lib.SA_FAMILY_AUTO, "tcgen05": _lib.SA_FAMILY_TCGEN05,
             "mma": _lib.SA_FAMILY_MMA_SYNC}
 
 
+def _kv_format(kv, kv_scale, b, d, dev):
+    """The kv format of a cache: bf16 [b, rows, d] without scales; with them, uint8 [b, rows, d] is
+    e4m3 and uint8 [b, rows, d / 2] is e2m1."""
+    _need(kv, "kv", torch.bfloat16 if kv_scale is None else torch.uint8, dev)
+    widths = {d: SA_KV_BF16} if kv_scale is None else {d: SA_KV_FP8_E4M3, d // 2: SA_KV_FP4_E2M1}
+    if kv.dim() != 3 or kv.shape[0] != b or kv.shape[2] not in widths:
+        raise ValueError(f"kv shape {tuple(kv.shape)} does not match {b} sequences of head_dim {d}")
+    if kv_scale is not None:
+        _need(kv_scale, "kv_scale", torch.uint8, dev)
+        if tuple(kv_scale.shape) != (b, kv.shape[1], d // 32):
+            raise ValueError(f"kv_scale shape {tuple(kv_scale.shape)} != "
+                             f"{(b, kv.shape[1], d // 32)}")
+    return widths[kv.shape[2]]
+
+
 def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, workspace=None,
-                rope=None, family=None, stream=None) -> torch.Tensor:
+                rope=None, family=None, lse=None, stream=None) -> torch.Tensor:
     """o[b, s, h, d] (bf16) = sparse_attn(q, kv, sink, idx, softmax_scale).
 
-    q [b, s, h, d] bf16; kv [b, rows, d] bf16, or uint8 e4m3 codes with kv_scale [b, rows, d/32]
+    q [b, s, h, d] bf16; kv [b, rows, d] bf16, or uint8 e4m3 codes [b, rows, d] or uint8 e2m1
+    codes [b, rows, d / 2] (two to a byte, see act_quant_fp4) with kv_scale [b, rows, d/32]
     uint8 e8m0; sink [h] f32; idx [b, s, topk] int32 (-1 = empty).
+    lse: an f32 tensor [b, s, h] that receives the log of each softmax's denominator (the sink's
+    term included), e.g. for row_weights.
     rope=(rot, start_pos): also rotate o's last rot.shape[1] * 2 dims back by the inverse rotary
     embedding of positions start_pos + si, rot [positions, rope_dim / 2, 2] f32 (cos, sin).
     family: None (= "auto"), "tcgen05" or "mma" -- the kernel family that computes the call."""
     _need(q, "q", torch.bfloat16)
     dev = q.device
     b, s, h, d = q.shape
-    fmt = SA_KV_BF16 if kv_scale is None else SA_KV_FP8_E4M3
-    _need(kv, "kv", torch.bfloat16 if fmt == SA_KV_BF16 else torch.uint8, dev)
-    if kv.dim() != 3 or kv.shape[0] != b or kv.shape[2] != d:
-        raise ValueError(f"kv shape {tuple(kv.shape)} does not match q {tuple(q.shape)}")
+    fmt = _kv_format(kv, kv_scale, b, d, dev)
     rows = kv.shape[1]
-    if kv_scale is not None:
-        _need(kv_scale, "kv_scale", torch.uint8, dev)
-        if tuple(kv_scale.shape) != (b, rows, d // 32):
-            raise ValueError(f"kv_scale shape {tuple(kv_scale.shape)} != {(b, rows, d // 32)}")
     _need(sink, "sink", torch.float32, dev)
     if tuple(sink.shape) != (h,):
         raise ValueError(f"sink shape {tuple(sink.shape)} != ({h},)")
@@ -110,6 +145,20 @@ def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, wor
         _need(rot, "rot", torch.float32, dev)
         if rot.dim() != 3 or rot.shape[2] != 2:
             raise ValueError(f"rot shape {tuple(rot.shape)} is not [positions, rope_dim / 2, 2]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev)
+        if tuple(lse.shape) != (b, s, h):
+            raise ValueError(f"lse shape {tuple(lse.shape)} != {(b, s, h)}")
+        if family not in (None, "auto"):
+            raise ValueError("lse comes from the family that the call is routed to")
+        if rope is not None and rot.numel() == 0:
+            raise ValueError("rot is empty")
+        turn = (_ptr(rot), rot.shape[0], 2 * rot.shape[1], int(start_pos)) if rope else (None, 0, 0, 0)
+        _call("sa_sparse_attn_lse", dev, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
+              _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk, _ptr(out), _ptr(lse),
+              _ptr(workspace), workspace.numel(), *turn)
+        return out
+    if rope is not None:
         st = load().sa_sparse_attn_rope(_ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
                                         _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk,
                                         _ptr(out), _ptr(workspace), workspace.numel(), _ptr(rot),
@@ -299,6 +348,203 @@ def window_write(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=
                                 window, _ptr(rt), rts, rtb, _ptr(cd), cds, cdb, _ptr(sc), scs, scb,
                                 _stream(stream))
     _lib.check(st, "sa_window_write")
+
+
+def act_quant_fp4(x, *, out_rt=None, codes=None, scales=None, stream=None):
+    """Block-32 e2m1 quantisation of the rows of a 2-D bf16 tensor (last dim contiguous).
+
+    s = the smallest power of two with max|x| <= 6 s in the block (max|x| at least 1e-4, s at most
+    2^125), each code the e2m1 value nearest to x / s (ties to even, saturating; NaN counts as 0).
+    Writes the bf16 round trip into ``out_rt`` (may be ``x`` itself), the codes, two to a byte
+    (element 2k in the low four bits), into ``codes`` [n, d / 2] and the e8m0 block scales into
+    ``scales`` [n, d / 32] (each a 2-D tensor with unit column stride; rows may be strided)."""
+    if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda or (x.shape[1] > 1
+                                                                      and x.stride(1) != 1):
+        raise ValueError("x must be a 2-D CUDA bf16 tensor with unit column stride")
+    n, d = x.shape
+
+    def rows_of(t, name, dtype, width):
+        if t is None:
+            return None, 0
+        if (t.dim() != 2 or t.dtype != dtype or tuple(t.shape) != (n, width)
+                or (width > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name} must be a 2-D {dtype} tensor of shape ({n}, {width}) with "
+                             "unit column stride")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        return t, t.stride(0) if n > 1 else max(width, t.stride(0))
+
+    rt, rts = rows_of(out_rt, "out_rt", torch.bfloat16, d)
+    cd, cds = rows_of(codes, "codes", torch.uint8, d // 2)
+    sc, scs = rows_of(scales, "scales", torch.uint8, d // 32)
+    _call("sa_act_quant_fp4", x.device, stream, _ptr(x), n, d,
+          x.stride(0) if n > 1 else max(d, x.stride(0)), _ptr(rt), rts, _ptr(cd), cds, _ptr(sc), scs)
+
+
+def window_write_fp4(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=None):
+    """The ring write into a 4-bit cache: window_write with rows quantised as act_quant_fp4 does.
+
+    x is a 3-D CUDA bf16 tensor [nbatch, seqlen, d] (last dim contiguous, rows of a sequence
+    equally spaced, sequences seqlen rows apart); row t of x[bi] goes to ring slot
+    (start_pos + t) % window.  The rings are 3-D tensors ``codes`` [nbatch, window, d / 2],
+    ``scales`` [nbatch, window, d / 32] and ``ring_rt`` [nbatch, window, d] (bf16 round trip)
+    with unit column stride; they may be strided views of a larger cache."""
+    if x.dim() != 3 or x.stride(2) != 1 or x.dtype != torch.bfloat16 or not x.is_cuda:
+        raise ValueError("x must be a 3-D CUDA bf16 tensor with unit column stride")
+    nb, sl, d = x.shape
+    xs = x.stride(1) if sl > 1 else x.stride(0) if nb > 1 else d
+    if nb > 1 and x.stride(0) != sl * xs:
+        raise ValueError("the sequences of x must be seqlen rows apart")
+    window = None
+
+    def ring_of(t, name, dtype, width):
+        nonlocal window
+        if t is None:
+            return None, 0, 0
+        if (t.dim() != 3 or t.dtype != dtype or t.shape[0] != nb or t.shape[2] != width
+                or (width > 1 and t.stride(2) != 1)):
+            raise ValueError(f"{name} must be a 3-D {dtype} tensor of shape ({nb}, window, {width})"
+                             " with unit column stride")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        if window is None:
+            window = t.shape[1]
+        elif t.shape[1] != window:
+            raise ValueError("the rings must have the same window")
+        return t, t.stride(1) if window > 1 else max(width, t.stride(1)), t.stride(0)
+
+    rt, rts, rtb = ring_of(ring_rt, "ring_rt", torch.bfloat16, d)
+    cd, cds, cdb = ring_of(codes, "codes", torch.uint8, d // 2)
+    sc, scs, scb = ring_of(scales, "scales", torch.uint8, d // 32)
+    if window is None:
+        raise ValueError("give at least one of ring_rt, codes, scales")
+    _call("sa_window_write_fp4", x.device, stream, _ptr(x), nb, sl, d, xs, int(start_pos), window,
+          _ptr(rt), rts, rtb, _ptr(cd), cds, cdb, _ptr(sc), scs, scb)
+
+
+def row_weights(q, kv, lse, idx, softmax_scale, acc, *, kv_scale=None, workspace=None,
+                stream=None) -> torch.Tensor:
+    """Adds to acc the attention weight each cache row received:
+
+        acc[bi, idx[bi, si, c]] += sum over heads of e^(softmax_scale q.kv - lse)   (in units of 2^-32)
+
+    for every query and every entry that is not -1.  q, kv, kv_scale, idx and softmax_scale are
+    sparse_attn's; lse [b, s, h] f32 is what sparse_attn(..., lse=) wrote; acc [b, rows] int64 is
+    fixed point (acc * WEIGHT_UNIT are the weights), so the sums are the same in any order.
+    Returns acc."""
+    _need(q, "q", torch.bfloat16)
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError(f"q shape {tuple(q.shape)} is not [b, s, h, d]")
+    b, s, h, d = q.shape
+    fmt = _kv_format(kv, kv_scale, b, d, dev)
+    rows = kv.shape[1]
+    _need(lse, "lse", torch.float32, dev)
+    if tuple(lse.shape) != (b, s, h):
+        raise ValueError(f"lse shape {tuple(lse.shape)} != {(b, s, h)}")
+    _need(idx, "idx", torch.int32, dev)
+    if idx.dim() != 3 or idx.shape[0] != b or idx.shape[1] != s:
+        raise ValueError(f"idx shape {tuple(idx.shape)} does not match q {tuple(q.shape)}")
+    _need(acc, "acc", torch.int64, dev)
+    if tuple(acc.shape) != (b, rows):
+        raise ValueError(f"acc shape {tuple(acc.shape)} != {(b, rows)}")
+    if workspace is None:
+        workspace = torch.zeros(SA_STATUS_BYTES, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+    _call("sa_row_weights", dev, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(lse), _ptr(idx),
+          float(softmax_scale), b, s, h, d, rows, idx.shape[2], _ptr(acc), _ptr(workspace),
+          workspace.numel())
+    return acc
+
+
+def evict_select(acc, n_keep, *, keep_first=0, keep_last=0, live=None, stream=None):
+    """Which rows of each sequence's cache stay: (kept [b, n_keep], remap [b, rows]) int32.
+
+    acc [b, rows] int64 (row_weights'); live [b] int32: the sequences' rows in use (None: all).
+    Of a sequence's L rows in use min(n_keep, L) stay: its first keep_first and last keep_last, and
+    of the others those with the largest acc (equal ones lowest row first).  kept lists them in
+    ascending order, then -1; remap holds each row's place in kept, -1 for a row that goes."""
+    _need(acc, "acc", torch.int64)
+    if acc.dim() != 2:
+        raise ValueError(f"acc shape {tuple(acc.shape)} is not [b, rows]")
+    b, rows = acc.shape
+    if live is not None:
+        _need(live, "live", torch.int32, acc.device)
+        if tuple(live.shape) != (b,):
+            raise ValueError(f"live shape {tuple(live.shape)} != ({b},)")
+    n_keep = int(n_keep)
+    if not 0 <= n_keep <= rows:
+        raise ValueError(f"n_keep {n_keep} is not within [0, {rows}]")
+    kept = torch.empty((b, n_keep), dtype=torch.int32, device=acc.device)
+    remap = torch.empty((b, rows), dtype=torch.int32, device=acc.device)
+    _call("sa_evict_select", acc.device, stream, _ptr(acc), _ptr(live), b, rows, n_keep,
+          int(keep_first), int(keep_last), _ptr(kept), _ptr(remap))
+    return kept, remap
+
+
+def compact_rows(tensors, kept, *, out=None, stream=None):
+    """Gathers the kept rows of a list of tensors [b, rows, ...] (any dtype; e.g. a cache's codes,
+    its scales and its accumulators): row j of each result is row kept[bi, j], zeros where that is
+    -1.
+
+    ``out``: None (new tensors [b, n_keep, ...]), or a list of tensors [b, n_keep or more, ...]
+    whose first n_keep rows are written; a tensor may be its own out (in place; kept then has to
+    ascend, as evict_select's does).  Rows of a sequence are contiguous; sequences may be apart
+    (a cache's leading rows).  Returns the list of results."""
+    tensors = list(tensors)
+    _need(kept, "kept", torch.int32)
+    if kept.dim() != 2:
+        raise ValueError(f"kept shape {tuple(kept.shape)} is not [b, n_keep]")
+    b, n_keep = kept.shape
+    if not 0 < len(tensors) <= _lib.SA_COMPACT_MAX_TENSORS:
+        raise ValueError(f"give 1 to {_lib.SA_COMPACT_MAX_TENSORS} tensors")
+    outs = [None] * len(tensors) if out is None else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError("out must list one tensor for each of tensors")
+    n = len(tensors)
+    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
+    row_bytes, src_b, dst_b = ((ctypes.c_int64 * n)() for _ in range(3))
+    rows = tensors[0].shape[1] if tensors[0].dim() > 1 else -1
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or t.device != kept.device:
+            raise TypeError(f"tensors[{i}] must be a tensor on {kept.device}")
+        if t.dim() < 2 or t.shape[0] != b or t.shape[1] != rows or (b and not t[0].is_contiguous()):
+            raise ValueError(f"tensors[{i}] must be [{b}, {rows}, ...] with contiguous rows")
+        o = outs[i]
+        if o is None:
+            o = outs[i] = torch.empty((b, n_keep) + tuple(t.shape[2:]), dtype=t.dtype, device=t.device)
+        elif (o.device != t.device or o.dtype != t.dtype or o.dim() != t.dim() or o.shape[0] != b
+              or o.shape[1] < n_keep or o.shape[2:] != t.shape[2:]
+              or (b and not o[0].is_contiguous())):
+            raise ValueError(f"out[{i}] must be a {t.dtype} tensor [{b}, {n_keep} or more, ...] like "
+                             f"tensors[{i}], with contiguous rows")
+        size = t.element_size()
+        src[i], dst[i] = t.data_ptr(), o.data_ptr()
+        row_bytes[i] = size * t[0, 0].numel() if b and rows else size
+        src_b[i], dst_b[i] = size * t.stride(0), size * o.stride(0)
+    _call("sa_compact_rows", kept.device, stream, n, src, dst, row_bytes, src_b, dst_b, b, rows,
+          n_keep, _ptr(kept))
+    return outs
+
+
+def remap_idx(idx, remap, *, out=None, stream=None) -> torch.Tensor:
+    """A table of row numbers after an eviction: out[bi, ...] = remap[bi, idx[bi, ...]], -1 where
+    idx is -1.  idx int32 [b, ...], remap int32 [b, rows]; out may be idx itself."""
+    _need(idx, "idx", torch.int32)
+    _need(remap, "remap", torch.int32, idx.device)
+    if remap.dim() != 2 or idx.dim() < 1 or idx.shape[0] != remap.shape[0]:
+        raise ValueError(f"remap shape {tuple(remap.shape)} does not match idx {tuple(idx.shape)}")
+    if out is None:
+        out = torch.empty_like(idx)
+    else:
+        _need(out, "out", torch.int32, idx.device)
+        if out.shape != idx.shape:
+            raise ValueError("out must have idx's shape")
+    b, rows = remap.shape
+    _call("sa_remap_idx", idx.device, stream, _ptr(idx), b, idx.numel() // b if b else 0, _ptr(remap),
+          rows, _ptr(out))
+    return out
 
 
 def read_status(workspace, clear=False, stream=None) -> int:

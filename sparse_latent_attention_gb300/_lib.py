@@ -19,11 +19,12 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "sparse_attn.h")
 
 (SA_OK, SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_CUDA, SA_ERR_INDEX, SA_ERR_WORKSPACE,
  SA_ERR_TIMEOUT) = range(7)
-SA_KV_BF16, SA_KV_FP8_E4M3 = 0, 1
+SA_KV_BF16, SA_KV_FP8_E4M3, SA_KV_FP4_E2M1 = 0, 1, 2
 SA_FAMILY_AUTO, SA_FAMILY_TCGEN05, SA_FAMILY_MMA_SYNC = 0, 1, 2
 SA_SCORE_F32, SA_SCORE_BF16 = 0, 1
 SA_INDEXER_MAX_POSITIONS = 49152
 SA_STATUS_BYTES = 256
+SA_COMPACT_MAX_TENSORS = 8
 
 _lock = threading.Lock()
 _lib = None
@@ -73,6 +74,23 @@ def load() -> ctypes.CDLL:
         lib.sa_window_write.restype = i32
         lib.sa_window_write.argtypes = [P, i64, i64, i32, i64, i64, i32, P, i64, i64, P, i64, i64,
                                         P, i64, i64, P]
+        # include/cache/
+        lib.sa_act_quant_fp4.restype = i32
+        lib.sa_act_quant_fp4.argtypes = lib.sa_act_quant_fp8.argtypes
+        lib.sa_window_write_fp4.restype = i32
+        lib.sa_window_write_fp4.argtypes = lib.sa_window_write.argtypes
+        lib.sa_sparse_attn_lse.restype = i32
+        lib.sa_sparse_attn_lse.argtypes = [P, P, P, i32, P, P, f32, i64, i64, i32, i32, i64, i32, P,
+                                           P, P, sz, P, i64, i32, i64, P]
+        lib.sa_row_weights.restype = i32
+        lib.sa_row_weights.argtypes = [P, P, P, i32, P, P, f32, i64, i64, i32, i32, i64, i32, P, P,
+                                       sz, P]
+        lib.sa_evict_select.restype = i32
+        lib.sa_evict_select.argtypes = [P, P, i64, i64, i64, i64, i64, P, P, P]
+        lib.sa_compact_rows.restype = i32
+        lib.sa_compact_rows.argtypes = [i32, P, P, P, P, P, i64, i64, i64, P, P]
+        lib.sa_remap_idx.restype = i32
+        lib.sa_remap_idx.argtypes = [P, i64, i64, P, i64, P, P]
         lib.sa_read_status.restype = i32
         lib.sa_read_status.argtypes = [P, i32, P]
         lib.sa_status_string.restype = ctypes.c_char_p
@@ -83,10 +101,11 @@ def load() -> ctypes.CDLL:
         return lib
 
 
-def declared_symbols() -> list[str]:
-    """Names of the functions the headers under include/ declare."""
+def declared_symbols(folder: str = "") -> list[str]:
+    """Names of the functions that the headers in include/ declare, or those in a folder of it
+    ("cache": the 4-bit cache and eviction)."""
     names = set()
-    for header in sorted(glob.glob(os.path.join(os.path.dirname(HEADER), "*.h"))):
+    for header in sorted(glob.glob(os.path.join(os.path.dirname(HEADER), folder, "*.h"))):
         text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
         names.update(re.findall(r"\b(sa_[a-z0-9_]+)\s*\(", text))
     return sorted(names)

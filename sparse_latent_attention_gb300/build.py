@@ -38,7 +38,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+        os.path.join(INCLUDE, "**", "*.h"), recursive=True) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:

@@ -4,12 +4,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "cache/sa_evict.h"
 #include "sa_internal.cuh"
 #include "sparse_attn.h"
 
 namespace {
 
-constexpr int kVersion = 200;  // 0.2.0: tcgen05 family for head_dim 512 (bf16 and fp8 kv)
+constexpr int kVersion = 300;  // 0.3.0: 4-bit kv, the log-sum-exp output, row weights and eviction
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -30,12 +31,28 @@ bool supported_shape(int64_t b, int64_t s, int h, int d, int64_t rows, int topk)
 
 sa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 
+// The rotation arguments of a call (rot, npos, rope_dim, start_pos).
+sa_status check_rotation(const void* o, int64_t b, int64_t s, int h, int d, int64_t rows, int kv_format,
+                         const float* rot, int64_t npos, int rope_dim, int64_t start_pos) {
+    if (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 0 || start_pos < 0)
+        return SA_ERR_INVALID_ARG;
+    if (start_pos > npos - s) return SA_ERR_INVALID_ARG;  // positions start_pos .. start_pos + s - 1
+    if (!sa::kv_format_known(kv_format)) return SA_ERR_INVALID_ARG;
+    // the rotation is fused into the tcgen05 kernel's epilogue only
+    if (!sa::attn_tc_supports(h, d, kv_format, b, rows)) return SA_ERR_UNSUPPORTED;
+    if (b * s > 0 && (!rot || !aligned(rot, 8))) return SA_ERR_INVALID_ARG;
+    if (b * s > 0 && overlaps(o, (size_t)(b * s) * h * (size_t)d * 2, rot,
+                              (size_t)npos * rope_dim * sizeof(float)))
+        return SA_ERR_INVALID_ARG;
+    return SA_OK;
+}
+
 // The whole sparse_attn call; rope == nullptr for none (checked by the caller).
 sa_status attn_call(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,
                     const float* sink, const int32_t* idx, float softmax_scale, int64_t b, int64_t s,
                     int h, int d, int64_t rows, int topk, void* o, void* workspace,
                     size_t workspace_bytes, const float* rope, int rope_dim, int64_t rope_pos0,
-                    int family, void* stream);
+                    int family, void* stream, float* lse = nullptr);
 
 }  // namespace
 
@@ -64,7 +81,7 @@ extern "C" {
 
 size_t sa_sparse_attn_workspace_size(int64_t b, int64_t s, int h, int d, int64_t rows, int topk,
                                      int kv_format) {
-    if (kv_format != SA_KV_BF16 && kv_format != SA_KV_FP8_E4M3) return 0;
+    if (!sa::kv_format_known(kv_format)) return 0;
     if (!supported_shape(b, s, h, d, rows, topk)) return 0;
     // enough for either kernel family, whichever a call is routed to
     size_t scratch = sa::attn_mma_scratch_bytes(b, s, h, d, topk);
@@ -100,19 +117,30 @@ sa_status sa_sparse_attn_rope(const void* q, const void* kv, const uint8_t* kv_s
                               int64_t rows, int topk, void* o, void* workspace,
                               size_t workspace_bytes, const float* rot, int64_t npos, int rope_dim,
                               int64_t start_pos, void* stream) {
-    if (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 0 || start_pos < 0)
-        return SA_ERR_INVALID_ARG;
-    if (start_pos > npos - s) return SA_ERR_INVALID_ARG;  // positions start_pos .. start_pos + s - 1
-    if (kv_format != SA_KV_BF16 && kv_format != SA_KV_FP8_E4M3) return SA_ERR_INVALID_ARG;
-    // the rotation is fused into the tcgen05 kernel's epilogue only
-    if (!sa::attn_tc_supports(h, d, kv_format, b, rows)) return SA_ERR_UNSUPPORTED;
-    if (b * s > 0 && (!rot || !aligned(rot, 8))) return SA_ERR_INVALID_ARG;
-    if (b * s > 0 && overlaps(o, (size_t)(b * s) * h * (size_t)d * 2, rot,
-                              (size_t)npos * rope_dim * sizeof(float)))
-        return SA_ERR_INVALID_ARG;
+    const sa_status r = check_rotation(o, b, s, h, d, rows, kv_format, rot, npos, rope_dim, start_pos);
+    if (r != SA_OK) return r;
     return attn_call(q, kv, kv_scale, kv_format, sink, idx, softmax_scale, b, s, h, d, rows, topk,
                      o, workspace, workspace_bytes, rot, rope_dim, start_pos, SA_FAMILY_TCGEN05,
                      stream);
+}
+
+sa_status sa_sparse_attn_lse(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,
+                             const float* sink, const int32_t* idx, float softmax_scale,
+                             int64_t b, int64_t s, int h, int d, int64_t rows, int topk,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             const float* rot, int64_t npos, int rope_dim, int64_t start_pos,
+                             void* stream) {
+    if (rot) {
+        const sa_status r = check_rotation(o, b, s, h, d, rows, kv_format, rot, npos, rope_dim, start_pos);
+        if (r != SA_OK) return r;
+    }
+    if (b > 0 && s > 0 && (!lse || !aligned(lse, 4))) return SA_ERR_INVALID_ARG;
+    if (rot && b > 0 && s > 0 && h > 0 &&
+        overlaps(lse, (size_t)(b * s) * h * sizeof(float), rot, (size_t)npos * rope_dim * sizeof(float)))
+        return SA_ERR_INVALID_ARG;
+    return attn_call(q, kv, kv_scale, kv_format, sink, idx, softmax_scale, b, s, h, d, rows, topk,
+                     o, workspace, workspace_bytes, rot, rot ? rope_dim : 0, rot ? start_pos : 0,
+                     rot ? SA_FAMILY_TCGEN05 : SA_FAMILY_AUTO, stream, lse);
 }
 
 }  // extern "C"
@@ -123,8 +151,8 @@ sa_status attn_call(const void* q, const void* kv, const uint8_t* kv_scale, int 
                     const float* sink, const int32_t* idx, float softmax_scale, int64_t b, int64_t s,
                     int h, int d, int64_t rows, int topk, void* o, void* workspace,
                     size_t workspace_bytes, const float* rope, int rope_dim, int64_t rope_pos0,
-                    int family, void* stream) {
-    if (kv_format != SA_KV_BF16 && kv_format != SA_KV_FP8_E4M3) return SA_ERR_INVALID_ARG;
+                    int family, void* stream, float* lse) {
+    if (!sa::kv_format_known(kv_format)) return SA_ERR_INVALID_ARG;
     if (b < 0 || s < 0 || h < 1 || d < 1 || rows < 0 || topk < 0) return SA_ERR_INVALID_ARG;
     if (!supported_shape(b, s, h, d, rows, topk)) return SA_ERR_UNSUPPORTED;
     const int fam = sa::routed_family(family, h, d, kv_format, b, rows);
@@ -133,24 +161,33 @@ sa_status attn_call(const void* q, const void* kv, const uint8_t* kv_scale, int 
     if (b * s == 0) return SA_OK;  // nothing to compute; pointers of empty tensors may be NULL
     // kv (and kv_scale) may be NULL only when there are no rows, idx only when topk == 0
     if (!q || !sink || !o || (rows > 0 && !kv) || (topk > 0 && !idx)) return SA_ERR_INVALID_ARG;
-    if (kv_format == SA_KV_FP8_E4M3 && rows > 0 && !kv_scale) return SA_ERR_INVALID_ARG;
+    if (kv_format != SA_KV_BF16 && rows > 0 && !kv_scale) return SA_ERR_INVALID_ARG;
+    // (the tcgen05 kernel copies a row's 16 scales at once)
+    if (fam == SA_FAMILY_TCGEN05 && !aligned(kv_scale, 16)) return SA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) ||
         !aligned(idx, 4))
         return SA_ERR_INVALID_ARG;
     const size_t n_tok = (size_t)(b * s);
     const size_t o_bytes = n_tok * h * (size_t)d * 2;
-    const size_t kv_bytes = (size_t)b * rows * d * (kv_format == SA_KV_BF16 ? 2 : 1);
+    const size_t kv_bytes = (size_t)b * rows * sa::kv_row_bytes(kv_format, d);
+    const size_t lse_bytes = n_tok * h * sizeof(float);
     // every argument other than the workspace is checked before the workspace is looked at, so a
     // call without one validates the others (and enqueues nothing)
     if (overlaps(o, o_bytes, q, o_bytes) || overlaps(o, o_bytes, kv, kv_bytes) ||
         overlaps(o, o_bytes, idx, n_tok * topk * 4) || overlaps(o, o_bytes, sink, h * 4) ||
         (kv_scale && overlaps(o, o_bytes, kv_scale, (size_t)b * rows * (d / 32))))
         return SA_ERR_INVALID_ARG;
+    if (lse && (overlaps(lse, lse_bytes, o, o_bytes) || overlaps(lse, lse_bytes, q, o_bytes) ||
+                overlaps(lse, lse_bytes, kv, kv_bytes) || overlaps(lse, lse_bytes, sink, h * 4) ||
+                overlaps(lse, lse_bytes, idx, n_tok * topk * 4) ||
+                overlaps(lse, lse_bytes, kv_scale, (size_t)b * rows * (d / 32))))
+        return SA_ERR_INVALID_ARG;
     // the family this call runs in needs no more than sa_sparse_attn_workspace_size returns
     const size_t need = sa::routed_workspace_bytes(fam, b, s, h, d, rows, topk);
     if (!workspace || workspace_bytes < need) return SA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SA_ERR_INVALID_ARG;
-    if (overlaps(o, o_bytes, workspace, need)) return SA_ERR_INVALID_ARG;
+    if (overlaps(o, o_bytes, workspace, need) || overlaps(lse, lse_bytes, workspace, need))
+        return SA_ERR_INVALID_ARG;
 
     sa::AttnCall c;
     c.q = q;
@@ -174,6 +211,7 @@ sa_status attn_call(const void* q, const void* kv, const uint8_t* kv_scale, int 
     c.rope = rope;
     c.rope_dim = rope_dim;
     c.rope_pos0 = rope_pos0;
+    c.lse = lse;
     if (fam == SA_FAMILY_TCGEN05) return from_cuda(sa::attn_tc_launch(c));
     return from_cuda(sa::attn_mma_launch(c));
 }

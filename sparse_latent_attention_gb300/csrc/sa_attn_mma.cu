@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "sa_fp4.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.cuh"
 
@@ -36,6 +37,7 @@ struct Params {
     const float* sink;
     const int32_t* idx;
     __nv_bfloat16* o;
+    float* lse;       // [tokens][h] log-sum-exp output, or nullptr
     float* part_ml;   // [tokens][splits][h][2]  (running max in log2 units, sum)
     float* part_o;    // [tokens][splits][h][d]
     uint32_t* status;
@@ -99,7 +101,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 using fp8::dequant16;
 using fp8::e8m0_to_f32;
 
-template <int D, bool kFp8>
+template <int D, int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
     constexpr int LD = D + kPad;          // smem row stride in elements
     constexpr int DH = D / 2;             // d columns per warp
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
     // it copies; an index outside [-1, rows) counts as -1 and raises the status bit.
     auto gather = [&](int t, int st) {
         __nv_bfloat16* base = sKV + st * kTN * LD;
-        if constexpr (!kFp8) {
+        if constexpr (kFmt == SA_KV_BF16) {
             const __nv_bfloat16* kvb =
                 reinterpret_cast<const __nv_bfloat16*>(p.kv) + bi * p.rows * (int64_t)D;
             for (int c = threadIdx.x; c < kTN * CH; c += kThreads) {
@@ -163,9 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
                 cp_async16(base + r * LD + k * 8, src, j >= 0 ? 16 : 0);
             }
         } else {
-            const uint8_t* kvb = reinterpret_cast<const uint8_t*>(p.kv) + bi * p.rows * (int64_t)D;
+            // 16 bytes of codes a step: 16 e4m3 or 32 e2m1
+            constexpr int kPer = kFmt == SA_KV_FP4_E2M1 ? 32 : 16;
+            constexpr int kRowBytes = 16 * D / kPer;
+            const uint8_t* kvb = reinterpret_cast<const uint8_t*>(p.kv) + bi * p.rows * (int64_t)kRowBytes;
             const uint8_t* scb = p.kv_scale + bi * p.rows * (int64_t)(D / 32);
-            constexpr int CH8 = D / 16;  // 16-code chunks per row
+            constexpr int CH8 = D / kPer;
             for (int c = threadIdx.x; c < kTN * CH8; c += kThreads) {
                 const int r = c / CH8, k = c - r * CH8;
                 const int col = t * kTN + r;
@@ -175,16 +180,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
                     j = -1;
                 }
                 if (k == 0) sRow[st * kTN + r] = j;
-                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                uint4 v[kPer / 8];
+#pragma unroll
+                for (int i = 0; i < kPer / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
                 if (j >= 0) {
                     const uint4 codes =
-                        __ldg(reinterpret_cast<const uint4*>(kvb + (int64_t)j * D + k * 16));
-                    const float sc = e8m0_to_f32(__ldg(scb + (int64_t)j * (D / 32) + k / 2));
-                    dequant16(codes, sc, lo, hi);
+                        __ldg(reinterpret_cast<const uint4*>(kvb + (int64_t)j * kRowBytes + k * 16));
+                    const uint32_t se = __ldg(scb + (int64_t)j * (D / 32) + k * kPer / 32);
+                    if constexpr (kFmt == SA_KV_FP4_E2M1) {
+                        const float sc = fp4::scale_f32(se);
+                        fp4::dequant16(make_uint2(codes.x, codes.y), sc, v[0], v[1]);
+                        fp4::dequant16(make_uint2(codes.z, codes.w), sc, v[2], v[3]);
+                    } else {
+                        dequant16(codes, e8m0_to_f32(se), v[0], v[1]);
+                    }
                 }
-                uint4* dst = reinterpret_cast<uint4*>(base + r * LD + k * 16);
-                dst[0] = lo;
-                dst[1] = hi;
+                uint4* dst = reinterpret_cast<uint4*>(base + r * LD + k * kPer);
+#pragma unroll
+                for (int i = 0; i < kPer / 8; ++i) dst[i] = v[i];
             }
         }
     };
@@ -318,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
         float inv0 = 0.f, inv1 = 0.f;
         if (r0 < hc && l0 > 0.f) inv0 = 1.f / (l0 + fast_exp2(p.sink[h0 + r0] * kLog2e - mu0));
         if (r1 < hc && l1 > 0.f) inv1 = 1.f / (l1 + fast_exp2(p.sink[h0 + r1] * kLog2e - mu1));
+        if (p.lse && t4 == 0 && dh == 0) {
+            if (r0 < hc) p.lse[token * p.h + h0 + r0] = log_sum_exp(l0, mu0, p.sink[h0 + r0]);
+            if (r1 < hc) p.lse[token * p.h + h0 + r1] = log_sum_exp(l1, mu1, p.sink[h0 + r1]);
+        }
         __nv_bfloat16* orow0 = p.o + (token * p.h + h0 + r0) * (int64_t)D + dh * DH;
         __nv_bfloat16* orow1 = p.o + (token * p.h + h0 + r1) * (int64_t)D + dh * DH;
 #pragma unroll
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
 __global__ void attn_combine_kernel(const float* __restrict__ part_ml,
                                     const float* __restrict__ part_o,
                                     const float* __restrict__ sink, __nv_bfloat16* __restrict__ o,
-                                    int h, int d, int n_splits) {
+                                    float* __restrict__ lse, int h, int d, int n_splits) {
     // the attention kernel this launch depends on has completed and its partials are visible
     // after this point
     pdl_wait();
@@ -405,10 +422,18 @@ __global__ void attn_combine_kernel(const float* __restrict__ part_ml,
     }
     const float Mu = M == -INFINITY ? 0.f : M;
     const float inv = L > 0.f ? 1.f / (L + fast_exp2(sink[hh] * kLog2e - Mu)) : 0.f;
+    if (lse && threadIdx.x == 0) lse[th] = log_sum_exp(L, Mu, sink[hh]);
     uint2 out;
     out.x = pack_bf16(acc.x * inv, acc.y * inv);
     out.y = pack_bf16(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(o + th * (int64_t)d + c) = out;
+}
+
+__global__ void lse_of_sinks_kernel(float* lse, const float* sink, int64_t n, int h) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (i < n) lse[i] = sink[i % h];
 }
 
 struct Geometry {
@@ -438,7 +463,7 @@ size_t smem_bytes(int d) {
     return (size_t)(kHeadsPerCta + 2 * kTN) * (d + kPad) * 2 + 2 * kTN * sizeof(int);
 }
 
-template <int D, bool kFp8>
+template <int D, int kFmt>
 cudaError_t launch_t(const AttnCall& c, const Params& p, dim3 grid) {
     static bool configured[64] = {};  // per template instance and device
     const size_t smem = smem_bytes(D);
@@ -446,25 +471,25 @@ cudaError_t launch_t(const AttnCall& c, const Params& p, dim3 grid) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(attn_mma_kernel<D, kFp8>,
+        e = cudaFuncSetAttribute(attn_mma_kernel<D, kFmt>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
-    return launch_pdl(attn_mma_kernel<D, kFp8>, grid, dim3(kThreads), smem, c.stream, p);
+    return launch_pdl(attn_mma_kernel<D, kFmt>, grid, dim3(kThreads), smem, c.stream, p);
 }
 
-template <bool kFp8>
+template <int kFmt>
 cudaError_t launch_d(const AttnCall& c, const Params& p, dim3 grid) {
     switch (c.d) {
-        case 64: return launch_t<64, kFp8>(c, p, grid);
-        case 128: return launch_t<128, kFp8>(c, p, grid);
-        case 192: return launch_t<192, kFp8>(c, p, grid);
-        case 256: return launch_t<256, kFp8>(c, p, grid);
-        case 320: return launch_t<320, kFp8>(c, p, grid);
-        case 384: return launch_t<384, kFp8>(c, p, grid);
-        case 448: return launch_t<448, kFp8>(c, p, grid);
-        case 512: return launch_t<512, kFp8>(c, p, grid);
+        case 64: return launch_t<64, kFmt>(c, p, grid);
+        case 128: return launch_t<128, kFmt>(c, p, grid);
+        case 192: return launch_t<192, kFmt>(c, p, grid);
+        case 256: return launch_t<256, kFmt>(c, p, grid);
+        case 320: return launch_t<320, kFmt>(c, p, grid);
+        case 384: return launch_t<384, kFmt>(c, p, grid);
+        case 448: return launch_t<448, kFmt>(c, p, grid);
+        case 512: return launch_t<512, kFmt>(c, p, grid);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -490,6 +515,7 @@ cudaError_t attn_mma_launch(const AttnCall& c) {
     p.sink = c.sink;
     p.idx = c.idx;
     p.o = reinterpret_cast<__nv_bfloat16*>(c.o);
+    p.lse = c.lse;
     p.status = c.status;
     p.scale_log2 = c.softmax_scale * kLog2e;
     p.s_len = c.s;
@@ -508,21 +534,31 @@ cudaError_t attn_mma_launch(const AttnCall& c) {
     }
     if (n_tokens > 0x7FFFFFFF) return cudaErrorInvalidValue;
     dim3 grid((unsigned)n_tokens, g.n_splits, g.hblocks);
-    cudaError_t e = c.kv_format == SA_KV_BF16 ? launch_d<false>(c, p, grid) : launch_d<true>(c, p, grid);
+    cudaError_t e = c.kv_format == SA_KV_BF16       ? launch_d<SA_KV_BF16>(c, p, grid)
+                    : c.kv_format == SA_KV_FP8_E4M3 ? launch_d<SA_KV_FP8_E4M3>(c, p, grid)
+                                                    : launch_d<SA_KV_FP4_E2M1>(c, p, grid);
     if (e != cudaSuccess || g.n_splits == 1) return e;
-    return attn_combine_launch(p.part_ml, p.part_o, c.sink, p.o, n_tokens, c.h, c.d, g.n_splits,
+    return attn_combine_launch(p.part_ml, p.part_o, c.sink, p.o, c.lse, n_tokens, c.h, c.d, g.n_splits,
                                c.stream);
 }
 
 cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const float* sink,
-                                void* o, int64_t n_tokens, int h, int d, int n_splits,
+                                void* o, float* lse, int64_t n_tokens, int h, int d, int n_splits,
                                 cudaStream_t stream) {
     if (n_tokens * h == 0) return cudaSuccess;
     // a programmatic dependent of the attention kernel just queued on the stream: its blocks can
     // be scheduled while that kernel drains, and wait for its partials
     return launch_pdl(attn_combine_kernel, dim3((unsigned)(n_tokens * h)), dim3((unsigned)(d / 4)), 0,
-                      stream, part_ml, part_o, sink, reinterpret_cast<__nv_bfloat16*>(o), h, d,
+                      stream, part_ml, part_o, sink, reinterpret_cast<__nv_bfloat16*>(o), lse, h, d,
                       n_splits);
+}
+
+cudaError_t lse_of_sinks_launch(float* lse, const float* sink, int64_t n_tokens, int h,
+                                cudaStream_t stream) {
+    const int64_t n = n_tokens * h;  // below 2^31
+    if (n == 0) return cudaSuccess;
+    return launch_pdl(lse_of_sinks_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, lse,
+                      sink, n, h);
 }
 
 }  // namespace sa

@@ -27,10 +27,10 @@
 //               its tile and the softmax and P.V of the other tile overlap
 //   warp 1      Q loads (TMA, 128-byte swizzle) and an L2 prefetch of the next task's Q
 //   warps 2-5   kv row gather: the 128 idx columns of a pair of tiles at a time, one per thread;
-//               cp.async 16 B into the swizzled layout (fp8 rows are staged raw and widened in
+//               cp.async 16 B into the swizzled layout (rows of codes are staged raw and widened in
 //               place); rows already resident from the previous pair are kept -- see below
 //   warps 6-9   softmax: S -> P (bf16, shared memory), running max and sum, O rescale
-//   warps 10-13 epilogue: O^T -> o (bf16) or split partials; with fp8 kv, between epilogues,
+//   warps 10-13 epilogue: O^T -> o (bf16) or split partials; with fp8 or fp4 kv, between epilogues,
 //               they widen the second half (d 256-511) of every staged tile
 // Every wait is bounded; a wait that gives up raises the timeout bit and every role unwinds.
 //
@@ -50,6 +50,7 @@
 
 #include <mutex>
 
+#include "sa_fp4.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.cuh"
 #include "sa_tc.cuh"
@@ -119,11 +120,12 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 struct Params {
     const __nv_bfloat16* q;    // for the L2 prefetch of the next task's rows
     const __nv_bfloat16* kv;   // bf16 rows (bf16 kv)
-    const uint8_t* kv8;        // e4m3 rows and their e8m0 scales (fp8 kv)
+    const uint8_t* kv8;        // e4m3 or e2m1 rows and their e8m0 scales (fp8, fp4 kv)
     const uint8_t* kv_scale;
     const float* sink;
     const int32_t* idx;
     __nv_bfloat16* o;
+    float* lse;           // [token][h] log-sum-exp output, or nullptr
     float* part_ml;
     float* part_o;
     uint32_t* status;
@@ -289,11 +291,12 @@ __device__ __forceinline__ uint32_t kv_unit_off(int ps, int u) {
            ((((uint32_t)u & 7) ^ ((uint32_t)ps & 7)) << 4);
 }
 
-// Widens 128-d chunks c0 .. c1 - 1 of the fp8 rows a warp lists, in place: the e4m3 codes of chunk
-// c sit raw in 64-d block 2c + 1 of the row's slot and become bf16 in blocks 2c and 2c + 1 (exact:
-// see sa_fp8.cuh).  Lane l moves 16-code unit l % 8 (`unit`) of list entries l / 8 + 4 i (ent[i],
-// x < 0 = none); the row's 16 e8m0 scales are in fp8_sc.
-__device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const int2 (&ent)[8], int unit,
+// Widens 128-d chunks c0 .. c1 - 1 of the fp8 or fp4 rows a warp lists, in place: the codes of chunk c
+// (128 bytes of e4m3, 64 of e2m1) sit raw in 64-d block 2c + 1 of the row's slot and become bf16 in
+// blocks 2c and 2c + 1 (exact: see sa_fp8.cuh, sa_fp4.cuh).  Lane l moves 16-code unit l % 8 (`unit`)
+// of list entries l / 8 + 4 i (ent[i], x < 0 = none); the row's 16 e8m0 scales are in fp8_sc.
+template <int kFmt>
+__device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const int2 (&ent)[8], int unit,
                                           int c0, int c1) {
     // Per entry, once: the slot's offset inside a 64-d block (buffer and row) and the byte offset
     // of this lane's first bf16 unit in it.  Unit u = 16 c + 2 unit of the row sits in block
@@ -307,10 +310,11 @@ __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const in
         rb[i] = (r >> 6) * kBlkBytes + (r & 63) * 128;
         xo[i] = rb[i] + (uo ^ ((r & 7) << 4));
     }
+    constexpr int kUnitBytes = kFmt == SA_KV_FP4_E2M1 ? 8 : 16;  // sixteen codes
     const uint8_t* sc_base = &M.fp8_sc[0][0] + (unit >> 1);
 #pragma unroll 1
     for (int cw = c0; cw < c1; ++cw) {
-        const uint32_t code_at = s_kv + (2 * cw + 1) * kDBlkBytes + unit * 16;
+        const uint32_t code_at = s_kv + (2 * cw + 1) * kDBlkBytes + unit * kUnitBytes;
         const uint32_t out_at = s_kv + (2 * cw + (unit >> 2)) * kDBlkBytes;
         // entries in two groups of four; a row's 8 lanes read all its codes before any writes
 #pragma unroll
@@ -321,11 +325,19 @@ __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const in
             for (int i = 0; i < 4; ++i) {
                 const int2 en = ent[4 * g + i];
                 if (en.x < 0) break;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
-                             : "r"(code_at + rb[4 * g + i])
-                             : "memory");
-                sc[i] = fp8::e8m0_to_f32(sc_base[en.y * 16 + 4 * cw]);
+                if constexpr (kFmt == SA_KV_FP4_E2M1) {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                 : "=r"(code[i].x), "=r"(code[i].y)
+                                 : "r"(code_at + rb[4 * g + i])
+                                 : "memory");
+                    sc[i] = fp4::scale_f32(sc_base[en.y * 16 + 4 * cw]);
+                } else {
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
+                                 : "r"(code_at + rb[4 * g + i])
+                                 : "memory");
+                    sc[i] = fp8::e8m0_to_f32(sc_base[en.y * 16 + 4 * cw]);
+                }
             }
             __syncwarp();
 #pragma unroll
@@ -333,7 +345,10 @@ __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const in
                 const int2 en = ent[4 * g + i];
                 if (en.x < 0) break;
                 uint4 lo, hi;
-                fp8::dequant16(code[i], sc[i], lo, hi);
+                if constexpr (kFmt == SA_KV_FP4_E2M1)
+                    fp4::dequant16(make_uint2(code[i].x, code[i].y), sc[i], lo, hi);
+                else
+                    fp8::dequant16(code[i], sc[i], lo, hi);
                 const uint32_t at = out_at + xo[4 * g + i];
                 st_shared_v4(at, lo.x, lo.y, lo.z, lo.w);
                 st_shared_v4(at ^ 16u, hi.x, hi.y, hi.z, hi.w);
@@ -344,9 +359,11 @@ __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const in
 
 // kRope: the inverse rotation of o's rope dims is fused into the epilogue (a separate
 // instantiation, so that the plain kernel carries none of its code)
-template <bool kFp8, bool kRope>
+template <int kFmt, bool kRope>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
+    constexpr bool kCodes = kFmt != SA_KV_BF16;  // rows of codes, widened in shared memory
+    constexpr int kRowBytes = kFmt == SA_KV_FP4_E2M1 ? kD / 2 : kD;  // a row's codes
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -363,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&M.q_full), 1);
         mbar_init(smem_addr(&M.q_empty), 1);
         for (int b = 0; b < 2; ++b) {
-            // fp8: the epilogue warps widen half of every tile, so they arrive too
-            mbar_init(smem_addr(&M.kv_full[b]), kFp8 ? kProdThreads + 128 : kProdThreads);
+            // codes: the epilogue warps widen half of every tile, so they arrive too
+            mbar_init(smem_addr(&M.kv_full[b]), kCodes ? kProdThreads + 128 : kProdThreads);
             mbar_init(smem_addr(&M.staged[b]), kProdThreads);
             mbar_init(smem_addr(&M.kv_empty[b]), 1);
             mbar_init(smem_addr(&M.s_full[b]), 1);
@@ -605,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int half = slot >> 6;
                 const uint32_t mh0 = __ballot_sync(0xFFFFFFFFu, copy && half == 0);
                 const uint32_t mh1 = __ballot_sync(0xFFFFFFFFu, copy && half == 1);
-                if constexpr (kFp8) {
+                if constexpr (kCodes) {
                     // the epilogue warps read the previous pair's lists until they have widened
                     // its tiles (their arrival completes a tile's kv_full)
                     if (T > 0 && !(ok = mbar_wait(smem_addr(&M.kv_full[(T - 1) & 1]), ((T - 1) >> 1) & 1, abort)))
@@ -622,20 +639,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     M.copy_list[pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
                     // the buffers are usually still in use: pull the new rows into L2 now, so
                     // that the copies issued once a buffer is released hit L2
-                    if constexpr (kFp8) {
-                        prefetch_l2(p.kv8 + (bi * p.rows + j) * (int64_t)kD, kD);
+                    if constexpr (kCodes) {
+                        prefetch_l2(p.kv8 + (bi * p.rows + j) * (int64_t)kRowBytes, kRowBytes);
                         prefetch_l2(p.kv_scale + (bi * p.rows + j) * (int64_t)(kD / 32), kD / 32);
                     } else {
                         prefetch_l2(p.kv + (bi * p.rows + j) * (int64_t)kD, kD * 2);
                     }
                 }
                 __syncwarp();
-                if constexpr (kFp8) {
-                    // e4m3 rows: chunk c's 128 codes of each listed row are staged raw in block
+                if constexpr (kCodes) {
+                    // rows of codes: chunk c's 128 codes of each listed row are staged raw in block
                     // 2c + 1 of the row's slot (dead until the row is written), then widened in
-                    // place to bf16 in blocks 2c and 2c + 1.  Lane l moves 16-code unit l % 8 of
-                    // rows l / 8 + 4 i.
-                    const uint8_t* kvb8 = p.kv8 + bi * p.rows * (int64_t)kD;
+                    // place to bf16 in blocks 2c and 2c + 1.  Lane l moves 16-byte units l % 8,
+                    // l % 8 + 8, ... of rows l / 8 + 4 i.
+                    const uint8_t* kvb8 = p.kv8 + bi * p.rows * (int64_t)kRowBytes;
                     const uint8_t* scb = p.kv_scale + bi * p.rows * (int64_t)(kD / 32);
                     const int unit = lane & 7;
                     // stage each tile as soon as its buffer is released (one commit group per
@@ -668,13 +685,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i) {
                             if (ent8[i].x < 0) break;
                             const uint32_t r = (uint32_t)ent8[i].y;
-                            const uint32_t sb =
-                                s_kv + kDBlkBytes + (r >> 6) * kBlkBytes + (r & 63) * 128 + unit * 16;
-                            const uint8_t* gb = kvb8 + (int64_t)ent8[i].x * kD + unit * 16;
-                            cp_async16_at<0, 0>(sb, gb);
-                            cp_async16_at<2 * kDBlkBytes, 128>(sb, gb);
-                            cp_async16_at<4 * kDBlkBytes, 256>(sb, gb);
-                            cp_async16_at<6 * kDBlkBytes, 384>(sb, gb);
+                            const uint32_t row_at = s_kv + kDBlkBytes + (r >> 6) * kBlkBytes + (r & 63) * 128;
+                            const uint8_t* gb = kvb8 + (int64_t)ent8[i].x * kRowBytes + unit * 16;
+                            if constexpr (kFmt == SA_KV_FP4_E2M1) {
+                                // a chunk is four 16-byte units: units 0-3 chunk 0, 4-7 chunk 1, ...
+                                const uint32_t sb = row_at + (uint32_t)(unit >> 2) * (2 * kDBlkBytes) +
+                                                    (uint32_t)(unit & 3) * 16;
+                                cp_async16_at<0, 0>(sb, gb);
+                                cp_async16_at<4 * kDBlkBytes, 128>(sb, gb);
+                            } else {
+                                const uint32_t sb = row_at + unit * 16;
+                                cp_async16_at<0, 0>(sb, gb);
+                                cp_async16_at<2 * kDBlkBytes, 128>(sb, gb);
+                                cp_async16_at<4 * kDBlkBytes, 256>(sb, gb);
+                                cp_async16_at<6 * kDBlkBytes, 384>(sb, gb);
+                            }
                         }
                         cp_async_commit();
                     }
@@ -689,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(smem_addr(&M.staged[b]));
                         int2 ent8[8];
                         load_ent(hx, ent8);
-                        widen_fp8(s_kv, M, ent8, unit, 0, 2);
+                        widen_codes<kFmt>(s_kv, M, ent8, unit, 0, 2);
                         fence_proxy_async_smem();
                         mbar_arrive(smem_addr(&M.kv_full[b]));
                     }
@@ -903,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t k = 0;
         bool ok = true;
         Task t = task_of(p, tb);
-        // fp8: the next tile whose chunks 2 and 3 this warpgroup widens (warp q4 takes the rows
+        // codes: the next tile whose chunks 2 and 3 this warpgroup widens (warp q4 takes the rows
         // producer warp q4 listed)
         int64_t wtau = p.n_tiles > 0 ? tb : te;
         int wsplit = t.split, wt0 = t.t0, wt1 = t.t1, wti = t.t0;
@@ -921,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rope_last = reinterpret_cast<const float2*>(
                         p.rope)[(p.rope_pos0 + t.pos) * (p.rope_dim / 2) + ((dd - first) >> 1)];
             }
-            if constexpr (kFp8) {
+            if constexpr (kCodes) {
                 // widen every tile the producers have staged until this task's O is complete
                 // (its last tile needs this warpgroup's widening first); the poll is bounded
                 uint32_t idle = 0;
@@ -936,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int e = (lane >> 3) + 4 * i;
                             ent8[i] = e < ncopy ? M.copy_list[q4][hx][e] : make_int2(-1, 0);
                         }
-                        widen_fp8(s_kv, M, ent8, lane & 7, 2, 4);
+                        widen_codes<kFmt>(s_kv, M, ent8, lane & 7, 2, 4);
                         fence_proxy_async_smem();
                         mbar_arrive(smem_addr(&M.kv_full[wT & 1]));
                         ++wT;
@@ -976,8 +1001,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p.part_ml[(pbase + h) * 2 + 0] = mu;
                             p.part_ml[(pbase + h) * 2 + 1] = l;
                         }
-                    } else if (l > 0.f) {
-                        inv = 1.f / (l + fast_exp2(M.sink[h] * kLog2e - mu));
+                    } else {
+                        if (l > 0.f) inv = 1.f / (l + fast_exp2(M.sink[h] * kLog2e - mu));
+                        if (p.lse && q4 == 0)
+                            p.lse[t.token * p.h + h0 + h] = log_sum_exp(l, mu, M.sink[h]);
                     }
                 }
                 M.inv[q4][h] = inv;
@@ -1081,6 +1108,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// by kv format, without and with the fused rotation
+void (*const kKernels[6])(const CUtensorMap, Params) = {
+    attn_tc_kernel<SA_KV_BF16, false>,     attn_tc_kernel<SA_KV_BF16, true>,
+    attn_tc_kernel<SA_KV_FP8_E4M3, false>, attn_tc_kernel<SA_KV_FP8_E4M3, true>,
+    attn_tc_kernel<SA_KV_FP4_E2M1, false>, attn_tc_kernel<SA_KV_FP4_E2M1, true>};
+
 struct TcGeometry {
     int n_tiles, hblocks, n_splits, tiles_per_split;
 };
@@ -1116,7 +1149,7 @@ bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows) {
     (void)h;
     (void)b;
     (void)rows;
-    return d == kD && (kv_format == SA_KV_BF16 || kv_format == SA_KV_FP8_E4M3);
+    return d == kD && kv_format_known(kv_format);
 }
 
 size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk) {
@@ -1129,8 +1162,10 @@ size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk) {
 
 cudaError_t attn_tc_launch(const AttnCall& c) {
     const int64_t n_tokens = c.b * c.s;
-    if (c.topk == 0)  // no row at all: o is the zero of an empty sum (rotated or not)
-        return cudaMemsetAsync(c.o, 0, (size_t)n_tokens * c.h * kD * 2, c.stream);
+    if (c.topk == 0) {  // no row at all: o is the zero of an empty sum (rotated or not)
+        const cudaError_t e = cudaMemsetAsync(c.o, 0, (size_t)n_tokens * c.h * kD * 2, c.stream);
+        return e == cudaSuccess && c.lse ? lse_of_sinks_launch(c.lse, c.sink, n_tokens, c.h, c.stream) : e;
+    }
     const TcGeometry g = tc_geometry(n_tokens, c.h, c.topk, device_sm_count());
     auto encode = encode_fn();
     if (!encode) return cudaErrorNotSupported;
@@ -1146,14 +1181,15 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
 
     Params p;
-    const bool fp8 = c.kv_format == SA_KV_FP8_E4M3;
+    const bool codes = c.kv_format != SA_KV_BF16;
     p.q = reinterpret_cast<const __nv_bfloat16*>(c.q);
     p.rope = c.rope;
     p.rope_dim = c.rope_dim;
     p.rope_pos0 = c.rope_pos0;
-    p.kv = fp8 ? nullptr : reinterpret_cast<const __nv_bfloat16*>(c.kv);
-    p.kv8 = fp8 ? reinterpret_cast<const uint8_t*>(c.kv) : nullptr;
-    p.kv_scale = fp8 ? c.kv_scale : nullptr;
+    p.kv = codes ? nullptr : reinterpret_cast<const __nv_bfloat16*>(c.kv);
+    p.kv8 = codes ? reinterpret_cast<const uint8_t*>(c.kv) : nullptr;
+    p.kv_scale = codes ? c.kv_scale : nullptr;
+    p.lse = c.lse;
     p.sink = c.sink;
     p.idx = c.idx;
     p.o = reinterpret_cast<__nv_bfloat16*>(c.o);
@@ -1181,10 +1217,7 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !configured[dev]) {
-        void (*const fns[4])(const CUtensorMap, Params) = {
-            attn_tc_kernel<false, false>, attn_tc_kernel<true, false>, attn_tc_kernel<false, true>,
-            attn_tc_kernel<true, true>};
-        for (auto fn : fns) {
+        for (auto fn : kKernels) {
             e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)kSmemBytes);
             if (e != cudaSuccess) return e;
@@ -1196,11 +1229,10 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     if (groups < 1) groups = 1;
     const int64_t grid = groups * g.hblocks;
     const bool rope = c.rope != nullptr;
-    auto kernel = fp8 ? (rope ? attn_tc_kernel<true, true> : attn_tc_kernel<true, false>)
-                      : (rope ? attn_tc_kernel<false, true> : attn_tc_kernel<false, false>);
+    auto kernel = kKernels[2 * c.kv_format + (rope ? 1 : 0)];
     e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, c.stream, qmap, p);
     if (e != cudaSuccess || g.n_splits == 1) return e;
-    return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, n_tokens, c.h, kD, g.n_splits,
+    return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, n_tokens, c.h, kD, g.n_splits,
                                c.stream);
 }
 

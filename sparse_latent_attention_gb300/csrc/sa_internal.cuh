@@ -44,19 +44,40 @@ struct AttnCall {
     const float* rope = nullptr;
     int rope_dim = 0;
     int64_t rope_pos0 = 0;
+    float* lse = nullptr;  // [tokens][h] log-sum-exp output, or none
 };
+
+// The three kv formats: whether a value names one, and the bytes of a row's kv and scales.
+inline bool kv_format_known(int f) {
+    return f == SA_KV_BF16 || f == SA_KV_FP8_E4M3 || f == SA_KV_FP4_E2M1;
+}
+inline int64_t kv_row_bytes(int f, int d) {
+    return f == SA_KV_BF16 ? 2 * (int64_t)d : f == SA_KV_FP8_E4M3 ? d : d / 2;
+}
+
+// The logarithm of a softmax denominator l 2^m + e^sink (m in log2 units; l = 0: no row, the sink
+// alone), relative to the larger of the two terms so that neither overflows.
+__device__ __forceinline__ float log_sum_exp(float l, float m, float sink) {
+    if (!(l > 0.f)) return sink;
+    const float s2 = sink * 1.4426950408889634f, top = fmaxf(m, s2);
+    return (top + log2f(fmaf(l, exp2f(m - top), exp2f(s2 - top)))) * 0.6931471805599453f;
+}
+
+// lse[t][h] = sink[h]: a call whose queries list no row (sa_attn_mma.cu)
+cudaError_t lse_of_sinks_launch(float* lse, const float* sink, int64_t n_tokens, int h,
+                                cudaStream_t stream);
 
 // mma.sync family (sa_attn_mma.cu)
 size_t attn_mma_scratch_bytes(int64_t b, int64_t s, int h, int d, int topk);
 cudaError_t attn_mma_launch(const AttnCall& c);
 // merge of split partials: part_ml [tokens][splits][h][2] (max in log2 units, sum),
-// part_o [tokens][splits][h][d] f32 -> o bf16 (sa_attn_mma.cu)
+// part_o [tokens][splits][h][d] f32 -> o bf16, and lse unless it is nullptr (sa_attn_mma.cu)
 cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const float* sink,
-                                void* o, int64_t n_tokens, int h, int d, int n_splits,
+                                void* o, float* lse, int64_t n_tokens, int h, int d, int n_splits,
                                 cudaStream_t stream);
 
 // tcgen05 family (sa_attn_tc.cu)
-// d = 512 with bf16 kv
+// d = 512, every kv format
 bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows);
 size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk);
 cudaError_t attn_tc_launch(const AttnCall& c);

@@ -62,7 +62,7 @@ extern "C" sa_status sa_sparse_attn_static_scratch(
     const void* q, const void* kv, const uint8_t* kv_scale, int kv_format, const float* sink,
     const int32_t* idx, float softmax_scale, int64_t b, int64_t s, int h, int d, int64_t rows,
     int topk, void* o, uint32_t* status_out, void* stream) {
-    if (kv_format != SA_KV_BF16 && kv_format != SA_KV_FP8_E4M3) return SA_ERR_INVALID_ARG;
+    if (!sa::kv_format_known(kv_format)) return SA_ERR_INVALID_ARG;
     if (b < 0 || s < 0 || h < 1 || d < 1 || rows < 0 || topk < 0) return SA_ERR_INVALID_ARG;
     if (sa_sparse_attn_workspace_size(b, s, h, d, rows, topk, kv_format) == 0) return SA_ERR_UNSUPPORTED;
     // the scratch of the family sa_sparse_attn routes this call to
