@@ -190,26 +190,12 @@ __device__ __forceinline__ void task_step(const Params& p, Task& t) {
     if (t.t1 < t.t0) t.t1 = t.t0;
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Three-input maximum and minimum, and f32 pairs (two lanes of one 64-bit register) for the packed
-// FMA and add.
+// Three-input maximum and minimum.
 __device__ __forceinline__ float max3f(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -218,24 +204,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
 __device__ __forceinline__ float min3f(float a, float b, float c) {
     float r;
     asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -264,24 +232,12 @@ __device__ __forceinline__ uint32_t pack_bf16_2(uint64_t v) {
     return pack_bf16(lo, hi);
 }
 
-// mbar_wait by every lane of a converged warp, with a warp-uniform result.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
-
 // Barrier among the 128 threads of one warpgroup, on an mbarrier so that it is bounded.
 __device__ __forceinline__ bool wg_sync(uint32_t bar, uint32_t& phase, volatile int* abort) {
     mbar_arrive(bar);
     const bool ok = mbar_wait(bar, phase & 1, abort);
     ++phase;
     return ok;
-}
-
-// A 16-byte cp.async at constant offsets from a shared and a global base address.
-template <uint32_t kSOff, int kGOff>
-__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(dst), "l"(src), "n"(kSOff),
-                 "n"(kGOff));
 }
 
 // Byte offset, inside the kv buffers, of 16-byte unit u (of 64) of the row in slot ps (bit 6 =
@@ -1094,20 +1050,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
 // by kv format, without and with the fused rotation
 void (*const kKernels[6])(const CUtensorMap, Params) = {
     attn_tc_kernel<SA_KV_BF16, false>,     attn_tc_kernel<SA_KV_BF16, true>,
@@ -1145,6 +1087,33 @@ TcGeometry tc_geometry(int64_t n_tokens, int h, int topk, int sms) {
 
 }  // namespace
 
+// The driver's encoder, looked up once.
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+bool encode_rows_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows) {
+    auto encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t gdim[2] = {(cuuint64_t)d, (cuuint64_t)n};
+    const cuuint64_t gstride[1] = {(cuuint64_t)d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t estride[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(rows), gdim, gstride, box,
+                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows) {
     (void)h;
     (void)b;
@@ -1167,18 +1136,8 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
         return e == cudaSuccess && c.lse ? lse_of_sinks_launch(c.lse, c.sink, n_tokens, c.h, c.stream) : e;
     }
     const TcGeometry g = tc_geometry(n_tokens, c.h, c.topk, device_sm_count());
-    auto encode = encode_fn();
-    if (!encode) return cudaErrorNotSupported;
     CUtensorMap qmap;
-    const cuuint64_t gdim[2] = {(cuuint64_t)kD, (cuuint64_t)(n_tokens * c.h)};
-    const cuuint64_t gstride[1] = {(cuuint64_t)kD * 2};
-    const cuuint32_t box[2] = {64, 64};
-    const cuuint32_t estride[2] = {1, 1};
-    CUresult r = encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.q), gdim,
-                        gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    if (!encode_rows_map(qmap, c.q, kD, n_tokens * c.h, kHeads)) return cudaErrorInvalidValue;
 
     Params p;
     const bool codes = c.kv_format != SA_KV_BF16;

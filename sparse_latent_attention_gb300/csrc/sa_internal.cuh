@@ -1,6 +1,7 @@
 // Internal declarations shared by the library's CUDA translation units (not part of the ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -81,6 +82,10 @@ cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const
 bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows);
 size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk);
 cudaError_t attn_tc_launch(const AttnCall& c);
+
+// The TMA map of n bf16 rows of d, in boxes of [box_rows x 64] with the 128-byte swizzle; false when the
+// driver has no encoder or refuses it (sa_attn_tc.cu).
+bool encode_rows_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows);
 
 // helpers (sa_helpers.cu)
 cudaError_t window_idxs_launch(int64_t start_pos, int64_t seqlen, int window, int32_t* idx,
