@@ -232,14 +232,6 @@ __device__ __forceinline__ uint32_t pack_bf16_2(uint64_t v) {
     return pack_bf16(lo, hi);
 }
 
-// Barrier among the 128 threads of one warpgroup, on an mbarrier so that it is bounded.
-__device__ __forceinline__ bool wg_sync(uint32_t bar, uint32_t& phase, volatile int* abort) {
-    mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, phase & 1, abort);
-    ++phase;
-    return ok;
-}
-
 // Byte offset, inside the kv buffers, of 16-byte unit u (of 64) of the row in slot ps (bit 6 =
 // the buffer, bits 0-5 = the row of the tile): 64-d block u / 8, 128-byte swizzle.
 __device__ __forceinline__ uint32_t kv_unit_off(int ps, int u) {

@@ -10,14 +10,21 @@
 // over the SMs whatever the batch.  The accumulators are integers, so the order of the additions does
 // not matter.
 //
-// Roles (persistent CTAs, 22 warps; every wait is bounded, as in the attention kernel):
-//   warp 0      MMA issue (one elected lane): per 64-d chunk of a tile four MMAs of 128 x kN x 16
-//   warp 1      Q by TMA (128-byte swizzle), chunk by chunk: a chunk of the next token's Q is loaded as
-//               soon as the last tile's product has passed it
-//   warps 2-5   epilogue: exponentials, sum over heads, accumulation
-//   warps 6-21  gather, eight rows of the tile each, one 64-d chunk [128 rows x 128 bytes] a stage: bf16
-//               rows with 16-byte cp.async; rows of codes are loaded eight chunks ahead into registers and
-//               widened into the stage (exact: see sa_fp8.cuh, sa_fp4.cuh)
+// The product's d is cut into two ranges with an accumulator each, added up in the epilogue in f32: the
+// tensor core cuts its running sum after every 16 products, and over all of d = 512 in one accumulator
+// that came to a relative error of 1.9e-6 in the weights.
+//
+// Roles (persistent CTAs, 26 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
+// tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
+// short latencies (a copy phase ~270 cycles, a hand-over ~250, a tile's epilogue ~3500), longer than the
+// product itself takes, so two groups of warps take turns at the stages and two at the tiles:
+//   warp 0       MMA issue (one elected lane): per stage eight MMAs of 128 x kN x 16
+//   warp 1       Q by TMA (128-byte swizzle), 128 d at a time: that part of the next token's Q is loaded as
+//                soon as the last tile's product has passed it
+//   warps 2-9    epilogue: exponentials, sum over heads, accumulation; four warps a tile
+//   warps 10-25  gather, eight warps a stage, 16 rows each: bf16 rows with 16-byte cp.async; rows of codes
+//                are loaded a turn ahead into registers and widened into the stage (exact: see
+//                sa_fp8.cuh, sa_fp4.cuh)
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,32 +45,31 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUnits = 4294967296.f;  // 2^32 units of the accumulator to a weight of 1
 
 constexpr int kTile = 128;              // entries per tile (M)
-constexpr int kWarpEpilogue = 2, kWarpGather = 6, kGatherWarps = 16;
-constexpr int kThreads = 32 * (kWarpGather + kGatherWarps);
-constexpr int kMaxChunks = 8;           // 64-d chunks of a row: d <= 512
-constexpr uint32_t kStageBytes = kTile * 128;
-constexpr int kMaxStages = 9;
+constexpr int kWarpEpilogue = 2, kWarpGather = 10, kGroupWarps = 8;
+constexpr int kThreads = 32 * (kWarpGather + 2 * kGroupWarps);
+constexpr int kWarpRows = kTile / kGroupWarps;       // rows of a stage that a gather warp fills
+constexpr int kMaxSteps = 4;            // 128-d stages of a row: d <= 512
+constexpr uint32_t kBlockBytes = kTile * 128;        // 64 d of a tile
+constexpr uint32_t kStageBytes = 2 * kBlockBytes;
 
-// By the heads a product covers (kN = 64 or 128): the stages that fit beside Q, and how many stages a
-// bf16 gather warp keeps in flight before it waits for the oldest (at most stages - 1).
+// By the heads a product covers (kN = 64 or 128): the stages that fit beside Q.
 template <int kN>
 struct Shape {
-    static constexpr uint32_t kQChunkBytes = kN * 128;
-    static constexpr uint32_t kQBytes = kMaxChunks * kQChunkBytes;
-    static constexpr int kStages = kN == 64 ? 9 : 5;
-    static constexpr int kLag = kN == 64 ? 5 : 3;
+    static constexpr uint32_t kQBlockBytes = kN * 128;  // 64 d of Q
+    static constexpr uint32_t kQBytes = 2 * kMaxSteps * kQBlockBytes;
+    static constexpr int kStages = kN == 64 ? 5 : 3;
     static constexpr uint32_t kOffQ = kStages * kStageBytes;
     static constexpr uint32_t kOffMisc = kOffQ + kQBytes;
 };
 
 struct Misc {
-    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-    uint64_t q_full[kMaxChunks], q_empty[kMaxChunks];
-    uint64_t s_full[2], s_empty[2];  // per accumulator (TMEM)
-    uint64_t done;
+    uint64_t kv_full[5], kv_empty[5];
+    uint64_t q_full[kMaxSteps], q_empty[kMaxSteps];
+    uint64_t s_full[2], s_empty[2];  // per set of accumulators (TMEM)
+    uint64_t lse_bar[2], done;
     uint32_t tmem_base;
     int abort;
-    alignas(16) float nlse[4][128];  // -lse log2(e) of the token's heads, a table per epilogue warp
+    alignas(16) float nlse[2][128];  // -lse log2(e) of a token's heads, a table per epilogue group
 };
 
 template <int kN>
@@ -73,6 +79,8 @@ constexpr uint32_t smem_bytes() {
 static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory budget");
 
 struct Params {
+    const uint8_t* q;   // for the L2 prefetch; q_row bytes a head
+    int64_t q_row;
     const uint8_t* kv;
     const uint8_t* kv_scale;
     const float* lse;
@@ -81,7 +89,8 @@ struct Params {
     uint32_t* status;
     float scale_log2;
     int64_t s_len;
-    int h, chunks;
+    int h, steps;   // 128-d stages of a row; the last is half of one when d is not a multiple of 128
+    bool half;
     int64_t rows;
     int topk, n_tiles;
     int64_t n_units;  // (token, tile)
@@ -121,18 +130,48 @@ struct Unit {
     }
 };
 
-// The entry in row r of a unit's tile: its cache row, or -1 (empty, past the columns, or out of range).
-__device__ __forceinline__ int entry_of(const Params& p, const Unit& u, int r, bool& bad) {
+// The entry in row r of a unit's tile as it stands in idx (-1 past the columns).  It is loaded a tile
+// ahead, so it must not be looked at before it is needed: valid() then makes it a cache row or -1.
+__device__ __forceinline__ int entry_of(const Params& p, const Unit& u, int r) {
     const int col = u.tile * kTile + r;
-    int j = col < p.topk ? __ldg(p.idx + u.token * (int64_t)p.topk + col) : -1;
-    bad = j < -1 || j >= p.rows;
+    return col < p.topk ? __ldg(p.idx + u.token * (int64_t)p.topk + col) : -1;
+}
+__device__ __forceinline__ int valid(const Params& p, int j, bool& any_bad) {
+    asm volatile("" : "+r"(j));  // (no test of it moves up to the load)
+    const bool bad = j < -1 || j >= p.rows;
+    any_bad |= bad;
     return bad ? -1 : j;
 }
 
-// Sixteen codes of a row and their scale, on their way from memory to a stage.
+// A gather group's place in the sequence of stages: it takes every other one.
+struct Cursor {
+    Unit u;
+    int64_t i;  // the unit, from the CTA's first
+    int c;      // the stage in it
+    __device__ __forceinline__ Cursor(const Params& p, int64_t begin, int group) : u(p, begin), i(0), c(0) {
+        if (group) advance(p, 1);
+    }
+    __device__ __forceinline__ void advance(const Params& p, int by) {
+        c += by;
+        while (c >= p.steps) {
+            c -= p.steps;
+            ++i;
+            u.step(p);
+        }
+    }
+    // the next unit that the group has a stage of
+    __device__ __forceinline__ Cursor next_unit(const Params& p) const {
+        Cursor n = *this;
+        do n.advance(p, 2);
+        while (n.i == i);
+        return n;
+    }
+};
+
+// The 32 codes of a scale's block and the scale, on their way from memory to a stage.
 template <int kFmt>
 struct Codes {
-    uint32_t w[kFmt == SA_KV_FP4_E2M1 ? 2 : 4];
+    uint32_t w[kFmt == SA_KV_FP4_E2M1 ? 4 : 8];
     uint32_t scale;  // the e8m0 byte; kNone: no row
 };
 constexpr uint32_t kNone = 0xFFFFFFFFu;
@@ -152,23 +191,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&M.kv_full[i]), kGatherWarps);
+            mbar_init(smem_addr(&M.kv_full[i]), kGroupWarps);
             mbar_init(smem_addr(&M.kv_empty[i]), 1);
         }
-        for (int i = 0; i < kMaxChunks; ++i) {
+        for (int i = 0; i < kMaxSteps; ++i) {
             mbar_init(smem_addr(&M.q_full[i]), 1);
             mbar_init(smem_addr(&M.q_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&M.s_full[i]), 1);
             mbar_init(smem_addr(&M.s_empty[i]), 4);
+            mbar_init(smem_addr(&M.lse_bar[i]), 128);
         }
         mbar_init(smem_addr(&M.done), 1);
         M.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
-        tmem_alloc(smem_addr(&M.tmem_base), 256);
+        tmem_alloc(smem_addr(&M.tmem_base), 512);
         tmem_relinquish();
     }
     if (warp == 1 && lane == 0) tma_prefetch_desc(&q_map);
@@ -194,17 +234,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool last = i == range.end - 1 || u.tile == p.n_tiles - 1;
             const uint32_t b = k & 1;
             if (!(ok = warp_wait(smem_addr(&M.s_empty[b]), ((k >> 1) & 1) ^ 1, abort))) break;
-            const uint32_t col = tmem + 128 * b;
-            for (int c = 0; c < p.chunks; ++c) {
+            for (int c = 0; c < p.steps; ++c) {
                 ok = (!first || warp_wait(smem_addr(&M.q_full[c]), qph, abort)) &&
                      warp_wait(smem_addr(&M.kv_full[st]), ph, abort);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
-                const uint32_t blo = (uint32_t)b0 + c * (Sh::kQChunkBytes >> 4);
+                const uint32_t col = tmem + 256 * b + kN * (c >> 1);  // stages 0, 1 and 2, 3
+                uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
+                uint32_t blo = (uint32_t)b0 + 2 * c * (Sh::kQBlockBytes >> 4);
+                const int blocks = c == p.steps - 1 && p.half ? 1 : 2;
+#pragma unroll 1
+                for (int k64 = 0; k64 < blocks; ++k64) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mma_lohi_elect(col, alo + 2 * q, ahi, blo + 2 * q, bhi, id, (c | q) != 0);
+                    for (int q = 0; q < 4; ++q)
+                        mma_lohi_elect(col, alo + 2 * q, ahi, blo + 2 * q, bhi, id,
+                                       (uint32_t)(c & 1) | (uint32_t)k64 | (uint32_t)q);
+                    alo += kBlockBytes >> 4;
+                    blo += Sh::kQBlockBytes >> 4;
+                }
                 mma_commit_elect(smem_addr(&M.kv_empty[st]));
                 if (last) mma_commit_elect(smem_addr(&M.q_empty[c]));
                 if (++st == kStages) {
@@ -225,241 +272,279 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             bool ok = true;
             uint32_t n = 0;  // tokens begun
-            int loaded = 0;  // chunks of the last of them that were asked for
+            int loaded = 0;  // parts of the last of them that were asked for
             Unit u(p, range.begin);
-            const int64_t last_token = range.end > range.begin ? (range.end - 1) / p.n_tiles : -1;
+            const int64_t last_token = (range.end - 1) / p.n_tiles;
             for (int64_t token = u.token; token <= last_token && ok; ++token) {
                 ++n;
                 loaded = 0;
-                for (int c = 0; c < p.chunks; ++c) {
+                for (int c = 0; c < p.steps; ++c) {
                     if (!(ok = mbar_wait(smem_addr(&M.q_empty[c]), n & 1, abort))) break;
-                    mbar_arrive_expect_tx(smem_addr(&M.q_full[c]), Sh::kQChunkBytes);
-                    tma_load_2d(s_q + c * Sh::kQChunkBytes, &q_map, 64 * c, (int32_t)(token * p.h),
-                                smem_addr(&M.q_full[c]));
+                    const int blocks = c == p.steps - 1 && p.half ? 1 : 2;
+                    const uint32_t bar = smem_addr(&M.q_full[c]);
+                    mbar_arrive_expect_tx(bar, blocks * Sh::kQBlockBytes);
+                    for (int k64 = 0; k64 < blocks; ++k64)
+                        tma_load_2d(s_q + (2 * c + k64) * Sh::kQBlockBytes, &q_map, 128 * c + 64 * k64,
+                                    (int32_t)(token * p.h), bar);
                     ++loaded;
                 }
+                // the next token's heads into L2 meanwhile
+                if (token < last_token)
+                    for (int i = 0; i < p.h; i += 8)
+                        prefetch_l2(p.q + ((token + 1) * p.h + i) * p.q_row,
+                                    (uint32_t)(min(8, p.h - i) * p.q_row));
             }
             // after a failed wait, let the loads under way land before the CTA exits
             if (*abort)
-                for (int c = 0; c < p.chunks; ++c) {
-                    const uint32_t uses = n - (c < loaded ? 0u : 1u);  // times chunk c was asked for
+                for (int c = 0; c < p.steps; ++c) {
+                    const uint32_t uses = n - (c < loaded ? 0u : 1u);  // times part c was asked for
                     if (uses > 0) mbar_drain(smem_addr(&M.q_full[c]), (uses - 1) & 1);
                 }
         }
         __syncwarp();
     } else if (warp < kWarpGather) {
         // ------------------------------------------------------------------ epilogue
+        const int group = (warp - kWarpEpilogue) >> 2;  // takes the CTA's units group, group + 2, ...
         const int q4 = warp & 3;  // the TMEM lanes this warp may read: 32 q4 .. 32 q4 + 31
         const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-        float* table = M.nlse[q4];
-        bool ok = true, bad;
-        uint32_t k = 0;
-        Unit u(p, range.begin), un = u;  // un: a unit ahead, whose entry is loaded meanwhile
-        int jn = -1;
-        float ln[kN / 32];  // the next token's lse, heads lane + 32 i
-        auto load_lse = [&](int64_t token) {
-#pragma unroll
-            for (int i = 0; i < kN / 32; ++i)
-                ln[i] = lane + 32 * i < p.h ? __ldg(p.lse + token * p.h + lane + 32 * i) : 0.f;
-        };
-        if (range.begin < range.end) {
-            jn = entry_of(p, u, 32 * q4 + lane, bad);
-            load_lse(u.token);
-        }
+        const int et = 32 * q4 + lane;  // 0 .. 127: its entry of the tile, and the head whose lse it brings
+        const bool two = p.steps > 2;   // both accumulators are used
+        const uint32_t s_at = tmem + lane_base + 256 * group;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        for (int64_t i = range.begin; i < range.end && ok; ++i, ++k) {
-            const uint32_t b = k & 1;
-            const int j = jn;
-            if (i == range.begin || u.tile == 0) {
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < kN / 32; ++q) table[lane + 32 * q] = -ln[q] * kLog2e;
-                __syncwarp();
-                if (range.end - i > p.n_tiles - u.tile) load_lse(u.token + 1);
+        float* table = M.nlse[group];
+        bool ok = true, bad = false;
+        uint32_t n = 0, lse_phase = 0;
+        int64_t token = -1;  // whose lse the table holds
+        const int64_t count = range.end - range.begin;
+        Unit u(p, range.begin), un = u;  // un: the group's next unit, whose entry is loaded meanwhile
+        if (group) un.step(p);
+        int jn = group < count ? entry_of(p, un, et) : -1;
+        float ln = group < count && et < p.h ? __ldg(p.lse + un.token * p.h + et) : 0.f;
+        for (int64_t i = group; i < count && ok; i += 2, ++n) {
+            u = un;
+            const int j = valid(p, jn, bad);
+            if (u.token != token) {
+                token = u.token;
+                // every warp of the group has read the old table; the new one is there
+                if (!(ok = wg_sync(smem_addr(&M.lse_bar[group]), lse_phase, abort))) break;
+                table[et] = -ln * kLog2e;
+                if (!(ok = wg_sync(smem_addr(&M.lse_bar[group]), lse_phase, abort))) break;
             }
             un.step(p);
-            if (i + 1 < range.end) jn = entry_of(p, un, 32 * q4 + lane, bad);
-            if (!(ok = warp_wait(smem_addr(&M.s_full[b]), (k >> 1) & 1, abort))) break;
+            un.step(p);
+            if (i + 2 < count) {
+                jn = entry_of(p, un, et);
+                if (un.token != token && et < p.h) ln = __ldg(p.lse + un.token * p.h + et);
+            }
+            if (!(ok = warp_wait(smem_addr(&M.s_full[group]), n & 1, abort))) break;
             tc_fence_after();
-            uint64_t sum[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-            for (int q = 0; q < kN / 32; ++q) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem + lane_base + 128 * b + 32 * q, r);
+            uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+            // 16 heads at a time: their partial products from both accumulators, added up
+#pragma unroll 1
+            for (int q = 0; q < kN / 16; ++q) {
+                uint32_t r[16], v[16];
+                tmem_ld_32x32b_x16(s_at + 16 * q, r);
+                if (two) tmem_ld_32x32b_x16(s_at + kN + 16 * q, v);
                 tmem_wait_ld();
-                if (q == kN / 32 - 1) {
+                if (q == kN / 16 - 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&M.s_empty[b]));
+                    if (lane == 0) mbar_arrive(smem_addr(&M.s_empty[group]));
                 }
-                if (32 * q >= p.h) continue;
-                const int heads = p.h - 32 * q;  // of these 32
+                const int heads = p.h - 16 * q;  // of these 16
+                if (heads <= 0) continue;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 n4 = *reinterpret_cast<const float4*>(&table[32 * q + 4 * c]);
-                    float x[4];
-                    f2_split(ffma2(f2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])), sc2,
-                                   f2(n4.x, n4.y)), x[0], x[1]);
-                    f2_split(ffma2(f2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])), sc2,
-                                   f2(n4.z, n4.w)), x[2], x[3]);
-                    float e[4];
+                for (int c = 0; c < 4; ++c) {
+                    const float4 n4 = *reinterpret_cast<const float4*>(&table[16 * q + 4 * c]);
+                    uint64_t v0 = f2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]));
+                    uint64_t v1 = f2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
+                    if (two) {
+                        v0 = fadd2(v0, f2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])));
+                        v1 = fadd2(v1, f2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])));
+                    }
+                    float x[4], e[4];
+                    f2_split(ffma2(v0, sc2, f2(n4.x, n4.y)), x[0], x[1]);
+                    f2_split(ffma2(v1, sc2, f2(n4.z, n4.w)), x[2], x[3]);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) e[y] = fast_exp2(x[y]);
-                    if (heads < 32) {
+                    if (heads < 16) {
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             if (4 * c + y >= heads) e[y] = 0.f;
                     }
-                    sum[2 * (c & 1)] = fadd2(sum[2 * (c & 1)], f2(e[0], e[1]));
-                    sum[2 * (c & 1) + 1] = fadd2(sum[2 * (c & 1) + 1], f2(e[2], e[3]));
+                    sum[0] = fadd2(sum[0], f2(e[0], e[1]));
+                    sum[1] = fadd2(sum[1], f2(e[2], e[3]));
                 }
             }
             float w0, w1;
-            f2_split(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])), w0, w1);
+            f2_split(fadd2(sum[0], sum[1]), w0, w1);
             const float w = fminf(fmaxf(w0 + w1, 0.f), (float)p.h);  // (a NaN becomes 0)
             if (j >= 0) atomicAdd(p.acc + u.seq * p.rows + j, __float2ull_rn(w * kUnits));
-            u = un;
         }
     } else if constexpr (kFmt == SA_KV_BF16) {
         // ------------------------------------------------------------------ gather, bf16
-        // Lane l copies 16-byte unit l % 8 of rows l / 8 and l / 8 + 4 of the warp's eight.
-        const int gw = warp - kWarpGather, unit = lane & 7;
-        const int r0 = 8 * gw + (lane >> 3), r1 = r0 + 4;
-        const uint32_t d0 = s_kv + r0 * 128 + ((uint32_t)(unit ^ (r0 & 7)) << 4);
-        const uint32_t d1 = s_kv + r1 * 128 + ((uint32_t)(unit ^ (r1 & 7)) << 4);
-        const int64_t row_bytes = (int64_t)p.chunks * 128;
-        bool ok = true, bad0, bad1;
-        int st = 0, st_full = 0;  // the stage to fill next, and the oldest one still under way
-        uint32_t ph = 1, under_way = 0;
-        Unit u(p, range.begin);
-        int j0 = -1, j1 = -1;
-        for (int64_t i = range.begin; i < range.end && ok; ++i) {
-            if (i == range.begin) {
-                j0 = entry_of(p, u, r0, bad0);
-                j1 = entry_of(p, u, r1, bad1);
-                if (bad0 || bad1) atomicOr(p.status, kStatusBadIndex);
-            }
-            const uint8_t* base = p.kv + u.seq * p.rows * row_bytes + unit * 16;
-            const uint8_t* g0 = base + j0 * row_bytes;
-            const uint8_t* g1 = base + j1 * row_bytes;
-            const bool v0 = j0 >= 0, v1 = j1 >= 0;
-            u.step(p);
-            if (i + 1 < range.end) {  // the next unit's entries
-                j0 = entry_of(p, u, r0, bad0);
-                j1 = entry_of(p, u, r1, bad1);
-                if (bad0 || bad1) atomicOr(p.status, kStatusBadIndex);
-            }
-            for (int c = 0; c < p.chunks; ++c) {
-                if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
-                if (v0) cp_async16(d0 + st * kStageBytes, g0 + c * 128, 16u);
-                if (v1) cp_async16(d1 + st * kStageBytes, g1 + c * 128, 16u);
-                cp_async_commit();
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
+        // Lane l copies 16-byte unit l % 16 (of a stage's 256 bytes) of rows l / 16, l / 16 + 2, ... of the
+        // warp's 16: two rows' 256 bytes an instruction.
+        constexpr int kPer = kWarpRows / 2;
+        const int group = (warp - kWarpGather) / kGroupWarps, unit = lane & 15;
+        const int r0 = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane >> 4);  // row r0 + 2 i
+        uint32_t d[4];  // where the unit of rows r0 + 2 i, i % 4, goes, from row r0 + 2 i (i % 4 = 0) on
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = s_kv + (uint32_t)(unit >> 3) * kBlockBytes + (r0 + 2 * i) * 128 +
+                   ((uint32_t)((unit ^ (r0 + 2 * i)) & 7) << 4);
+        const int64_t row_bytes = (int64_t)p.steps * 256 - (p.half ? 128 : 0);
+        const int64_t count = range.end - range.begin;
+        bool ok = true, any_bad = false;
+        int st = group, under_way = -1;  // the stage to fill; the one filled but not handed over
+        uint32_t ph = 1;
+        auto hand_over = [&] {
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[under_way]));
+        };
+        Cursor cur(p, range.begin, group);
+        const uint8_t* src[kPer];
+        uint32_t there = 0;  // bit i: row r0 + 2 i has an entry
+        int jn[kPer];
+        int64_t unit_at = -1;  // the unit that src points into
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) jn[i] = cur.i < count ? entry_of(p, cur.u, r0 + 2 * i) : -1;
+        while (cur.i < count) {
+            if (cur.i != unit_at) {
+                unit_at = cur.i;
+                const uint8_t* base = p.kv + cur.u.seq * p.rows * row_bytes + unit * 16;
+                there = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int j = valid(p, jn[i], any_bad);
+                    there |= j >= 0 ? 1u << i : 0u;
+                    src[i] = base + j * row_bytes;
                 }
-                if (++under_way > (uint32_t)Sh::kLag) {
-                    cp_async_wait<Sh::kLag>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[st_full]));
-                    if (++st_full == kStages) st_full = 0;
-                    --under_way;
+                const Cursor nu = cur.next_unit(p);
+                if (nu.i < count) {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) jn[i] = entry_of(p, nu.u, r0 + 2 * i);
                 }
             }
+            // the stage of the group's last turn is handed over before the wait for a free one, so that
+            // the product has work while this warp waits for it
+            if (under_way >= 0) hand_over();
+            under_way = -1;
+            if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
+            if (!(cur.c == p.steps - 1 && p.half && unit >= 8)) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (there >> i & 1)
+                        cp_async16(d[i & 3] + st * kStageBytes + (i >> 2) * 1024, src[i] + cur.c * 256, 16u);
+            }
+            cp_async_commit();
+            under_way = st;
+            if ((st += 2) >= kStages) {
+                st -= kStages;
+                ph ^= 1;
+            }
+            cur.advance(p, 2);
         }
+        if (ok && under_way >= 0) hand_over();
         cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        for (; ok && under_way > 0; --under_way) {
-            if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[st_full]));
-            if (++st_full == kStages) st_full = 0;
-        }
+        if (any_bad) atomicOr(p.status, kStatusBadIndex);
     } else {
         // ------------------------------------------------------------------ gather, rows of codes
-        // Four lanes a row: lane l widens codes 16 (l % 4) .. + 15 of each 64-d chunk of row l / 4 of the
-        // warp's eight.  The loads run kAhead chunks before the widening, over the ends of tiles.
-        constexpr int kAhead = 8;
-        constexpr int kLaneBytes = kFmt == SA_KV_FP4_E2M1 ? 8 : 16;
-        const int gw = warp - kWarpGather, sub = lane & 3;
-        const int r = 8 * gw + (lane >> 2);
-        const uint32_t dst = s_kv + r * 128 + ((uint32_t)((2 * sub) ^ (r & 7)) << 4);
-        const int64_t row_bytes = (int64_t)p.chunks * (4 * kLaneBytes);
-        const int64_t n_steps = (range.end - range.begin) * p.chunks;
-        // the chunk to load next
-        Unit u(p, range.begin);
-        const uint8_t *codes = nullptr, *scales = nullptr;
-        int64_t left = range.end - range.begin;  // tiles not yet begun
-        int c = 0, jn = -1;
-        bool there = false, bad;
-        if (left > 0) {
-            jn = entry_of(p, u, r, bad);
-            if (bad) atomicOr(p.status, kStatusBadIndex);
-        }
-        auto load = [&](Codes<kFmt>& x) {
-            if (c == 0) {
-                there = left > 0 && jn >= 0;
-                if (there) {
-                    const int64_t row = u.seq * p.rows + jn;
-                    codes = p.kv + row * row_bytes + sub * kLaneBytes;
-                    scales = p.kv_scale + row * (2 * p.chunks) + (sub >> 1);
+        // Lane l widens a scale's block, codes 32 (l / 8) .. + 31 of a 128-d stage, of rows l % 8 and
+        // l % 8 + 8 of the warp's 16 (a store instruction's eight lanes meet eight rows: no bank conflict).
+        // The codes of the group's next stage are loaded before it waits for that stage.
+        constexpr int kLaneBytes = kFmt == SA_KV_FP4_E2M1 ? 16 : 32;
+        const int group = (warp - kWarpGather) / kGroupWarps, part = lane >> 3;
+        const int r0 = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane & 7);  // rows r0, r0 + 8
+        // the lane's 16-byte units 4 (part % 2) .. + 3 of 64-d block part / 2; row r0 + 8 is 1024 bytes on
+        const uint32_t dst = s_kv + (uint32_t)(part >> 1) * kBlockBytes + r0 * 128 +
+                             ((uint32_t)((4 * (part & 1)) ^ (r0 & 7)) << 4);
+        const int64_t row_bytes = (int64_t)p.steps * (4 * kLaneBytes) - (p.half ? 2 * kLaneBytes : 0);
+        const int row_scales = 4 * p.steps - (p.half ? 2 : 0);
+        const int64_t count = range.end - range.begin;
+        bool ok = true, any_bad = false;
+        Cursor cur(p, range.begin, group);  // the stage to load next
+        const uint8_t *codes[2] = {nullptr, nullptr}, *scales[2] = {nullptr, nullptr};
+        bool there[2] = {false, false};
+        int jn[2];
+        int64_t unit_at = -1;  // the unit that codes points into
+#pragma unroll
+        for (int y = 0; y < 2; ++y) jn[y] = cur.i < count ? entry_of(p, cur.u, r0 + 8 * y) : -1;
+        Codes<kFmt> x[2];
+        auto load = [&] {
+            if (cur.i >= count) return;
+            if (cur.i != unit_at) {
+                unit_at = cur.i;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = valid(p, jn[y], any_bad);
+                    const int64_t row = cur.u.seq * p.rows + j;
+                    there[y] = j >= 0;
+                    codes[y] = p.kv + row * row_bytes + part * kLaneBytes;
+                    scales[y] = p.kv_scale + row * row_scales + part;
                 }
-                u.step(p);
-                if (--left > 0) {
-                    jn = entry_of(p, u, r, bad);
-                    if (bad) atomicOr(p.status, kStatusBadIndex);
+                const Cursor nu = cur.next_unit(p);
+                if (nu.i < count) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) jn[y] = entry_of(p, nu.u, r0 + 8 * y);
                 }
             }
-            x.scale = kNone;
-            if (there) {
-                if constexpr (kFmt == SA_KV_FP4_E2M1) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(codes + c * 32));
-                    x.w[0] = v.x;
-                    x.w[1] = v.y;
-                } else {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + c * 64));
-                    x.w[0] = v.x;
-                    x.w[1] = v.y;
-                    x.w[2] = v.z;
-                    x.w[3] = v.w;
+            const bool inside = !(cur.c == p.steps - 1 && p.half && part >= 2);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                x[y].scale = kNone;
+                if (there[y] && inside) {
+                    const uint4* at = reinterpret_cast<const uint4*>(codes[y] + cur.c * (4 * kLaneBytes));
+#pragma unroll
+                    for (int i = 0; i < kLaneBytes / 16; ++i) {
+                        const uint4 v = __ldg(at + i);
+                        x[y].w[4 * i] = v.x;
+                        x[y].w[4 * i + 1] = v.y;
+                        x[y].w[4 * i + 2] = v.z;
+                        x[y].w[4 * i + 3] = v.w;
+                    }
+                    x[y].scale = __ldg(scales[y] + 4 * cur.c);
                 }
-                x.scale = __ldg(scales + 2 * c);
             }
-            if (++c == p.chunks) c = 0;
+            cur.advance(p, 2);
         };
-        Codes<kFmt> ring[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(ring[i]);
-        bool ok = true;
-        int st = 0;
+        const int64_t n_stages = count * p.steps;
+        load();
+        int st = group;
         uint32_t ph = 1;
-        for (int64_t s = 0; s < n_steps && ok; s += kAhead) {
+        for (int64_t s = group; s < n_stages; s += 2) {
+            if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (s + i >= n_steps) break;
-                if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
-                if (ring[i].scale != kNone) {
+            for (int y = 0; y < 2; ++y) {
+                if (x[y].scale == kNone) continue;
+                const uint32_t at = dst + st * kStageBytes + 1024 * y;
+                const float sc = kFmt == SA_KV_FP4_E2M1 ? fp4::scale_f32(x[y].scale)
+                                                        : fp8::e8m0_to_f32(x[y].scale);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t(&w)[kLaneBytes / 4] = x[y].w;
                     uint4 lo, hi;
                     if constexpr (kFmt == SA_KV_FP4_E2M1)
-                        fp4::dequant16(make_uint2(ring[i].w[0], ring[i].w[1]),
-                                       fp4::scale_f32(ring[i].scale), lo, hi);
+                        fp4::dequant16(make_uint2(w[2 * i], w[2 * i + 1]), sc, lo, hi);
                     else
-                        fp8::dequant16(make_uint4(ring[i].w[0], ring[i].w[1], ring[i].w[2], ring[i].w[3]),
-                                       fp8::e8m0_to_f32(ring[i].scale), lo, hi);
-                    const uint32_t at = dst + st * kStageBytes;
-                    st_shared_v4(at, lo.x, lo.y, lo.z, lo.w);
-                    st_shared_v4(at ^ 16u, hi.x, hi.y, hi.z, hi.w);
+                        fp8::dequant16(make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]), sc,
+                                       lo, hi);
+                    st_shared_v4(at ^ (32u * i), lo.x, lo.y, lo.z, lo.w);
+                    st_shared_v4(at ^ (32u * i + 16u), hi.x, hi.y, hi.z, hi.w);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[st]));
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                load(ring[i]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[st]));
+            if ((st += 2) >= kStages) {
+                st -= kStages;
+                ph ^= 1;
+            }
+            load();
         }
+        if (any_bad) atomicOr(p.status, kStatusBadIndex);
     }
 
     tc_fence_before();
@@ -467,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && M.abort) atomicOr(p.status, kStatusTimeout);
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -535,6 +620,8 @@ extern "C" sa_status sa_row_weights(const void* q, const void* kv, const uint8_t
     CUtensorMap map;
     if (!encode_rows_map(map, q, d, (int64_t)n_tok * h, n)) return SA_ERR_CUDA;
     Params p;
+    p.q = reinterpret_cast<const uint8_t*>(q);
+    p.q_row = 2 * (int64_t)d;
     p.kv = reinterpret_cast<const uint8_t*>(kv);
     p.kv_scale = kv_scale;
     p.lse = lse;
@@ -544,7 +631,8 @@ extern "C" sa_status sa_row_weights(const void* q, const void* kv, const uint8_t
     p.scale_log2 = softmax_scale * kLog2e;
     p.s_len = s;
     p.h = h;
-    p.chunks = d / 64;
+    p.steps = (d + 127) / 128;
+    p.half = d % 128 != 0;
     p.rows = rows;
     p.topk = topk;
     p.n_tiles = (topk + kTile - 1) / kTile;
