@@ -94,7 +94,7 @@ sa_status sa_evict_select(const int64_t* acc, const int32_t* live, int64_t b, in
  * of the source, or zero bytes when r is -1 (or outside [0, rows)).  Rows n_keep and up of a destination
  * are left as they are.
  *   src, dst    arrays of n_tensors device pointers (the arrays are host memory)
- *   row_bytes   bytes of a row of each tensor; rows of a sequence are packed
+ *   row_bytes   bytes of a row of each tensor, below 2^25; rows of a sequence are packed
  *   src_batch_bytes, dst_batch_bytes   distance between sequences of each tensor, in bytes
  *   kept        int32 [b][n_keep]
  * A destination may be its own source (dst[t] == src[t], the same batch distance): the rows then move

@@ -40,23 +40,28 @@ __all__ = ["sparse_attn", "window_idxs", "act_quant_fp8", "window_write", "index
 WEIGHT_UNIT = 2.0 ** -32
 
 
-def _ptr(t) -> ctypes.c_void_p | None:
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# What a call costs on the host is mostly attribute reads and argument objects, so pointers and streams go
+# to ctypes as integers (its argument types are declared) and a tensor's properties are read once.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream) -> int:
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _call(name, dev, stream, *args):
-    """A library call on the device its tensors are on: with that device current, on ``stream`` or
-    the device's current stream."""
-    if dev.index != torch.cuda.current_device():
+    """A library call on the device (its index) that the tensors are on: with that device current, on
+    ``stream`` or the device's current stream."""
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    _lib.check(getattr(load(), name)(*args, ctypes.c_void_p(s.cuda_stream)), name)
+    st = getattr(load(), name)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _lib.check(st, name)
 
 
 def _need(t, name, dtype, device=None):
@@ -66,7 +71,7 @@ def _need(t, name, dtype, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
@@ -91,15 +96,20 @@ def _kv_format(kv, kv_scale, b, d, dev):
     """The kv format of a cache: bf16 [b, rows, d] without scales; with them, uint8 [b, rows, d] is
     e4m3 and uint8 [b, rows, d / 2] is e2m1."""
     _need(kv, "kv", torch.bfloat16 if kv_scale is None else torch.uint8, dev)
-    widths = {d: SA_KV_BF16} if kv_scale is None else {d: SA_KV_FP8_E4M3, d // 2: SA_KV_FP4_E2M1}
-    if kv.dim() != 3 or kv.shape[0] != b or kv.shape[2] not in widths:
-        raise ValueError(f"kv shape {tuple(kv.shape)} does not match {b} sequences of head_dim {d}")
+    shape = tuple(kv.shape)
+    if len(shape) != 3 or shape[0] != b:
+        fmt = None
+    elif kv_scale is None:
+        fmt = SA_KV_BF16 if shape[2] == d else None
+    else:
+        fmt = SA_KV_FP8_E4M3 if shape[2] == d else SA_KV_FP4_E2M1 if 2 * shape[2] == d else None
+    if fmt is None:
+        raise ValueError(f"kv shape {shape} does not match {b} sequences of head_dim {d}")
     if kv_scale is not None:
         _need(kv_scale, "kv_scale", torch.uint8, dev)
-        if tuple(kv_scale.shape) != (b, kv.shape[1], d // 32):
-            raise ValueError(f"kv_scale shape {tuple(kv_scale.shape)} != "
-                             f"{(b, kv.shape[1], d // 32)}")
-    return widths[kv.shape[2]]
+        if kv_scale.shape != (b, shape[1], d // 32):
+            raise ValueError(f"kv_scale shape {tuple(kv_scale.shape)} != {(b, shape[1], d // 32)}")
+    return fmt
 
 
 def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, workspace=None,
@@ -154,7 +164,7 @@ def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, wor
         if rope is not None and rot.numel() == 0:
             raise ValueError("rot is empty")
         turn = (_ptr(rot), rot.shape[0], 2 * rot.shape[1], int(start_pos)) if rope else (None, 0, 0, 0)
-        _call("sa_sparse_attn_lse", dev, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
+        _call("sa_sparse_attn_lse", dev.index, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
               _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk, _ptr(out), _ptr(lse),
               _ptr(workspace), workspace.numel(), *turn)
         return out
@@ -358,27 +368,28 @@ def act_quant_fp4(x, *, out_rt=None, codes=None, scales=None, stream=None):
     Writes the bf16 round trip into ``out_rt`` (may be ``x`` itself), the codes, two to a byte
     (element 2k in the low four bits), into ``codes`` [n, d / 2] and the e8m0 block scales into
     ``scales`` [n, d / 32] (each a 2-D tensor with unit column stride; rows may be strided)."""
-    if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda or (x.shape[1] > 1
-                                                                      and x.stride(1) != 1):
+    shape, stride = x.shape, x.stride()
+    if (len(shape) != 2 or x.dtype != torch.bfloat16 or not x.is_cuda
+            or (shape[1] > 1 and stride[1] != 1)):
         raise ValueError("x must be a 2-D CUDA bf16 tensor with unit column stride")
-    n, d = x.shape
+    n, d = shape
+    dev = x.get_device()
 
     def rows_of(t, name, dtype, width):
         if t is None:
             return None, 0
-        if (t.dim() != 2 or t.dtype != dtype or tuple(t.shape) != (n, width)
-                or (width > 1 and t.stride(1) != 1)):
+        stride = t.stride()
+        if t.dtype != dtype or t.shape != (n, width) or (width > 1 and stride[1] != 1):
             raise ValueError(f"{name} must be a 2-D {dtype} tensor of shape ({n}, {width}) with "
                              "unit column stride")
-        if t.device != x.device:
+        if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-        return t, t.stride(0) if n > 1 else max(width, t.stride(0))
+        return t.data_ptr(), stride[0] if n > 1 else max(width, stride[0])
 
-    rt, rts = rows_of(out_rt, "out_rt", torch.bfloat16, d)
-    cd, cds = rows_of(codes, "codes", torch.uint8, d // 2)
-    sc, scs = rows_of(scales, "scales", torch.uint8, d // 32)
-    _call("sa_act_quant_fp4", x.device, stream, _ptr(x), n, d,
-          x.stride(0) if n > 1 else max(d, x.stride(0)), _ptr(rt), rts, _ptr(cd), cds, _ptr(sc), scs)
+    _call("sa_act_quant_fp4", dev, stream, x.data_ptr(), n, d,
+          stride[0] if n > 1 else max(d, stride[0]), *rows_of(out_rt, "out_rt", torch.bfloat16, d),
+          *rows_of(codes, "codes", torch.uint8, d // 2),
+          *rows_of(scales, "scales", torch.uint8, d // 32))
 
 
 def window_write_fp4(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=None):
@@ -389,37 +400,34 @@ def window_write_fp4(x, start_pos, *, ring_rt=None, codes=None, scales=None, str
     (start_pos + t) % window.  The rings are 3-D tensors ``codes`` [nbatch, window, d / 2],
     ``scales`` [nbatch, window, d / 32] and ``ring_rt`` [nbatch, window, d] (bf16 round trip)
     with unit column stride; they may be strided views of a larger cache."""
-    if x.dim() != 3 or x.stride(2) != 1 or x.dtype != torch.bfloat16 or not x.is_cuda:
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or stride[2] != 1 or x.dtype != torch.bfloat16 or not x.is_cuda:
         raise ValueError("x must be a 3-D CUDA bf16 tensor with unit column stride")
-    nb, sl, d = x.shape
-    xs = x.stride(1) if sl > 1 else x.stride(0) if nb > 1 else d
-    if nb > 1 and x.stride(0) != sl * xs:
+    nb, sl, d = shape
+    xs = stride[1] if sl > 1 else stride[0] if nb > 1 else d
+    if nb > 1 and stride[0] != sl * xs:
         raise ValueError("the sequences of x must be seqlen rows apart")
-    window = None
+    dev = x.get_device()
+    given = [t for t in (ring_rt, codes, scales) if t is not None]
+    if not given or given[0].dim() != 3:
+        raise ValueError("give at least one of ring_rt, codes, scales, as 3-D tensors")
+    window = given[0].shape[1]
 
     def ring_of(t, name, dtype, width):
-        nonlocal window
         if t is None:
             return None, 0, 0
-        if (t.dim() != 3 or t.dtype != dtype or t.shape[0] != nb or t.shape[2] != width
-                or (width > 1 and t.stride(2) != 1)):
-            raise ValueError(f"{name} must be a 3-D {dtype} tensor of shape ({nb}, window, {width})"
-                             " with unit column stride")
-        if t.device != x.device:
+        stride = t.stride()
+        if t.dtype != dtype or t.shape != (nb, window, width) or (width > 1 and stride[2] != 1):
+            raise ValueError(f"{name} must be a {dtype} tensor of shape ({nb}, {window}, {width}) with "
+                             "unit column stride")
+        if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-        if window is None:
-            window = t.shape[1]
-        elif t.shape[1] != window:
-            raise ValueError("the rings must have the same window")
-        return t, t.stride(1) if window > 1 else max(width, t.stride(1)), t.stride(0)
+        return t.data_ptr(), stride[1] if window > 1 else max(width, stride[1]), stride[0]
 
-    rt, rts, rtb = ring_of(ring_rt, "ring_rt", torch.bfloat16, d)
-    cd, cds, cdb = ring_of(codes, "codes", torch.uint8, d // 2)
-    sc, scs, scb = ring_of(scales, "scales", torch.uint8, d // 32)
-    if window is None:
-        raise ValueError("give at least one of ring_rt, codes, scales")
-    _call("sa_window_write_fp4", x.device, stream, _ptr(x), nb, sl, d, xs, int(start_pos), window,
-          _ptr(rt), rts, rtb, _ptr(cd), cds, cdb, _ptr(sc), scs, scb)
+    _call("sa_window_write_fp4", dev, stream, x.data_ptr(), nb, sl, d, xs, int(start_pos), window,
+          *ring_of(ring_rt, "ring_rt", torch.bfloat16, d),
+          *ring_of(codes, "codes", torch.uint8, d // 2),
+          *ring_of(scales, "scales", torch.uint8, d // 32))
 
 
 def row_weights(q, kv, lse, idx, softmax_scale, acc, *, kv_scale=None, workspace=None,
@@ -440,20 +448,21 @@ def row_weights(q, kv, lse, idx, softmax_scale, acc, *, kv_scale=None, workspace
     fmt = _kv_format(kv, kv_scale, b, d, dev)
     rows = kv.shape[1]
     _need(lse, "lse", torch.float32, dev)
-    if tuple(lse.shape) != (b, s, h):
+    if lse.shape != (b, s, h):
         raise ValueError(f"lse shape {tuple(lse.shape)} != {(b, s, h)}")
     _need(idx, "idx", torch.int32, dev)
-    if idx.dim() != 3 or idx.shape[0] != b or idx.shape[1] != s:
+    shape = idx.shape
+    if len(shape) != 3 or shape[0] != b or shape[1] != s:
         raise ValueError(f"idx shape {tuple(idx.shape)} does not match q {tuple(q.shape)}")
     _need(acc, "acc", torch.int64, dev)
-    if tuple(acc.shape) != (b, rows):
+    if acc.shape != (b, rows):
         raise ValueError(f"acc shape {tuple(acc.shape)} != {(b, rows)}")
     if workspace is None:
         workspace = torch.zeros(SA_STATUS_BYTES, dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, dev)
-    _call("sa_row_weights", dev, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(lse), _ptr(idx),
-          float(softmax_scale), b, s, h, d, rows, idx.shape[2], _ptr(acc), _ptr(workspace),
+    _call("sa_row_weights", dev.index, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(lse), _ptr(idx),
+          float(softmax_scale), b, s, h, d, rows, shape[2], _ptr(acc), _ptr(workspace),
           workspace.numel())
     return acc
 
@@ -478,7 +487,7 @@ def evict_select(acc, n_keep, *, keep_first=0, keep_last=0, live=None, stream=No
         raise ValueError(f"n_keep {n_keep} is not within [0, {rows}]")
     kept = torch.empty((b, n_keep), dtype=torch.int32, device=acc.device)
     remap = torch.empty((b, rows), dtype=torch.int32, device=acc.device)
-    _call("sa_evict_select", acc.device, stream, _ptr(acc), _ptr(live), b, rows, n_keep,
+    _call("sa_evict_select", acc.get_device(), stream, _ptr(acc), _ptr(live), b, rows, n_keep,
           int(keep_first), int(keep_last), _ptr(kept), _ptr(remap))
     return kept, remap
 
@@ -496,35 +505,53 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
     _need(kept, "kept", torch.int32)
     if kept.dim() != 2:
         raise ValueError(f"kept shape {tuple(kept.shape)} is not [b, n_keep]")
-    b, n_keep = kept.shape
-    if not 0 < len(tensors) <= _lib.SA_COMPACT_MAX_TENSORS:
-        raise ValueError(f"give 1 to {_lib.SA_COMPACT_MAX_TENSORS} tensors")
-    outs = [None] * len(tensors) if out is None else list(out)
-    if len(outs) != len(tensors):
-        raise ValueError("out must list one tensor for each of tensors")
+    (b, n_keep), dev = kept.shape, kept.get_device()
     n = len(tensors)
-    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
-    row_bytes, src_b, dst_b = ((ctypes.c_int64 * n)() for _ in range(3))
-    rows = tensors[0].shape[1] if tensors[0].dim() > 1 else -1
+    if not 0 < n <= _lib.SA_COMPACT_MAX_TENSORS:
+        raise ValueError(f"give 1 to {_lib.SA_COMPACT_MAX_TENSORS} tensors")
+    outs = [None] * n if out is None else list(out)
+    if len(outs) != n:
+        raise ValueError("out must list one tensor for each of tensors")
+    rows = None
+    src, dst, row_bytes, src_b, dst_b = [], [], [], [], []
+
+    def of(t, what, shape, stride):
+        """The bytes of a row of t, whose rows are contiguous."""
+        size = t.element_size()
+        elements = 1
+        for extent, step in zip(reversed(shape[1:]), reversed(stride[1:])):
+            if extent > 1 and step != elements:
+                raise ValueError(f"{what} must have contiguous rows")
+            elements *= extent
+        return size * (elements // shape[1] if shape[1] else 1)
+
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or t.device != kept.device:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
             raise TypeError(f"tensors[{i}] must be a tensor on {kept.device}")
-        if t.dim() < 2 or t.shape[0] != b or t.shape[1] != rows or (b and not t[0].is_contiguous()):
-            raise ValueError(f"tensors[{i}] must be [{b}, {rows}, ...] with contiguous rows")
+        shape, stride = t.shape, t.stride()
+        if rows is None and len(shape) > 1:
+            rows = shape[1]
+        if len(shape) < 2 or shape[0] != b or shape[1] != rows:
+            raise ValueError(f"tensors[{i}] must be [{b}, {rows}, ...]")
+        row_bytes.append(of(t, f"tensors[{i}]", shape, stride))
         o = outs[i]
         if o is None:
-            o = outs[i] = torch.empty((b, n_keep) + tuple(t.shape[2:]), dtype=t.dtype, device=t.device)
-        elif (o.device != t.device or o.dtype != t.dtype or o.dim() != t.dim() or o.shape[0] != b
-              or o.shape[1] < n_keep or o.shape[2:] != t.shape[2:]
-              or (b and not o[0].is_contiguous())):
+            o = outs[i] = torch.empty((b, n_keep, *shape[2:]), dtype=t.dtype, device=t.device)
+        elif (o.get_device() != dev or o.dtype != t.dtype or o.dim() != len(shape) or o.shape[0] != b
+              or o.shape[1] < n_keep or o.shape[2:] != shape[2:]):
             raise ValueError(f"out[{i}] must be a {t.dtype} tensor [{b}, {n_keep} or more, ...] like "
-                             f"tensors[{i}], with contiguous rows")
-        size = t.element_size()
-        src[i], dst[i] = t.data_ptr(), o.data_ptr()
-        row_bytes[i] = size * t[0, 0].numel() if b and rows else size
-        src_b[i], dst_b[i] = size * t.stride(0), size * o.stride(0)
-    _call("sa_compact_rows", kept.device, stream, n, src, dst, row_bytes, src_b, dst_b, b, rows,
-          n_keep, _ptr(kept))
+                             f"tensors[{i}]")
+        else:
+            of(o, f"out[{i}]", o.shape, o.stride())
+        src.append(t.data_ptr())
+        dst.append(o.data_ptr())
+        src_b.append(stride[0] * t.element_size())
+        dst_b.append(o.stride(0) * t.element_size())
+    # one array of 64-bit words holds the five lists
+    words = (ctypes.c_int64 * (5 * n))(*src, *dst, *row_bytes, *src_b, *dst_b)
+    at = ctypes.addressof(words)
+    _call("sa_compact_rows", dev, stream, n, at, at + 8 * n, at + 16 * n, at + 24 * n, at + 32 * n, b,
+          rows, n_keep, kept.data_ptr())
     return outs
 
 
@@ -542,7 +569,7 @@ def remap_idx(idx, remap, *, out=None, stream=None) -> torch.Tensor:
         if out.shape != idx.shape:
             raise ValueError("out must have idx's shape")
     b, rows = remap.shape
-    _call("sa_remap_idx", idx.device, stream, _ptr(idx), b, idx.numel() // b if b else 0, _ptr(remap),
+    _call("sa_remap_idx", idx.get_device(), stream, _ptr(idx), b, idx.numel() // b if b else 0, _ptr(remap),
           rows, _ptr(out))
     return out
 

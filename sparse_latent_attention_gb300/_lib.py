@@ -39,6 +39,8 @@ class SparseAttnError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libsa.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

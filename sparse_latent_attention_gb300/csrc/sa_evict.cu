@@ -18,103 +18,216 @@ namespace {
 // selection
 // ---------------------------------------------------------------------------------------------
 
-// Order-preserving unsigned key of a signed accumulator.
-__device__ __forceinline__ uint64_t key_of(int64_t a) { return (uint64_t)a ^ (uint64_t(1) << 63); }
+// A row's 32-bit key: the accumulator as f32, cut towards zero (which keeps the order, but may make
+// neighbours equal), in an order-preserving unsigned form.  Weights are spread over many powers of two, so
+// the first digit of this key (exponent and two bits) already tells most of them apart, where the first
+// bytes of the integer are zeros for almost all.
+__device__ __forceinline__ uint32_t key_of(int64_t a) {
+    const uint32_t bits = __float_as_uint(__ll2float_rz(a));
+    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+}
+// The whole accumulator in an order-preserving unsigned form.
+__device__ __forceinline__ uint64_t full_key_of(int64_t a) { return (uint64_t)a ^ (uint64_t(1) << 63); }
 
-constexpr int kSelThreads = 1024;
+constexpr int kBins = 2048;  // 11 bits a pass
+constexpr int kCachedRows = 49152;  // rows whose keys (192 KB) fit in shared memory beside the rest
+
+struct SelectSmem {
+    uint32_t hist[kBins];
+    uint32_t warp_sum[32];
+    uint32_t bin, before, count;  // the bin that holds the wanted key, the keys above it and in it
+    uint32_t warp_in[32], warp_eq[32];
+};
+
+// Finds the bin of S.hist, from the top, in which the want-th key lies (1 <= want <= all keys counted).
+template <int kThreads>
+__device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want) {
+    constexpr int kPer = kBins / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += c[i] = S.hist[kBins - 1 - (kPer * tid + i)];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) S.warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += S.warp_sum[w];
+    if (before < want && want <= before + sum) {  // one thread
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (want > before && want <= before + c[i]) {
+                S.bin = (uint32_t)(kBins - 1 - (kPer * tid + i));
+                S.before = before;
+                S.count = c[i];
+            }
+            before += c[i];
+        }
+    }
+    __syncthreads();
+}
 
 // One CTA per sequence.  Rows [0, lo) and [hi, live) are protected; of the candidates [lo, hi) the `want`
-// largest stay.  A radix select (eight bits a pass from the top) finds the want-th largest key T and how
-// many of the picks equal it; one pass in row order then numbers the rows that stay.
-__global__ void __launch_bounds__(kSelThreads)
+// largest stay.  A radix select over the 32-bit keys (11 bits a pass from the top; it ends as soon as a
+// whole bin stays) finds the want-th largest.  Where several candidates share its key and not all of them
+// stay, they are told apart by their accumulators, the same way, and equal accumulators by their row.  Then
+// each warp counts the rows that stay in its share of the rows and, knowing the earlier warps' counts,
+// numbers them in row order.  kCached: the candidates' keys are kept in shared memory; else they are made
+// again from the accumulators (in L2) in every pass.
+template <int kThreads, bool kCached>
+__global__ void __launch_bounds__(kThreads)
     evict_select_kernel(const int64_t* __restrict__ acc, const int32_t* __restrict__ live, int rows,
                         int n_keep, int keep_first, int keep_last, int32_t* __restrict__ kept,
                         int32_t* __restrict__ remap) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t sel[2];
-    __shared__ uint32_t tot[2][32][2];
+    extern __shared__ uint32_t keys[];
+    __shared__ SelectSmem S;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreads / 32;
     const int64_t bi = blockIdx.x;
     const int64_t* a = acc + bi * rows;
     int L = rows;
     if (live) L = min(max(live[bi], 0), rows);
-    const int lo = min(keep_first, L), hi = max(lo, L - keep_last);
+    const int lo = min(keep_first, L), hi = max(lo, L - keep_last), n = hi - lo;
     const int n_stay = min(n_keep, L);
-    const int want = n_stay - (L - (hi - lo));  // of the hi - lo candidates; >= 0
-    uint64_t T = 0;
-    uint32_t need = 0;
-    const bool all = want == hi - lo, none = want == 0;
-    if (!all && !none) {
-        uint64_t mask = 0;
-        uint32_t krem = (uint32_t)want;
-        for (int shift = 56; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
+    const uint32_t want = (uint32_t)(n_stay - (L - n));  // of the n candidates
+    auto key = [&](int i) { return kCached ? keys[i] : key_of(a[lo + i]); };
+
+    // a candidate stays when its key is at least `from`, or when its key is `tie` and its accumulator above
+    // `full`, or equal to it and fewer than `need` such come before it
+    uint32_t from = want == 0 ? 0xFFFFFFFFu : 0u, tie = 0xFFFFFFFFu, need = 0;  // (no key is 2^32 - 1)
+    uint64_t full = 0;
+    if (want > 0 && want < (uint32_t)n) {
+        uint32_t prefix = 0, mask = 0, krem = want;
+        bool exact = true;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digit = pass == 2 ? 0x3FFu : 0x7FFu;
+            for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
             __syncthreads();
-            for (int i = lo + tid; i < hi; i += kSelThreads) {
-                const uint64_t k = key_of(a[i]);
-                if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & 255], 1u);
+#pragma unroll 4
+            for (int i = tid; i < n; i += kThreads) {
+                uint32_t k;
+                if (pass == 0) {
+                    k = key_of(a[lo + i]);
+                    if (kCached) keys[i] = k;
+                } else {
+                    k = key(i);
+                }
+                if ((k & mask) == prefix) atomicAdd(&S.hist[k >> shift & digit], 1u);
             }
             __syncthreads();
-            if (tid == 0) {
-                uint32_t cum = 0;
-                int bin = 255;
-                while (bin > 0 && cum + hist[bin] < krem) cum += hist[bin--];
-                sel[0] = (uint32_t)bin;
-                sel[1] = krem - cum;
+            find_bin<kThreads>(S, krem);
+            prefix |= S.bin << shift;
+            mask |= digit << shift;
+            krem -= S.before;
+            if (S.count == krem) {  // the whole bin stays
+                exact = false;
+                break;
             }
-            __syncthreads();
-            T |= (uint64_t)sel[0] << shift;
-            mask |= uint64_t(0xFF) << shift;
-            krem = sel[1];
         }
-        need = krem;
+        from = prefix;
+        if (exact) {
+            from = prefix + 1;
+            tie = prefix;
+            // an accumulator below 2^24 is its f32 exactly: candidates with this key are equal
+            const uint32_t bits = prefix & 0x80000000u ? prefix & 0x7FFFFFFFu : ~prefix;
+            const float value = __uint_as_float(bits);
+            if (fabsf(value) < 16777216.f) {
+                full = full_key_of((int64_t)value);
+            } else {
+                uint64_t m = 0;
+#pragma unroll 1
+                for (int shift = 53; shift >= -2; shift -= 11) {
+                    const int sh = max(shift, 0);
+                    const uint32_t digit = shift < 0 ? 0x1FFu : 0x7FFu;  // 64 = 5 * 11 + 9
+                    for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
+                    __syncthreads();
+                    for (int i = tid; i < n; i += kThreads) {
+                        if (key(i) != tie) continue;
+                        const uint64_t f = full_key_of(a[lo + i]);
+                        if ((f & m) == full) atomicAdd(&S.hist[(uint32_t)(f >> sh) & digit], 1u);
+                    }
+                    __syncthreads();
+                    find_bin<kThreads>(S, krem);
+                    full |= (uint64_t)S.bin << sh;
+                    m |= (uint64_t)digit << sh;
+                    krem -= S.before;
+                }
+            }
+            need = krem;
+        }
+        __syncthreads();
+    }
+
+    // state of row i: stays (1), one of the candidates equal to the last (2), goes (0)
+    auto state = [&](int i) {
+        if (i >= L) return 0;
+        if (i < lo || i >= hi || (from == 0u && tie == 0xFFFFFFFFu)) return 1;
+        if (want == 0) return 0;
+        const uint32_t k = key(i - lo);
+        if (k >= from) return 1;
+        if (k != tie) return 0;
+        const uint64_t f = full_key_of(a[i]);
+        return f > full ? 1 : f == full ? 2 : 0;
+    };
+    const int share = ((rows + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int i0 = warp * share, i1 = min(i0 + share, rows);
+    uint32_t n_in = 0, n_eq = 0;
+    for (int i = i0; i < i1; i += 32) {
+        const int s = i + lane < i1 ? state(i + lane) : 0;
+        n_in += __popc(__ballot_sync(0xFFFFFFFFu, s == 1));
+        n_eq += __popc(__ballot_sync(0xFFFFFFFFu, s == 2));
+    }
+    if (lane == 0) {
+        S.warp_in[warp] = n_in;
+        S.warp_eq[warp] = n_eq;
+    }
+    __syncthreads();
+    uint32_t in_before = 0, eq_before = 0;
+    for (int w = 0; w < warp; ++w) {
+        in_before += S.warp_in[w];
+        eq_before += S.warp_eq[w];
     }
     int32_t* kb = kept + bi * (int64_t)n_keep;
     int32_t* rb = remap + bi * (int64_t)rows;
-    uint32_t run = 0, run_eq = 0;
-    int buf = 0;
-    for (int base = 0; base < rows; base += kSelThreads, buf ^= 1) {
-        const int i = base + tid;
-        bool in = false, eq = false;
-        if (i < L) {
-            if (i < lo || i >= hi || all) {
-                in = true;
-            } else if (!none) {
-                const uint64_t k = key_of(a[i]);
-                in = k > T;
-                eq = k == T;
-            }
+    const uint32_t lt = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += 32) {
+        const int s = i + lane < i1 ? state(i + lane) : 0;
+        const uint32_t b_in = __ballot_sync(0xFFFFFFFFu, s == 1), b_eq = __ballot_sync(0xFFFFFFFFu, s == 2);
+        const uint32_t eq = eq_before + __popc(b_eq & lt);
+        const uint32_t slot = in_before + __popc(b_in & lt) + min(eq, need);
+        const bool stays = s == 1 || (s == 2 && eq < need);
+        if (i + lane < i1) {
+            rb[i + lane] = stays ? (int32_t)slot : -1;
+            // (a slot is below n_keep; the check keeps every store inside the row regardless)
+            if (stays && slot < (uint32_t)n_keep) kb[slot] = i + lane;
         }
-        const uint32_t bin = __ballot_sync(0xFFFFFFFFu, in), beq = __ballot_sync(0xFFFFFFFFu, eq);
-        if (lane == 0) {
-            tot[buf][warp][0] = __popc(bin);
-            tot[buf][warp][1] = __popc(beq);
-        }
-        __syncthreads();
-        uint32_t before = run, eq_before = run_eq, round = 0, eq_round = 0;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) {
-                before += tot[buf][w][0];
-                eq_before += tot[buf][w][1];
-            }
-            round += tot[buf][w][0];
-            eq_round += tot[buf][w][1];
-        }
-        const uint32_t lt = (1u << lane) - 1u;
-        before += __popc(bin & lt);
-        eq_before += __popc(beq & lt);
-        const bool stays = in || (eq && eq_before < need);
-        const uint32_t slot = before + min(eq_before, need);
-        if (i < rows) {
-            rb[i] = stays ? (int32_t)slot : -1;
-            if (stays && slot < (uint32_t)n_keep) kb[slot] = i;
-        }
-        run += round;
-        run_eq += eq_round;
+        in_before += __popc(b_in);
+        eq_before += __popc(b_eq);
     }
-    for (int j = n_stay + tid; j < n_keep; j += kSelThreads) kb[j] = -1;
+    for (int j = n_stay + tid; j < n_keep; j += kThreads) kb[j] = -1;
+}
+
+template <int kThreads, bool kCached>
+cudaError_t select_launch(const int64_t* acc, const int32_t* live, int64_t b, int rows, int n_keep,
+                          int keep_first, int keep_last, int32_t* kept, int32_t* remap,
+                          cudaStream_t stream) {
+    auto kernel = evict_select_kernel<kThreads, kCached>;
+    const size_t smem = kCached ? (size_t)rows * sizeof(uint32_t) : 0;
+    if (smem > 32 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, dim3((unsigned)b), dim3(kThreads), smem, stream, acc, live, rows, n_keep,
+                      keep_first, keep_last, kept, remap);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -135,33 +248,61 @@ struct Compact {
     const int32_t* kept;
 };
 
+// Into another buffer.  A block moves kChunk rows of one sequence, every tensor's; their entries of kept are
+// read once, and each thread has several units under way.
+constexpr int kChunk = 64, kOutThreads = 256;
+
 template <class T>
-__device__ __forceinline__ void compact_units(const Compact& c, const Tensor& t) {
-    const int64_t per_row = t.row_bytes / (int64_t)sizeof(T);
-    const int64_t total = c.b * c.n_keep * per_row;
-    for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t br = e / per_row, u = e - br * per_row;
-        const int64_t bi = br / c.n_keep, j = br - bi * c.n_keep;
-        const int32_t r = c.kept[br];
-        T v{};
-        if (r >= 0 && r < c.rows)
-            v = *reinterpret_cast<const T*>(t.src + bi * t.src_batch + r * t.row_bytes + u * (int64_t)sizeof(T));
-        *reinterpret_cast<T*>(t.dst + bi * t.dst_batch + j * t.row_bytes + u * (int64_t)sizeof(T)) = v;
+__device__ __forceinline__ void compact_units(const Tensor& t, int64_t bi, int64_t j0, int n,
+                                              const int32_t* from) {
+    const uint32_t per_row = (uint32_t)(t.row_bytes / (int64_t)sizeof(T));
+    const uint8_t* src = t.src + bi * t.src_batch;
+    uint8_t* dst = t.dst + bi * t.dst_batch + j0 * t.row_bytes;
+    // rows narrower than a block's threads share it; wider ones are walked by all of it
+    const uint32_t total = per_row * (uint32_t)n;  // below 2^31: the host checks
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 4 * kOutThreads) {
+        T v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t e = e0 + i * kOutThreads;
+            v[i] = T{};
+            if (e >= total) continue;
+            const uint32_t row = e / per_row;
+            const int32_t r = from[row];
+            if (r >= 0)
+                v[i] = *reinterpret_cast<const T*>(src + r * t.row_bytes + (e - row * per_row) * (uint32_t)sizeof(T));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t e = e0 + i * kOutThreads;
+            if (e < total) *reinterpret_cast<T*>(dst + e * (int64_t)sizeof(T)) = v[i];
+        }
     }
 }
 
-__global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ Compact c) {
+__global__ void __launch_bounds__(kOutThreads) compact_kernel(const __grid_constant__ Compact c) {
+    __shared__ int32_t from[kChunk];
     pdl_wait();
     pdl_trigger();
-    for (int i = 0; i < c.n; ++i) {
-        const Tensor& t = c.t[i];
-        switch (t.unit) {
-            case 16: compact_units<uint4>(c, t); break;
-            case 8: compact_units<uint2>(c, t); break;
-            case 4: compact_units<uint32_t>(c, t); break;
-            case 2: compact_units<uint16_t>(c, t); break;
-            default: compact_units<uint8_t>(c, t); break;
+    const int64_t chunks = (c.n_keep + kChunk - 1) / kChunk, items = c.b * chunks;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t bi = item / chunks, j0 = (item - bi * chunks) * kChunk;
+        const int n = (int)min((int64_t)kChunk, c.n_keep - j0);
+        __syncthreads();
+        if ((int)threadIdx.x < n) {
+            const int32_t r = c.kept[bi * c.n_keep + j0 + threadIdx.x];
+            from[threadIdx.x] = r < c.rows ? r : -1;
+        }
+        __syncthreads();
+        for (int i = 0; i < c.n; ++i) {
+            const Tensor& t = c.t[i];
+            switch (t.unit) {
+                case 16: compact_units<uint4>(t, bi, j0, n, from); break;
+                case 8: compact_units<uint2>(t, bi, j0, n, from); break;
+                case 4: compact_units<uint32_t>(t, bi, j0, n, from); break;
+                case 2: compact_units<uint16_t>(t, bi, j0, n, from); break;
+                default: compact_units<uint8_t>(t, bi, j0, n, from); break;
+            }
         }
     }
 }
@@ -296,9 +437,10 @@ extern "C" sa_status sa_evict_select(const int64_t* acc, const int32_t* live, in
     if (overlap(kept, kb, acc, ab) || overlap(remap, rb, acc, ab) || overlap(kept, kb, remap, rb) ||
         overlap(kept, kb, live, lb) || overlap(remap, rb, live, lb))
         return SA_ERR_INVALID_ARG;
-    return from_cuda(launch_pdl(evict_select_kernel, dim3((unsigned)b), dim3(kSelThreads), 0,
-                                reinterpret_cast<cudaStream_t>(stream), acc, live, (int)rows, (int)n_keep,
-                                (int)keep_first, (int)keep_last, kept, remap));
+    auto run = rows <= 2048 ? select_launch<256, true>
+               : rows <= kCachedRows ? select_launch<1024, true> : select_launch<1024, false>;
+    return from_cuda(run(acc, live, b, (int)rows, (int)n_keep, (int)keep_first, (int)keep_last, kept, remap,
+                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" sa_status sa_compact_rows(int n_tensors, const void* const* src, void* const* dst,
@@ -319,7 +461,7 @@ extern "C" sa_status sa_compact_rows(int n_tensors, const void* const* src, void
     out.rows = in.rows = rows;
     out.n_keep = in.n_keep = n_keep;
     out.kept = in.kept = kept;
-    int64_t src_len[SA_COMPACT_MAX_TENSORS], dst_len[SA_COMPACT_MAX_TENSORS], units = 0, in_blocks = 0;
+    int64_t src_len[SA_COMPACT_MAX_TENSORS], dst_len[SA_COMPACT_MAX_TENSORS], in_blocks = 0;
     for (int i = 0; i < n_tensors; ++i) {
         const int64_t rb = row_bytes[i];
         if (rb < 1 || !dst[i] || (rows > 0 && !src[i])) return SA_ERR_INVALID_ARG;
@@ -342,9 +484,8 @@ extern "C" sa_status sa_compact_rows(int n_tensors, const void* const* src, void
             in.t[in.n++] = t;
             in_blocks += b * groups_of(t);
         } else {
+            if (rb / t.unit > INT32_MAX / kChunk) return SA_ERR_UNSUPPORTED;
             out.t[out.n++] = t;
-            const int64_t n = b * n_keep * (rb / t.unit);
-            if (n > units) units = n;
         }
     }
     if (in_blocks >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
@@ -358,7 +499,9 @@ extern "C" sa_status sa_compact_rows(int n_tensors, const void* const* src, void
     }
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (out.n) {
-        const cudaError_t e = launch_pdl(compact_kernel, dim3(grid_for(units)), dim3(256), 0, st, out);
+        const int64_t items = b * ((n_keep + kChunk - 1) / kChunk);
+        const cudaError_t e = launch_pdl(compact_kernel, dim3((unsigned)(items < INT32_MAX ? items : INT32_MAX)),
+                                         dim3(kOutThreads), 0, st, out);
         if (e != cudaSuccess) return SA_ERR_CUDA;
     }
     if (in.n)
