@@ -6,7 +6,9 @@
 // otherwise: the scale comes from amax's bits, with no division.  1 / s is a power of two, so x_k / s is one
 // exact multiplication and the code the only rounding.
 //
-// Memory bound: 2 bytes an element in, 0.53 out (2.53 with the round trip).
+// Bound by memory (2 bytes an element in, 0.53 out, 2.53 with the round trip) only as long as a group of
+// eight elements takes less than about a hundred instructions: the common path looks for a NaN once a
+// group, multiplies 32-bit indices, and divides once in four groups.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,9 +33,10 @@ struct Quant4 {
     int64_t cs, cb;
     uint8_t* scales;
     int64_t ss, sb;
-    // ring write: row r of the n is token t_first + r % per_seq of sequence r / per_seq
-    int64_t seqlen, per_seq, t_first, start_pos;
-    int window;
+    // ring write: row r of the n is token r % per_seq (from t_first on) of sequence r / per_seq, and goes
+    // to slot (slot0 + r % per_seq) mod window; per_seq <= window
+    int64_t seqlen, per_seq, t_first;
+    int window, slot0;
 };
 
 // Where row r comes from and goes to (element and byte offsets).
@@ -41,21 +44,29 @@ struct Place {
     int64_t x, rt, codes, scales;
 };
 
-template <bool kRing>
-__device__ __forceinline__ Place place_of(const Quant4& p, int64_t r) {
+// The product of a row number and a stride: one instruction when both fit 32 bits (Index is uint32_t).
+template <class Index>
+__device__ __forceinline__ int64_t times(Index r, int64_t stride) {
+    if constexpr (sizeof(Index) == 4) return (int64_t)((uint64_t)r * (uint32_t)stride);
+    else return (int64_t)r * stride;
+}
+
+template <bool kRing, class Index>
+__device__ __forceinline__ Place place_of(const Quant4& p, Index r) {
     Place o;
     if constexpr (kRing) {
-        const int64_t bi = r / p.per_seq, t = p.t_first + (r - bi * p.per_seq);
-        const int64_t slot = (p.start_pos + t) % p.window;
-        o.x = (bi * p.seqlen + t) * p.xs;
-        o.rt = bi * p.rtb + slot * p.rts;
-        o.codes = bi * p.cb + slot * p.cs;
-        o.scales = bi * p.sb + slot * p.ss;
+        const Index bi = r / (Index)p.per_seq, t = r - bi * (Index)p.per_seq;
+        Index slot = (Index)p.slot0 + t;
+        if (slot >= (Index)p.window) slot -= (Index)p.window;
+        o.x = ((int64_t)bi * p.seqlen + p.t_first + (int64_t)t) * p.xs;
+        o.rt = (int64_t)bi * p.rtb + times(slot, p.rts);
+        o.codes = (int64_t)bi * p.cb + times(slot, p.cs);
+        o.scales = (int64_t)bi * p.sb + times(slot, p.ss);
     } else {
-        o.x = r * p.xs;
-        o.rt = r * p.rts;
-        o.codes = r * p.cs;
-        o.scales = r * p.ss;
+        o.x = times(r, p.xs);
+        o.rt = times(r, p.rts);
+        o.codes = times(r, p.cs);
+        o.scales = times(r, p.ss);
     }
     return o;
 }
@@ -75,63 +86,99 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t bits) {
     return a > 0x7F800000u ? 0u : a;
 }
 
-// Eight f32 values times inv -> eight e2m1 codes in a word (round to nearest even, saturating; a NaN 0).
+// Eight f32 values times inv -> eight e2m1 codes in a word (round to nearest even, saturating).
 __device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv) {
-    float y[8];
+    uint64_t y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = v[i] * inv;
-        if (y[i] != y[i]) y[i] = 0.f;
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("{\n .reg .b64 a, b;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %3};\n mul.rn.f32x2 %0, a, b;\n}"
+            : "=l"(y[i])
+            : "f"(v[2 * i]), "f"(v[2 * i + 1]), "f"(inv));
     uint32_t c;
-    asm("{\n .reg .b8 b0, b1, b2, b3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n .reg .f32 l, h;\n"
+        " mov.b64 {l, h}, %1;\n cvt.rn.satfinite.e2m1x2.f32 b0, h, l;\n"
+        " mov.b64 {l, h}, %2;\n cvt.rn.satfinite.e2m1x2.f32 b1, h, l;\n"
+        " mov.b64 {l, h}, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, h, l;\n"
+        " mov.b64 {l, h}, %4;\n cvt.rn.satfinite.e2m1x2.f32 b3, h, l;\n"
         " mov.b32 %0, {b0, b1, b2, b3};\n}"
         : "=r"(c)
-        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+        : "l"(y[0]), "l"(y[1]), "l"(y[2]), "l"(y[3]));
     return c;
 }
 
-// Eight consecutive elements a thread, four threads a block: the block's maximum takes two shuffles.
-// Needs 16-byte aligned x and round trip rows and 4-byte aligned code rows.
-template <bool kRing>
-__global__ void __launch_bounds__(256) quant4_kernel(Quant4 p) {
+constexpr int kThreads = 256;
+
+// Eight consecutive elements a thread, four threads a block: the block's maximum takes two shuffles.  A
+// thread has kPer such groups, kThreads apart, whose loads are all under way before the first is looked at
+// (kPer = 4 where there are groups enough for it, 1 for few rows, where only the latency counts).  Needs
+// 16-byte aligned x and round trip rows and 4-byte aligned code rows; Index holds the number of groups and
+// every stride.
+template <bool kRing, class Index, int kPer>
+__global__ void __launch_bounds__(kThreads) quant4_kernel(const __grid_constant__ Quant4 p) {
     pdl_wait();
     pdl_trigger();
-    const int g8 = p.d >> 3;
-    const int64_t total = p.n * g8;
-    for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = e / g8;
-        const int c = 8 * (int)(e - r * g8);
-        const Place o = place_of<kRing>(p, r);
-        const uint4 in = *reinterpret_cast<const uint4*>(p.x + o.x + c);
-        const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-        float v[8];
-        uint32_t amax = 0;
+    const Index g8 = (Index)(p.d >> 3), total = (Index)(p.n * (p.d >> 3));
+    const Index e0 = (Index)blockIdx.x * (kThreads * kPer) + threadIdx.x;
+    Place o[kPer];
+    Index c[kPer];  // the group in its row
+    uint4 in[kPer];
+    Index r = e0 / g8, at = e0 - r * g8;
+    const Index step_r = (Index)kThreads / g8, step_c = (Index)kThreads - step_r * g8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            amax = max(amax, max(magnitude(w[i] << 16), magnitude(w[i] & 0xFFFF0000u)));
+    for (int i = 0; i < kPer; ++i) {
+        if (e0 + i * kThreads < total) {
+            o[i] = place_of<kRing, Index>(p, r);
+            c[i] = at;
+            in[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + o[i].x) + at);
         }
-        // (a block's four lanes enter and leave the loop together: total is a multiple of four)
+        r += step_r;
+        at += step_c;
+        if (at >= g8) {
+            at -= g8;
+            ++r;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        // (a block's four lanes are inside or outside together: total is a multiple of four)
+        if (e0 + i * kThreads >= total) continue;
+        uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
         const unsigned grp = 0xFu << (threadIdx.x & 28);
-        amax = max(amax, __shfl_xor_sync(grp, amax, 1, 4));
-        amax = max(amax, __shfl_xor_sync(grp, amax, 2, 4));
-        const uint32_t se = scale_byte(amax);
+        // magnitudes order like their bits, so the maximum is one of 16-bit integers, two at a time
+        auto block_max = [&] {
+            uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                  __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            m = __vmaxu2(m, __shfl_xor_sync(grp, m, 1, 4));
+            m = __vmaxu2(m, __shfl_xor_sync(grp, m, 2, 4));
+            return max(m >> 16, m & 0xFFFFu);
+        };
+        uint32_t top = block_max();
+        if (top > 0x7F80u) {  // a NaN in the block: those count as 0
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                if ((w[y] & 0x7FFFu) > 0x7F80u) w[y] &= 0xFFFF0000u;
+                if ((w[y] >> 16 & 0x7FFFu) > 0x7F80u) w[y] &= 0x0000FFFFu;
+            }
+            top = block_max();
+        }
+        float v[8];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            v[2 * y] = __uint_as_float(w[y] << 16);
+            v[2 * y + 1] = __uint_as_float(w[y] & 0xFFFF0000u);
+        }
+        const uint32_t se = scale_byte(top << 16);
         const uint32_t cw = codes8(v, __uint_as_float((254u - se) << 23));
-        if (p.codes) *reinterpret_cast<uint32_t*>(p.codes + o.codes + (c >> 1)) = cw;
+        if (p.codes) reinterpret_cast<uint32_t*>(p.codes + o[i].codes)[c[i]] = cw;
         if (p.rt)
-            *reinterpret_cast<uint4*>(p.rt + o.rt + c) = fp4::dequant8(cw, __uint_as_float(se << 23));
-        if (p.scales && (c & 31) == 0) p.scales[o.scales + (c >> 5)] = (uint8_t)se;
+            reinterpret_cast<uint4*>(p.rt + o[i].rt)[c[i]] = fp4::dequant8(cw, __uint_as_float(se << 23));
+        if (p.scales && (c[i] & 3) == 0) (p.scales + o[i].scales)[c[i] >> 2] = (uint8_t)se;
     }
 }
 
 // Any alignment: a thread per block of 32.
 template <bool kRing>
-__global__ void __launch_bounds__(256) quant4_any_kernel(Quant4 p) {
+__global__ void __launch_bounds__(kThreads) quant4_any_kernel(Quant4 p) {
     pdl_wait();
     pdl_trigger();
     const int nb = p.d >> 5;
@@ -140,7 +187,7 @@ __global__ void __launch_bounds__(256) quant4_any_kernel(Quant4 p) {
          e += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = e / nb;
         const int c0 = 32 * (int)(e - r * nb);
-        const Place o = place_of<kRing>(p, r);
+        const Place o = place_of<kRing, int64_t>(p, r);
         const __nv_bfloat16* x = p.x + o.x + c0;
         uint32_t amax = 0;
         for (int i = 0; i < 32; ++i) amax = max(amax, magnitude(__float_as_uint(__bfloat162float(x[i]))));
@@ -149,7 +196,10 @@ __global__ void __launch_bounds__(256) quant4_any_kernel(Quant4 p) {
         for (int i = 0; i < 32; i += 8) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(x[i + j]);
+            for (int j = 0; j < 8; ++j) {
+                v[j] = __bfloat162float(x[i + j]);
+                if (v[j] != v[j]) v[j] = 0.f;  // a NaN counts as 0
+            }
             const uint32_t cw = codes8(v, inv);
             if (p.codes)
 #pragma unroll
@@ -181,13 +231,25 @@ sa_status launch(const Quant4& p, void* stream) {
     const bool wide = is_aligned(p.x, 16) && p.xs % 8 == 0 &&
                       (!p.rt || (is_aligned(p.rt, 16) && p.rts % 8 == 0 && p.rtb % 8 == 0)) &&
                       (!p.codes || (is_aligned(p.codes, 4) && p.cs % 4 == 0 && p.cb % 4 == 0));
-    const int64_t threads = p.n * (int64_t)(wide ? p.d / 8 : p.d / 32);
-    int64_t grid = (threads + 255) / 256;
-    const int64_t cap = (int64_t)device_sm_count() * 32;
-    if (grid > cap) grid = cap;
-    const cudaError_t e = launch_pdl(wide ? quant4_kernel<kRing> : quant4_any_kernel<kRing>,
-                                     dim3((unsigned)grid), dim3(256), 0,
-                                     reinterpret_cast<cudaStream_t>(stream), p);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (wide) {
+        const int64_t groups = p.n * (int64_t)(p.d / 8), most = int64_t(1) << 31;
+        const bool narrow = groups < most && p.xs < most && p.rts < most && p.cs < most && p.ss < most;
+        auto go = [&](auto kernel, int per) -> cudaError_t {
+            const int64_t grid = (groups + kThreads * per - 1) / (kThreads * per);
+            if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+            return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
+        };
+        if (!narrow) e = go(quant4_kernel<kRing, uint64_t, 4>, 4);
+        else if (groups < (int64_t)device_sm_count() * 8 * kThreads) e = go(quant4_kernel<kRing, uint32_t, 1>, 1);
+        else e = go(quant4_kernel<kRing, uint32_t, 4>, 4);
+    } else {
+        int64_t grid = (p.n * (int64_t)(p.d / 32) + kThreads - 1) / kThreads;
+        const int64_t cap = (int64_t)device_sm_count() * 32;
+        if (grid > cap) grid = cap;
+        e = launch_pdl(quant4_any_kernel<kRing>, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
+    }
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -260,8 +322,8 @@ extern "C" sa_status sa_window_write_fp4(const void* x, int64_t nbatch, int64_t 
     p.seqlen = seqlen;
     p.per_seq = seqlen < window ? seqlen : (int64_t)window;
     p.t_first = seqlen - p.per_seq;  // an earlier token's slot belongs to a later one
-    p.start_pos = start_pos;
     p.window = window;
+    p.slot0 = (int)((start_pos + p.t_first) % window);
     p.n = nbatch * p.per_seq;
     p.rt = reinterpret_cast<__nv_bfloat16*>(ring_rt);
     p.rts = rt_stride;

@@ -159,11 +159,12 @@ struct Cursor {
             u.step(p);
         }
     }
-    // the next unit that the group has a stage of
-    __device__ __forceinline__ Cursor next_unit(const Params& p) const {
-        Cursor n = *this;
-        do n.advance(p, 2);
-        while (n.i == i);
+    // the next unit that the group has a stage of (with one stage a unit, every other unit)
+    __device__ __forceinline__ Unit next_unit(const Params& p, int64_t& at) const {
+        Unit n = u;
+        n.step(p);
+        if (p.steps == 1) n.step(p);
+        at = i + (p.steps == 1 ? 2 : 1);
         return n;
     }
 };
@@ -175,6 +176,18 @@ struct Codes {
     uint32_t scale;  // the e8m0 byte; kNone: no row
 };
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// A bf16 gather warp's copies of a stage: 16 bytes of row i (of eight a lane) from kOff bytes into it.
+template <int kOff>
+__device__ __forceinline__ void copy_rows(const uint32_t (&dst)[4], const uint8_t* const (&src)[8],
+                                          uint32_t there) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (there >> i & 1) cp_async16_at<0, kOff>(dst[i], src[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (there >> (4 + i) & 1) cp_async16_at<1024, kOff>(dst[i], src[4 + i]);
+}
 
 template <int kFmt, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i)
             d[i] = s_kv + (uint32_t)(unit >> 3) * kBlockBytes + (r0 + 2 * i) * 128 +
                    ((uint32_t)((unit ^ (r0 + 2 * i)) & 7) << 4);
-        const int64_t row_bytes = (int64_t)p.steps * 256 - (p.half ? 128 : 0);
+        const uint32_t row_bytes = (uint32_t)p.steps * 256 - (p.half ? 128 : 0);
         const int64_t count = range.end - range.begin;
         bool ok = true, any_bad = false;
         int st = group, under_way = -1;  // the stage to fill; the one filled but not handed over
@@ -407,26 +420,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         Cursor cur(p, range.begin, group);
         const uint8_t* src[kPer];
         uint32_t there = 0;  // bit i: row r0 + 2 i has an entry
-        int jn[kPer];
+        // each lane brings the entry of one of the warp's rows
+        const int my_row = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane & 15);
+        int jn = cur.i < count ? entry_of(p, cur.u, my_row) : -1;
         int64_t unit_at = -1;  // the unit that src points into
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) jn[i] = cur.i < count ? entry_of(p, cur.u, r0 + 2 * i) : -1;
         while (cur.i < count) {
             if (cur.i != unit_at) {
                 unit_at = cur.i;
                 const uint8_t* base = p.kv + cur.u.seq * p.rows * row_bytes + unit * 16;
+                const int j = valid(p, jn, any_bad);
                 there = 0;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const int j = valid(p, jn[i], any_bad);
-                    there |= j >= 0 ? 1u << i : 0u;
-                    src[i] = base + j * row_bytes;
+                    const int ji = __shfl_sync(0xFFFFFFFFu, j, (lane >> 4) + 2 * i);
+                    there |= ji >= 0 ? 1u << i : 0u;
+                    src[i] = base + (uint64_t)(uint32_t)ji * row_bytes;
                 }
-                const Cursor nu = cur.next_unit(p);
-                if (nu.i < count) {
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) jn[i] = entry_of(p, nu.u, r0 + 2 * i);
-                }
+                int64_t at;
+                const Unit nu = cur.next_unit(p, at);
+                if (at < count) jn = entry_of(p, nu, my_row);
             }
             // the stage of the group's last turn is handed over before the wait for a free one, so that
             // the product has work while this warp waits for it
@@ -434,10 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             under_way = -1;
             if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
             if (!(cur.c == p.steps - 1 && p.half && unit >= 8)) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (there >> i & 1)
-                        cp_async16(d[i & 3] + st * kStageBytes + (i >> 2) * 1024, src[i] + cur.c * 256, 16u);
+                const uint32_t at = st * kStageBytes;
+                const uint32_t dd[4] = {d[0] + at, d[1] + at, d[2] + at, d[3] + at};
+                switch (cur.c) {
+                    case 0: copy_rows<0>(dd, src, there); break;
+                    case 1: copy_rows<256>(dd, src, there); break;
+                    case 2: copy_rows<512>(dd, src, there); break;
+                    default: copy_rows<768>(dd, src, there); break;
+                }
             }
             cp_async_commit();
             under_way = st;
@@ -461,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the lane's 16-byte units 4 (part % 2) .. + 3 of 64-d block part / 2; row r0 + 8 is 1024 bytes on
         const uint32_t dst = s_kv + (uint32_t)(part >> 1) * kBlockBytes + r0 * 128 +
                              ((uint32_t)((4 * (part & 1)) ^ (r0 & 7)) << 4);
-        const int64_t row_bytes = (int64_t)p.steps * (4 * kLaneBytes) - (p.half ? 2 * kLaneBytes : 0);
-        const int row_scales = 4 * p.steps - (p.half ? 2 : 0);
+        const uint32_t row_bytes = (uint32_t)p.steps * (4 * kLaneBytes) - (p.half ? 2 * kLaneBytes : 0);
+        const uint32_t row_scales = 4 * p.steps - (p.half ? 2 : 0);
         const int64_t count = range.end - range.begin;
         bool ok = true, any_bad = false;
         Cursor cur(p, range.begin, group);  // the stage to load next
@@ -477,18 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (cur.i >= count) return;
             if (cur.i != unit_at) {
                 unit_at = cur.i;
+                const int64_t first = cur.u.seq * p.rows;
+                const uint8_t* cb = p.kv + first * row_bytes + part * kLaneBytes;
+                const uint8_t* sb = p.kv_scale + first * row_scales + part;
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int j = valid(p, jn[y], any_bad);
-                    const int64_t row = cur.u.seq * p.rows + j;
                     there[y] = j >= 0;
-                    codes[y] = p.kv + row * row_bytes + part * kLaneBytes;
-                    scales[y] = p.kv_scale + row * row_scales + part;
+                    codes[y] = cb + (uint64_t)(uint32_t)j * row_bytes;
+                    scales[y] = sb + (uint64_t)(uint32_t)j * row_scales;
                 }
-                const Cursor nu = cur.next_unit(p);
-                if (nu.i < count) {
+                int64_t at;
+                const Unit nu = cur.next_unit(p, at);
+                if (at < count) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) jn[y] = entry_of(p, nu.u, r0 + 8 * y);
+                    for (int y = 0; y < 2; ++y) jn[y] = entry_of(p, nu, r0 + 8 * y);
                 }
             }
             const bool inside = !(cur.c == p.steps - 1 && p.half && part >= 2);
