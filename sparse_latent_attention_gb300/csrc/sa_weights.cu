@@ -14,7 +14,7 @@
 // tensor core cuts its running sum after every 16 products, and over all of d = 512 in one accumulator
 // that came to a relative error of 1.9e-6 in the weights.
 //
-// Roles (persistent CTAs, 26 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
+// Roles (persistent CTAs, 18 or 26 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
 // tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
 // short latencies (a copy phase ~270 cycles, a hand-over ~250, a tile's epilogue ~3500), longer than the
 // product itself takes, so two groups of warps take turns at the stages and two at the tiles:
@@ -22,7 +22,7 @@
 //   warp 1       Q by TMA (128-byte swizzle), 128 d at a time: that part of the next token's Q is loaded as
 //                soon as the last tile's product has passed it
 //   warps 2-9    epilogue: exponentials, sum over heads, accumulation; four warps a tile
-//   warps 10-25  gather, eight warps a stage, 16 rows each: bf16 rows with 16-byte cp.async; rows of codes
+//   warps 10-    gather, four or eight warps a stage: bf16 rows with 16-byte cp.async; rows of codes
 //                are loaded a turn ahead into registers and widened into the stage (exact: see
 //                sa_fp8.cuh, sa_fp4.cuh)
 
@@ -45,12 +45,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUnits = 4294967296.f;  // 2^32 units of the accumulator to a weight of 1
 
 constexpr int kTile = 128;              // entries per tile (M)
-constexpr int kWarpEpilogue = 2, kWarpGather = 10, kGroupWarps = 8;
-constexpr int kThreads = 32 * (kWarpGather + 2 * kGroupWarps);
-constexpr int kWarpRows = kTile / kGroupWarps;       // rows of a stage that a gather warp fills
+constexpr int kWarpEpilogue = 2, kWarpGather = 10;
 constexpr int kMaxSteps = 4;            // 128-d stages of a row: d <= 512
 constexpr uint32_t kBlockBytes = kTile * 128;        // 64 d of a tile
 constexpr uint32_t kStageBytes = 2 * kBlockBytes;
+
+// By the kv format: the warps of a gather group, and the rows of a stage that each fills.  Copying takes few
+// instructions, and fewer warps leave the others quicker (a prefill's 4096 queries x 640 bf16 rows, 64 heads:
+// 257 us with four, 298 with eight); widening takes many (a long decode's 256 x 2176 4-bit rows, 128 heads:
+// 106 us with eight, 121 with four).
+template <int kFmt>
+struct Gather {
+    static constexpr int kWarps = kFmt == SA_KV_BF16 ? 4 : 8;
+    static constexpr int kRows = kTile / kWarps;
+    static constexpr int kThreads = 32 * (kWarpGather + 2 * kWarps);
+};
 
 // By the heads a product covers (kN = 64 or 128): the stages that fit beside Q.
 template <int kN>
@@ -177,23 +186,22 @@ struct Codes {
 };
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-// A bf16 gather warp's copies of a stage: 16 bytes of row i (of eight a lane) from kOff bytes into it.
-template <int kOff>
-__device__ __forceinline__ void copy_rows(const uint32_t (&dst)[4], const uint8_t* const (&src)[8],
+// A bf16 gather warp's copies of a stage: 16 bytes of each of a lane's kPer rows from kOff bytes into it.
+// Row i's place is 1024 bytes (eight rows) on from row i - 4's.
+template <int kOff, int kPer, int kI = 0>
+__device__ __forceinline__ void copy_rows(const uint32_t (&dst)[4], const uint8_t* const (&src)[kPer],
                                           uint32_t there) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (there >> i & 1) cp_async16_at<0, kOff>(dst[i], src[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (there >> (4 + i) & 1) cp_async16_at<1024, kOff>(dst[i], src[4 + i]);
+    if constexpr (kI < kPer) {
+        if (there >> kI & 1) cp_async16_at<(kI / 4) * 1024, kOff>(dst[kI % 4], src[kI]);
+        copy_rows<kOff, kPer, kI + 1>(dst, src, there);
+    }
 }
 
 template <int kFmt, int kN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
     row_weights_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
     using Sh = Shape<kN>;
-    constexpr int kStages = Sh::kStages;
+    constexpr int kStages = Sh::kStages, kGroupWarps = Gather<kFmt>::kWarps, kWarpRows = Gather<kFmt>::kRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -256,8 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
                 uint32_t blo = (uint32_t)b0 + 2 * c * (Sh::kQBlockBytes >> 4);
                 const int blocks = c == p.steps - 1 && p.half ? 1 : 2;
-#pragma unroll 1
-                for (int k64 = 0; k64 < blocks; ++k64) {
+#pragma unroll
+                for (int k64 = 0; k64 < 2; ++k64) {
+                    if (k64 == blocks) break;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mma_lohi_elect(col, alo + 2 * q, ahi, blo + 2 * q, bhi, id,
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if constexpr (kFmt == SA_KV_BF16) {
         // ------------------------------------------------------------------ gather, bf16
         // Lane l copies 16-byte unit l % 16 (of a stage's 256 bytes) of rows l / 16, l / 16 + 2, ... of the
-        // warp's 16: two rows' 256 bytes an instruction.
+        // warp's 32: two rows' 256 bytes an instruction.
         constexpr int kPer = kWarpRows / 2;
         const int group = (warp - kWarpGather) / kGroupWarps, unit = lane & 15;
         const int r0 = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane >> 4);  // row r0 + 2 i
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* src[kPer];
         uint32_t there = 0;  // bit i: row r0 + 2 i has an entry
         // each lane brings the entry of one of the warp's rows
-        const int my_row = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane & 15);
+        const int my_row = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + lane % kWarpRows;
         int jn = cur.i < count ? entry_of(p, cur.u, my_row) : -1;
         int64_t unit_at = -1;  // the unit that src points into
         while (cur.i < count) {
@@ -449,10 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t at = st * kStageBytes;
                 const uint32_t dd[4] = {d[0] + at, d[1] + at, d[2] + at, d[3] + at};
                 switch (cur.c) {
-                    case 0: copy_rows<0>(dd, src, there); break;
-                    case 1: copy_rows<256>(dd, src, there); break;
-                    case 2: copy_rows<512>(dd, src, there); break;
-                    default: copy_rows<768>(dd, src, there); break;
+                    case 0: copy_rows<0, kPer>(dd, src, there); break;
+                    case 1: copy_rows<256, kPer>(dd, src, there); break;
+                    case 2: copy_rows<512, kPer>(dd, src, there); break;
+                    default: copy_rows<768, kPer>(dd, src, there); break;
                 }
             }
             cp_async_commit();
@@ -468,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any_bad) atomicOr(p.status, kStatusBadIndex);
     } else {
         // ------------------------------------------------------------------ gather, rows of codes
-        // Lane l widens a scale's block, codes 32 (l / 8) .. + 31 of a 128-d stage, of rows l % 8 and
-        // l % 8 + 8 of the warp's 16 (a store instruction's eight lanes meet eight rows: no bank conflict).
+        // Lane l widens a scale's block, codes 32 (l / 8) .. + 31 of a 128-d stage, of rows l % 8,
+        // l % 8 + 8, ... of the warp's (a store instruction's eight lanes meet eight rows: no bank conflict).
         // The codes of the group's next stage are loaded before it waits for that stage.
-        constexpr int kLaneBytes = kFmt == SA_KV_FP4_E2M1 ? 16 : 32;
+        constexpr int kLaneBytes = kFmt == SA_KV_FP4_E2M1 ? 16 : 32, kPer = kWarpRows / 8;
         const int group = (warp - kWarpGather) / kGroupWarps, part = lane >> 3;
-        const int r0 = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane & 7);  // rows r0, r0 + 8
+        const int r0 = kWarpRows * ((warp - kWarpGather) % kGroupWarps) + (lane & 7);  // row r0 + 8 y
         // the lane's 16-byte units 4 (part % 2) .. + 3 of 64-d block part / 2; row r0 + 8 is 1024 bytes on
         const uint32_t dst = s_kv + (uint32_t)(part >> 1) * kBlockBytes + r0 * 128 +
                              ((uint32_t)((4 * (part & 1)) ^ (r0 & 7)) << 4);
@@ -482,24 +491,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t count = range.end - range.begin;
         bool ok = true, any_bad = false;
         Cursor cur(p, range.begin, group);  // the stage to load next
-        const uint8_t *codes[2] = {nullptr, nullptr}, *scales[2] = {nullptr, nullptr};
-        bool there[2] = {false, false};
-        int jn[2];
+        const uint8_t *codes[kPer], *scales[kPer];
+        uint32_t there = 0;  // bit y: row r0 + 8 y has an entry
+        int jn[kPer];
         int64_t unit_at = -1;  // the unit that codes points into
 #pragma unroll
-        for (int y = 0; y < 2; ++y) jn[y] = cur.i < count ? entry_of(p, cur.u, r0 + 8 * y) : -1;
-        Codes<kFmt> x[2];
+        for (int y = 0; y < kPer; ++y) jn[y] = cur.i < count ? entry_of(p, cur.u, r0 + 8 * y) : -1;
+        Codes<kFmt> x[kPer];
         auto load = [&] {
             if (cur.i >= count) return;
             if (cur.i != unit_at) {
                 unit_at = cur.i;
                 const int64_t first = cur.u.seq * p.rows;
+                there = 0;
                 const uint8_t* cb = p.kv + first * row_bytes + part * kLaneBytes;
                 const uint8_t* sb = p.kv_scale + first * row_scales + part;
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                for (int y = 0; y < kPer; ++y) {
                     const int j = valid(p, jn[y], any_bad);
-                    there[y] = j >= 0;
+                    there |= j >= 0 ? 1u << y : 0u;
                     codes[y] = cb + (uint64_t)(uint32_t)j * row_bytes;
                     scales[y] = sb + (uint64_t)(uint32_t)j * row_scales;
                 }
@@ -507,14 +517,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Unit nu = cur.next_unit(p, at);
                 if (at < count) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) jn[y] = entry_of(p, nu, r0 + 8 * y);
+                    for (int y = 0; y < kPer; ++y) jn[y] = entry_of(p, nu, r0 + 8 * y);
                 }
             }
             const bool inside = !(cur.c == p.steps - 1 && p.half && part >= 2);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < kPer; ++y) {
                 x[y].scale = kNone;
-                if (there[y] && inside) {
+                if ((there >> y & 1) && inside) {
                     const uint4* at = reinterpret_cast<const uint4*>(codes[y] + cur.c * (4 * kLaneBytes));
 #pragma unroll
                     for (int i = 0; i < kLaneBytes / 16; ++i) {
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t s = group; s < n_stages; s += 2) {
             if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < kPer; ++y) {
                 if (x[y].scale == kNone) continue;
                 const uint32_t at = dst + st * kStageBytes + 1024 * y;
                 const float sc = kFmt == SA_KV_FP4_E2M1 ? fp4::scale_f32(x[y].scale)
@@ -589,7 +599,7 @@ cudaError_t launch(const CUtensorMap& map, const Params& p, cudaStream_t stream)
     }
     const int64_t sms = device_sm_count();
     const dim3 grid((unsigned)(p.n_units < sms ? p.n_units : sms));
-    return launch_pdl(row_weights_kernel<kFmt, kN>, grid, dim3(kThreads), smem_bytes<kN>(), stream, map, p);
+    return launch_pdl(row_weights_kernel<kFmt, kN>, grid, dim3(Gather<kFmt>::kThreads), smem_bytes<kN>(), stream, map, p);
 }
 
 template <int kN>
