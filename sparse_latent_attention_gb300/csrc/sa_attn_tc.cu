@@ -30,8 +30,11 @@
 //               cp.async 16 B into the swizzled layout (rows of codes are staged raw and widened in
 //               place); rows already resident from the previous pair are kept -- see below
 //   warps 6-9   softmax: S -> P (bf16, shared memory), running max and sum, O rescale
-//   warps 10-13 epilogue: O^T -> o (bf16) or split partials; with fp8 or fp4 kv, between epilogues,
+//   warps 10-13 epilogue: O^T -> o (bf16) or split partials; with fp8 kv, between epilogues,
 //               they widen the second half (d 256-511) of every staged tile
+//   warps 15-18 (e2m1 rows only) gather helpers: half of the rows of gather warps 2-5.  A 4-bit row is small
+//               enough to wait in registers: its 256 bytes are loaded while the buffer is still in use
+//               and widened straight into it, with no staging in between
 // Every wait is bounded; a wait that gives up raises the timeout bit and every role unwinds.
 //
 // Row placement.  The order of the gathered rows inside a tile does not matter (the softmax and
@@ -69,7 +72,9 @@ constexpr int kProdThreads = 32 * kProdWarps;       // = the 128 columns of a pa
 constexpr int kWarpSoftmax = 2 + kProdWarps;        // first softmax warp
 constexpr int kWarpEpilogue = kWarpSoftmax + 4;     // first epilogue warp
 constexpr int kWarpPv = kWarpEpilogue + 4;         // P.V issue
+constexpr int kWarpHelp = kWarpPv + 1;             // four more gather warps with e2m1 rows
 constexpr int kThreads = 32 * (kWarpPv + 1);
+constexpr int threads_of(int fmt) { return fmt == SA_KV_FP4_E2M1 ? kThreads + 32 * kProdWarps : kThreads; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // TMEM columns: O^T chunks (4 x 64), the two S buffers (2 x 64)
@@ -91,7 +96,9 @@ constexpr uint32_t kOffMisc = kOffP + 2 * kPBytes;
 struct Misc {
     uint64_t q_full, q_empty;
     uint64_t kv_full[2], kv_empty[2];  // per kv buffer
-    uint64_t staged[2];                // fp8: a tile's raw codes have landed (per kv buffer)
+    uint64_t staged[2];                // fp8: a tile's raw codes have landed (per kv buffer);
+                                       // fp4: a pair's lists are there (per pair parity)
+    uint64_t list_empty[2];            // fp4: those lists have been read
     uint64_t s_full[2], s_empty[2];    // per S buffer (TMEM)
     uint64_t p_full[2], p_empty[2];    // per P buffer (shared memory)
     uint64_t o_full, o_empty[kChunks];
@@ -105,14 +112,16 @@ struct Misc {
     int ring_count[3];                 // number of valid rows of a pair
     int64_t pair_seq[3];               // sequence whose rows a pair holds
     int row_id[2 * kRows];             // kv row held by each slot of the two buffers, -1 = none
-    int2 copy_list[kProdWarps][2][32];  // per producer warp and tile: (kv row, slot) to copy
-    int copy_n[kProdWarps][2];          // the lengths of those lists
+    int2 copy_list[2][kProdWarps][2][32];  // per gather warp and tile: (kv row, slot) to copy
+    int copy_n[2][kProdWarps][2];          // the lengths of those lists (fp4: two pairs' lists in turn,
+    uint32_t claim[2][kProdWarps];         // and their claimed slots; the others use the first)
     float alpha[2][kHeads];            // rescale factor of the tile, per tile parity
     float stats_m[2][kHeads];          // final max (0 when none) per task parity
     float stats_l[2][kHeads];          // final sum per task parity
     alignas(16) float inv[4][kHeads];  // epilogue: 1 / denominator, a table per epilogue warp
     float sink[kHeads];                // the sinks of the CTA's head block
-    alignas(16) uint8_t fp8_sc[2 * kRows][16];  // e8m0 scales of the rows an fp8 tile widens
+    // e8m0 scales of the rows that an fp8 tile (fp4: a pair of tiles, two pairs in turn) widens, by slot
+    alignas(16) uint8_t row_sc[2][2 * kRows][16];
 };
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -239,12 +248,11 @@ __device__ __forceinline__ uint32_t kv_unit_off(int ps, int u) {
            ((((uint32_t)u & 7) ^ ((uint32_t)ps & 7)) << 4);
 }
 
-// Widens 128-d chunks c0 .. c1 - 1 of the fp8 or fp4 rows a warp lists, in place: the codes of chunk c
-// (128 bytes of e4m3, 64 of e2m1) sit raw in 64-d block 2c + 1 of the row's slot and become bf16 in
-// blocks 2c and 2c + 1 (exact: see sa_fp8.cuh, sa_fp4.cuh).  Lane l moves 16-code unit l % 8 (`unit`)
-// of list entries l / 8 + 4 i (ent[i], x < 0 = none); the row's 16 e8m0 scales are in fp8_sc.
-template <int kFmt>
-__device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const int2 (&ent)[8], int unit,
+// Widens 128-d chunks c0 .. c1 - 1 of the fp8 rows a warp lists, in place: the e4m3 codes of chunk
+// c sit raw in 64-d block 2c + 1 of the row's slot and become bf16 in blocks 2c and 2c + 1 (exact:
+// see sa_fp8.cuh).  Lane l moves 16-code unit l % 8 (`unit`) of list entries l / 8 + 4 i (ent[i],
+// x < 0 = none); the row's 16 e8m0 scales are in row_sc.
+__device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const int2 (&ent)[8], int unit,
                                           int c0, int c1) {
     // Per entry, once: the slot's offset inside a 64-d block (buffer and row) and the byte offset
     // of this lane's first bf16 unit in it.  Unit u = 16 c + 2 unit of the row sits in block
@@ -258,11 +266,10 @@ __device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const 
         rb[i] = (r >> 6) * kBlkBytes + (r & 63) * 128;
         xo[i] = rb[i] + (uo ^ ((r & 7) << 4));
     }
-    constexpr int kUnitBytes = kFmt == SA_KV_FP4_E2M1 ? 8 : 16;  // sixteen codes
-    const uint8_t* sc_base = &M.fp8_sc[0][0] + (unit >> 1);
+    const uint8_t* sc_base = &M.row_sc[0][0][0] + (unit >> 1);
 #pragma unroll 1
     for (int cw = c0; cw < c1; ++cw) {
-        const uint32_t code_at = s_kv + (2 * cw + 1) * kDBlkBytes + unit * kUnitBytes;
+        const uint32_t code_at = s_kv + (2 * cw + 1) * kDBlkBytes + unit * 16;
         const uint32_t out_at = s_kv + (2 * cw + (unit >> 2)) * kDBlkBytes;
         // entries in two groups of four; a row's 8 lanes read all its codes before any writes
 #pragma unroll
@@ -273,19 +280,11 @@ __device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const 
             for (int i = 0; i < 4; ++i) {
                 const int2 en = ent[4 * g + i];
                 if (en.x < 0) break;
-                if constexpr (kFmt == SA_KV_FP4_E2M1) {
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                 : "=r"(code[i].x), "=r"(code[i].y)
-                                 : "r"(code_at + rb[4 * g + i])
-                                 : "memory");
-                    sc[i] = fp4::scale_f32(sc_base[en.y * 16 + 4 * cw]);
-                } else {
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
-                                 : "r"(code_at + rb[4 * g + i])
-                                 : "memory");
-                    sc[i] = fp8::e8m0_to_f32(sc_base[en.y * 16 + 4 * cw]);
-                }
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
+                             : "r"(code_at + rb[4 * g + i])
+                             : "memory");
+                sc[i] = fp8::e8m0_to_f32(sc_base[en.y * 16 + 4 * cw]);
             }
             __syncwarp();
 #pragma unroll
@@ -293,10 +292,7 @@ __device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const 
                 const int2 en = ent[4 * g + i];
                 if (en.x < 0) break;
                 uint4 lo, hi;
-                if constexpr (kFmt == SA_KV_FP4_E2M1)
-                    fp4::dequant16(make_uint2(code[i].x, code[i].y), sc[i], lo, hi);
-                else
-                    fp8::dequant16(code[i], sc[i], lo, hi);
+                fp8::dequant16(code[i], sc[i], lo, hi);
                 const uint32_t at = out_at + xo[4 * g + i];
                 st_shared_v4(at, lo.x, lo.y, lo.z, lo.w);
                 st_shared_v4(at ^ 16u, hi.x, hi.y, hi.z, hi.w);
@@ -305,13 +301,120 @@ __device__ __forceinline__ void widen_codes(uint32_t s_kv, const Misc& M, const 
     }
 }
 
+// The 32 codes of one e2m1 scale block (units u of 16 to a row) widened to bf16 in the kv buffers, in slot
+// ps.  They are four 16-byte units of a 64-d block; lanes of a row store theirs in an order that differs by
+// u / 2, so that eight lanes of one row (four 64-d blocks, a multiple of 128 bytes apart) meet eight banks.
+__device__ __forceinline__ void widen_fp4(uint32_t s_kv, uint4 c, uint32_t scale, int ps, int u) {
+    const int rot = (u >> 1) & 3;
+    if (rot & 1) {
+        uint32_t x = c.x, z = c.z;
+        c.x = c.y;
+        c.y = x;
+        c.z = c.w;
+        c.w = z;
+    }
+    if (rot & 2) {
+        uint32_t x = c.x, y = c.y;
+        c.x = c.z;
+        c.z = x;
+        c.y = c.w;
+        c.w = y;
+    }
+    const uint32_t at = s_kv + (uint32_t)(u >> 1) * kDBlkBytes + (uint32_t)(ps >> 6) * kBlkBytes +
+                        (uint32_t)(ps & 63) * 128 + ((uint32_t)((4 * (u & 1)) ^ (ps & 7) ^ rot) << 4);
+    const float sc = fp4::scale_f32(scale);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint4 v = fp4::dequant8(w[k], sc);
+        st_shared_v4(at ^ ((uint32_t)k << 4), v.x, v.y, v.z, v.w);
+    }
+}
+
+// Walks the pairs of tiles of a CTA's tasks in order.
+struct Pair {
+    Task t;
+    int64_t tau;
+    int ti;      // its first tile
+    uint32_t T;  // that tile's number among all the CTA works on
+    __device__ __forceinline__ Pair(const Params& p, int64_t tb, int64_t te) : t(task_of(p, tb)), tau(tb), T(0) {
+        ti = t.t0;
+        settle(p, te);
+    }
+    __device__ __forceinline__ int tiles() const { return min(2, t.t1 - ti); }
+    __device__ __forceinline__ void settle(const Params& p, int64_t te) {
+        while (tau < te && ti >= t.t1) {
+            ++tau;
+            task_step(p, t);
+            ti = t.t0;
+        }
+    }
+    __device__ __forceinline__ void step(const Params& p, int64_t te) {
+        T += tiles();
+        ti += 2;
+        settle(p, te);
+    }
+};
+
+// The gather of e2m1 rows, by eight warps: gather warp pw and its helper (who = 0, 1) share the rows that the
+// gather warp lists.  A row's 256 bytes of codes go to 16 lanes, two rows an instruction; its codes wait in
+// registers from one pair of tiles to the next, and are widened straight into the buffer once it is released.
+// The gather warps resolve and list a pair (as described for the other formats) before the one in front of
+// it is widened, and pull its rows into L2, so that a list's latency, and then the codes', pass behind the
+// widening.  The scales go to shared memory, 16 bytes a row (a byte load for every lane filled the L1's
+// few lines beside 224 KB of shared memory: a long decode took 512 us instead of 351).
+constexpr int kHeld = 4;  // rows of a tile that a lane holds codes of (a list of 16 split in two); more are
+                          // loaded when they are widened
+
+struct Held {
+    uint4 code[kHeld];
+};
+
+__device__ __forceinline__ void load_fp4(const Params& p, Misc& M, Held& x, int64_t seq, int buf, int pw, int hx,
+                                         int who, int lane) {
+    const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4);
+    const uint8_t* kvb = p.kv8 + seq * p.rows * (int64_t)(kD / 2) + 16 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (e0 + 4 * i < n) {
+            const uint32_t j = (uint32_t)M.copy_list[buf][pw][hx][e0 + 4 * i].x;
+            x.code[i] = __ldg(reinterpret_cast<const uint4*>(kvb + (uint64_t)j * (kD / 2)));
+        }
+    // a lane a row: the warp's entries are 4 i + 2 who and 4 i + 2 who + 1
+    const int e = 4 * (lane >> 1) + 2 * who + (lane & 1);
+    if (e < n) {
+        const int2 en = M.copy_list[buf][pw][hx][e];
+        cp_async16(smem_addr(&M.row_sc[buf][en.y][0]),
+                   p.kv_scale + (seq * p.rows + en.x) * (int64_t)(kD / 32), 16u);
+    }
+    cp_async_commit();
+}
+
+__device__ __forceinline__ void widen_tile_fp4(const Params& p, const Misc& M, uint32_t s_kv, const Held& x,
+                                               int64_t seq, int buf, int pw, int hx, int who, int lane) {
+    const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4), u = lane & 15;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (e0 + 4 * i < n) {
+            const int ps = M.copy_list[buf][pw][hx][e0 + 4 * i].y;
+            widen_fp4(s_kv, x.code[i], M.row_sc[buf][ps][u], ps, u);
+        }
+#pragma unroll 1
+    for (int e = e0 + 4 * kHeld; e < n; e += 4) {
+        const int2 en = M.copy_list[buf][pw][hx][e];
+        const uint4 c = __ldg(reinterpret_cast<const uint4*>(p.kv8 + (seq * p.rows + en.x) * (kD / 2) + 16 * u));
+        widen_fp4(s_kv, c, M.row_sc[buf][en.y][u], en.y, u);
+    }
+}
+
 // kRope: the inverse rotation of o's rope dims is fused into the epilogue (a separate
 // instantiation, so that the plain kernel carries none of its code)
 template <int kFmt, bool kRope>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kFmt), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
-    constexpr bool kCodes = kFmt != SA_KV_BF16;  // rows of codes, widened in shared memory
-    constexpr int kRowBytes = kFmt == SA_KV_FP4_E2M1 ? kD / 2 : kD;  // a row's codes
+    // rows of codes: e4m3 is staged raw in shared memory and widened in place there; e2m1 comes through
+    // registers, widened on its way by the gather warps and their four helpers
+    constexpr bool kCodes = kFmt != SA_KV_BF16, kStaged = kFmt == SA_KV_FP8_E4M3, kDirect = kCodes && !kStaged;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -328,9 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&M.q_full), 1);
         mbar_init(smem_addr(&M.q_empty), 1);
         for (int b = 0; b < 2; ++b) {
-            // codes: the epilogue warps widen half of every tile, so they arrive too
-            mbar_init(smem_addr(&M.kv_full[b]), kCodes ? kProdThreads + 128 : kProdThreads);
-            mbar_init(smem_addr(&M.staged[b]), kProdThreads);
+            // fp8: the epilogue warps widen half of every tile, so they arrive too; fp4: a lane of each
+            // gather warp and helper arrives
+            mbar_init(smem_addr(&M.kv_full[b]), kStaged   ? kProdThreads + 128
+                                                : kDirect ? 2 * kProdWarps
+                                                          : kProdThreads);
+            mbar_init(smem_addr(&M.staged[b]), kDirect ? kProdWarps : kProdThreads);
+            mbar_init(smem_addr(&M.list_empty[b]), 2 * kProdWarps);
             mbar_init(smem_addr(&M.kv_empty[b]), 1);
             mbar_init(smem_addr(&M.s_full[b]), 1);
             mbar_init(smem_addr(&M.s_empty[b]), 128);
@@ -352,21 +459,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     // every slot starts as a finite (zero) row that no tile claims
-    for (int i = tid; i < 2 * kRows; i += kThreads) M.row_id[i] = -1;
+    for (int i = tid; i < 2 * kRows; i += threads_of(kFmt)) M.row_id[i] = -1;
     if (tid < 12) (&M.ring_bits[0][0])[tid] = 0;
     if (tid < 3) {
         M.ring_count[tid] = 0;
         M.pair_seq[tid] = -1;
         M.need_corr[tid] = 0;
     }
-    for (uint32_t i = tid; i < kKvBytes / 16; i += kThreads)
+    for (uint32_t i = tid; i < kKvBytes / 16; i += threads_of(kFmt))
         reinterpret_cast<uint4*>(smem + kOffKv)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == 1 && lane == 0) tma_prefetch_desc(&q_map);
     // the set-up above touches no global memory; everything below may read what the work queued
     // before this launch writes
     pdl_wait();
-    for (int i = tid; i < kHeads; i += kThreads)
+    for (int i = tid; i < kHeads; i += threads_of(kFmt))
         M.sink[i] = hb * kHeads + i < p.h ? p.sink[hb * kHeads + i] : 0.f;
     tc_fence_before();
     __syncthreads();
@@ -494,6 +601,139 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok && k > 0) mbar_drain(smem_addr(&M.q_full), (uint32_t)((k - 1) & 1));
         }
         __syncwarp();
+    } else if (kDirect && (warp < kWarpSoftmax || warp >= kWarpHelp)) {
+        // ------------------------------------------------------------------ kv gather, e2m1 rows
+        const int who = warp >= kWarpHelp ? 1 : 0, pw = warp - (who ? kWarpHelp : 2);
+        const int pt = (lane >> 4) * kRows + 16 * pw + (lane & 15);  // a gather thread's pair column
+        uint32_t pr_phase = 0, g3 = 0, k = 0;
+        bool ok = true;
+        // the entry of a gather thread's column, loaded a pair ahead
+        auto raw_entry = [&](const Pair& a) {
+            const int col = a.ti * kRows + pt;
+            return a.tau < te && col < min(p.topk, a.t.t1 * kRows) ? __ldg(p.idx + a.t.token * (int64_t)p.topk + col)
+                                                                   : -1;
+        };
+        // resolves pair `a` (entries j) into list `buf`: the placement and bookkeeping of the gather below
+        auto resolve = [&](const Pair& a, int j, int buf) {
+            asm volatile("" : "+r"(j));  // (no test of it moves up to the load)
+            const int nt = a.tiles();
+            const uint32_t gprev = g3 == 0 ? 2 : g3 - 1, gnext = g3 == 2 ? 0 : g3 + 1;
+            if (j < -1 || j >= p.rows) {
+                atomicOr(p.status, kStatusBadIndex);
+                j = -1;
+            }
+            const uint32_t w = (uint32_t)(j & 127) >> 5, bit = j >= 0 ? 1u << (j & 31) : 0u;
+            uint32_t wb[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wb[q] = __reduce_or_sync(0xffffffffu, w == (uint32_t)q ? bit : 0u);
+            const uint32_t nv = (uint32_t)__popc(__ballot_sync(0xffffffffu, j >= 0));
+            if (lane == 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (wb[q]) atomicOr(&M.ring_bits[g3][q], wb[q]);
+                if (nv) atomicAdd(&M.ring_count[g3], (int)nv);
+            }
+            if (pt == 0) M.pair_seq[g3] = a.t.seq;
+            if (!__all_sync(0xFFFFFFFFu, wg_sync(smem_addr(&M.pr_bar), pr_phase, abort))) return false;
+            const bool same_seq = M.pair_seq[gprev] == a.t.seq;
+            const bool ring = nt == 2 && __popc(M.ring_bits[g3][0]) + __popc(M.ring_bits[g3][1]) +
+                                                 __popc(M.ring_bits[g3][2]) + __popc(M.ring_bits[g3][3]) ==
+                                             M.ring_count[g3];
+            const bool claimed = ring ? ((M.ring_bits[g3][pt >> 5] >> (pt & 31)) & 1) != 0 : j >= 0;
+            const int slot = ring ? (j & 127) : pt;
+            const int ps_own = (int)((((a.T + (uint32_t)(pt >> 6)) & 1) << 6) | (uint32_t)(pt & 63));
+            const int ps = (int)((((a.T + (uint32_t)(slot >> 6)) & 1) << 6) | (uint32_t)(slot & 63));
+            if (!claimed) M.row_id[ps_own] = -1;
+            const bool copy = j >= 0 && !(same_seq && M.row_id[ps] == j);
+            if (j >= 0) M.row_id[ps] = j;
+            if (pt == 0) {
+                M.ring_bits[gprev][0] = M.ring_bits[gprev][1] = 0;
+                M.ring_bits[gprev][2] = M.ring_bits[gprev][3] = 0;
+                M.ring_count[gprev] = 0;
+            }
+            g3 = gnext;
+            const uint32_t m_claim = __ballot_sync(0xFFFFFFFFu, claimed);
+            const int half = slot >> 6;
+            const uint32_t mh0 = __ballot_sync(0xFFFFFFFFu, copy && half == 0);
+            const uint32_t mh1 = __ballot_sync(0xFFFFFFFFu, copy && half == 1);
+            if (lane == 0) {
+                M.copy_n[buf][pw][0] = __popc(mh0);
+                M.copy_n[buf][pw][1] = __popc(mh1);
+                M.claim[buf][pw] = m_claim;
+            }
+            if (copy) {
+                const uint32_t mh = half ? mh1 : mh0;
+                M.copy_list[buf][pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
+                const int64_t row = a.t.seq * p.rows + j;
+                prefetch_l2_line(p.kv8 + row * (kD / 2));
+                prefetch_l2_line(p.kv8 + row * (kD / 2) + 128);
+                prefetch_l2_line(p.kv_scale + row * (kD / 32));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&M.staged[buf]));
+            return true;
+        };
+        Pair a(p, tb, te), ahead = a;
+        Held held[2];
+        int jn = -1;
+        if (a.tau < te) {
+            if (who == 0) {
+                ok = resolve(a, raw_entry(a), 0);
+                ahead.step(p, te);
+                jn = raw_entry(ahead);
+                ahead = a;
+            } else {
+                ok = warp_wait(smem_addr(&M.staged[0]), 0, abort);
+            }
+#pragma unroll
+            for (int hx = 0; hx < 2; ++hx)
+                if (ok && hx < a.tiles()) load_fp4(p, M, held[hx], a.t.seq, 0, pw, hx, who, lane);
+        }
+        for (; a.tau < te && ok; a = ahead, ++k) {
+            const int buf = k & 1, nbuf = buf ^ 1, nt = a.tiles();
+            ahead.step(p, te);
+            const bool more = ahead.tau < te;
+            if (more) {  // the next pair's lists
+                if (who == 0) {
+                    // (their place was last read two pairs back)
+                    if (!(ok = warp_wait(smem_addr(&M.list_empty[nbuf]), (((k + 1) >> 1) & 1) ^ 1, abort))) break;
+                    const int j = jn;
+                    Pair after = ahead;
+                    after.step(p, te);
+                    jn = raw_entry(after);
+                    ok = resolve(ahead, j, nbuf);
+                } else {
+                    ok = warp_wait(smem_addr(&M.staged[nbuf]), ((k + 1) >> 1) & 1, abort);
+                }
+                if (!ok) break;
+            }
+#pragma unroll
+            for (int hx = 0; hx < 2; ++hx) {
+                if (hx < nt) {
+                    const uint32_t Tx = a.T + hx, b = Tx & 1;
+                    if (!(ok = warp_wait(smem_addr(&M.kv_empty[b]), ((Tx >> 1) & 1) ^ 1, abort))) break;
+                    if (who == 0) {
+                        const uint32_t m = M.claim[buf][pw];
+                        M.vmask16[b][pw] = (uint16_t)(hx ? m >> 16 : m);
+                    }
+                    // this warp's scales of the tile: one later group of copies may still be under way, the
+                    // second tile's here, or the next pair's first
+                    if (hx == 0 ? nt == 2 : more)
+                        cp_async_wait<1>();
+                    else
+                        cp_async_wait<0>();
+                    __syncwarp();
+                    widen_tile_fp4(p, M, s_kv, held[hx], a.t.seq, buf, pw, hx, who, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&M.kv_full[b]));
+                }
+                if (more && hx < ahead.tiles()) load_fp4(p, M, held[hx], ahead.t.seq, nbuf, pw, hx, who, lane);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&M.list_empty[buf]));
+        }
+        cp_async_wait<0>();
     } else if (warp < kWarpSoftmax) {
         // ------------------------------------------------------------------ kv gather
         // Each thread resolves one of the 128 columns of a pair of tiles; every warp lists the
@@ -570,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int half = slot >> 6;
                 const uint32_t mh0 = __ballot_sync(0xFFFFFFFFu, copy && half == 0);
                 const uint32_t mh1 = __ballot_sync(0xFFFFFFFFu, copy && half == 1);
-                if constexpr (kCodes) {
+                if constexpr (kStaged) {
                     // the epilogue warps read the previous pair's lists until they have widened
                     // its tiles (their arrival completes a tile's kv_full)
                     if (T > 0 && !(ok = mbar_wait(smem_addr(&M.kv_full[(T - 1) & 1]), ((T - 1) >> 1) & 1, abort)))
@@ -578,29 +818,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (T > 1 && !(ok = mbar_wait(smem_addr(&M.kv_full[(T - 2) & 1]), ((T - 2) >> 1) & 1, abort)))
                         break;
                     if (lane == 0) {
-                        M.copy_n[pw][0] = __popc(mh0);
-                        M.copy_n[pw][1] = __popc(mh1);
+                        M.copy_n[0][pw][0] = __popc(mh0);
+                        M.copy_n[0][pw][1] = __popc(mh1);
                     }
                 }
                 if (copy) {
                     const uint32_t mh = half ? mh1 : mh0;
-                    M.copy_list[pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
+                    M.copy_list[0][pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
                     // the buffers are usually still in use: pull the new rows into L2 now, so
                     // that the copies issued once a buffer is released hit L2
-                    if constexpr (kCodes) {
-                        prefetch_l2(p.kv8 + (bi * p.rows + j) * (int64_t)kRowBytes, kRowBytes);
+                    if constexpr (kStaged) {
+                        prefetch_l2(p.kv8 + (bi * p.rows + j) * (int64_t)kD, kD);
                         prefetch_l2(p.kv_scale + (bi * p.rows + j) * (int64_t)(kD / 32), kD / 32);
                     } else {
                         prefetch_l2(p.kv + (bi * p.rows + j) * (int64_t)kD, kD * 2);
                     }
                 }
                 __syncwarp();
-                if constexpr (kCodes) {
-                    // rows of codes: chunk c's 128 codes of each listed row are staged raw in block
+                if constexpr (kStaged) {
+                    // e4m3 rows: chunk c's 128 codes of each listed row are staged raw in block
                     // 2c + 1 of the row's slot (dead until the row is written), then widened in
-                    // place to bf16 in blocks 2c and 2c + 1.  Lane l moves 16-byte units l % 8,
-                    // l % 8 + 8, ... of rows l / 8 + 4 i.
-                    const uint8_t* kvb8 = p.kv8 + bi * p.rows * (int64_t)kRowBytes;
+                    // place to bf16 in blocks 2c and 2c + 1.  Lane l moves 16-code unit l % 8 of
+                    // rows l / 8 + 4 i.
+                    const uint8_t* kvb8 = p.kv8 + bi * p.rows * (int64_t)kD;
                     const uint8_t* scb = p.kv_scale + bi * p.rows * (int64_t)(kD / 32);
                     const int unit = lane & 7;
                     // stage each tile as soon as its buffer is released (one commit group per
@@ -612,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int e = (lane >> 3) + 4 * i;
-                            ent[i] = e < ncopy ? M.copy_list[pw][hx][e] : make_int2(-1, 0);
+                            ent[i] = e < ncopy ? M.copy_list[0][pw][hx][e] : make_int2(-1, 0);
                         }
                     };
 #pragma unroll
@@ -625,29 +865,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = mbar_wait(smem_addr(&M.kv_empty[b]), ((Tx >> 1) & 1) ^ 1, abort))) break;
                         M.vmask16[b][pw] = (uint16_t)(hx ? m_claim >> 16 : m_claim);
                         if (lane < ncopy) {  // the row's 16 scales
-                            const int2 en = M.copy_list[pw][hx][lane];
-                            cp_async16(smem_addr(&M.fp8_sc[en.y][0]), scb + (int64_t)en.x * (kD / 32), 16u);
+                            const int2 en = M.copy_list[0][pw][hx][lane];
+                            cp_async16(smem_addr(&M.row_sc[0][en.y][0]), scb + (int64_t)en.x * (kD / 32), 16u);
                         }
                         // per row one shared and one global base, chunk c at constant offsets
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             if (ent8[i].x < 0) break;
                             const uint32_t r = (uint32_t)ent8[i].y;
-                            const uint32_t row_at = s_kv + kDBlkBytes + (r >> 6) * kBlkBytes + (r & 63) * 128;
-                            const uint8_t* gb = kvb8 + (int64_t)ent8[i].x * kRowBytes + unit * 16;
-                            if constexpr (kFmt == SA_KV_FP4_E2M1) {
-                                // a chunk is four 16-byte units: units 0-3 chunk 0, 4-7 chunk 1, ...
-                                const uint32_t sb = row_at + (uint32_t)(unit >> 2) * (2 * kDBlkBytes) +
-                                                    (uint32_t)(unit & 3) * 16;
-                                cp_async16_at<0, 0>(sb, gb);
-                                cp_async16_at<4 * kDBlkBytes, 128>(sb, gb);
-                            } else {
-                                const uint32_t sb = row_at + unit * 16;
-                                cp_async16_at<0, 0>(sb, gb);
-                                cp_async16_at<2 * kDBlkBytes, 128>(sb, gb);
-                                cp_async16_at<4 * kDBlkBytes, 256>(sb, gb);
-                                cp_async16_at<6 * kDBlkBytes, 384>(sb, gb);
-                            }
+                            const uint32_t sb =
+                                s_kv + kDBlkBytes + (r >> 6) * kBlkBytes + (r & 63) * 128 + unit * 16;
+                            const uint8_t* gb = kvb8 + (int64_t)ent8[i].x * kD + unit * 16;
+                            cp_async16_at<0, 0>(sb, gb);
+                            cp_async16_at<2 * kDBlkBytes, 128>(sb, gb);
+                            cp_async16_at<4 * kDBlkBytes, 256>(sb, gb);
+                            cp_async16_at<6 * kDBlkBytes, 384>(sb, gb);
                         }
                         cp_async_commit();
                     }
@@ -662,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(smem_addr(&M.staged[b]));
                         int2 ent8[8];
                         load_ent(hx, ent8);
-                        widen_codes<kFmt>(s_kv, M, ent8, unit, 0, 2);
+                        widen_fp8(s_kv, M, ent8, unit, 0, 2);
                         fence_proxy_async_smem();
                         mbar_arrive(smem_addr(&M.kv_full[b]));
                     }
@@ -680,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = __popc(hx ? mh1 : mh0);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        ent_r[hx][e] = (hx < nt && n <= 2 && e < n) ? M.copy_list[pw][hx][e] : make_int2(-1, 0);
+                        ent_r[hx][e] = (hx < nt && n <= 2 && e < n) ? M.copy_list[0][pw][hx][e] : make_int2(-1, 0);
                         if (ent_r[hx][e].x >= 0) {
                             const uint4* src = reinterpret_cast<const uint4*>(kvb + (int64_t)ent_r[hx][e].x * kD);
                             v[hx][e][0] = __ldg(src + lane);
@@ -716,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const char* g_lane = reinterpret_cast<const char*>(kvb) + (lane & 15) * 16;
 #pragma unroll 1
                         for (int e = lane >> 4; e < ncopy; e += 2) {
-                            const int2 en = M.copy_list[pw][hx][e];
+                            const int2 en = M.copy_list[0][pw][hx][e];
                             const uint32_t ps = (uint32_t)en.y;
                             const uint32_t sb = (s_lane ^ ((ps & 7) << 4)) + (ps >> 6) * kBlkBytes +
                                                 (ps & 63) * 128;
@@ -876,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t k = 0;
         bool ok = true;
         Task t = task_of(p, tb);
-        // codes: the next tile whose chunks 2 and 3 this warpgroup widens (warp q4 takes the rows
+        // fp8: the next tile whose chunks 2 and 3 this warpgroup widens (warp q4 takes the rows
         // producer warp q4 listed)
         int64_t wtau = p.n_tiles > 0 ? tb : te;
         int wsplit = t.split, wt0 = t.t0, wt1 = t.t1, wti = t.t0;
@@ -894,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rope_last = reinterpret_cast<const float2*>(
                         p.rope)[(p.rope_pos0 + t.pos) * (p.rope_dim / 2) + ((dd - first) >> 1)];
             }
-            if constexpr (kCodes) {
+            if constexpr (kStaged) {
                 // widen every tile the producers have staged until this task's O is complete
                 // (its last tile needs this warpgroup's widening first); the poll is bounded
                 uint32_t idle = 0;
@@ -902,14 +1134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (wtau < te &&
                         __all_sync(0xffffffffu, mbar_test_wait(smem_addr(&M.staged[wT & 1]), (wT >> 1) & 1))) {
                         const int hx = (wti - wt0) & 1;
-                        const int ncopy = M.copy_n[q4][hx];
+                        const int ncopy = M.copy_n[0][q4][hx];
                         int2 ent8[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int e = (lane >> 3) + 4 * i;
-                            ent8[i] = e < ncopy ? M.copy_list[q4][hx][e] : make_int2(-1, 0);
+                            ent8[i] = e < ncopy ? M.copy_list[0][q4][hx][e] : make_int2(-1, 0);
                         }
-                        widen_codes<kFmt>(s_kv, M, ent8, lane & 7, 2, 4);
+                        widen_fp8(s_kv, M, ent8, lane & 7, 2, 4);
                         fence_proxy_async_smem();
                         mbar_arrive(smem_addr(&M.kv_full[wT & 1]));
                         ++wT;
@@ -1181,7 +1413,7 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     const int64_t grid = groups * g.hblocks;
     const bool rope = c.rope != nullptr;
     auto kernel = kKernels[2 * c.kv_format + (rope ? 1 : 0)];
-    e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, c.stream, qmap, p);
+    e = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(c.kv_format)), kSmemBytes, c.stream, qmap, p);
     if (e != cudaSuccess || g.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, n_tokens, c.h, kD, g.n_splits,
                                c.stream);

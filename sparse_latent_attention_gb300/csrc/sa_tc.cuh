@@ -159,6 +159,11 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// The same for the 128-byte line at an address, through the load/store units.
+__device__ __forceinline__ void prefetch_l2_line(const void* src) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
