@@ -178,13 +178,11 @@ struct Cursor {
     }
 };
 
-// The 32 codes of a scale's block and the scale, on their way from memory to a stage.
+// The 32 codes of a scale's block, on their way from memory to a stage.
 template <int kFmt>
 struct Codes {
     uint32_t w[kFmt == SA_KV_FP4_E2M1 ? 4 : 8];
-    uint32_t scale;  // the e8m0 byte; kNone: no row
 };
-constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 // A bf16 gather warp's copies of a stage: 16 bytes of each of a lane's kPer rows from kOff bytes into it.
 // Row i's place is 1024 bytes (eight rows) on from row i - 4's.
@@ -491,8 +489,12 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
         const int64_t count = range.end - range.begin;
         bool ok = true, any_bad = false;
         Cursor cur(p, range.begin, group);  // the stage to load next
-        const uint8_t *codes[kPer], *scales[kPer];
+        const uint8_t* codes[kPer];
+        // the scales of stage `part` of each row: a row's four lanes hold all of them (a byte load for every
+        // lane and stage filled the few lines that the L1 has beside the stages)
+        uint32_t scales[kPer];
         uint32_t there = 0;  // bit y: row r0 + 8 y has an entry
+        int at_c = 0;        // the stage whose codes x holds
         int jn[kPer];
         int64_t unit_at = -1;  // the unit that codes points into
 #pragma unroll
@@ -505,13 +507,23 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
                 const int64_t first = cur.u.seq * p.rows;
                 there = 0;
                 const uint8_t* cb = p.kv + first * row_bytes + part * kLaneBytes;
-                const uint8_t* sb = p.kv_scale + first * row_scales + part;
+                const uint8_t* sb = p.kv_scale + first * row_scales + 4 * part;
 #pragma unroll
                 for (int y = 0; y < kPer; ++y) {
                     const int j = valid(p, jn[y], any_bad);
                     there |= j >= 0 ? 1u << y : 0u;
                     codes[y] = cb + (uint64_t)(uint32_t)j * row_bytes;
-                    scales[y] = sb + (uint64_t)(uint32_t)j * row_scales;
+                    scales[y] = 0;
+                    const uint8_t* sc = sb + (uint64_t)(uint32_t)j * row_scales;
+                    if (j >= 0 && part < p.steps) {
+                        if (!p.half) {
+                            scales[y] = __ldg(reinterpret_cast<const uint32_t*>(sc));
+                        } else {  // rows of an odd number of halfwords
+                            scales[y] = __ldg(reinterpret_cast<const uint16_t*>(sc));
+                            if (part < p.steps - 1)
+                                scales[y] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(sc + 2)) << 16;
+                        }
+                    }
                 }
                 int64_t at;
                 const Unit nu = cur.next_unit(p, at);
@@ -520,10 +532,10 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
                     for (int y = 0; y < kPer; ++y) jn[y] = entry_of(p, nu, r0 + 8 * y);
                 }
             }
+            at_c = cur.c;
             const bool inside = !(cur.c == p.steps - 1 && p.half && part >= 2);
 #pragma unroll
             for (int y = 0; y < kPer; ++y) {
-                x[y].scale = kNone;
                 if ((there >> y & 1) && inside) {
                     const uint4* at = reinterpret_cast<const uint4*>(codes[y] + cur.c * (4 * kLaneBytes));
 #pragma unroll
@@ -534,7 +546,6 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
                         x[y].w[4 * i + 2] = v.z;
                         x[y].w[4 * i + 3] = v.w;
                     }
-                    x[y].scale = __ldg(scales[y] + 4 * cur.c);
                 }
             }
             cur.advance(p, 2);
@@ -547,10 +558,10 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
             if (!(ok = warp_wait(smem_addr(&M.kv_empty[st]), ph, abort))) break;
 #pragma unroll
             for (int y = 0; y < kPer; ++y) {
-                if (x[y].scale == kNone) continue;
+                const uint32_t se = __shfl_sync(0xFFFFFFFFu, scales[y], 8 * at_c + (lane & 7)) >> (8 * part) & 255u;
+                if (!(there >> y & 1) || (at_c == p.steps - 1 && p.half && part >= 2)) continue;
                 const uint32_t at = dst + st * kStageBytes + 1024 * y;
-                const float sc = kFmt == SA_KV_FP4_E2M1 ? fp4::scale_f32(x[y].scale)
-                                                        : fp8::e8m0_to_f32(x[y].scale);
+                const float sc = kFmt == SA_KV_FP4_E2M1 ? fp4::scale_f32(se) : fp8::e8m0_to_f32(se);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t(&w)[kLaneBytes / 4] = x[y].w;
