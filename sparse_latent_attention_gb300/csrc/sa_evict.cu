@@ -37,16 +37,41 @@ struct SelectSmem {
     uint32_t warp_sum[32];
     uint32_t bin, before, count;  // the bin that holds the wanted key, the keys above it and in it
     uint32_t warp_in[32], warp_eq[32];
+    uint32_t cta_in, cta_eq;
 };
 
-// Finds the bin of S.hist, from the top, in which the want-th key lies (1 <= want <= all keys counted).
+// The CTAs of a cluster share a sequence: a barrier of all of them, and a word of another one's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t load_remote(const uint32_t* here, uint32_t rank) {
+    uint32_t at, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(here)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// Finds the bin of the histogram (of all the cluster's CTAs), from the top, in which the want-th key lies
+// (1 <= want <= all keys counted).  Every thread of the cluster calls it once its CTA's counts are complete;
+// the counts may be cleared afterwards.
 template <int kThreads>
-__device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want) {
+__device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want, uint32_t ctas) {
     constexpr int kPer = kBins / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
     uint32_t c[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += c[i] = S.hist[kBins - 1 - (kPer * tid + i)];
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t* bin = &S.hist[kBins - 1 - (kPer * tid + i)];
+        c[i] = 0;
+        if (ctas == 1) c[i] = *bin;
+        else
+            for (uint32_t r = 0; r < ctas; ++r) c[i] += load_remote(bin, r);
+        sum += c[i];
+    }
+    if (ctas > 1) cluster_sync();  // every CTA has read the counts
     uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -71,7 +96,7 @@ __device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want) {
     __syncthreads();
 }
 
-// One CTA per sequence.  Rows [0, lo) and [hi, live) are protected; of the candidates [lo, hi) the `want`
+// A cluster of `ctas` CTAs per sequence, an even share of the rows each.  Rows [0, lo) and [hi, live) are protected; of the candidates [lo, hi) the `want`
 // largest stay.  A radix select over the 32-bit keys (11 bits a pass from the top; it ends as soon as a
 // whole bin stays) finds the want-th largest.  Where several candidates share its key and not all of them
 // stay, they are told apart by their accumulators, the same way, and equal accumulators by their row.  Then
@@ -79,24 +104,28 @@ __device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want) {
 // numbers them in row order.  kCached: the candidates' keys are kept in shared memory; else they are made
 // again from the accumulators (in L2) in every pass.
 template <int kThreads, bool kCached>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
     evict_select_kernel(const int64_t* __restrict__ acc, const int32_t* __restrict__ live, int rows,
                         int n_keep, int keep_first, int keep_last, int32_t* __restrict__ kept,
-                        int32_t* __restrict__ remap) {
+                        int32_t* __restrict__ remap, int share, uint32_t ctas) {
     extern __shared__ uint32_t keys[];
     __shared__ SelectSmem S;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
-    const int64_t bi = blockIdx.x;
+    const int64_t bi = blockIdx.x / ctas;
+    const uint32_t rank = blockIdx.x % ctas;
     const int64_t* a = acc + bi * rows;
     int L = rows;
     if (live) L = min(max(live[bi], 0), rows);
     const int lo = min(keep_first, L), hi = max(lo, L - keep_last), n = hi - lo;
     const int n_stay = min(n_keep, L);
     const uint32_t want = (uint32_t)(n_stay - (L - n));  // of the n candidates
-    auto key = [&](int i) { return kCached ? keys[i] : key_of(a[lo + i]); };
+    // this CTA's rows and candidates
+    const int r0 = (int)min((int64_t)rank * share, (int64_t)rows), r1 = min(r0 + share, rows);
+    const int c0 = min(max(lo, r0), r1), c1 = max(c0, min(hi, r1));
+    auto key = [&](int i) { return kCached ? keys[i - c0] : key_of(a[i]); };
 
     // a candidate stays when its key is at least `from`, or when its key is `tie` and its accumulator above
     // `full`, or equal to it and fewer than `need` such come before it
@@ -112,18 +141,17 @@ __global__ void __launch_bounds__(kThreads)
             for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
             __syncthreads();
 #pragma unroll 4
-            for (int i = tid; i < n; i += kThreads) {
+            for (int i = c0 + tid; i < c1; i += kThreads) {
                 uint32_t k;
                 if (pass == 0) {
-                    k = key_of(a[lo + i]);
-                    if (kCached) keys[i] = k;
+                    k = key_of(a[i]);
+                    if (kCached) keys[i - c0] = k;
                 } else {
                     k = key(i);
                 }
                 if ((k & mask) == prefix) atomicAdd(&S.hist[k >> shift & digit], 1u);
             }
-            __syncthreads();
-            find_bin<kThreads>(S, krem);
+            find_bin<kThreads>(S, krem, ctas);
             prefix |= S.bin << shift;
             mask |= digit << shift;
             krem -= S.before;
@@ -149,13 +177,12 @@ __global__ void __launch_bounds__(kThreads)
                     const uint32_t digit = shift < 0 ? 0x1FFu : 0x7FFu;  // 64 = 5 * 11 + 9
                     for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
                     __syncthreads();
-                    for (int i = tid; i < n; i += kThreads) {
+                    for (int i = c0 + tid; i < c1; i += kThreads) {
                         if (key(i) != tie) continue;
-                        const uint64_t f = full_key_of(a[lo + i]);
+                        const uint64_t f = full_key_of(a[i]);
                         if ((f & m) == full) atomicAdd(&S.hist[(uint32_t)(f >> sh) & digit], 1u);
                     }
-                    __syncthreads();
-                    find_bin<kThreads>(S, krem);
+                    find_bin<kThreads>(S, krem, ctas);
                     full |= (uint64_t)S.bin << sh;
                     m |= (uint64_t)digit << sh;
                     krem -= S.before;
@@ -166,24 +193,40 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
     }
 
-    // state of row i: stays (1), one of the candidates equal to the last (2), goes (0)
-    auto state = [&](int i) {
-        if (i >= L) return 0;
-        if (i < lo || i >= hi || (from == 0u && tie == 0xFFFFFFFFu)) return 1;
-        if (want == 0) return 0;
-        const uint32_t k = key(i - lo);
-        if (k >= from) return 1;
-        if (k != tie) return 0;
-        const uint64_t f = full_key_of(a[i]);
-        return f > full ? 1 : f == full ? 2 : 0;
+    // Which of the 32 rows from i on stay (bits of `in`), and which equal the last that does (bits of `eq`).
+    const int end = min(r1, L);
+    auto ballots = [&](int i, int i1, uint32_t& in, uint32_t& eq) {
+        i += lane;
+        uint32_t k = 0xFFFFFFFFu;  // a protected row
+        if (i >= c0 && i < c1) k = want == 0 ? 0u : from == 0 ? k : key(i);  // (else no keys were made)
+        const bool there = i < i1;
+        in = __ballot_sync(0xFFFFFFFFu, there && k >= from);
+        eq = 0;
+        if (need) {
+            bool above = false, same = false;
+            if (there && k == tie) {
+                const uint64_t f = full_key_of(a[i]);
+                above = f > full;
+                same = f == full;
+            }
+            in |= __ballot_sync(0xFFFFFFFFu, above);
+            eq = __ballot_sync(0xFFFFFFFFu, same);
+        }
     };
-    const int share = ((rows + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int i0 = warp * share, i1 = min(i0 + share, rows);
-    uint32_t n_in = 0, n_eq = 0;
-    for (int i = i0; i < i1; i += 32) {
-        const int s = i + lane < i1 ? state(i + lane) : 0;
-        n_in += __popc(__ballot_sync(0xFFFFFFFFu, s == 1));
-        n_eq += __popc(__ballot_sync(0xFFFFFFFFu, s == 2));
+    // a warp's share; of up to 32 groups of 32 rows lane l keeps group l's ballots for the numbering
+    const int warp_share = ((share + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int i0 = min(r0 + warp * warp_share, r1), i1 = min(i0 + warp_share, r1), live1 = min(i1, end);
+    uint32_t n_in = 0, n_eq = 0, my_in = 0, my_eq = 0;
+#pragma unroll 2
+    for (int i = i0, g = 0; i < live1; i += 32, ++g) {
+        uint32_t in, eq;
+        ballots(i, live1, in, eq);
+        n_in += __popc(in);
+        n_eq += __popc(eq);
+        if (lane == g) {
+            my_in = in;
+            my_eq = eq;
+        }
     }
     if (lane == 0) {
         S.warp_in[warp] = n_in;
@@ -191,6 +234,22 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
     uint32_t in_before = 0, eq_before = 0;
+    if (ctas > 1) {
+        if (tid == 0) {
+            S.cta_in = S.cta_eq = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                S.cta_in += S.warp_in[w];
+                S.cta_eq += S.warp_eq[w];
+            }
+        }
+        cluster_sync();
+        for (uint32_t r = 0; r < rank; ++r) {
+            in_before += load_remote(&S.cta_in, r);
+            eq_before += load_remote(&S.cta_eq, r);
+        }
+        cluster_sync();  // no CTA leaves before its words are read
+    }
+    // (the earlier CTAs' equal ones that stay are among the earlier rows that stay)
     for (int w = 0; w < warp; ++w) {
         in_before += S.warp_in[w];
         eq_before += S.warp_eq[w];
@@ -198,36 +257,56 @@ __global__ void __launch_bounds__(kThreads)
     int32_t* kb = kept + bi * (int64_t)n_keep;
     int32_t* rb = remap + bi * (int64_t)rows;
     const uint32_t lt = (1u << lane) - 1u;
-    for (int i = i0; i < i1; i += 32) {
-        const int s = i + lane < i1 ? state(i + lane) : 0;
-        const uint32_t b_in = __ballot_sync(0xFFFFFFFFu, s == 1), b_eq = __ballot_sync(0xFFFFFFFFu, s == 2);
-        const uint32_t eq = eq_before + __popc(b_eq & lt);
-        const uint32_t slot = in_before + __popc(b_in & lt) + min(eq, need);
-        const bool stays = s == 1 || (s == 2 && eq < need);
+#pragma unroll 2
+    for (int i = i0, g = 0; i < i1; i += 32, ++g) {
+        uint32_t in = 0, eq = 0;
+        if (g < 32) {
+            in = __shfl_sync(0xFFFFFFFFu, my_in, g);
+            eq = __shfl_sync(0xFFFFFFFFu, my_eq, g);
+        } else if (i < live1) {
+            ballots(i, live1, in, eq);
+        }
+        const uint32_t eq_rank = eq_before + __popc(eq & lt);
+        const uint32_t slot = in_before + __popc(in & lt) + min(eq_rank, need);
+        const bool stays = (in >> lane & 1u) || ((eq >> lane & 1u) && eq_rank < need);
         if (i + lane < i1) {
             rb[i + lane] = stays ? (int32_t)slot : -1;
             // (a slot is below n_keep; the check keeps every store inside the row regardless)
             if (stays && slot < (uint32_t)n_keep) kb[slot] = i + lane;
         }
-        in_before += __popc(b_in);
-        eq_before += __popc(b_eq);
+        in_before += __popc(in);
+        eq_before += __popc(eq);
     }
-    for (int j = n_stay + tid; j < n_keep; j += kThreads) kb[j] = -1;
+    if (rank == 0)
+        for (int j = n_stay + tid; j < n_keep; j += kThreads) kb[j] = -1;
 }
 
 template <int kThreads, bool kCached>
 cudaError_t select_launch(const int64_t* acc, const int32_t* live, int64_t b, int rows, int n_keep,
-                          int keep_first, int keep_last, int32_t* kept, int32_t* remap,
+                          int keep_first, int keep_last, int32_t* kept, int32_t* remap, int share, int ctas,
                           cudaStream_t stream) {
     auto kernel = evict_select_kernel<kThreads, kCached>;
-    const size_t smem = kCached ? (size_t)rows * sizeof(uint32_t) : 0;
+    const size_t smem = kCached ? (size_t)share * sizeof(uint32_t) : 0;
     if (smem > 32 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kernel, dim3((unsigned)b), dim3(kThreads), smem, stream, acc, live, rows, n_keep,
-                      keep_first, keep_last, kept, remap);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(b * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, acc, live, rows, n_keep, keep_first, keep_last, kept, remap, share,
+                              (uint32_t)ctas);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -437,10 +516,17 @@ extern "C" sa_status sa_evict_select(const int64_t* acc, const int32_t* live, in
     if (overlap(kept, kb, acc, ab) || overlap(remap, rb, acc, ab) || overlap(kept, kb, remap, rb) ||
         overlap(kept, kb, live, lb) || overlap(remap, rb, live, lb))
         return SA_ERR_INVALID_ARG;
-    auto run = rows <= 2048 ? select_launch<256, true>
-               : rows <= kCachedRows ? select_launch<1024, true> : select_launch<1024, false>;
-    return from_cuda(run(acc, live, b, (int)rows, (int)n_keep, (int)keep_first, (int)keep_last, kept, remap,
-                         reinterpret_cast<cudaStream_t>(stream)));
+    // as many CTAs a sequence (up to 8, a portable cluster) as there are SMs for, with at least 8192 rows each:
+    // below that the cluster's barriers cost what the shares save (8320 rows of one sequence: 9.5 us with one
+    // CTA, 10 with four; 64 x 32896 rows: 31 us with one, 25 with two)
+    int ctas = 1;
+    while (ctas < 8 && 2 * ctas * b <= device_sm_count() && rows >= 2 * ctas * 8192) ctas *= 2;
+    const int share = (int)((rows + ctas - 1) / ctas);
+    auto run = share <= 2048          ? select_launch<256, true>
+               : share <= kCachedRows ? select_launch<1024, true>
+                                      : select_launch<1024, false>;
+    return from_cuda(run(acc, live, b, (int)rows, (int)n_keep, (int)keep_first, (int)keep_last, kept, remap, share,
+                         ctas, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" sa_status sa_compact_rows(int n_tensors, const void* const* src, void* const* dst,
