@@ -515,15 +515,18 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
     rows = None
     src, dst, row_bytes, src_b, dst_b = [], [], [], [], []
 
-    def of(t, what, shape, stride):
+    def of(t, what, shape, stride, size):
         """The bytes of a row of t, whose rows are contiguous."""
-        size = t.element_size()
+        if not shape[1] or not b:
+            return size
+        if t.is_contiguous():
+            return size * (t.numel() // (b * shape[1]))
         elements = 1
         for extent, step in zip(reversed(shape[1:]), reversed(stride[1:])):
             if extent > 1 and step != elements:
                 raise ValueError(f"{what} must have contiguous rows")
             elements *= extent
-        return size * (elements // shape[1] if shape[1] else 1)
+        return size * (elements // shape[1])
 
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor) or t.get_device() != dev:
@@ -533,7 +536,8 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
             rows = shape[1]
         if len(shape) < 2 or shape[0] != b or shape[1] != rows:
             raise ValueError(f"tensors[{i}] must be [{b}, {rows}, ...]")
-        row_bytes.append(of(t, f"tensors[{i}]", shape, stride))
+        size = t.element_size()
+        row_bytes.append(of(t, "a tensor", shape, stride, size))
         o = outs[i]
         if o is None:
             o = outs[i] = torch.empty((b, n_keep, *shape[2:]), dtype=t.dtype, device=t.device)
@@ -542,11 +546,11 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
             raise ValueError(f"out[{i}] must be a {t.dtype} tensor [{b}, {n_keep} or more, ...] like "
                              f"tensors[{i}]")
         else:
-            of(o, f"out[{i}]", o.shape, o.stride())
+            of(o, "an out", o.shape, o.stride(), size)
         src.append(t.data_ptr())
         dst.append(o.data_ptr())
-        src_b.append(stride[0] * t.element_size())
-        dst_b.append(o.stride(0) * t.element_size())
+        src_b.append(stride[0] * size)
+        dst_b.append(o.stride(0) * size)
     # one array of 64-bit words holds the five lists
     words = (ctypes.c_int64 * (5 * n))(*src, *dst, *row_bytes, *src_b, *dst_b)
     at = ctypes.addressof(words)

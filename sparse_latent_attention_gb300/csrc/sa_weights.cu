@@ -12,7 +12,8 @@
 //
 // The product's d is cut into two ranges with an accumulator each, added up in the epilogue in f32: the
 // tensor core cuts its running sum after every 16 products, and over all of d = 512 in one accumulator
-// that came to a relative error of 1.9e-6 in the weights.
+// that came to a relative error of 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  Products with
+// e2m1's two significant bits leave it little to cut: 8e-8 with one accumulator, which those rows use.
 //
 // Roles (persistent CTAs, 18 or 26 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
 // tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
@@ -199,6 +200,7 @@ template <int kFmt, int kN>
 __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
     row_weights_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
     using Sh = Shape<kN>;
+    constexpr bool kTwo = kFmt != SA_KV_FP4_E2M1;  // two accumulators (see above)
     constexpr int kStages = Sh::kStages, kGroupWarps = Gather<kFmt>::kWarps, kWarpRows = Gather<kFmt>::kRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
                      warp_wait(smem_addr(&M.kv_full[st]), ph, abort);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t col = tmem + 256 * b + kN * (c >> 1);  // stages 0, 1 and 2, 3
+                const uint32_t col = tmem + 256 * b + (kTwo ? kN * (c >> 1) : 0);  // stages 0, 1 and 2, 3
                 uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
                 uint32_t blo = (uint32_t)b0 + 2 * c * (Sh::kQBlockBytes >> 4);
                 const int blocks = c == p.steps - 1 && p.half ? 1 : 2;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mma_lohi_elect(col, alo + 2 * q, ahi, blo + 2 * q, bhi, id,
-                                       (uint32_t)(c & 1) | (uint32_t)k64 | (uint32_t)q);
+                                       (uint32_t)(kTwo ? c & 1 : c) | (uint32_t)k64 | (uint32_t)q);
                     alo += kBlockBytes >> 4;
                     blo += Sh::kQBlockBytes >> 4;
                 }
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
         const int q4 = warp & 3;  // the TMEM lanes this warp may read: 32 q4 .. 32 q4 + 31
         const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
         const int et = 32 * q4 + lane;  // 0 .. 127: its entry of the tile, and the head whose lse it brings
-        const bool two = p.steps > 2;   // both accumulators are used
+        const bool two = kTwo && p.steps > 2;  // both accumulators are used
         const uint32_t s_at = tmem + lane_base + 256 * group;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
         float* table = M.nlse[group];
