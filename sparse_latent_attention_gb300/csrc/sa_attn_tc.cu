@@ -374,12 +374,12 @@ __device__ __forceinline__ void load_fp4(const Params& p, Misc& M, Held& x, int6
                                          int who, int lane) {
     const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4);
     const uint8_t* kvb = p.kv8 + seq * p.rows * (int64_t)(kD / 2) + 16 * (lane & 15);
+    uint32_t j[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) j[i] = (uint32_t)M.copy_list[buf][pw][hx][e0 + 4 * i].x;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if (e0 + 4 * i < n) {
-            const uint32_t j = (uint32_t)M.copy_list[buf][pw][hx][e0 + 4 * i].x;
-            x.code[i] = __ldg(reinterpret_cast<const uint4*>(kvb + (uint64_t)j * (kD / 2)));
-        }
+        if (e0 + 4 * i < n) x.code[i] = __ldg(reinterpret_cast<const uint4*>(kvb + (uint64_t)j[i] * (kD / 2)));
     // a lane a row: the warp's entries are 4 i + 2 who and 4 i + 2 who + 1
     const int e = 4 * (lane >> 1) + 2 * who + (lane & 1);
     if (e < n) {
@@ -393,12 +393,16 @@ __device__ __forceinline__ void load_fp4(const Params& p, Misc& M, Held& x, int6
 __device__ __forceinline__ void widen_tile_fp4(const Params& p, const Misc& M, uint32_t s_kv, const Held& x,
                                                int64_t seq, int buf, int pw, int hx, int who, int lane) {
     const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4), u = lane & 15;
+    // (slots and scales of all of them at once; past the list's end: whatever is there, in bounds)
+    int ps[kHeld];
+    uint32_t sc[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) ps[i] = M.copy_list[buf][pw][hx][e0 + 4 * i].y & 127;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) sc[i] = M.row_sc[buf][ps[i]][u];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if (e0 + 4 * i < n) {
-            const int ps = M.copy_list[buf][pw][hx][e0 + 4 * i].y;
-            widen_fp4(s_kv, x.code[i], M.row_sc[buf][ps][u], ps, u);
-        }
+        if (e0 + 4 * i < n) widen_fp4(s_kv, x.code[i], sc[i], ps[i], u);
 #pragma unroll 1
     for (int e = e0 + 4 * kHeld; e < n; e += 4) {
         const int2 en = M.copy_list[buf][pw][hx][e];
