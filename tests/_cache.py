@@ -108,9 +108,12 @@ def select(acc: np.ndarray, n_keep, first, last, live=None):
     remap = np.full((b, rows), -1, np.int32)
     for bi in range(b):
         n = rows if live is None else int(min(max(live[bi], 0), rows))
-        forced = [j for j in range(n) if j < first or j >= n - last]
-        rest = sorted((j for j in range(n) if first <= j < n - last), key=lambda j: (-int(acc[bi, j]), j))
-        stay = sorted(forced + rest[:min(n_keep, n) - len(forced)])
+        lo = min(first, n)
+        hi = max(lo, n - last)
+        forced = np.r_[0:lo, hi:n]
+        # ~acc falls where acc rises (and has no overflow); a stable sort leaves the lower of equal rows first
+        rest = lo + np.argsort(~acc[bi, lo:hi], kind="stable")
+        stay = np.sort(np.r_[forced, rest[:min(n_keep, n) - len(forced)]])
         kept[bi, :len(stay)] = stay
         remap[bi, stay] = np.arange(len(stay))
     return kept, remap

@@ -3,12 +3,14 @@ against plain 64-bit implementations."""
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import sparse_latent_attention_gb300 as sa
-from sparse_latent_attention_gb300 import build, workloads
+from sparse_latent_attention_gb300 import _lib, build, workloads
 from tests import _cache, _gpu
 
 pytestmark = pytest.mark.gpu
@@ -170,6 +172,8 @@ CASES = [
     (1, 13, 64, 256, 640, 513, {}),
     (3, 1, 16, 128, 900, 700, {}),
     (1, 3, 64, 448, 90, 65, {}),
+    (2, 5, 70, 320, 200, 140, {}),
+    (1, 4, 128, 384, 300, 257, {}),
 ]
 
 
@@ -280,3 +284,115 @@ def test_fp4_bad_index_sets_status(dev):
     good = torch.where((bad >= 300) | (bad < -1), -1, bad)
     o2 = sa.sparse_attn(q, kv, sink, good, 0.05, kv_scale=sc, workspace=ws)
     assert sa.read_status(ws) == 0 and torch.equal(o, o2)
+
+
+# --------------------------------------------------------------------------------------------
+# calls at the edges
+# --------------------------------------------------------------------------------------------
+
+def test_quant_rows_gigabytes_apart(dev):
+    """Row offsets past 32 bits: a stride of 1 GB (32-bit products), and one past 2^31 elements."""
+    rng = np.random.default_rng(3)
+    for n, stride in ((6, (1 << 29) + 8), (3, (1 << 31) + 8)):
+        bits = _rows(rng, n, 64, special=False)
+        want_c, want_s, want_v = _cache.quantise(bits)
+        buf = torch.empty((n - 1) * stride + 64, dtype=torch.bfloat16, device=dev)
+        x = buf.as_strided((n, 64), (stride, 1))
+        x.copy_(_gpu.u16_to_bf16_tensor(bits, dev))
+        codes = torch.empty(n, 32, dtype=torch.uint8, device=dev)
+        scales = torch.empty(n, 2, dtype=torch.uint8, device=dev)
+        sa.act_quant_fp4(x, codes=codes, scales=scales, out_rt=x)
+        assert (codes.cpu().numpy() == want_c).all() and (scales.cpu().numpy() == want_s).all()
+        assert np.array_equal(x.double().cpu().numpy(), want_v)
+        del buf, x
+
+
+def far_inputs(dev, fmt, b, rows, h, d, topk, seed):
+    """inputs() over a long cache: only the rows that idx names are filled (the others hold whatever the
+    memory holds), among them the first and the last."""
+    q, kv, sc, sink, _ = inputs(dev, fmt, b, 1, h, d, topk, topk, seed, neg=0.0)
+    g = torch.Generator(device=dev).manual_seed(seed)
+    at = torch.stack([torch.randperm(rows - 2, device=dev, generator=g)[:topk] + 1 for _ in range(b)])
+    at[:, 0], at[:, -1] = 0, rows - 1
+    bi = torch.arange(b, device=dev)[:, None]
+    far = torch.empty((b, rows, kv.shape[2]), dtype=kv.dtype, device=dev)
+    far[bi, at] = kv
+    far_sc = None
+    if sc is not None:
+        far_sc = torch.empty((b, rows, sc.shape[2]), dtype=sc.dtype, device=dev)
+        far_sc[bi, at] = sc
+    near = torch.arange(topk, device=dev, dtype=torch.int32).expand(b, 1, topk).contiguous()
+    return q, (kv, sc, near), (far, far_sc, at.to(torch.int32)[:, None].contiguous()), sink
+
+
+@pytest.mark.parametrize("d", [512, 256])
+def test_fp4_cache_past_32_bits(dev, d):
+    rows = (1 << 32) // (d // 2) // 2 + 4000   # two sequences: codes past 4 GB
+    q, (kv, sc, near), (far, far_sc, idx), sink = far_inputs(dev, "fp4", 2, rows, 64, d, 200, 12)
+    lse = torch.empty(2, 1, 64, device=dev)
+    o = sa.sparse_attn(q, far, sink, idx, d ** -0.5, kv_scale=far_sc, lse=lse)
+    want, want_lse, tol, lse_tol = _cache.attention(q, _cache.rows_f64(kv, sc, d), sink, near, d ** -0.5)
+    check(o, want, tol, "o")
+    check(lse, want_lse, lse_tol, "lse")
+
+
+def test_fp4_nothing_listed_and_no_rows(dev):
+    for d in (512, 64):
+        q, kv, sc, sink, idx = inputs(dev, "fp4", 2, 3, 16, d, 40, 70, 9, neg=1.1, distinct=False)
+        lse = torch.empty(2, 3, 16, device=dev)
+        assert (idx == -1).all()
+        o = sa.sparse_attn(q, kv, sink, idx, 0.1, kv_scale=sc, lse=lse)
+        assert (o == 0).all() and (lse == sink).all()
+        o = sa.sparse_attn(q, kv[:, :0].contiguous(), sink, idx, 0.1, kv_scale=sc[:, :0].contiguous(), lse=lse)
+        assert (o == 0).all() and (lse == sink).all()
+
+
+def test_fp4_through_the_static_scratch(dev):
+    q, kv, sc, sink, idx = inputs(dev, "fp4", 3, 1, 64, 512, 900, 640, 14)
+    want = sa.sparse_attn(q, kv, sink, idx, 0.05, kv_scale=sc)
+    o = torch.empty_like(q)
+    P = ctypes.c_void_p
+    st = _lib.load().sa_sparse_attn_static_scratch(
+        P(q.data_ptr()), P(kv.data_ptr()), P(sc.data_ptr()), 2, P(sink.data_ptr()), P(idx.data_ptr()),
+        ctypes.c_float(0.05), ctypes.c_int64(3), ctypes.c_int64(1), 64, 512, ctypes.c_int64(900), 640,
+        P(o.data_ptr()), None, P(torch.cuda.current_stream().cuda_stream))
+    assert st == 0 and torch.equal(o, want)
+
+
+def test_two_graphs_share_a_workspace(dev):
+    """Two captured decode steps that use one workspace, replayed in turn on one stream."""
+    scale = 512 ** -0.5
+    sets = [inputs(dev, "fp4", 2, 1, 64, 512, 700, 640, seed) for seed in (1, 2)]
+    ws = sa.new_workspace(2, 1, 64, 512, 700, 640, sa.SA_KV_FP4_E2M1)
+    want = [sa.sparse_attn(q, kv, sink, idx, scale, kv_scale=sc).clone() for q, kv, sc, sink, idx in sets]
+    outs = [torch.empty_like(s[0]) for s in sets]
+    graphs = []
+    for (q, kv, sc, sink, idx), o in zip(sets, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sa.sparse_attn(q, kv, sink, idx, scale, kv_scale=sc, out=o, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_two_streams_at_once(dev):
+    """Calls with workspaces of their own on two streams at the same time."""
+    scale = 512 ** -0.5
+    sets = [inputs(dev, fmt, 4, 1, 64, 512, 2000, 1152, 5) for fmt in ("fp4", "fp8")]
+    want = [sa.sparse_attn(q, kv, sink, idx, scale, kv_scale=sc) for q, kv, sc, sink, idx in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for i, ((q, kv, sc, sink, idx), st) in enumerate(zip(sets, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(sa.sparse_attn(q, kv, sink, idx, scale, kv_scale=sc))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)

@@ -9,7 +9,7 @@ import torch
 
 import sparse_latent_attention_gb300 as sa
 from tests import _cache
-from tests.test_gpu_cache import CASES, check, dev, inputs  # noqa: F401 (dev is a fixture)
+from tests.test_gpu_cache import CASES, check, dev, far_inputs, inputs  # noqa: F401 (dev is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,6 +90,40 @@ def test_row_weights_bad_index(dev):  # noqa: F811
     assert sa.read_status(ws) == 0 and torch.equal(acc, acc2)
 
 
+@pytest.mark.parametrize("fmt,d,rows", [("bf16", 512, (1 << 32) // 1024 + 3000), ("fp4", 512, (1 << 32) // 256 + 4000),
+                                        ("fp8", 64, (1 << 32) // 64 // 2 + 1000)])
+def test_row_weights_cache_past_32_bits(dev, fmt, d, rows):  # noqa: F811
+    b = 2 if d == 64 else 1
+    q, (kv, sc, near), (far, far_sc, idx), sink = far_inputs(dev, fmt, b, rows, 64, d, 300, 15)
+    lse = torch.empty(b, 1, 64, device=dev)
+    sa.sparse_attn(q, kv, sink, near, d ** -0.5, kv_scale=sc, lse=lse)
+    acc = torch.zeros(b, rows, dtype=torch.int64, device=dev)
+    sa.row_weights(q, far, lse, idx, d ** -0.5, acc, kv_scale=far_sc)
+    want = torch.zeros(b, 300, dtype=torch.int64, device=dev)
+    sa.row_weights(q, kv, lse, near, d ** -0.5, want, kv_scale=sc)
+    assert torch.equal(acc.gather(1, idx[:, 0].long()), want)
+    assert int((acc != 0).sum()) == int((want != 0).sum())
+    _close(want, q, kv, sc, lse, near, d ** -0.5)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_row_weights_nothing_listed_and_no_rows(dev, fmt):  # noqa: F811
+    q, kv, sc, sink, idx = inputs(dev, fmt, 2, 3, 16, 512, 40, 70, 9, neg=1.1, distinct=False)
+    lse = torch.zeros(2, 3, 16, device=dev)
+    acc = torch.full((2, 40), 5, dtype=torch.int64, device=dev)
+    sa.row_weights(q, kv, lse, idx, 0.1, acc, kv_scale=sc)
+    assert (acc == 5).all()
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    none = acc[:, :0].contiguous()
+    no_kv = kv[:, :0].contiguous()
+    no_sc = None if sc is None else sc[:, :0].contiguous()
+    sa.row_weights(q, no_kv, lse, idx, 0.1, none, kv_scale=no_sc, workspace=ws)
+    assert sa.read_status(ws) == 0
+    idx[1, 2, 69] = 0  # out of range: there is no row 0
+    sa.row_weights(q, no_kv, lse, idx, 0.1, none, kv_scale=no_sc, workspace=ws)
+    assert sa.read_status(ws) == 4
+
+
 # --------------------------------------------------------------------------------------------
 # eviction
 # --------------------------------------------------------------------------------------------
@@ -107,6 +141,11 @@ SELECT = [
     (4, 300, 200, 128, 64, "random", [100, 130, 190, 250]),  # fewer rows than are protected
     (2, 40000, 16384, 128, 256, "random", None), (1, 100003, 777, 1, 0, "random", None),
     (1, 300000, 150000, 128, 1000, "heavy", None), (200, 64, 16, 4, 4, "ties", None),
+    (2, 1000003, 400000, 128, 1000, "heavy", None),        # more rows than the cluster's shared memory holds
+    (2, 1000003, 400000, 128, 1000, "ties", [999999, 5000]),
+    (3, 16384, 5000, 0, 0, "near", None), (3, 70000, 30000, 3, 3, "near", None),  # equal as f32, not as integers
+    (90, 20000, 7000, 128, 0, "zero", None), (1, 20000, 0, 0, 0, "random", None), (1, 20000, 20000, 0, 0, "random", None),
+    (2, 50000, 300, 200, 100, "random", None),             # a cluster with nothing to choose
 ]
 
 
@@ -121,6 +160,8 @@ def _acc(rng, b, rows, kind):
         a = rng.integers(-2**63, 2**63 - 1, (b, rows))
         a[:, ::7], a[:, 1::7], a[:, 2::7] = 2**63 - 1, -2**63, 0
         return a
+    if kind == "near":  # within one f32 step of one another: 2^44 and a step of 2^21
+        return (1 << 44) + rng.integers(0, 1 << 20, (b, rows)) // 7
     if kind == "heavy":
         return (rng.random((b, rows)) ** 8 * 2.0 ** 45).astype(np.int64)
     return rng.integers(0, 1 << 45, (b, rows))
@@ -202,6 +243,20 @@ def test_compact_rows_entries_out_of_range(dev):  # noqa: F811
     kept = torch.tensor([[1, 4, -5]], dtype=torch.int32, device=dev)
     out, = sa.compact_rows([t], kept)
     assert (out[0, 0] == 1).all() and (out[0, 1:] == 0).all()
+
+
+def test_compact_rows_past_32_bits(dev):  # noqa: F811
+    rows = (1 << 32) // 256 + 5000
+    t = torch.empty(1, rows, 256, dtype=torch.uint8, device=dev)
+    kept = torch.cat([torch.arange(0, 3000, 7), torch.arange(rows - 4000, rows, 3)]).to(dev)
+    n = len(kept)
+    marks = torch.randint(0, 256, (n, 256), device=dev, dtype=torch.uint8)
+    t[0, kept] = marks
+    kept = kept.to(torch.int32)[None].contiguous()
+    out, = sa.compact_rows([t], kept)
+    assert torch.equal(out[0], marks)
+    sa.compact_rows([t], kept, out=[t])
+    assert torch.equal(t[0, :n], marks)
 
 
 def test_remap_idx(dev):  # noqa: F811
