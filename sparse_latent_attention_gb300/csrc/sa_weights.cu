@@ -10,16 +10,16 @@
 // over the SMs whatever the batch.  The accumulators are integers, so the order of the additions does
 // not matter.
 //
-// The product's d is cut into two ranges with an accumulator each, added up in the epilogue in f32: the
-// tensor core cuts its running sum after every 16 products, and over all of d = 512 in one accumulator
-// that came to a relative error of 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  Products with
-// e2m1's two significant bits leave it little to cut: 8e-8 with one accumulator, which those rows use.
+// The product's d is cut into two ranges with an accumulator and an issuing warp each, added up in the
+// epilogue in f32.  One accumulator over all of d = 512, cut by the tensor core after every 16 products, came
+// to a relative error of 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  And a stage's products take
+// about as long as the wait and the commits around them, which two warps pass behind each other's products.
 //
-// Roles (persistent CTAs, 18 or 26 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
+// Roles (persistent CTAs, 19 or 27 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
 // tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
 // short latencies (a copy phase ~270 cycles, a hand-over ~250, a tile's epilogue ~3500), longer than the
 // product itself takes, so two groups of warps take turns at the stages and two at the tiles:
-//   warp 0       MMA issue (one elected lane): per stage eight MMAs of 128 x kN x 16
+//   warp 0 and the last  MMA issue (one elected lane): per stage eight MMAs of 128 x kN x 16
 //   warp 1       Q by TMA (128-byte swizzle), 128 d at a time: that part of the next token's Q is loaded as
 //                soon as the last tile's product has passed it
 //   warps 2-9    epilogue: exponentials, sum over heads, accumulation; four warps a tile
@@ -59,7 +59,8 @@ template <int kFmt>
 struct Gather {
     static constexpr int kWarps = kFmt == SA_KV_BF16 ? 4 : 8;
     static constexpr int kRows = kTile / kWarps;
-    static constexpr int kThreads = 32 * (kWarpGather + 2 * kWarps);
+    static constexpr int kWarpMma2 = kWarpGather + 2 * kWarps;  // the second MMA issuer
+    static constexpr int kThreads = 32 * (kWarpMma2 + 1);
 };
 
 // By the heads a product covers (kN = 64 or 128): the stages that fit beside Q.
@@ -200,7 +201,6 @@ template <int kFmt, int kN>
 __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
     row_weights_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
     using Sh = Shape<kN>;
-    constexpr bool kTwo = kFmt != SA_KV_FP4_E2M1;  // two accumulators (see above)
     constexpr int kStages = Sh::kStages, kGroupWarps = Gather<kFmt>::kWarps, kWarpRows = Gather<kFmt>::kRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -220,11 +220,11 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
             mbar_init(smem_addr(&M.q_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&M.s_full[i]), 1);
+            mbar_init(smem_addr(&M.s_full[i]), p.steps > 2 ? 2 : 1);
             mbar_init(smem_addr(&M.s_empty[i]), 4);
             mbar_init(smem_addr(&M.lse_bar[i]), 128);
         }
-        mbar_init(smem_addr(&M.done), 1);
+        mbar_init(smem_addr(&M.done), 2);
         M.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -240,27 +240,37 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
     const uint32_t tmem = M.tmem_base;
     const Range range = unit_range(p);
 
-    if (warp == 0) {
+    if (warp == 0 || warp == Gather<kFmt>::kWarpMma2) {
         // ------------------------------------------------------------------ MMA issue
+        // Warp 0 issues a tile's stages 0 and 1, into the first accumulator, the other warp stages 2 and 3,
+        // into the second: one's waits and commits pass behind the other's products.
         constexpr uint32_t id = idesc_bf16_f32(kTile, kN, false, false);
         const uint64_t a0 = smem_desc_sw128(s_kv, 16, 1024);  // tile rows, K-major
         const uint64_t b0 = smem_desc_sw128(s_q, 16, 1024);   // heads, K-major
         const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
+        const int half = warp == 0 ? 0 : 1, c0 = 2 * half, c1 = min(p.steps, c0 + 2);
         bool ok = true;
-        int st = 0;
+        int st = c0 % kStages;
         uint32_t ph = 0, k = 0, qph = 0;
+        auto skip = [&](int n) {  // the stages that the other warp issues
+            st += n;
+            if (st >= kStages) {
+                st -= kStages;
+                ph ^= 1;
+            }
+        };
         Unit u(p, range.begin);
-        for (int64_t i = range.begin; i < range.end && ok; ++i, ++k) {
+        for (int64_t i = range.begin; i < range.end && ok && c0 < c1; ++i, ++k) {
             const bool first = i == range.begin || u.tile == 0;
             const bool last = i == range.end - 1 || u.tile == p.n_tiles - 1;
             const uint32_t b = k & 1;
             if (!(ok = warp_wait(smem_addr(&M.s_empty[b]), ((k >> 1) & 1) ^ 1, abort))) break;
-            for (int c = 0; c < p.steps; ++c) {
+            const uint32_t col = tmem + 256 * b + kN * half;
+            for (int c = c0; c < c1; ++c) {
                 ok = (!first || warp_wait(smem_addr(&M.q_full[c]), qph, abort)) &&
                      warp_wait(smem_addr(&M.kv_full[st]), ph, abort);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t col = tmem + 256 * b + (kTwo ? kN * (c >> 1) : 0);  // stages 0, 1 and 2, 3
                 uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
                 uint32_t blo = (uint32_t)b0 + 2 * c * (Sh::kQBlockBytes >> 4);
                 const int blocks = c == p.steps - 1 && p.half ? 1 : 2;
@@ -270,20 +280,18 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mma_lohi_elect(col, alo + 2 * q, ahi, blo + 2 * q, bhi, id,
-                                       (uint32_t)(kTwo ? c & 1 : c) | (uint32_t)k64 | (uint32_t)q);
+                                       (uint32_t)(c & 1) | (uint32_t)k64 | (uint32_t)q);
                     alo += kBlockBytes >> 4;
                     blo += Sh::kQBlockBytes >> 4;
                 }
                 mma_commit_elect(smem_addr(&M.kv_empty[st]));
                 if (last) mma_commit_elect(smem_addr(&M.q_empty[c]));
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
+                skip(1);
             }
             if (!ok) break;
             mma_commit_elect(smem_addr(&M.s_full[b]));
             if (last) qph ^= 1;
+            skip(p.steps - (c1 - c0));
             u.step(p);
         }
         // let every issued MMA finish before the accumulators are released
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
         const int q4 = warp & 3;  // the TMEM lanes this warp may read: 32 q4 .. 32 q4 + 31
         const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
         const int et = 32 * q4 + lane;  // 0 .. 127: its entry of the tile, and the head whose lse it brings
-        const bool two = kTwo && p.steps > 2;  // both accumulators are used
+        const bool two = p.steps > 2;  // both accumulators are used
         const uint32_t s_at = tmem + lane_base + 256 * group;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
         float* table = M.nlse[group];
