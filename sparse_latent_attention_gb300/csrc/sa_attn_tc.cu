@@ -93,12 +93,20 @@ constexpr uint32_t kOffQ = kOffKv + kKvBytes;
 constexpr uint32_t kOffP = kOffQ + kQBytes;
 constexpr uint32_t kOffMisc = kOffP + 2 * kPBytes;
 
+// fp4: the lists, claimed slots and e8m0 scales (by slot) of two pairs of tiles in turn
+struct Fp4Lists {
+    uint64_t empty[2];                         // a pair's lists have been read
+    int2 copy_list[2][kProdWarps][2][32];      // per gather warp and tile: (kv row, slot) to copy
+    int copy_n[2][kProdWarps][2];
+    uint32_t claim[2][kProdWarps];
+    alignas(16) uint8_t sc[2][2 * kRows][16];
+};
+
 struct Misc {
     uint64_t q_full, q_empty;
     uint64_t kv_full[2], kv_empty[2];  // per kv buffer
     uint64_t staged[2];                // fp8: a tile's raw codes have landed (per kv buffer);
                                        // fp4: a pair's lists are there (per pair parity)
-    uint64_t list_empty[2];            // fp4: those lists have been read
     uint64_t s_full[2], s_empty[2];    // per S buffer (TMEM)
     uint64_t p_full[2], p_empty[2];    // per P buffer (shared memory)
     uint64_t o_full, o_empty[kChunks];
@@ -112,16 +120,15 @@ struct Misc {
     int ring_count[3];                 // number of valid rows of a pair
     int64_t pair_seq[3];               // sequence whose rows a pair holds
     int row_id[2 * kRows];             // kv row held by each slot of the two buffers, -1 = none
-    int2 copy_list[2][kProdWarps][2][32];  // per gather warp and tile: (kv row, slot) to copy
-    int copy_n[2][kProdWarps][2];          // the lengths of those lists (fp4: two pairs' lists in turn,
-    uint32_t claim[2][kProdWarps];         // and their claimed slots; the others use the first)
+    int2 copy_list[kProdWarps][2][32];  // per producer warp and tile: (kv row, slot) to copy
+    int copy_n[kProdWarps][2];          // the lengths of those lists
     float alpha[2][kHeads];            // rescale factor of the tile, per tile parity
     float stats_m[2][kHeads];          // final max (0 when none) per task parity
     float stats_l[2][kHeads];          // final sum per task parity
     alignas(16) float inv[4][kHeads];  // epilogue: 1 / denominator, a table per epilogue warp
     float sink[kHeads];                // the sinks of the CTA's head block
-    // e8m0 scales of the rows that an fp8 tile (fp4: a pair of tiles, two pairs in turn) widens, by slot
-    alignas(16) uint8_t row_sc[2][2 * kRows][16];
+    alignas(16) uint8_t fp8_sc[2 * kRows][16];  // e8m0 scales of the rows an fp8 tile widens
+    Fp4Lists fp4;
 };
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -251,7 +258,7 @@ __device__ __forceinline__ uint32_t kv_unit_off(int ps, int u) {
 // Widens 128-d chunks c0 .. c1 - 1 of the fp8 rows a warp lists, in place: the e4m3 codes of chunk
 // c sit raw in 64-d block 2c + 1 of the row's slot and become bf16 in blocks 2c and 2c + 1 (exact:
 // see sa_fp8.cuh).  Lane l moves 16-code unit l % 8 (`unit`) of list entries l / 8 + 4 i (ent[i],
-// x < 0 = none); the row's 16 e8m0 scales are in row_sc.
+// x < 0 = none); the row's 16 e8m0 scales are in fp8_sc.
 __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const int2 (&ent)[8], int unit,
                                           int c0, int c1) {
     // Per entry, once: the slot's offset inside a 64-d block (buffer and row) and the byte offset
@@ -266,7 +273,7 @@ __device__ __forceinline__ void widen_fp8(uint32_t s_kv, const Misc& M, const in
         rb[i] = (r >> 6) * kBlkBytes + (r & 63) * 128;
         xo[i] = rb[i] + (uo ^ ((r & 7) << 4));
     }
-    const uint8_t* sc_base = &M.row_sc[0][0][0] + (unit >> 1);
+    const uint8_t* sc_base = &M.fp8_sc[0][0] + (unit >> 1);
 #pragma unroll 1
     for (int cw = c0; cw < c1; ++cw) {
         const uint32_t code_at = s_kv + (2 * cw + 1) * kDBlkBytes + unit * 16;
@@ -372,19 +379,19 @@ struct Held {
 
 __device__ __forceinline__ void load_fp4(const Params& p, Misc& M, Held& x, int64_t seq, int buf, int pw, int hx,
                                          int who, int lane) {
-    const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4);
+    const int n = M.fp4.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4);
     const uint8_t* kvb = p.kv8 + seq * p.rows * (int64_t)(kD / 2) + 16 * (lane & 15);
     uint32_t j[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) j[i] = (uint32_t)M.copy_list[buf][pw][hx][e0 + 4 * i].x;
+    for (int i = 0; i < kHeld; ++i) j[i] = (uint32_t)M.fp4.copy_list[buf][pw][hx][e0 + 4 * i].x;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
         if (e0 + 4 * i < n) x.code[i] = __ldg(reinterpret_cast<const uint4*>(kvb + (uint64_t)j[i] * (kD / 2)));
     // a lane a row: the warp's entries are 4 i + 2 who and 4 i + 2 who + 1
     const int e = 4 * (lane >> 1) + 2 * who + (lane & 1);
     if (e < n) {
-        const int2 en = M.copy_list[buf][pw][hx][e];
-        cp_async16(smem_addr(&M.row_sc[buf][en.y][0]),
+        const int2 en = M.fp4.copy_list[buf][pw][hx][e];
+        cp_async16(smem_addr(&M.fp4.sc[buf][en.y][0]),
                    p.kv_scale + (seq * p.rows + en.x) * (int64_t)(kD / 32), 16u);
     }
     cp_async_commit();
@@ -392,28 +399,29 @@ __device__ __forceinline__ void load_fp4(const Params& p, Misc& M, Held& x, int6
 
 __device__ __forceinline__ void widen_tile_fp4(const Params& p, const Misc& M, uint32_t s_kv, const Held& x,
                                                int64_t seq, int buf, int pw, int hx, int who, int lane) {
-    const int n = M.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4), u = lane & 15;
+    const int n = M.fp4.copy_n[buf][pw][hx], e0 = 2 * who + (lane >> 4), u = lane & 15;
     // (slots and scales of all of them at once; past the list's end: whatever is there, in bounds)
     int ps[kHeld];
     uint32_t sc[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) ps[i] = M.copy_list[buf][pw][hx][e0 + 4 * i].y & 127;
+    for (int i = 0; i < kHeld; ++i) ps[i] = M.fp4.copy_list[buf][pw][hx][e0 + 4 * i].y & 127;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) sc[i] = M.row_sc[buf][ps[i]][u];
+    for (int i = 0; i < kHeld; ++i) sc[i] = M.fp4.sc[buf][ps[i]][u];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
         if (e0 + 4 * i < n) widen_fp4(s_kv, x.code[i], sc[i], ps[i], u);
 #pragma unroll 1
     for (int e = e0 + 4 * kHeld; e < n; e += 4) {
-        const int2 en = M.copy_list[buf][pw][hx][e];
+        const int2 en = M.fp4.copy_list[buf][pw][hx][e];
         const uint4 c = __ldg(reinterpret_cast<const uint4*>(p.kv8 + (seq * p.rows + en.x) * (kD / 2) + 16 * u));
-        widen_fp4(s_kv, c, M.row_sc[buf][en.y][u], en.y, u);
+        widen_fp4(s_kv, c, M.fp4.sc[buf][en.y][u], en.y, u);
     }
 }
 
 // kRope: the inverse rotation of o's rope dims is fused into the epilogue (a separate
 // instantiation, so that the plain kernel carries none of its code)
-template <int kFmt, bool kRope>
+// kLse: the log-sum-exp output, likewise.
+template <int kFmt, bool kRope, bool kLse>
 __global__ void __launch_bounds__(threads_of(kFmt), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap q_map, Params p) {
     // rows of codes: e4m3 is staged raw in shared memory and widened in place there; e2m1 comes through
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                                                 : kDirect ? 2 * kProdWarps
                                                           : kProdThreads);
             mbar_init(smem_addr(&M.staged[b]), kDirect ? kProdWarps : kProdThreads);
-            mbar_init(smem_addr(&M.list_empty[b]), 2 * kProdWarps);
+            mbar_init(smem_addr(&M.fp4.empty[b]), 2 * kProdWarps);
             mbar_init(smem_addr(&M.kv_empty[b]), 1);
             mbar_init(smem_addr(&M.s_full[b]), 1);
             mbar_init(smem_addr(&M.s_empty[b]), 128);
@@ -661,13 +669,13 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
             const uint32_t mh0 = __ballot_sync(0xFFFFFFFFu, copy && half == 0);
             const uint32_t mh1 = __ballot_sync(0xFFFFFFFFu, copy && half == 1);
             if (lane == 0) {
-                M.copy_n[buf][pw][0] = __popc(mh0);
-                M.copy_n[buf][pw][1] = __popc(mh1);
-                M.claim[buf][pw] = m_claim;
+                M.fp4.copy_n[buf][pw][0] = __popc(mh0);
+                M.fp4.copy_n[buf][pw][1] = __popc(mh1);
+                M.fp4.claim[buf][pw] = m_claim;
             }
             if (copy) {
                 const uint32_t mh = half ? mh1 : mh0;
-                M.copy_list[buf][pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
+                M.fp4.copy_list[buf][pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
                 const int64_t row = a.t.seq * p.rows + j;
                 prefetch_l2_line(p.kv8 + row * (kD / 2));
                 prefetch_l2_line(p.kv8 + row * (kD / 2) + 128);
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
             if (more) {  // the next pair's lists
                 if (who == 0) {
                     // (their place was last read two pairs back)
-                    if (!(ok = warp_wait(smem_addr(&M.list_empty[nbuf]), (((k + 1) >> 1) & 1) ^ 1, abort))) break;
+                    if (!(ok = warp_wait(smem_addr(&M.fp4.empty[nbuf]), (((k + 1) >> 1) & 1) ^ 1, abort))) break;
                     const int j = jn;
                     Pair after = ahead;
                     after.step(p, te);
@@ -717,7 +725,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                     const uint32_t Tx = a.T + hx, b = Tx & 1;
                     if (!(ok = warp_wait(smem_addr(&M.kv_empty[b]), ((Tx >> 1) & 1) ^ 1, abort))) break;
                     if (who == 0) {
-                        const uint32_t m = M.claim[buf][pw];
+                        const uint32_t m = M.fp4.claim[buf][pw];
                         M.vmask16[b][pw] = (uint16_t)(hx ? m >> 16 : m);
                     }
                     // this warp's scales of the tile: one later group of copies may still be under way, the
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                 if (more && hx < ahead.tiles()) load_fp4(p, M, held[hx], ahead.t.seq, nbuf, pw, hx, who, lane);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&M.list_empty[buf]));
+            if (lane == 0) mbar_arrive(smem_addr(&M.fp4.empty[buf]));
         }
         cp_async_wait<0>();
     } else if (warp < kWarpSoftmax) {
@@ -822,13 +830,13 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                     if (T > 1 && !(ok = mbar_wait(smem_addr(&M.kv_full[(T - 2) & 1]), ((T - 2) >> 1) & 1, abort)))
                         break;
                     if (lane == 0) {
-                        M.copy_n[0][pw][0] = __popc(mh0);
-                        M.copy_n[0][pw][1] = __popc(mh1);
+                        M.copy_n[pw][0] = __popc(mh0);
+                        M.copy_n[pw][1] = __popc(mh1);
                     }
                 }
                 if (copy) {
                     const uint32_t mh = half ? mh1 : mh0;
-                    M.copy_list[0][pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
+                    M.copy_list[pw][half][__popc(mh & ((1u << lane) - 1u))] = make_int2(j, ps);
                     // the buffers are usually still in use: pull the new rows into L2 now, so
                     // that the copies issued once a buffer is released hit L2
                     if constexpr (kStaged) {
@@ -856,7 +864,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int e = (lane >> 3) + 4 * i;
-                            ent[i] = e < ncopy ? M.copy_list[0][pw][hx][e] : make_int2(-1, 0);
+                            ent[i] = e < ncopy ? M.copy_list[pw][hx][e] : make_int2(-1, 0);
                         }
                     };
 #pragma unroll
@@ -869,8 +877,8 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                         if (!(ok = mbar_wait(smem_addr(&M.kv_empty[b]), ((Tx >> 1) & 1) ^ 1, abort))) break;
                         M.vmask16[b][pw] = (uint16_t)(hx ? m_claim >> 16 : m_claim);
                         if (lane < ncopy) {  // the row's 16 scales
-                            const int2 en = M.copy_list[0][pw][hx][lane];
-                            cp_async16(smem_addr(&M.row_sc[0][en.y][0]), scb + (int64_t)en.x * (kD / 32), 16u);
+                            const int2 en = M.copy_list[pw][hx][lane];
+                            cp_async16(smem_addr(&M.fp8_sc[en.y][0]), scb + (int64_t)en.x * (kD / 32), 16u);
                         }
                         // per row one shared and one global base, chunk c at constant offsets
 #pragma unroll
@@ -916,7 +924,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                     const int n = __popc(hx ? mh1 : mh0);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        ent_r[hx][e] = (hx < nt && n <= 2 && e < n) ? M.copy_list[0][pw][hx][e] : make_int2(-1, 0);
+                        ent_r[hx][e] = (hx < nt && n <= 2 && e < n) ? M.copy_list[pw][hx][e] : make_int2(-1, 0);
                         if (ent_r[hx][e].x >= 0) {
                             const uint4* src = reinterpret_cast<const uint4*>(kvb + (int64_t)ent_r[hx][e].x * kD);
                             v[hx][e][0] = __ldg(src + lane);
@@ -952,7 +960,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                         const char* g_lane = reinterpret_cast<const char*>(kvb) + (lane & 15) * 16;
 #pragma unroll 1
                         for (int e = lane >> 4; e < ncopy; e += 2) {
-                            const int2 en = M.copy_list[0][pw][hx][e];
+                            const int2 en = M.copy_list[pw][hx][e];
                             const uint32_t ps = (uint32_t)en.y;
                             const uint32_t sb = (s_lane ^ ((ps & 7) << 4)) + (ps >> 6) * kBlkBytes +
                                                 (ps & 63) * 128;
@@ -1138,12 +1146,12 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                     if (wtau < te &&
                         __all_sync(0xffffffffu, mbar_test_wait(smem_addr(&M.staged[wT & 1]), (wT >> 1) & 1))) {
                         const int hx = (wti - wt0) & 1;
-                        const int ncopy = M.copy_n[0][q4][hx];
+                        const int ncopy = M.copy_n[q4][hx];
                         int2 ent8[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int e = (lane >> 3) + 4 * i;
-                            ent8[i] = e < ncopy ? M.copy_list[0][q4][hx][e] : make_int2(-1, 0);
+                            ent8[i] = e < ncopy ? M.copy_list[q4][hx][e] : make_int2(-1, 0);
                         }
                         widen_fp8(s_kv, M, ent8, lane & 7, 2, 4);
                         fence_proxy_async_smem();
@@ -1185,11 +1193,12 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                             p.part_ml[(pbase + h) * 2 + 0] = mu;
                             p.part_ml[(pbase + h) * 2 + 1] = l;
                         }
-                    } else {
-                        if (l > 0.f) inv = 1.f / (l + fast_exp2(M.sink[h] * kLog2e - mu));
-                        if (p.lse && q4 == 0)
-                            p.lse[t.token * p.h + h0 + h] = log_sum_exp(l, mu, M.sink[h]);
+                    } else if (l > 0.f) {
+                        inv = 1.f / (l + fast_exp2(M.sink[h] * kLog2e - mu));
                     }
+                    if constexpr (kLse)
+                        if (!split && q4 == 0)
+                            p.lse[t.token * p.h + h0 + h] = log_sum_exp(l, mu, M.sink[h]);
                 }
                 M.inv[q4][h] = inv;
             }
@@ -1278,11 +1287,14 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
 // host side
 // ---------------------------------------------------------------------------------------------
 
-// by kv format, without and with the fused rotation
-void (*const kKernels[6])(const CUtensorMap, Params) = {
-    attn_tc_kernel<SA_KV_BF16, false>,     attn_tc_kernel<SA_KV_BF16, true>,
-    attn_tc_kernel<SA_KV_FP8_E4M3, false>, attn_tc_kernel<SA_KV_FP8_E4M3, true>,
-    attn_tc_kernel<SA_KV_FP4_E2M1, false>, attn_tc_kernel<SA_KV_FP4_E2M1, true>};
+// by kv format, fused rotation and log-sum-exp output
+void (*const kKernels[3][2][2])(const CUtensorMap, Params) = {
+    {{attn_tc_kernel<SA_KV_BF16, false, false>, attn_tc_kernel<SA_KV_BF16, false, true>},
+     {attn_tc_kernel<SA_KV_BF16, true, false>, attn_tc_kernel<SA_KV_BF16, true, true>}},
+    {{attn_tc_kernel<SA_KV_FP8_E4M3, false, false>, attn_tc_kernel<SA_KV_FP8_E4M3, false, true>},
+     {attn_tc_kernel<SA_KV_FP8_E4M3, true, false>, attn_tc_kernel<SA_KV_FP8_E4M3, true, true>}},
+    {{attn_tc_kernel<SA_KV_FP4_E2M1, false, false>, attn_tc_kernel<SA_KV_FP4_E2M1, false, true>},
+     {attn_tc_kernel<SA_KV_FP4_E2M1, true, false>, attn_tc_kernel<SA_KV_FP4_E2M1, true, true>}}};
 
 struct TcGeometry {
     int n_tiles, hblocks, n_splits, tiles_per_split;
@@ -1404,11 +1416,12 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !configured[dev]) {
-        for (auto fn : kKernels) {
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-            if (e != cudaSuccess) return e;
-        }
+        for (auto& by_rope : kKernels)
+            for (auto& by_lse : by_rope)
+                for (auto fn : by_lse) {
+                    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                    if (e != cudaSuccess) return e;
+                }
         if (dev < 64) configured[dev] = true;
     }
     int64_t groups = device_sm_count() / g.hblocks;  // CTA groups, one CTA per head block
@@ -1416,7 +1429,7 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     if (groups < 1) groups = 1;
     const int64_t grid = groups * g.hblocks;
     const bool rope = c.rope != nullptr;
-    auto kernel = kKernels[2 * c.kv_format + (rope ? 1 : 0)];
+    auto kernel = kKernels[c.kv_format][rope ? 1 : 0][c.lse ? 1 : 0];
     e = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(c.kv_format)), kSmemBytes, c.stream, qmap, p);
     if (e != cudaSuccess || g.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, n_tokens, c.h, kD, g.n_splits,
