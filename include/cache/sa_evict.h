@@ -77,7 +77,7 @@ sa_status sa_row_weights(const void* q, const void* kv, const uint8_t* kv_scale,
  *   kept    int32 [b][n_keep], written: the rows that stay, ascending; then -1 where fewer than n_keep
  *   remap   int32 [b][rows], written: a staying row's place in kept, -1 for every other row
  * acc is int64 [b][rows], 8-byte aligned.  Requires 0 <= keep_first, 0 <= keep_last,
- * keep_first + keep_last <= n_keep <= rows, rows < 2^31.  No output may overlap an input or the other
+ * keep_first + keep_last <= n_keep <= rows, rows <= 2^31 - 2^16.  No output may overlap an input or the other
  * output.  b == 0 or rows == 0 is a no-op.
  */
 sa_status sa_evict_select(const int64_t* acc, const int32_t* live, int64_t b, int64_t rows,

@@ -507,7 +507,8 @@ extern "C" sa_status sa_evict_select(const int64_t* acc, const int32_t* live, in
     if (b < 0 || rows < 0 || keep_first < 0 || keep_last < 0 || n_keep < 0 || n_keep > rows)
         return SA_ERR_INVALID_ARG;
     if (keep_first > n_keep || keep_last > n_keep - keep_first) return SA_ERR_INVALID_ARG;
-    if (rows >= (int64_t(1) << 31) || b >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
+    // (a row's number is 32 bits in the kernel, which steps past the last one by less than 2^16)
+    if (rows > (int64_t(1) << 31) - (1 << 16) || b >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
     if (b == 0 || rows == 0) return SA_OK;
     if (!acc || !remap || (n_keep > 0 && !kept)) return SA_ERR_INVALID_ARG;
     if (!is_aligned(acc, 8) || !is_aligned(live, 4) || !is_aligned(kept, 4) || !is_aligned(remap, 4))

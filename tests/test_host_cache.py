@@ -118,6 +118,7 @@ def test_row_weights_refuses(lib, change, code):
     (dict(b=0), OK), (dict(rows=0, keep=0, first=0, last=0), OK), (dict(keep=101), INVALID),
     (dict(keep=-1), INVALID), (dict(first=-1), INVALID), (dict(last=-1), INVALID),
     (dict(first=40, last=11), INVALID), (dict(first=51, last=0), INVALID), (dict(rows=1 << 31), UNSUPPORTED),
+    (dict(rows=(1 << 31) - 65535), UNSUPPORTED), (dict(rows=(1 << 31) - 65536, acc=None), INVALID),
     (dict(first=2**63 - 1, last=2**63 - 1), INVALID), (dict(acc=None), INVALID), (dict(kept=None), INVALID),
     (dict(remap=None), INVALID), (dict(acc=at(1, 4)), INVALID), (dict(kept=at(3, 2)), INVALID),
     (dict(live=at(2, 2)), INVALID), (dict(kept=at(1, 8)), INVALID), (dict(remap=at(1, 8)), INVALID),
