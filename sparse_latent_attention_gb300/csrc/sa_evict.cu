@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_stay = min(n_keep, L);
     const uint32_t want = (uint32_t)(n_stay - (L - n));  // of the n candidates
     // this CTA's rows and candidates
-    const int r0 = (int)min((int64_t)rank * share, (int64_t)rows), r1 = min(r0 + share, rows);
+    const int r0 = (int)min((int64_t)rank * share, (int64_t)rows), r1 = r0 + min(share, rows - r0);
     const int c0 = min(max(lo, r0), r1), c1 = max(c0, min(hi, r1));
     auto key = [&](int i) { return kCached ? keys[i - c0] : key_of(a[i]); };
 
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // a warp's share; of up to 32 groups of 32 rows lane l keeps group l's ballots for the numbering
     const int warp_share = ((share + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int i0 = min(r0 + warp * warp_share, r1), i1 = min(i0 + warp_share, r1), live1 = min(i1, end);
+    const int i0 = min(r0 + warp * warp_share, r1), i1 = i0 + min(warp_share, r1 - i0), live1 = min(i1, end);
     uint32_t n_in = 0, n_eq = 0, my_in = 0, my_eq = 0;
 #pragma unroll 2
     for (int i = i0, g = 0; i < live1; i += 32, ++g) {
