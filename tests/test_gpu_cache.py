@@ -242,6 +242,20 @@ def test_fp4_with_rope_and_lse(dev):
     check(o, want, tol, "rotated")
 
 
+@pytest.mark.parametrize("d,s,topk", [(512, 40, 130), (512, 1, 1200), (256, 3, 70)])
+def test_lse_of_logits_that_are_not_numbers(dev, d, s, topk):
+    """A NaN in a head's q makes that head's lse NaN; the other heads' stay."""
+    q, kv, sc, sink, idx = inputs(dev, "bf16", 1, s, 16, d, 1500, topk, 7)
+    idx[0, s - 1] = torch.arange(topk, device=dev, dtype=torch.int32)
+    want, got = (torch.empty((1, s, 16), dtype=torch.float32, device=dev) for _ in range(2))
+    sa.sparse_attn(q, kv, sink, idx, d ** -0.5, lse=want)
+    q[0, s - 1, 5, 3] = float("nan")
+    sa.sparse_attn(q, kv, sink, idx, d ** -0.5, lse=got)
+    assert got[0, s - 1, 5].isnan()
+    got[0, s - 1, 5] = want[0, s - 1, 5]
+    assert torch.equal(got, want)
+
+
 def test_no_columns_and_no_tokens(dev):
     for d in (512, 128):
         q, kv, sc, sink, idx = inputs(dev, "fp4", 2, 3, 16, d, 40, 0, 9)
