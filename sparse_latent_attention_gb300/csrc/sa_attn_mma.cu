@@ -402,7 +402,7 @@ __global__ void attn_combine_kernel(const float* __restrict__ part_ml,
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (!(ml[i].y > 0.f)) continue;
+            if (ml[i].y == 0.f) continue;  // (a NaN goes into the sums)
             if (ml[i].x > M) {  // a new maximum: rescale what was summed so far (0 at the start)
                 const float r = M == -INFINITY ? 0.f : fast_exp2(M - ml[i].x);
                 L *= r;
