@@ -64,6 +64,18 @@ def _call(name, dev, stream, *args):
         _lib.check(st, name)
 
 
+def _new(stream, make):
+    """make()'s tensor, for a call that runs on ``stream``: from that stream's memory when one is given,
+    where it is filled and where a block that other work still reads is not handed out, and kept while the
+    current stream, on which the caller will use it, has work queued."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _need(t, name, dtype, device=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -137,13 +149,13 @@ def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, wor
         raise ValueError(f"idx shape {tuple(idx.shape)} does not match q {tuple(q.shape)}")
     topk = idx.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, lambda: torch.empty_like(q))
     else:
         _need(out, "out", torch.bfloat16, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = new_workspace(b, s, h, d, rows, topk, fmt, device=dev)
+        workspace = _new(stream, lambda: new_workspace(b, s, h, d, rows, topk, fmt, device=dev))
     else:
         _need(workspace, "workspace", torch.uint8, dev)
     if family is not None and family not in FAMILIES:
@@ -458,7 +470,7 @@ def row_weights(q, kv, lse, idx, softmax_scale, acc, *, kv_scale=None, workspace
     if acc.shape != (b, rows):
         raise ValueError(f"acc shape {tuple(acc.shape)} != {(b, rows)}")
     if workspace is None:
-        workspace = torch.zeros(SA_STATUS_BYTES, dtype=torch.uint8, device=dev)
+        workspace = _new(stream, lambda: torch.zeros(SA_STATUS_BYTES, dtype=torch.uint8, device=dev))
     else:
         _need(workspace, "workspace", torch.uint8, dev)
     _call("sa_row_weights", dev.index, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(lse), _ptr(idx),
@@ -485,8 +497,9 @@ def evict_select(acc, n_keep, *, keep_first=0, keep_last=0, live=None, stream=No
     n_keep = int(n_keep)
     if not 0 <= n_keep <= rows:
         raise ValueError(f"n_keep {n_keep} is not within [0, {rows}]")
-    kept = torch.empty((b, n_keep), dtype=torch.int32, device=acc.device)
-    remap = torch.empty((b, rows), dtype=torch.int32, device=acc.device)
+    dev = acc.device
+    kept = _new(stream, lambda: torch.empty((b, n_keep), dtype=torch.int32, device=dev))
+    remap = _new(stream, lambda: torch.empty((b, rows), dtype=torch.int32, device=dev))
     _call("sa_evict_select", acc.get_device(), stream, _ptr(acc), _ptr(live), b, rows, n_keep,
           int(keep_first), int(keep_last), _ptr(kept), _ptr(remap))
     return kept, remap
@@ -540,7 +553,8 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
         row_bytes.append(of(t, "a tensor", shape, stride, size))
         o = outs[i]
         if o is None:
-            o = outs[i] = torch.empty((b, n_keep, *shape[2:]), dtype=t.dtype, device=t.device)
+            o = outs[i] = _new(stream, lambda: torch.empty((b, n_keep, *shape[2:]), dtype=t.dtype,
+                                                           device=t.device))
         elif (o.get_device() != dev or o.dtype != t.dtype or o.dim() != len(shape) or o.shape[0] != b
               or o.shape[1] < n_keep or o.shape[2:] != shape[2:]):
             raise ValueError(f"out[{i}] must be a {t.dtype} tensor [{b}, {n_keep} or more, ...] like "
@@ -567,7 +581,7 @@ def remap_idx(idx, remap, *, out=None, stream=None) -> torch.Tensor:
     if remap.dim() != 2 or idx.dim() < 1 or idx.shape[0] != remap.shape[0]:
         raise ValueError(f"remap shape {tuple(remap.shape)} does not match idx {tuple(idx.shape)}")
     if out is None:
-        out = torch.empty_like(idx)
+        out = _new(stream, lambda: torch.empty_like(idx))
     else:
         _need(out, "out", torch.int32, idx.device)
         if out.shape != idx.shape:

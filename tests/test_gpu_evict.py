@@ -364,3 +364,47 @@ def test_captured_and_replayed_on_a_side_stream(dev):  # noqa: F811
         torch.cuda.synchronize()
         for g_, w in zip(got, want):
             assert torch.equal(g_, w)
+
+
+@pytest.mark.parametrize("call", ["sparse_attn", "evict_select", "compact_rows", "remap_idx"])
+def test_outputs_of_a_call_on_another_stream(dev, call):  # noqa: F811
+    """A call on a stream of its own does not write into memory that the current stream still reads."""
+    n = 300000
+    acc = torch.arange(n, device=dev)[None]
+    kept = torch.arange(n, device=dev, dtype=torch.int32)[None]
+    q, kv, sc, sink, idx = inputs(dev, "fp4", 1, 10, 64, 512, 700, 64, 3)
+    run = {"sparse_attn": lambda st: [sa.sparse_attn(q, kv, sink, idx, 0.05, kv_scale=sc, stream=st)],
+           "evict_select": lambda st: sa.evict_select(acc, n, stream=st),
+           "compact_rows": lambda st: sa.compact_rows([kept], kept, stream=st),
+           "remap_idx": lambda st: [sa.remap_idx(kept, kept, stream=st)]}[call]
+    want = [t.clone() for t in run(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nbytes = want[0].numel() * want[0].element_size()
+    old, copy = (torch.full((nbytes,), 7, dtype=torch.uint8, device=dev) for _ in range(2))
+    copy.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    copy.copy_(old)
+    del old
+    got = run(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert (copy == 7).all()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_no_columns_captured(dev):  # noqa: F811
+    """The call without columns (a memset and the sinks) in a graph."""
+    q, kv, sc, sink, idx = inputs(dev, "fp4", 2, 3, 16, 512, 40, 0, 9)
+    lse, o = torch.empty(2, 3, 16, device=dev), torch.empty_like(q)
+    ws = sa.new_workspace(2, 3, 16, 512, 40, 0, sa.SA_KV_FP4_E2M1)
+    graph = torch.cuda.CUDAGraph()
+    sa.sparse_attn(q, kv, sink, idx, 0.1, kv_scale=sc, lse=lse, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        sa.sparse_attn(q, kv, sink, idx, 0.1, kv_scale=sc, lse=lse, out=o, workspace=ws)
+    lse.fill_(5)
+    o.fill_(5)
+    graph.replay()
+    assert (o == 0).all() and (lse == sink).all()
