@@ -60,7 +60,9 @@ sa_status sa_sparse_attn_lse(const void* q, const void* kv, const uint8_t* kv_sc
  *   acc         int64 [b][rows], 8-byte aligned, added to; must not overlap an input
  *   workspace   at least SA_STATUS_BYTES, 256-byte aligned: the status word, as for sa_sparse_attn (one
  *               workspace can serve both calls)
- * Supported: as sa_sparse_attn.  b * s == 0 or topk == 0 is a no-op.
+ * Supported: as sa_sparse_attn, topk < 2^31 - 128.  b * s == 0 or topk == 0 is a no-op.  An accumulator
+ * holds 2^31 - 1 weights of 1; what goes past that wraps (a row that takes all the weight of 128 heads gets
+ * there after 2^24 queries).
  */
 sa_status sa_row_weights(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,
                          const float* lse, const int32_t* idx, float softmax_scale,

@@ -650,6 +650,7 @@ extern "C" sa_status sa_row_weights(const void* q, const void* kv, const uint8_t
     if (b < 0 || s < 0 || h < 1 || d < 1 || rows < 0 || topk < 0) return SA_ERR_INVALID_ARG;
     // (the shapes sparse_attn takes)
     if (sa_sparse_attn_workspace_size(b, s, h, d, rows, topk, kv_format) == 0) return SA_ERR_UNSUPPORTED;
+    if (topk > INT32_MAX - kTile) return SA_ERR_UNSUPPORTED;  // a tile's last column is a 32-bit number
     if (kv_format == SA_KV_BF16 && kv_scale) return SA_ERR_INVALID_ARG;
     if (b * s == 0 || topk == 0) return SA_OK;
     if (!q || !lse || !idx || (rows > 0 && (!kv || !acc))) return SA_ERR_INVALID_ARG;

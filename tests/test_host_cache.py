@@ -105,7 +105,8 @@ def test_sparse_attn_lse_refuses(lib, change, code):
     (dict(acc=at(1, 64)), INVALID), (dict(acc=at(2, 64)), INVALID), (dict(acc=at(3)), INVALID),
     (dict(acc=at(4)), INVALID), (dict(rows=0, kv=None, acc=None), WORKSPACE),
     (dict(ws=at(8), ws_bytes=255), WORKSPACE), (dict(ws=at(8, 64), ws_bytes=256), INVALID),
-    (dict(ws=at(6), ws_bytes=256), INVALID),
+    (dict(ws=at(6), ws_bytes=256), INVALID), (dict(topk=2**31 - 1), UNSUPPORTED),
+    (dict(topk=2**31 - 129), WORKSPACE),
 ])
 def test_row_weights_refuses(lib, change, code):
     a = dict(q=at(1), kv=at(2), kv_scale=None, fmt=0, lse=at(3), idx=at(4), scale=0.1, b=1, s=2, h=64, d=512,
