@@ -15,8 +15,12 @@
 // to a relative error of 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  And a stage's products take
 // about as long as the wait and the commits around them, which two warps pass behind each other's products.
 //
-// Roles (persistent CTAs, 19 or 27 warps; every wait is bounded, as in the attention kernel).  A stage is 128 d of a
-// tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
+// What bounds it: that prefill reads 2.7 GB of rows out of L2 in 214 us, 12.5 TB/s or 44 bytes a cycle and
+// SM (the products alone would take 90 us, at the measured bf16 rate); the long decode, 144 MB of codes and
+// scales once (38 us at the measured copy rate), is held up by the widening.
+//
+// Roles (persistent CTAs, 19 or 27 warps; every wait is bounded, as in the attention kernel).  A stage is
+// 128 d of a tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
 // short latencies (a copy phase ~270 cycles, a hand-over ~250, a tile's epilogue ~3500), longer than the
 // product itself takes, so two groups of warps take turns at the stages and two at the tiles:
 //   warp 0 and the last  MMA issue (one elected lane): per stage eight MMAs of 128 x kN x 16
@@ -53,8 +57,8 @@ constexpr uint32_t kStageBytes = 2 * kBlockBytes;
 
 // By the kv format: the warps of a gather group, and the rows of a stage that each fills.  Copying takes few
 // instructions, and fewer warps leave the others quicker (a prefill's 4096 queries x 640 bf16 rows, 64 heads:
-// 257 us with four, 298 with eight); widening takes many (a long decode's 256 x 2176 4-bit rows, 128 heads:
-// 106 us with eight, 121 with four).
+// 214 us with four, 249 with eight); widening takes many (a long decode's 256 x 2176 4-bit rows, 128 heads:
+// 108 us with eight, 120 with four).
 template <int kFmt>
 struct Gather {
     static constexpr int kWarps = kFmt == SA_KV_BF16 ? 4 : 8;
