@@ -8,7 +8,7 @@
 //
 // Bound by memory (2 bytes an element in, 0.53 out, 2.53 with the round trip) only as long as a group of
 // eight elements takes less than about a hundred instructions: the common path looks for a NaN once a
-// group, multiplies 32-bit indices, and divides once in four groups.
+// group, multiplies 32-bit indices, and divides once a thread.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -106,15 +106,17 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv) {
     return c;
 }
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Eight consecutive elements a thread, four threads a block: the block's maximum takes two shuffles.  A
 // thread has kPer such groups, kThreads apart, whose loads are all under way before the first is looked at
-// (kPer = 4 where there are groups enough for it, 1 for few rows, where only the latency counts).  Needs
-// 16-byte aligned x and round trip rows and 4-byte aligned code rows; Index holds the number of groups and
-// every stride.
+// (kPer = 2 where there are groups enough for it, 1 for few rows, where only the latency counts).  Loads
+// under way are threads times groups: 532480 rows of 512 took 186 us with two groups at twelve blocks of 128
+// threads a SM, 203 with four groups and the registers that they ask for, 199 with one, 191 with blocks of
+// 256.  Needs 16-byte aligned x and round trip rows and 4-byte aligned code rows; Index holds the number of
+// groups and every stride.
 template <bool kRing, class Index, int kPer>
-__global__ void __launch_bounds__(kThreads) quant4_kernel(const __grid_constant__ Quant4 p) {
+__global__ void __launch_bounds__(kThreads, 12) quant4_kernel(const __grid_constant__ Quant4 p) {
     pdl_wait();
     pdl_trigger();
     const Index g8 = (Index)(p.d >> 3), total = (Index)(p.n * (p.d >> 3));
@@ -241,9 +243,9 @@ sa_status launch(const Quant4& p, void* stream) {
             if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
             return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
         };
-        if (!narrow) e = go(quant4_kernel<kRing, uint64_t, 4>, 4);
-        else if (groups < (int64_t)device_sm_count() * 8 * kThreads) e = go(quant4_kernel<kRing, uint32_t, 1>, 1);
-        else e = go(quant4_kernel<kRing, uint32_t, 4>, 4);
+        if (!narrow) e = go(quant4_kernel<kRing, uint64_t, 2>, 2);
+        else if (groups < (int64_t)device_sm_count() * 2048) e = go(quant4_kernel<kRing, uint32_t, 1>, 1);
+        else e = go(quant4_kernel<kRing, uint32_t, 2>, 2);
     } else {
         int64_t grid = (p.n * (int64_t)(p.d / 32) + kThreads - 1) / kThreads;
         const int64_t cap = (int64_t)device_sm_count() * 32;
