@@ -10,10 +10,11 @@
 // over the SMs whatever the batch.  The accumulators are integers, so the order of the additions does
 // not matter.
 //
-// The product's d is cut into two ranges with an accumulator and an issuing warp each, added up in the
-// epilogue in f32.  One accumulator over all of d = 512, cut by the tensor core after every 16 products, came
-// to a relative error of 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  And a stage's products take
-// about as long as the wait and the commits around them, which two warps pass behind each other's products.
+// The product's d is cut into two ranges with an accumulator each, added up in the epilogue in f32.  One
+// accumulator over all of d = 512, cut by the tensor core after every 16 products, came to a relative error of
+// 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  Up to 64 heads each range has an issuing warp too: a
+// stage's products take about as long as the wait and the commits around them, which two warps pass behind
+// each other's products (214 us against 257 for the prefill below).
 //
 // What bounds it: that prefill reads 2.7 GB of rows out of L2 in 214 us, 12.5 TB/s or 44 bytes a cycle and
 // SM (the products alone would take 90 us, at the measured bf16 rate); the long decode, 144 MB of codes and
@@ -23,7 +24,8 @@
 // 128 d of a tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
 // short latencies (a copy phase ~270 cycles, a hand-over ~250, a tile's epilogue ~3500), longer than the
 // product itself takes, so two groups of warps take turns at the stages and two at the tiles:
-//   warp 0 and the last  MMA issue (one elected lane): per stage eight MMAs of 128 x kN x 16
+//   warp 0 (and the last, up to 64 heads)  MMA issue (one elected lane): per stage eight MMAs of
+//                128 x kN x 16
 //   warp 1       Q by TMA (128-byte swizzle), 128 d at a time: that part of the next token's Q is loaded as
 //                soon as the last tile's product has passed it
 //   warps 2-9    epilogue: exponentials, sum over heads, accumulation; four warps a tile
@@ -73,6 +75,13 @@ struct Shape {
     static constexpr uint32_t kQBlockBytes = kN * 128;  // 64 d of Q
     static constexpr uint32_t kQBytes = 2 * kMaxSteps * kQBlockBytes;
     static constexpr int kStages = kN == 64 ? 5 : 3;
+    // Two issuing warps release the stages out of order, one range's later stage before the other's earlier
+    // one.  A gather warp that waits for stage n (n - kStages released) must not do so while the use before
+    // (n - 2 kStages) is still in progress: the barrier's parity would answer for the wrong use.  It has seen
+    // n - 9 and n - 7 released when it comes to n with five stages, one of which the warp that issued n - 10
+    // released after it.  With three stages it has only seen n - 5 and n - 7, both of which can precede
+    // n - 6: those have one issuing warp.
+    static constexpr bool kTwoIssuers = kStages == 5;
     static constexpr uint32_t kOffQ = kStages * kStageBytes;
     static constexpr uint32_t kOffMisc = kOffQ + kQBytes;
 };
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
             mbar_init(smem_addr(&M.q_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&M.s_full[i]), p.steps > 2 ? 2 : 1);
+            mbar_init(smem_addr(&M.s_full[i]), Sh::kTwoIssuers && p.steps > 2 ? 2 : 1);
             mbar_init(smem_addr(&M.s_empty[i]), 4);
             mbar_init(smem_addr(&M.lse_bar[i]), 128);
         }
@@ -246,13 +255,14 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
 
     if (warp == 0 || warp == Gather<kFmt>::kWarpMma2) {
         // ------------------------------------------------------------------ MMA issue
-        // Warp 0 issues a tile's stages 0 and 1, into the first accumulator, the other warp stages 2 and 3,
-        // into the second: one's waits and commits pass behind the other's products.
+        // A tile's stages 0 and 1 go into the first accumulator, 2 and 3 into the second.  With two issuers
+        // warp 0 takes the former and the other warp the latter.
         constexpr uint32_t id = idesc_bf16_f32(kTile, kN, false, false);
         const uint64_t a0 = smem_desc_sw128(s_kv, 16, 1024);  // tile rows, K-major
         const uint64_t b0 = smem_desc_sw128(s_q, 16, 1024);   // heads, K-major
         const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
-        const int half = warp == 0 ? 0 : 1, c0 = 2 * half, c1 = min(p.steps, c0 + 2);
+        const int c0 = warp == 0 ? 0 : Sh::kTwoIssuers ? 2 : p.steps;
+        const int c1 = Sh::kTwoIssuers ? min(p.steps, c0 + 2) : p.steps;
         bool ok = true;
         int st = c0 % kStages;
         uint32_t ph = 0, k = 0, qph = 0;
@@ -269,12 +279,12 @@ __global__ void __launch_bounds__(Gather<kFmt>::kThreads, 1)
             const bool last = i == range.end - 1 || u.tile == p.n_tiles - 1;
             const uint32_t b = k & 1;
             if (!(ok = warp_wait(smem_addr(&M.s_empty[b]), ((k >> 1) & 1) ^ 1, abort))) break;
-            const uint32_t col = tmem + 256 * b + kN * half;
             for (int c = c0; c < c1; ++c) {
                 ok = (!first || warp_wait(smem_addr(&M.q_full[c]), qph, abort)) &&
                      warp_wait(smem_addr(&M.kv_full[st]), ph, abort);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t col = tmem + 256 * b + kN * (c >> 1);
                 uint32_t alo = (uint32_t)a0 + st * (kStageBytes >> 4);
                 uint32_t blo = (uint32_t)b0 + 2 * c * (Sh::kQBlockBytes >> 4);
                 const int blocks = c == p.steps - 1 && p.half ? 1 : 2;

@@ -39,6 +39,25 @@ def test_row_weights(dev, case, fmt):  # noqa: F811
     assert torch.equal(again - start, acc)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("h,d,topk", [(128, 512, 1), (100, 512, 64), (128, 448, 130), (65, 384, 2), (128, 320, 200),
+                                      (128, 256, 64), (64, 512, 1), (33, 384, 130)])
+def test_row_weights_many_short_queries(dev, h, d, topk, fmt):  # noqa: F811
+    """Several queries a CTA, one or two tiles each: every stage and every part of q is used again and
+    again.  The same every time."""
+    b, s, rows = 17, 40, 128
+    q, kv, sc, sink, idx = inputs(dev, fmt, b, s, h, d, rows, topk, h + d + topk, distinct=topk <= rows)
+    lse = torch.empty(b, s, h, device=dev)
+    sa.sparse_attn(q, kv, sink, idx, d ** -0.5, kv_scale=sc, lse=lse)
+    acc = torch.zeros(b, rows, dtype=torch.int64, device=dev)
+    sa.row_weights(q, kv, lse, idx, d ** -0.5, acc, kv_scale=sc)
+    _close(acc, q, kv, sc, lse, idx, d ** -0.5)
+    for _ in range(20):
+        again = torch.zeros_like(acc)
+        sa.row_weights(q, kv, lse, idx, d ** -0.5, again, kv_scale=sc)
+        assert torch.equal(again, acc)
+
+
 def test_row_weights_negative_scale_and_special_lse(dev):  # noqa: F811
     q, kv, sc, sink, idx = inputs(dev, "fp4", 1, 6, 16, 512, 200, 150, 3)
     lse = torch.full((1, 6, 16), 4.0, device=dev)
