@@ -96,8 +96,8 @@ __device__ __forceinline__ void find_bin(SelectSmem& S, uint32_t want, uint32_t 
     __syncthreads();
 }
 
-// A cluster of `ctas` CTAs per sequence, an even share of the rows each.  Rows [0, lo) and [hi, live) are protected; of the candidates [lo, hi) the `want`
-// largest stay.  A radix select over the 32-bit keys (11 bits a pass from the top; it ends as soon as a
+// A cluster of `ctas` CTAs per sequence, an even share of the rows each.  Rows [0, lo) and [hi, live) are
+// protected; of the candidates [lo, hi) the `want` largest stay.  A radix select over the 32-bit keys (11 bits a pass from the top; it ends as soon as a
 // whole bin stays) finds the want-th largest.  Where several candidates share its key and not all of them
 // stay, they are told apart by their accumulators, the same way, and equal accumulators by their row.  Then
 // each warp counts the rows that stay in its share of the rows and, knowing the earlier warps' counts,
