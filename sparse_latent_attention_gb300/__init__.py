@@ -226,9 +226,9 @@ def hc_split_sinkhorn(mixes, hc_scale, hc_base, hc=4, sinkhorn_iters=20, eps=1e-
                          f"hc_base [{mix}]")
     lead = tuple(mixes.shape[:-1])
     n = mixes.numel() // mix
-    pre = torch.empty(lead + (hc,), dtype=torch.float32, device=mixes.device)
-    post = torch.empty_like(pre)
-    comb = torch.empty(lead + (hc, hc), dtype=torch.float32, device=mixes.device)
+    pre, post, comb = (_new(stream, lambda: torch.empty(lead + tail, dtype=torch.float32,
+                                                        device=mixes.device))
+                       for tail in ((hc,), (hc,), (hc, hc)))
     st = load().sa_hc_split_sinkhorn(_ptr(mixes), n, hc, _ptr(hc_scale), _ptr(hc_base),
                                      int(sinkhorn_iters), float(eps), _ptr(pre), _ptr(post),
                                      _ptr(comb), _stream(stream))
@@ -244,7 +244,7 @@ def candidate_blocks(logits, start_pos, ratio, topk_blocks, block_size, *, out=N
     fmt = _score_format(logits, "logits")
     b, s, n = logits.shape
     if out is None:
-        out = torch.empty((b, s, n), dtype=torch.bool, device=logits.device)
+        out = _new(stream, lambda: torch.empty((b, s, n), dtype=torch.bool, device=logits.device))
     elif out.dtype != torch.bool or tuple(out.shape) != (b, s, n) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bool tensor of shape {(b, s, n)}")
     st = load().sa_candidate_blocks(_ptr(logits), fmt, b, s, n, int(start_pos), int(ratio),
@@ -268,7 +268,7 @@ def indexer_topk(score, start_pos, ratio, index_topk, offset, *, candidates=None
         raise ValueError(f"candidates must be a contiguous bool tensor of shape {(b, s, n)}")
     k = min(int(index_topk), n)
     if out is None:
-        out = torch.empty((b, s, k), dtype=torch.int32, device=score.device)
+        out = _new(stream, lambda: torch.empty((b, s, k), dtype=torch.int32, device=score.device))
     if out.dtype != torch.int32 or not out.is_cuda or tuple(out.shape) != (b, s, k) or (
             k > 0 and out.stride(2) != 1):
         raise ValueError(f"out must be a CUDA int32 tensor of shape {(b, s, k)} with unit column "
@@ -287,7 +287,7 @@ def window_idxs(start_pos, seqlen, window, *, out=None, nbatch=1, stream=None, d
     """Window index table [nbatch, seqlen, window] (int32), written into ``out`` when given
     (``out`` may be a column slice of a wider idx tensor: its row and batch strides are used)."""
     if out is None:
-        out = torch.empty((nbatch, seqlen, window), dtype=torch.int32, device=device)
+        out = _new(stream, lambda: torch.empty((nbatch, seqlen, window), dtype=torch.int32, device=device))
     if out.dtype != torch.int32 or not out.is_cuda:
         raise TypeError("out must be a CUDA int32 tensor")
     if out.dim() == 2:
