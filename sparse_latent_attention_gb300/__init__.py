@@ -49,17 +49,18 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
-    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+def _status(dev, name, stream, *args) -> int:
+    """A library call's sa_status, on the device (its index) that the tensors are on: with that device
+    current, on ``stream`` or the device's current stream."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _status(dev, name, stream, *args)
+    return getattr(load(), name)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
 
 
 def _call(name, dev, stream, *args):
-    """A library call on the device (its index) that the tensors are on: with that device current, on
-    ``stream`` or the device's current stream."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(name, dev, stream, *args)
-    st = getattr(load(), name)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    """The same, an error raised."""
+    st = _status(dev, name, stream, *args)
     if st:
         _lib.check(st, name)
 
@@ -180,25 +181,15 @@ def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, wor
               _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk, _ptr(out), _ptr(lse),
               _ptr(workspace), workspace.numel(), *turn)
         return out
+    call = (_ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink), _ptr(idx), float(softmax_scale), b, s, h, d,
+            rows, topk, _ptr(out), _ptr(workspace), workspace.numel())
     if rope is not None:
-        st = load().sa_sparse_attn_rope(_ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
-                                        _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk,
-                                        _ptr(out), _ptr(workspace), workspace.numel(), _ptr(rot),
-                                        rot.shape[0], 2 * rot.shape[1], int(start_pos),
-                                        _stream(stream))
-        _lib.check(st, "sa_sparse_attn_rope")
-        return out
-    if family is not None:
-        st = load().sa_sparse_attn_family(_ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),
-                                          _ptr(idx), float(softmax_scale), b, s, h, d, rows, topk,
-                                          _ptr(out), _ptr(workspace), workspace.numel(),
-                                          FAMILIES[family], _stream(stream))
-        _lib.check(st, "sa_sparse_attn_family")
-        return out
-    st = load().sa_sparse_attn(_ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink), _ptr(idx),
-                               float(softmax_scale), b, s, h, d, rows, topk, _ptr(out),
-                               _ptr(workspace), workspace.numel(), _stream(stream))
-    _lib.check(st, "sa_sparse_attn")
+        _call("sa_sparse_attn_rope", dev.index, stream, *call, _ptr(rot), rot.shape[0], 2 * rot.shape[1],
+              int(start_pos))
+    elif family is not None:
+        _call("sa_sparse_attn_family", dev.index, stream, *call, FAMILIES[family])
+    else:
+        _call("sa_sparse_attn", dev.index, stream, *call)
     return out
 
 
@@ -229,10 +220,8 @@ def hc_split_sinkhorn(mixes, hc_scale, hc_base, hc=4, sinkhorn_iters=20, eps=1e-
     pre, post, comb = (_new(stream, lambda: torch.empty(lead + tail, dtype=torch.float32,
                                                         device=mixes.device))
                        for tail in ((hc,), (hc,), (hc, hc)))
-    st = load().sa_hc_split_sinkhorn(_ptr(mixes), n, hc, _ptr(hc_scale), _ptr(hc_base),
-                                     int(sinkhorn_iters), float(eps), _ptr(pre), _ptr(post),
-                                     _ptr(comb), _stream(stream))
-    _lib.check(st, "sa_hc_split_sinkhorn")
+    _call("sa_hc_split_sinkhorn", mixes.get_device(), stream, _ptr(mixes), n, hc, _ptr(hc_scale),
+          _ptr(hc_base), int(sinkhorn_iters), float(eps), _ptr(pre), _ptr(post), _ptr(comb))
     return pre, post, comb
 
 
@@ -247,10 +236,8 @@ def candidate_blocks(logits, start_pos, ratio, topk_blocks, block_size, *, out=N
         out = _new(stream, lambda: torch.empty((b, s, n), dtype=torch.bool, device=logits.device))
     elif out.dtype != torch.bool or tuple(out.shape) != (b, s, n) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bool tensor of shape {(b, s, n)}")
-    st = load().sa_candidate_blocks(_ptr(logits), fmt, b, s, n, int(start_pos), int(ratio),
-                                    int(topk_blocks), int(block_size), _ptr(out),
-                                    _stream(stream))
-    _lib.check(st, "sa_candidate_blocks")
+    _call("sa_candidate_blocks", logits.get_device(), stream, _ptr(logits), fmt, b, s, n, int(start_pos),
+          int(ratio), int(topk_blocks), int(block_size), _ptr(out))
     return out
 
 
@@ -275,11 +262,8 @@ def indexer_topk(score, start_pos, ratio, index_topk, offset, *, candidates=None
                          "stride")
     ld = out.stride(1) if s > 1 else max(k, out.stride(1))
     bstride = out.stride(0) if b > 1 else s * ld
-    st = load().sa_indexer_topk(_ptr(score), fmt, _ptr(candidates), b, s, n, int(start_pos),
-                                int(ratio),
-                                int(index_topk), int(offset), _ptr(out), ld, bstride,
-                                _stream(stream))
-    _lib.check(st, "sa_indexer_topk")
+    _call("sa_indexer_topk", score.get_device(), stream, _ptr(score), fmt, _ptr(candidates), b, s, n,
+          int(start_pos), int(ratio), int(index_topk), int(offset), _ptr(out), ld, bstride)
     return out
 
 
@@ -299,9 +283,8 @@ def window_idxs(start_pos, seqlen, window, *, out=None, nbatch=1, stream=None, d
                          f"{window}) with unit column stride")
     ld = out3.stride(1) if seqlen > 1 else max(window, out3.stride(1))
     bstride = out3.stride(0) if nbatch > 1 else seqlen * ld
-    st = load().sa_window_idxs(start_pos, seqlen, window, _ptr(out3), ld, nbatch, bstride,
-                               _stream(stream))
-    _lib.check(st, "sa_window_idxs")
+    _call("sa_window_idxs", out.get_device(), stream, start_pos, seqlen, window, _ptr(out3), ld, nbatch,
+          bstride)
     return out
 
 
@@ -326,9 +309,8 @@ def act_quant_fp8(x, *, out_rt=None, codes=None, scales=None, stream=None):
     rt, rts = rows_of(out_rt, "out_rt", torch.bfloat16, d)
     cd, cds = rows_of(codes, "codes", torch.uint8, d)
     sc, scs = rows_of(scales, "scales", torch.uint8, d // 32)
-    st = load().sa_act_quant_fp8(_ptr(x), n, d, x.stride(0), _ptr(rt), rts, _ptr(cd), cds,
-                                 _ptr(sc), scs, _stream(stream))
-    _lib.check(st, "sa_act_quant_fp8")
+    _call("sa_act_quant_fp8", x.get_device(), stream, _ptr(x), n, d, x.stride(0), _ptr(rt), rts, _ptr(cd),
+          cds, _ptr(sc), scs)
 
 
 def window_write(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=None):
@@ -366,10 +348,8 @@ def window_write(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=
     sc, scs, scb = ring_of(scales, "scales", torch.uint8, d // 32)
     if window is None:
         raise ValueError("give at least one of ring_rt, codes, scales")
-    st = load().sa_window_write(_ptr(x), nb, sl, d, x.stride(1) if sl > 1 else d, int(start_pos),
-                                window, _ptr(rt), rts, rtb, _ptr(cd), cds, cdb, _ptr(sc), scs, scb,
-                                _stream(stream))
-    _lib.check(st, "sa_window_write")
+    _call("sa_window_write", x.get_device(), stream, _ptr(x), nb, sl, d, x.stride(1) if sl > 1 else d,
+          int(start_pos), window, _ptr(rt), rts, rtb, _ptr(cd), cds, cdb, _ptr(sc), scs, scb)
 
 
 def act_quant_fp4(x, *, out_rt=None, codes=None, scales=None, stream=None):
@@ -594,4 +574,6 @@ def remap_idx(idx, remap, *, out=None, stream=None) -> torch.Tensor:
 
 def read_status(workspace, clear=False, stream=None) -> int:
     """The workspace status word as an sa_status (synchronises the stream)."""
-    return int(load().sa_read_status(_ptr(workspace), int(bool(clear)), _stream(stream)))
+    if not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    return _status(workspace.get_device(), "sa_read_status", stream, _ptr(workspace), int(bool(clear)))

@@ -82,3 +82,47 @@ def test_outputs_come_from_the_given_stream(calls, name):
     MAKE_OUTPUTS[name](st)
     assert [c[2] for c in calls["calls"]] == [77]
     assert calls["new"] and all(s is st for s in calls["new"])
+
+
+def _attn(**more):
+    return sa.sparse_attn(on_device(1, 2, 4, 64, dtype=bf16), on_device(1, 8, 64, dtype=bf16), on_device(4),
+                          on_device(1, 2, 4, dtype=i32), 0.1, **more)
+
+
+ROT = (on_device(16, 8, 2), 3)
+CALLS = {
+    "sa_sparse_attn": lambda: _attn(),
+    "sa_sparse_attn_family": lambda: _attn(family="mma"),
+    "sa_sparse_attn_rope": lambda: _attn(rope=ROT),
+    "sa_sparse_attn_lse": lambda: _attn(lse=on_device(1, 2, 4)),
+    "sa_hc_split_sinkhorn": lambda: MAKE_OUTPUTS["hc_split_sinkhorn"](None),
+    "sa_candidate_blocks": lambda: MAKE_OUTPUTS["candidate_blocks"](None),
+    "sa_indexer_topk": lambda: MAKE_OUTPUTS["indexer_topk"](None),
+    "sa_window_idxs": lambda: sa.window_idxs(0, 8, 4, out=on_device(8, 4, dtype=i32)),
+    "sa_act_quant_fp8": lambda: sa.act_quant_fp8(on_device(2, 64, dtype=bf16), codes=on_device(2, 64, dtype=u8)),
+    "sa_window_write": lambda: sa.window_write(on_device(1, 2, 64, dtype=bf16), 0,
+                                               codes=on_device(1, 8, 64, dtype=u8)),
+    "sa_act_quant_fp4": lambda: sa.act_quant_fp4(on_device(2, 64, dtype=bf16), codes=on_device(2, 32, dtype=u8)),
+    "sa_window_write_fp4": lambda: sa.window_write_fp4(on_device(1, 2, 64, dtype=bf16), 0,
+                                                       codes=on_device(1, 8, 32, dtype=u8)),
+    "sa_row_weights": lambda: sa.row_weights(
+        on_device(1, 2, 4, 64, dtype=bf16), on_device(1, 8, 64, dtype=bf16), on_device(1, 2, 4),
+        on_device(1, 2, 4, dtype=i32), 0.1, on_device(1, 8, dtype=torch.int64)),
+    "sa_evict_select": lambda: sa.evict_select(on_device(1, 8, dtype=torch.int64), 4),
+    "sa_compact_rows": lambda: sa.compact_rows([on_device(1, 8)], on_device(1, 4, dtype=i32)),
+    "sa_remap_idx": lambda: sa.remap_idx(on_device(1, 4, dtype=i32), on_device(1, 8, dtype=i32)),
+    "sa_read_status": lambda: sa.read_status(on_device(256, dtype=u8)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_run_on_their_tensors_device(calls, name):
+    """With another device current: that of the tensors is current for the call, on its own stream."""
+    CALLS[name]()
+    assert [c for c in calls["calls"] if c[0] != "sa_sparse_attn_workspace_size"] == [(name, DEV, 1000 + DEV)]
+    assert torch.cuda.current_device() == 0
+
+
+def test_status_of_a_host_tensor_is_refused():
+    with pytest.raises(TypeError):
+        sa.read_status(torch.zeros(256, dtype=u8))
