@@ -88,6 +88,12 @@ def _need(t, name, dtype, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _on(t, name, like):
+    """t (or None) is on like's device."""
+    if t is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
 def workspace_size(b, s, h, d, rows, topk, kv_format=SA_KV_BF16) -> int:
     n = int(load().sa_sparse_attn_workspace_size(b, s, h, d, rows, topk, kv_format))
     if n == 0:
@@ -236,6 +242,7 @@ def candidate_blocks(logits, start_pos, ratio, topk_blocks, block_size, *, out=N
         out = _new(stream, lambda: torch.empty((b, s, n), dtype=torch.bool, device=logits.device))
     elif out.dtype != torch.bool or tuple(out.shape) != (b, s, n) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bool tensor of shape {(b, s, n)}")
+    _on(out, "out", logits)
     _call("sa_candidate_blocks", logits.get_device(), stream, _ptr(logits), fmt, b, s, n, int(start_pos),
           int(ratio), int(topk_blocks), int(block_size), _ptr(out))
     return out
@@ -253,6 +260,7 @@ def indexer_topk(score, start_pos, ratio, index_topk, offset, *, candidates=None
     if candidates is not None and (candidates.dtype != torch.bool or tuple(candidates.shape) !=
                                    (b, s, n) or not candidates.is_contiguous()):
         raise ValueError(f"candidates must be a contiguous bool tensor of shape {(b, s, n)}")
+    _on(candidates, "candidates", score)
     k = min(int(index_topk), n)
     if out is None:
         out = _new(stream, lambda: torch.empty((b, s, k), dtype=torch.int32, device=score.device))
@@ -260,6 +268,7 @@ def indexer_topk(score, start_pos, ratio, index_topk, offset, *, candidates=None
             k > 0 and out.stride(2) != 1):
         raise ValueError(f"out must be a CUDA int32 tensor of shape {(b, s, k)} with unit column "
                          "stride")
+    _on(out, "out", score)
     ld = out.stride(1) if s > 1 else max(k, out.stride(1))
     bstride = out.stride(0) if b > 1 else s * ld
     _call("sa_indexer_topk", score.get_device(), stream, _ptr(score), fmt, _ptr(candidates), b, s, n,
@@ -304,6 +313,7 @@ def act_quant_fp8(x, *, out_rt=None, codes=None, scales=None, stream=None):
         if t.dim() != 2 or t.dtype != dtype or t.stride(1) != 1 or tuple(t.shape) != (n, width):
             raise ValueError(f"{name} must be a 2-D {dtype} tensor of shape ({n}, {width}) with "
                              "unit column stride")
+        _on(t, name, x)
         return t, t.stride(0)
 
     rt, rts = rows_of(out_rt, "out_rt", torch.bfloat16, d)
@@ -341,6 +351,7 @@ def window_write(x, start_pos, *, ring_rt=None, codes=None, scales=None, stream=
             window = t.shape[1]
         elif t.shape[1] != window:
             raise ValueError("the rings must have the same window")
+        _on(t, name, x)
         return t, t.stride(1), t.stride(0)
 
     rt, rts, rtb = ring_of(ring_rt, "ring_rt", torch.bfloat16, d)

@@ -126,3 +126,31 @@ def test_calls_run_on_their_tensors_device(calls, name):
 def test_status_of_a_host_tensor_is_refused():
     with pytest.raises(TypeError):
         sa.read_status(torch.zeros(256, dtype=u8))
+
+
+ELSEWHERE = {
+    "candidate_blocks out": lambda: sa.candidate_blocks(on_device(1, 8, 2), 0, 4, 1, 1,
+                                                        out=torch.zeros(1, 8, 2, dtype=torch.bool)),
+    "indexer_topk candidates": lambda: sa.indexer_topk(on_device(1, 8, 2), 0, 4, 2, 0,
+                                                       candidates=torch.zeros(1, 8, 2, dtype=torch.bool)),
+    "act_quant_fp8 out_rt": lambda: sa.act_quant_fp8(on_device(2, 64, dtype=bf16),
+                                                     out_rt=torch.zeros(2, 64, dtype=bf16)),
+    "act_quant_fp8 codes": lambda: sa.act_quant_fp8(on_device(2, 64, dtype=bf16),
+                                                    codes=torch.zeros(2, 64, dtype=u8)),
+    "act_quant_fp8 scales": lambda: sa.act_quant_fp8(on_device(2, 64, dtype=bf16),
+                                                     scales=torch.zeros(2, 2, dtype=u8)),
+    "window_write ring_rt": lambda: sa.window_write(on_device(1, 2, 64, dtype=bf16), 0,
+                                                    ring_rt=torch.zeros(1, 8, 64, dtype=bf16)),
+    "window_write codes": lambda: sa.window_write(on_device(1, 2, 64, dtype=bf16), 0,
+                                                  codes=torch.zeros(1, 8, 64, dtype=u8)),
+    "window_write scales": lambda: sa.window_write(on_device(1, 2, 64, dtype=bf16), 0,
+                                                   scales=torch.zeros(1, 8, 2, dtype=u8)),
+}
+
+
+@pytest.mark.parametrize("name", ELSEWHERE)
+def test_tensors_elsewhere_are_refused(calls, name):
+    """A tensor that is not on the call's device, a host tensor here: its address never reaches a kernel."""
+    with pytest.raises(ValueError):
+        ELSEWHERE[name]()
+    assert not calls["calls"]
