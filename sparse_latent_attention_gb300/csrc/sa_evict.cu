@@ -287,10 +287,19 @@ cudaError_t select_launch(const int64_t* acc, const int32_t* live, int64_t b, in
                           cudaStream_t stream) {
     auto kernel = evict_select_kernel<kThreads, kCached>;
     const size_t smem = kCached ? (size_t)share * sizeof(uint32_t) : 0;
-    if (smem > 32 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the limit belongs to the kernel and not to a launch: set to a launch's own size, another host
+    // thread's smaller one would lower it before this launch)
+    if constexpr (kCached && kThreads == 1024) {
+        static bool configured[64] = {};  // per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        if (dev >= 64 || !configured[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kCachedRows * (int)sizeof(uint32_t));
+            if (e != cudaSuccess) return e;
+            if (dev < 64) configured[dev] = true;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(b * ctas));
