@@ -229,6 +229,28 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
     return a0 < b0 + bn && b0 < a0 + an;
 }
 
+// The limit of a kernel's dynamic shared memory belongs to the kernel and not to a launch: set to a launch's
+// own size, another host thread's smaller one would lower it before this launch.  So it is set once, to the
+// largest.
+template <class K, int kThreads, class... Args>
+cudaError_t launch_one(int keys, int64_t rows, cudaStream_t stream, Args... args) {
+    const size_t smem = (size_t)keys * sizeof(uint32_t);
+    if (smem > 48 * 1024) {
+        static bool configured[64] = {};  // per kernel and device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= 64 || !configured[dev]) {
+            e = cudaFuncSetAttribute(K::fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     SA_INDEXER_MAX_POSITIONS * (int)sizeof(uint32_t));
+            if (e != cudaSuccess) return e;
+            if (dev < 64) configured[dev] = true;
+        }
+    }
+    K::fn<<<(unsigned)rows, kThreads, smem, stream>>>(args...);
+    return cudaGetLastError();
+}
+
 // Launch a per-row kernel with `keys` 32-bit keys of shared memory per row: 128 threads for up
 // to 4096 keys (many rows per SM), 1024 beyond (a long row's passes and rounds are its latency:
 // 1024 threads took the 64 x 8192 decode selection from 24.6 to 18.4 us, where 512 ran before;
@@ -239,18 +261,8 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
 // 12.3 / 30.7 us).
 template <template <int, bool> class K, bool kBf16, class... Args>
 cudaError_t launch_rows_n(int keys, int span, int64_t rows, cudaStream_t stream, Args... args) {
-    const size_t smem = (size_t)keys * sizeof(uint32_t);
-    auto go = [&](auto kernel, int threads) -> cudaError_t {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(
-                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
-        kernel<<<(unsigned)rows, threads, smem, stream>>>(args...);
-        return cudaGetLastError();
-    };
-    if (span <= 4096) return go(K<128, kBf16>::fn, 128);
-    return go(K<1024, kBf16>::fn, 1024);
+    if (span <= 4096) return launch_one<K<128, kBf16>, 128>(keys, rows, stream, args...);
+    return launch_one<K<1024, kBf16>, 1024>(keys, rows, stream, args...);
 }
 
 template <template <int, bool> class K, bool kBf16, class... Args>

@@ -52,3 +52,12 @@ def test_evict_select_of_two_sizes_at_once(dev):  # noqa: F811
     small = torch.randint(0, 1 << 40, (1, 8320), device=dev, generator=g)
     large = torch.randint(0, 1 << 40, (160, 40000), device=dev, generator=g)
     assert not at_once([lambda: sa.evict_select(small, 4000)[0], lambda: sa.evict_select(large, 20000)[0]])
+
+
+def test_indexer_topk_of_two_sizes_at_once(dev):  # noqa: F811
+    """Rows that take 52 KB of shared memory, and rows that take 192 KB."""
+    g = torch.Generator(device=dev).manual_seed(2)
+    small = torch.randn(4, 1, 13000, device=dev, generator=g)
+    large = torch.randn(4, 1, 49152, device=dev, generator=g)
+    assert not at_once([lambda: sa.indexer_topk(small, 4 * 13000 - 1, 4, 512, 0),
+                        lambda: sa.indexer_topk(large, 4 * 49152 - 1, 4, 512, 0)])
