@@ -41,7 +41,10 @@ struct SelectSmem {
 };
 
 // The CTAs of a cluster share a sequence: a barrier of all of them, and a word of another one's shared memory.
+// (the aligned form wants each warp converged, which the branches and loops of uneven length in front of it
+// do not promise)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t load_remote(const uint32_t* here, uint32_t rank) {
