@@ -521,16 +521,16 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
 
     def of(t, what, shape, stride, size):
         """The bytes of a row of t, whose rows are contiguous."""
-        if not shape[1] or not b:
-            return size
-        if t.is_contiguous():
+        if t.is_contiguous() and shape[1] and b:
             return size * (t.numel() // (b * shape[1]))
-        elements = 1
-        for extent, step in zip(reversed(shape[1:]), reversed(stride[1:])):
-            if extent > 1 and step != elements:
-                raise ValueError(f"{what} must have contiguous rows")
+        elements, apart = 1, False
+        for extent, step in zip(reversed(shape[2:]), reversed(stride[2:])):
+            apart |= extent > 1 and step != elements
             elements *= extent
-        return size * (elements // shape[1])
+        apart |= shape[1] > 1 and stride[1] != elements
+        if apart and t.numel():
+            raise ValueError(f"{what} must have contiguous rows")
+        return size * elements
 
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor) or t.get_device() != dev:
