@@ -59,8 +59,8 @@ inline int64_t kv_row_bytes(int f, int d) {
 // The logarithm of a softmax denominator l 2^m + e^sink (m in log2 units; l = 0: no row, the sink
 // alone), relative to the larger of the two terms so that neither overflows.
 __device__ __forceinline__ float log_sum_exp(float l, float m, float sink) {
-    if (l == 0.f) return sink;  // (a NaN stays one)
     const float s2 = sink * 1.4426950408889634f, top = fmaxf(m, s2);
+    if (l == 0.f || (s2 == INFINITY && l > 0.f)) return sink;  // (a NaN l stays one)
     return (top + log2f(fmaf(l, exp2f(m - top), exp2f(s2 - top)))) * 0.6931471805599453f;
 }
 
