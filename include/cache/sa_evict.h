@@ -56,6 +56,8 @@ sa_status sa_sparse_attn_lse(const void* q, const void* kv, const uint8_t* kv_sc
  *   q, kv, kv_scale, kv_format, idx, softmax_scale, b, s, h, d, rows, topk   as sa_sparse_attn.  An idx
  *               entry outside [-1, rows) is treated as -1 and sets SA_ERR_INDEX in the workspace's
  *               status word.
+ *   kv_scale    aligned to 16 bytes at d = 512, to 4 where d is another multiple of 128, else to 2 (what a
+ *               sequence of a packed [b][rows][d/32] has)
  *   lse         f32 [b][s][h], e.g. from sa_sparse_attn_lse
  *   acc         int64 [b][rows], 8-byte aligned, added to; must not overlap an input
  *   workspace   at least SA_STATUS_BYTES, 256-byte aligned: the status word, as for sa_sparse_attn (one

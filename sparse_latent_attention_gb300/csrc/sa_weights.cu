@@ -669,7 +669,10 @@ extern "C" sa_status sa_row_weights(const void* q, const void* kv, const uint8_t
     if (b * s == 0 || topk == 0) return SA_OK;
     if (!q || !lse || !idx || (rows > 0 && (!kv || !acc))) return SA_ERR_INVALID_ARG;
     if (kv_format != SA_KV_BF16 && rows > 0 && !kv_scale) return SA_ERR_INVALID_ARG;
-    if (!is_aligned(q, 16) || !is_aligned(kv, 16) || !is_aligned(kv_scale, 16) || !is_aligned(lse, 4) ||
+    // the kernel reads a row's scales in words (halfwords where a row is an odd number of them); at d = 512,
+    // as sparse_attn does
+    const uintptr_t scale_align = d == 512 ? 16 : d % 128 == 0 ? 4 : 2;
+    if (!is_aligned(q, 16) || !is_aligned(kv, 16) || !is_aligned(kv_scale, scale_align) || !is_aligned(lse, 4) ||
         !is_aligned(idx, 4) || !is_aligned(acc, 8))
         return SA_ERR_INVALID_ARG;
     const size_t n_tok = (size_t)(b * s), acc_bytes = (size_t)(b * rows) * 8;
