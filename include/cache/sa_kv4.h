@@ -36,7 +36,9 @@ extern "C" {
  * saturate.  A NaN counts as 0 (the format has none).
  * Outputs passed as NULL are skipped (at least one must be given).  Requires d % 32 == 0, d >= 32,
  * strides >= the row's length (codes d / 2 bytes, scales d / 32 bytes).  No output may overlap another,
- * or x (apart from x_rt == x with the same stride).
+ * or x (apart from x_rt == x with the same stride).  Rows equally many bytes apart may lie between one
+ * another's (a row's codes and its scales side by side); of others the spans from the first row to the last
+ * count.
  */
 sa_status sa_act_quant_fp4(const void* x, int64_t n, int d, int64_t x_stride,
                            void* x_rt, int64_t rt_stride,

@@ -227,6 +227,17 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
     return a0 < b0 + (uintptr_t)bn && b0 < a0 + (uintptr_t)an;
 }
 
+// Whether n rows of aw bytes, as bytes apart, share a byte with n rows of bw bytes, bs apart.  Rows equally far
+// apart may lie between one another (codes and scales of a row side by side); of others the whole spans count.
+bool rows_overlap(const void* a, int64_t as, int64_t aw, const void* b, int64_t bs, int64_t bw, int64_t n) {
+    if (!overlap(a, (n - 1) * as + aw, b, (n - 1) * bs + bw)) return false;
+    if (as != bs || n < 2) return true;
+    // b's place behind the row of a that it follows, modulo the distance
+    const uintptr_t s = (uintptr_t)as, a0 = reinterpret_cast<uintptr_t>(a) % s, b0 = reinterpret_cast<uintptr_t>(b) % s;
+    const uintptr_t at = (b0 + s - a0) % s;
+    return at < (uintptr_t)aw || at + (uintptr_t)bw > s;
+}
+
 template <bool kRing>
 sa_status launch(const Quant4& p, void* stream) {
     if (p.n * (int64_t)p.d == 0) return SA_OK;
@@ -269,12 +280,13 @@ extern "C" sa_status sa_act_quant_fp4(const void* x, int64_t n, int d, int64_t x
     if (x_rt && (!is_aligned(x_rt, 2) || rt_stride < d)) return SA_ERR_INVALID_ARG;
     if (codes && codes_stride < d / 2) return SA_ERR_INVALID_ARG;
     if (scales && scales_stride < d / 32) return SA_ERR_INVALID_ARG;
-    const int64_t xb = ((n - 1) * x_stride + d) * 2, rb = ((n - 1) * rt_stride + d) * 2;
-    const int64_t cb = (n - 1) * codes_stride + d / 2, sb = (n - 1) * scales_stride + d / 32;
     if (x_rt == x && rt_stride != x_stride) return SA_ERR_INVALID_ARG;
-    if (x_rt && x_rt != x && overlap(x_rt, rb, x, xb)) return SA_ERR_INVALID_ARG;
-    if (overlap(codes, cb, x, xb) || overlap(scales, sb, x, xb) || overlap(codes, cb, x_rt, rb) ||
-        overlap(scales, sb, x_rt, rb) || overlap(codes, cb, scales, sb))
+    const int64_t xs = 2 * x_stride, xw = 2 * (int64_t)d, rs = 2 * rt_stride, cw = d / 2, sw = d / 32;
+    if (x_rt != x && rows_overlap(x_rt, rs, xw, x, xs, xw, n)) return SA_ERR_INVALID_ARG;
+    if (rows_overlap(codes, codes_stride, cw, x, xs, xw, n) || rows_overlap(scales, scales_stride, sw, x, xs, xw, n) ||
+        rows_overlap(codes, codes_stride, cw, x_rt, rs, xw, n) ||
+        rows_overlap(scales, scales_stride, sw, x_rt, rs, xw, n) ||
+        rows_overlap(codes, codes_stride, cw, scales, scales_stride, sw, n))
         return SA_ERR_INVALID_ARG;
     Quant4 p = {};
     p.x = reinterpret_cast<const __nv_bfloat16*>(x);
