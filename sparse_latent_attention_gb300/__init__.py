@@ -42,7 +42,7 @@ WEIGHT_UNIT = 2.0 ** -32
 
 # What a call costs on the host is mostly attribute reads and argument objects, so pointers and streams go
 # to ctypes as integers (its argument types are declared) and a tensor's properties are read once.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (a PyTorch without CUDA has none)
 
 
 def _ptr(t) -> int | None:

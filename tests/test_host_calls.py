@@ -4,6 +4,9 @@ are stand-ins, and the tensors are host tensors that say they are on a device.""
 from __future__ import annotations
 
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -154,3 +157,11 @@ def test_tensors_elsewhere_are_refused(calls, name):
     with pytest.raises(ValueError):
         ELSEWHERE[name]()
     assert not calls["calls"]
+
+
+def test_imports_with_a_pytorch_without_cuda():
+    code = ("import torch\ndel torch._C._cuda_getCurrentRawStream\n"
+            "import sparse_latent_attention_gb300 as sa\nassert sa.workspace_size and sa.WEIGHT_UNIT")
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0, done.stderr
