@@ -180,7 +180,7 @@ def sparse_attn(q, kv, sink, idx, softmax_scale, *, kv_scale=None, out=None, wor
             raise ValueError(f"lse shape {tuple(lse.shape)} != {(b, s, h)}")
         if family not in (None, "auto"):
             raise ValueError("lse comes from the family that the call is routed to")
-        if rope is not None and rot.numel() == 0:
+        if rope is not None and rot.numel() == 0 and q.numel():  # (its address would say: no rotation)
             raise ValueError("rot is empty")
         turn = (_ptr(rot), rot.shape[0], 2 * rot.shape[1], int(start_pos)) if rope else (None, 0, 0, 0)
         _call("sa_sparse_attn_lse", dev.index, stream, _ptr(q), _ptr(kv), _ptr(kv_scale), fmt, _ptr(sink),

@@ -165,3 +165,15 @@ def test_imports_with_a_pytorch_without_cuda():
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                           cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert done.returncode == 0, done.stderr
+
+
+def test_an_empty_rotation_table(calls):
+    """None of the positions: fine where there are no tokens, refused where there are some."""
+    rope = (on_device(0, 8, 2), 0)
+    for lse in (None, on_device(1, 0, 4)):
+        o = sa.sparse_attn(on_device(1, 0, 4, 512, dtype=bf16), on_device(1, 8, 512, dtype=bf16), on_device(4),
+                           on_device(1, 0, 4, dtype=i32), 0.1, rope=rope, lse=lse,
+                           out=on_device(1, 0, 4, 512, dtype=bf16))
+        assert o.shape == (1, 0, 4, 512)
+    with pytest.raises(ValueError):
+        _attn(rope=rope, lse=on_device(1, 2, 4))
