@@ -96,7 +96,8 @@ sa_status sa_evict_select(const int64_t* acc, const int32_t* live, int64_t b, in
  *
  * For tensor t, sequence bi and j < n_keep, with r = kept[bi][j]: row j of the destination becomes row r
  * of the source, or zero bytes when r is -1 (or outside [0, rows)).  Rows n_keep and up of a destination
- * are left as they are.
+ * are left as they are: a program that appends to a cache it has compacted in place zeroes their
+ * accumulators first, or a new row starts with the weight of the one that was there.
  *   src, dst    arrays of n_tensors device pointers (the arrays are host memory)
  *   row_bytes   bytes of a row of each tensor, below 2^25; rows of a sequence are packed
  *   src_batch_bytes, dst_batch_bytes   distance between sequences of each tensor, in bytes
@@ -113,6 +114,7 @@ sa_status sa_compact_rows(int n_tensors, const void* const* src, void* const* ds
 /*
  * Renumbers a table of row numbers after an eviction:
  *   out[bi][i] = remap[bi][idx[bi][i]], -1 where idx[bi][i] is -1 (or outside [0, rows)).
+ * Any table of row numbers follows an eviction this way, an earlier eviction's remap too (the two in one).
  * idx and out are int32 [b][n] (out may equal idx), remap int32 [b][rows].
  */
 sa_status sa_remap_idx(const int32_t* idx, int64_t b, int64_t n, const int32_t* remap, int64_t rows,

@@ -503,8 +503,10 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
 
     ``out``: None (new tensors [b, n_keep, ...]), or a list of tensors [b, n_keep or more, ...]
     whose first n_keep rows are written; a tensor may be its own out (in place; kept then has to
-    ascend, as evict_select's does).  Rows of a sequence are contiguous; sequences may be apart
-    (a cache's leading rows).  Returns the list of results."""
+    ascend, as evict_select's does).  What lies behind them stays: before rows are appended there
+    again, their accumulators have to be zeroed (acc[:, n_keep:] = 0), or a new row starts with the
+    weight of the one that was there.  Rows of a sequence are contiguous; sequences may be apart (a
+    cache's leading rows).  Returns the list of results."""
     tensors = list(tensors)
     _need(kept, "kept", torch.int32)
     if kept.dim() != 2:
@@ -566,7 +568,8 @@ def compact_rows(tensors, kept, *, out=None, stream=None):
 
 def remap_idx(idx, remap, *, out=None, stream=None) -> torch.Tensor:
     """A table of row numbers after an eviction: out[bi, ...] = remap[bi, idx[bi, ...]], -1 where
-    idx is -1.  idx int32 [b, ...], remap int32 [b, rows]; out may be idx itself."""
+    idx is -1.  idx int32 [b, ...], remap int32 [b, rows]; out may be idx itself.  (An earlier
+    eviction's remap is such a table too: remap_idx(earlier, remap) is the two in one.)"""
     _need(idx, "idx", torch.int32)
     _need(remap, "remap", torch.int32, idx.device)
     if remap.dim() != 2 or idx.dim() < 1 or idx.shape[0] != remap.shape[0]:
