@@ -515,16 +515,20 @@ def time_device_steps(torch, path, flush, steps, warmup):
         path.step()
     torch.cuda.synchronize()
     ev = [tuple(torch.cuda.Event(enable_timing=True) for _ in range(4)) for _ in range(steps)]
-    # (a collection of the interpreter's, some 0.9 ms, outlasts the spin when it meets the first step)
-    gc.collect()
+    # (a collection of the interpreter's, some 0.9 ms, outlasts the spin when it meets a step; one made here, just
+    # before the steps, would leave the host's caches cold: a decode's first step then read 95 to 140 us and not 52)
+    enabled = gc.isenabled()
     gc.disable()
-    for e in ev:
-        flush.zero_()
-        torch.cuda._sleep(HEAD_START_CYCLES)  # not timed: lets the host queue the step first
-        e[0].record()
-        path.step(ev=(e[2], e[3]))
-        e[1].record()
-    gc.enable()
+    try:
+        for e in ev:
+            flush.zero_()
+            torch.cuda._sleep(HEAD_START_CYCLES)  # not timed: lets the host queue the step first
+            e[0].record()
+            path.step(ev=(e[2], e[3]))
+            e[1].record()
+    finally:
+        if enabled:
+            gc.enable()
     torch.cuda.synchronize()
     return ([a.elapsed_time(b) for a, b, _, _ in ev], [c.elapsed_time(d) for _, _, c, d in ev])
 
