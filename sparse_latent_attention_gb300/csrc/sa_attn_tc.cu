@@ -36,8 +36,9 @@
 //   warps 15-18 (e2m1 rows only) gather helpers: half of the rows of gather warps 2-5.  A 4-bit row is small
 //               enough to wait in registers: its 256 bytes are loaded while the buffer is still in use
 //               and widened straight into it, with no staging in between (256 sequences x 2176 rows,
-//               128 heads: 426 us with the rows staged as the fp8 ones are, 310 so).  The eight warps'
-//               widening bounds a tile: 4600 to 5100 cycles, where bf16 rows take 3450
+//               128 heads: 426 us with the rows staged as the fp8 ones are, 312 so).  The eight warps'
+//               widening bounds a tile: 2047 prompt queries x 639 rows, 140 tiles on the fullest CTA,
+//               take 328 us (4850 cycles a tile), 249 with bf16 rows (3700)
 // Every wait is bounded; a wait that gives up raises the timeout bit and every role unwinds.
 //
 // Row placement.  The order of the gathered rows inside a tile does not matter (the softmax and

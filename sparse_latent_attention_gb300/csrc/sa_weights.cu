@@ -12,13 +12,14 @@
 //
 // The product's d is cut into two ranges with an accumulator each, added up in the epilogue in f32.  One
 // accumulator over all of d = 512, cut by the tensor core after every 16 products, came to a relative error of
-// 1.9e-6 in the weights of bf16 rows (0.9e-6 with two).  Up to 64 heads each range has an issuing warp too: a
-// stage's products take about as long as the wait and the commits around them, which two warps pass behind
-// each other's products (214 us against 257 for the prefill below).
+// 1.9e-6 in the weights of bf16 rows (0.7e-6 to 1.04e-6 with two).  Up to 64 heads each range has an issuing
+// warp too: a stage's products take about as long as the wait and the commits around them, which two warps pass
+// behind each other's products (214 us against 257 for the prefill below).
 //
-// What bounds it: that prefill reads 2.7 GB of rows out of L2 in 214 us, 12.5 TB/s or 44 bytes a cycle and
-// SM (the products alone would take 90 us, at the measured bf16 rate); the long decode, 144 MB of codes and
-// scales once (38 us at the measured copy rate), is held up by the widening.
+// What bounds it: that prefill's 4096 queries have 2.09 M entries (80 % of their columns) and copy 2.1 GB of rows
+// out of L2 in 214 us, 10 TB/s or 32 bytes a cycle and SM (the products of all columns alone would take 90 us, at
+// the measured bf16 rate; units without an entry are computed like the others); the long decode, 144 MB of
+// codes and scales once (38 us at the measured copy rate), is held up by the widening.
 //
 // Roles (persistent CTAs, 19 or 27 warps; every wait is bounded, as in the attention kernel).  A stage is
 // 128 d of a tile [two 64-d blocks of 128 rows x 128 bytes].  What one warp does for a stage or a tile is a chain of
