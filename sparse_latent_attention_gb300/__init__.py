@@ -17,6 +17,12 @@ A cache held in 4 bits (e2m1 codes, two to a byte, and e8m0 scales), and its evi
     kept, remap = evict_select(acc, n_keep, keep_first=window)
     codes, scales, acc = compact_rows([codes, scales, acc], kept)
     idx = remap_idx(idx, remap)
+
+A cache in pages that sequences of different lengths share, attended to by position, and the norm before it:
+
+    h = add_rms_norm(x, weight, residual=stream)                # stream += x, its norm (or 8-bit codes of it)
+    page_write(rows, page_table, q_start, kv_len, pages=pages, weight=w, rope=rot)
+    o = window_attn(q, pages, sink, page_table, q_start, kv_len, scale, window, first=4)
 """
 
 from __future__ import annotations
@@ -33,6 +39,7 @@ __all__ = ["sparse_attn", "window_idxs", "act_quant_fp8", "window_write", "index
            "candidate_blocks", "hc_split_sinkhorn",
            "act_quant_fp4", "window_write_fp4", "row_weights", "evict_select", "compact_rows",
            "remap_idx", "WEIGHT_UNIT",
+           "add_rms_norm", "page_write", "window_attn", "window_workspace_size", "new_window_workspace",
            "workspace_size", "new_workspace", "read_status", "SparseAttnError", "SA_KV_BF16",
            "SA_KV_FP8_E4M3", "SA_KV_FP4_E2M1", "SA_SCORE_F32", "SA_SCORE_BF16", "load"]
 
@@ -591,3 +598,217 @@ def read_status(workspace, clear=False, stream=None) -> int:
     if not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
     return _status(workspace.get_device(), "sa_read_status", stream, _ptr(workspace), int(bool(clear)))
+
+
+def add_rms_norm(x, weight, *, residual=None, eps=1e-6, out=None, codes=None, scales=None, stream=None):
+    """residual += x (in place), and the root-mean-square norm of the sum (of x without a residual):
+    y = h * rsqrt(mean(h^2) + eps) * weight, h as the residual holds it.
+
+    x [n, d] bf16; weight [d] f32; residual [n, d] bf16 or f32.  y goes to ``out`` [n, d] bf16, which may be
+    ``x`` itself and is made (and returned) when neither it nor ``codes`` is given, and, quantised as
+    act_quant_fp8 quantises, to ``codes`` [n, d] and ``scales`` [n, d / 32] uint8.  All but the weight with
+    unit column stride; rows may be strided.  Returns out (None when only codes were asked for)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+        raise TypeError("x must be a CUDA bf16 tensor")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a 2-D tensor with unit column stride")
+    n, d = x.shape
+    dev = x.get_device()
+
+    def rows_of(t, name, dtypes, width):
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+            raise TypeError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor")
+        if tuple(t.shape) != (n, width) or (width > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must have shape ({n}, {width}) and unit column stride")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        return t.data_ptr(), t.stride(0) if n > 1 else width
+
+    _need(weight, "weight", torch.float32, x.device)
+    if tuple(weight.shape) != (d,):
+        raise ValueError(f"weight shape {tuple(weight.shape)} != ({d},)")
+    kind, res, rs = _lib.SA_RESIDUAL_NONE, None, 0
+    if residual is not None:
+        res, rs = rows_of(residual, "residual", (torch.bfloat16, torch.float32), d)
+        kind = _lib.SA_RESIDUAL_F32 if residual.dtype == torch.float32 else _lib.SA_RESIDUAL_BF16
+    if (codes is None) != (scales is None):
+        raise ValueError("give codes and scales together")
+    cd = sc = po = None
+    cs = ss = os_ = 0
+    if codes is not None:
+        if d % 32:
+            raise ValueError(f"blocks of 32 need a row of a multiple of 32, got {d}")
+        cd, cs = rows_of(codes, "codes", (torch.uint8,), d)
+        sc, ss = rows_of(scales, "scales", (torch.uint8,), d // 32)
+    elif out is None:
+        out = _new(stream, lambda: torch.empty((n, d), dtype=torch.bfloat16, device=x.device))
+    if out is not None:
+        po, os_ = rows_of(out, "out", (torch.bfloat16,), d)
+    if n and d:
+        _call("sa_add_rms_norm", dev, stream, x.data_ptr(), n, d, x.stride(0) if n > 1 else d, weight.data_ptr(),
+              float(eps), res, kind, rs, po, os_, cd, cs, sc, ss)
+    return out
+
+
+def _batch(page_table, q_start, kv_len, dev):
+    """The packed batch's tables: (b, the arguments they make)."""
+    for t, name, dim in ((page_table, "page_table", 2), (q_start, "q_start", 1), (kv_len, "kv_len", 1)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+            raise TypeError(f"{name} must be a CUDA int32 tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        if t.dim() != dim or (t.numel() and t.stride(-1) != 1):
+            raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''} and unit column stride")
+    b = kv_len.shape[0]
+    if page_table.shape[0] != b or q_start.shape[0] != b + 1:
+        raise ValueError(f"page_table {tuple(page_table.shape)} and q_start {tuple(q_start.shape)} do not fit "
+                         f"the {b} sequences of kv_len")
+    return b, page_table.shape[1], page_table.stride(0) if b > 1 else page_table.shape[1]
+
+
+_QUANT = {"fp8": SA_KV_FP8_E4M3, "fp4": SA_KV_FP4_E2M1}
+
+
+def page_write(x, page_table, q_start, kv_len, *, pages=None, codes=None, scales=None, quant=None, weight=None,
+               eps=1e-6, rope=None, workspace=None, stream=None):
+    """New latent rows into their pages (sa_page_write): normed (with ``weight`` [d] f32), their last dims
+    turned by their position's rotation (``rope`` [positions, rope_dim / 2, 2] f32: cos, sin), and held in bf16,
+    8 or 4 bits.
+
+    x [n, d] bf16: the packed batch's new tokens; q_start [b + 1], kv_len [b] and page_table [b, max_pages]
+    int32: sequence i owns tokens q_start[i] .. q_start[i + 1] - 1, the last of them at position kv_len[i] - 1,
+    and position p lies in page page_table[i][p // page].  Tokens from q_start[b] on are left out.
+    codes [n_pages, page, d] (e4m3) or [n_pages, page, d / 2] (e2m1) with scales [n_pages, page, d / 32], uint8,
+    receive the quantised rows.  pages [n_pages, page, d] bf16 receives the rows, as they are quantised where
+    codes are given or ``quant`` ("fp8", "fp4") says so, else rounded to bf16.  All with unit column stride; pages
+    and rows may be strided.
+    workspace: one of new_workspace or new_window_workspace, whose status word notes a position without a page
+    (or past the rotations); such a row is not written."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+        raise TypeError("x must be a CUDA bf16 tensor")
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D tensor with unit column stride")
+    n, d = x.shape
+    dev = x.get_device()
+    b, max_pages, table_stride = _batch(page_table, q_start, kv_len, dev)
+    shape = None
+
+    def pool_of(t, name, dtype, widths):
+        nonlocal shape
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+            raise TypeError(f"{name} must be a {dtype} tensor")
+        if t.dim() != 3 or t.shape[2] not in widths or t.stride(2) != 1 or shape not in (None, t.shape[:2]):
+            raise ValueError(f"{name} shape {tuple(t.shape)} does not fit rows of {d}"
+                             f"{'' if shape is None else f' in {shape[0]} pages of {shape[1]}'}"
+                             " with unit column stride")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        shape = t.shape[:2]
+        return t.data_ptr(), t.stride(1) if t.shape[1] > 1 else t.shape[2], t.stride(0)
+
+    if quant is not None and quant not in _QUANT:
+        raise ValueError(f"quant must be one of {sorted(_QUANT)}")
+    fmt = _QUANT.get(quant, SA_KV_BF16)
+    if (codes is None) != (scales is None):
+        raise ValueError("give codes and scales together")
+    pg = cd = sc = (None, 0, 0)
+    if codes is not None:
+        cd = pool_of(codes, "codes", torch.uint8, (d, d // 2))
+        sc = pool_of(scales, "scales", torch.uint8, (d // 32,))
+        held = SA_KV_FP8_E4M3 if codes.shape[2] == d else SA_KV_FP4_E2M1
+        if quant is not None and held != fmt:
+            raise ValueError(f"quant {quant} does not fit codes of shape {tuple(codes.shape)}")
+        fmt = held
+    if pages is not None:
+        pg = pool_of(pages, "pages", torch.bfloat16, (d,))
+    if shape is None:
+        raise ValueError("give pages, or codes and scales")
+    w = turn = None
+    npos = rope_dim = 0
+    if weight is not None:
+        _need(weight, "weight", torch.float32, x.device)
+        if tuple(weight.shape) != (d,):
+            raise ValueError(f"weight shape {tuple(weight.shape)} != ({d},)")
+        w = weight.data_ptr()
+    if rope is not None:
+        turn, npos, rope_dim = _rotation(rope, x.device)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, x.device)
+        if workspace.numel() < SA_STATUS_BYTES:
+            raise ValueError("workspace is too small")
+    _call("sa_page_write", dev, stream, x.data_ptr(), n, d, x.stride(0) if n > 1 else d, page_table.data_ptr(),
+          max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(), b, shape[0], shape[1], fmt, *pg, *cd, *sc,
+          w, float(eps), turn, npos, rope_dim, _ptr(workspace))
+
+
+def _rotation(rope, device):
+    """A table of rotations by position: (address, positions, rope_dim)."""
+    _need(rope, "rope", torch.float32, device)
+    if rope.dim() != 3 or rope.shape[2] != 2:
+        raise ValueError(f"rope shape {tuple(rope.shape)} is not [positions, rope_dim / 2, 2]")
+    if rope.numel() == 0:  # (its address would say: no rotation)
+        raise ValueError("rope is empty")
+    return rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+
+
+def window_workspace_size(n, b, h, d, window, first, page, kv_format=SA_KV_BF16) -> int:
+    """Bytes of workspace that window_attn needs for n tokens of b sequences."""
+    size = int(load().sa_window_attn_workspace_size(n, b, h, d, window, first, page, kv_format))
+    if size == 0:
+        raise SparseAttnError(_lib.SA_ERR_UNSUPPORTED, "sa_window_attn_workspace_size")
+    return size
+
+
+def new_window_workspace(n, b, h, d, window, first, page, kv_format=SA_KV_BF16, device="cuda") -> torch.Tensor:
+    """A workspace of that size, its status word cleared."""
+    ws = torch.empty(window_workspace_size(n, b, h, d, window, first, page, kv_format), dtype=torch.uint8,
+                     device=device)
+    ws[:SA_STATUS_BYTES].zero_()
+    return ws
+
+
+def window_attn(q, pages, sink, page_table, q_start, kv_len, softmax_scale, window, *, first=0, kv_scale=None,
+                out=None, lse=None, rope=None, workspace=None, stream=None) -> torch.Tensor:
+    """o[n, h, d] (bf16): each token of a packed batch attends to the last ``window`` positions of its sequence,
+    its own among them, and to the sequence's ``first`` first ones, over a cache held in pages (sa_window_attn).
+
+    q [n, h, d] bf16; pages [n_pages, page, d] bf16, or uint8 codes [n_pages, page, d] (e4m3) or
+    [n_pages, page, d / 2] (e2m1) with kv_scale [n_pages, page, d / 32] uint8; sink [h] f32; page_table, q_start
+    and kv_len as in page_write, the cache with the tokens' own rows in it.  Rows of ``out`` and ``lse`` from
+    q_start[b] on are left as they were.
+    lse: an f32 tensor [n, h] that receives the log of each softmax's denominator (the sink's term included).
+    rope [positions, rope_dim / 2, 2] f32: also turn o's last dims back by each token's position (d = 512)."""
+    _need(q, "q", torch.bfloat16)
+    device = q.device
+    if q.dim() != 3:
+        raise ValueError(f"q shape {tuple(q.shape)} is not [n, h, d]")
+    n, h, d = q.shape
+    dev = q.get_device()
+    if pages.dim() != 3:
+        raise ValueError(f"pages shape {tuple(pages.shape)} is not [n_pages, page, .]")
+    n_pages, page = pages.shape[:2]
+    fmt = _kv_format(pages, kv_scale, n_pages, d, device)
+    b, max_pages, table_stride = _batch(page_table, q_start, kv_len, dev)
+    _need(sink, "sink", torch.float32, device)
+    if tuple(sink.shape) != (h,):
+        raise ValueError(f"sink shape {tuple(sink.shape)} != ({h},)")
+    if out is None:
+        out = _new(stream, lambda: torch.empty_like(q))
+    else:
+        _need(out, "out", torch.bfloat16, device)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, device)
+        if tuple(lse.shape) != (n, h):
+            raise ValueError(f"lse shape {tuple(lse.shape)} != {(n, h)}")
+    turn, npos, rope_dim = (None, 0, 0) if rope is None else _rotation(rope, device)
+    if workspace is None:
+        workspace = _new(stream, lambda: new_window_workspace(n, b, h, d, window, first, page, fmt, device))
+    else:
+        _need(workspace, "workspace", torch.uint8, device)
+    _call("sa_window_attn", dev, stream, q.data_ptr(), pages.data_ptr(), _ptr(kv_scale), fmt, sink.data_ptr(),
+          page_table.data_ptr(), max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(),
+          float(softmax_scale), n, b, h, d, n_pages, page, window, first, out.data_ptr(), _ptr(lse), turn, npos,
+          rope_dim, workspace.data_ptr(), workspace.numel())
+    return out

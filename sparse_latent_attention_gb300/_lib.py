@@ -25,6 +25,7 @@ SA_SCORE_F32, SA_SCORE_BF16 = 0, 1
 SA_INDEXER_MAX_POSITIONS = 49152
 SA_STATUS_BYTES = 256
 SA_COMPACT_MAX_TENSORS = 8
+SA_RESIDUAL_NONE, SA_RESIDUAL_BF16, SA_RESIDUAL_F32 = 0, 1, 2
 
 _lock = threading.Lock()
 _lib = None
@@ -93,6 +94,17 @@ def load() -> ctypes.CDLL:
         lib.sa_compact_rows.argtypes = [i32, P, P, P, P, P, i64, i64, i64, P, P]
         lib.sa_remap_idx.restype = i32
         lib.sa_remap_idx.argtypes = [P, i64, i64, P, i64, P, P]
+        # include/serve/
+        lib.sa_add_rms_norm.restype = i32
+        lib.sa_add_rms_norm.argtypes = [P, i64, i32, i64, P, f32, P, i32, i64, P, i64, P, i64, P, i64, P]
+        lib.sa_page_write.restype = i32
+        lib.sa_page_write.argtypes = [P, i64, i32, i64, P, i64, i64, P, P, i64, i64, i32, i32, P, i64, i64, P,
+                                      i64, i64, P, i64, i64, P, f32, P, i64, i32, P, P]
+        lib.sa_window_attn_workspace_size.restype = sz
+        lib.sa_window_attn_workspace_size.argtypes = [i64, i64, i32, i32, i64, i64, i32, i32]
+        lib.sa_window_attn.restype = i32
+        lib.sa_window_attn.argtypes = [P, P, P, i32, P, P, i64, i64, P, P, f32, i64, i64, i32, i32, i64, i32, i64,
+                                       i64, P, P, P, i64, i32, P, sz, P]
         lib.sa_read_status.restype = i32
         lib.sa_read_status.argtypes = [P, i32, P]
         lib.sa_status_string.restype = ctypes.c_char_p
@@ -105,7 +117,7 @@ def load() -> ctypes.CDLL:
 
 def declared_symbols(folder: str = "") -> list[str]:
     """Names of the functions that the headers in include/ declare, or those in a folder of it
-    ("cache": the 4-bit cache and eviction)."""
+    ("cache": the 4-bit cache and eviction; "serve": the paged cache, its window attention and the norm)."""
     names = set()
     for header in sorted(glob.glob(os.path.join(os.path.dirname(HEADER), folder, "*.h"))):
         text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)

@@ -49,6 +49,7 @@ struct Params {
     int n_tiles;
     int n_splits;
     int tiles_per_split;
+    const int32_t* n_live;  // (see AttnCall)
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
     pdl_wait();
     pdl_trigger();
     const int64_t token = blockIdx.x;
+    if (p.n_live && token >= *p.n_live) return;
     const int split = blockIdx.y;
     const int h0 = blockIdx.z * kHeadsPerCta;
     const int hc = min(kHeadsPerCta, p.h - h0);
@@ -377,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(Params p) {
 __global__ void attn_combine_kernel(const float* __restrict__ part_ml,
                                     const float* __restrict__ part_o,
                                     const float* __restrict__ sink, __nv_bfloat16* __restrict__ o,
-                                    float* __restrict__ lse, int h, int d, int n_splits) {
+                                    float* __restrict__ lse, int h, int d, int n_splits,
+                                    const int32_t* n_live) {
     // the attention kernel this launch depends on has completed and its partials are visible
     // after this point
     pdl_wait();
@@ -385,6 +388,7 @@ __global__ void attn_combine_kernel(const float* __restrict__ part_ml,
     const int64_t th = blockIdx.x;  // token * h + head
     const int hh = (int)(th % h);
     const int64_t token = th / h;
+    if (n_live && token >= *n_live) return;
     const int c = 4 * threadIdx.x;
     const float2* ml0 = reinterpret_cast<const float2*>(part_ml) + token * n_splits * (int64_t)h + hh;
     const float* po0 = part_o + (token * n_splits * (int64_t)h + hh) * d + c;
@@ -517,6 +521,7 @@ cudaError_t attn_mma_launch(const AttnCall& c) {
     p.o = reinterpret_cast<__nv_bfloat16*>(c.o);
     p.lse = c.lse;
     p.status = c.status;
+    p.n_live = c.n_live;
     p.scale_log2 = c.softmax_scale * kLog2e;
     p.s_len = c.s;
     p.h = c.h;
@@ -539,18 +544,18 @@ cudaError_t attn_mma_launch(const AttnCall& c) {
                                                     : launch_d<SA_KV_FP4_E2M1>(c, p, grid);
     if (e != cudaSuccess || g.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, p.o, c.lse, n_tokens, c.h, c.d, g.n_splits,
-                               c.stream);
+                               c.n_live, c.stream);
 }
 
 cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const float* sink,
                                 void* o, float* lse, int64_t n_tokens, int h, int d, int n_splits,
-                                cudaStream_t stream) {
+                                const int32_t* n_live, cudaStream_t stream) {
     if (n_tokens * h == 0) return cudaSuccess;
     // a programmatic dependent of the attention kernel just queued on the stream: its blocks can
     // be scheduled while that kernel drains, and wait for its partials
     return launch_pdl(attn_combine_kernel, dim3((unsigned)(n_tokens * h)), dim3((unsigned)(d / 4)), 0,
                       stream, part_ml, part_o, sink, reinterpret_cast<__nv_bfloat16*>(o), lse, h, d,
-                      n_splits);
+                      n_splits, n_live);
 }
 
 cudaError_t lse_of_sinks_launch(float* lse, const float* sink, int64_t n_tokens, int h,

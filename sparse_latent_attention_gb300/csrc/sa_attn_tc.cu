@@ -167,6 +167,8 @@ struct Params {
     const float* rope;    // inverse rotation of o's last rope_dim dims, or nullptr (see AttnCall)
     int rope_dim;
     int64_t rope_pos0;
+    const int32_t* rope_at;   // (see AttnCall)
+    const int32_t* n_live;
 };
 
 struct Task {
@@ -184,6 +186,10 @@ __device__ __forceinline__ void task_range(const Params& p, int64_t& begin, int6
     const int64_t base = p.n_units / g, rem = p.n_units % g;
     begin = i * base + (i < rem ? i : rem);
     end = begin + base + (i < rem ? 1 : 0);
+    if (p.n_live) {  // (units of the tokens left out come last)
+        const int64_t live = max(*p.n_live, 0) * (int64_t)p.n_splits;
+        end = max(begin, min(end, live));
+    }
 }
 
 // The task of unit tau (token tau / n_splits, split tau % n_splits) for this CTA's head block.
@@ -198,6 +204,10 @@ __device__ __forceinline__ Task task_of(const Params& p, int64_t tau) {
     t.t1 = min(p.n_tiles, t.t0 + p.tiles_per_split);
     if (t.t1 < t.t0) t.t1 = t.t0;
     return t;
+}
+
+__device__ __forceinline__ int64_t rope_position(const Params& p, const Task& t) {
+    return p.rope_at ? __ldg(p.rope_at + t.token) : p.rope_pos0 + t.pos;
 }
 
 // The task of the next unit (splits fastest, then tokens), without divisions.
@@ -1145,7 +1155,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                 const int dd = 128 * (kChunks - 1) + 32 * q4 + lane, first = kD - p.rope_dim;
                 if (dd >= first)
                     rope_last = reinterpret_cast<const float2*>(
-                        p.rope)[(p.rope_pos0 + t.pos) * (p.rope_dim / 2) + ((dd - first) >> 1)];
+                        p.rope)[rope_position(p, t) * (p.rope_dim / 2) + ((dd - first) >> 1)];
             }
             if constexpr (kStaged) {
                 // widen every tile the producers have staged until this task's O is complete
@@ -1231,7 +1241,7 @@ __global__ void __launch_bounds__(threads_of(kFmt), 1)
                     float2 w = rope_last;  // the last chunk's pair was loaded before the wait
                     if (c != kChunks - 1 && mine)
                         w = reinterpret_cast<const float2*>(
-                            p.rope)[(p.rope_pos0 + t.pos) * (p.rope_dim / 2) + ((dd - first) >> 1)];
+                            p.rope)[rope_position(p, t) * (p.rope_dim / 2) + ((dd - first) >> 1)];
                     const float cs = w.x, sn = w.y;
 #pragma unroll
                     for (int i = 0; i < kHeads; ++i) {
@@ -1394,6 +1404,8 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     p.rope = c.rope;
     p.rope_dim = c.rope_dim;
     p.rope_pos0 = c.rope_pos0;
+    p.rope_at = c.rope_at;
+    p.n_live = c.n_live;
     p.kv = codes ? nullptr : reinterpret_cast<const __nv_bfloat16*>(c.kv);
     p.kv8 = codes ? reinterpret_cast<const uint8_t*>(c.kv) : nullptr;
     p.kv_scale = codes ? c.kv_scale : nullptr;
@@ -1442,7 +1454,7 @@ cudaError_t attn_tc_launch(const AttnCall& c) {
     e = launch_pdl(kernel, dim3((unsigned)grid), dim3(threads_of(c.kv_format)), smem_of(c.kv_format), c.stream, qmap, p);
     if (e != cudaSuccess || g.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, n_tokens, c.h, kD, g.n_splits,
-                               c.stream);
+                               c.n_live, c.stream);
 }
 
 }  // namespace sa

@@ -45,7 +45,10 @@ struct AttnCall {
     const float* rope = nullptr;
     int rope_dim = 0;
     int64_t rope_pos0 = 0;
+    const int32_t* rope_at = nullptr;  // each token's position instead, or none
     float* lse = nullptr;  // [tokens][h] log-sum-exp output, or none
+    // on the device, or none: the tokens from this number on are left out, and their outputs as they were
+    const int32_t* n_live = nullptr;
 };
 
 // The three kv formats: whether a value names one, and the bytes of a row's kv and scales.
@@ -72,10 +75,11 @@ cudaError_t lse_of_sinks_launch(float* lse, const float* sink, int64_t n_tokens,
 size_t attn_mma_scratch_bytes(int64_t b, int64_t s, int h, int d, int topk);
 cudaError_t attn_mma_launch(const AttnCall& c);
 // merge of split partials: part_ml [tokens][splits][h][2] (max in log2 units, sum),
-// part_o [tokens][splits][h][d] f32 -> o bf16, and lse unless it is nullptr (sa_attn_mma.cu)
+// part_o [tokens][splits][h][d] f32 -> o bf16, and lse unless it is nullptr; n_live as AttnCall's
+// (sa_attn_mma.cu)
 cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const float* sink,
                                 void* o, float* lse, int64_t n_tokens, int h, int d, int n_splits,
-                                cudaStream_t stream);
+                                const int32_t* n_live, cudaStream_t stream);
 
 // tcgen05 family (sa_attn_tc.cu)
 // d = 512, every kv format

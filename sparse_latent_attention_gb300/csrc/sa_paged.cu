@@ -1,0 +1,411 @@
+// The paged latent cache's write side, and the window attention over it: argument checks, and the index table
+// for the kernel families that gather by row (include/serve/sa_paged.h).
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sa_internal.cuh"
+#include "sa_paged.cuh"
+#include "sa_rows.cuh"
+#include "serve/sa_paged.h"
+
+namespace sa {
+namespace {
+
+using namespace rows;
+using paged::Batch;
+
+// ---------------------------------------------------------------------------------------------
+// page_write
+// ---------------------------------------------------------------------------------------------
+
+struct Write {
+    const __nv_bfloat16* x;
+    int64_t xs, n;
+    int d;
+    Batch a;
+    __nv_bfloat16* pages;
+    int64_t ps, pp;
+    uint8_t* codes;
+    int64_t cs, cp;
+    uint8_t* scales;
+    int64_t ss, sp;
+    const float* weight;
+    float eps;
+    const float* rot;
+    int64_t npos;
+    int rope_dim;
+    uint32_t* status;
+};
+
+// A warp a token, eight consecutive elements a lane and chunk (kPer chunks of 256).  kRun tokens one behind the
+// other a warp: their rows are under way before the first one's sequence and page are known, and the sequence is
+// looked for once.
+template <int kQuant, int kPer, int kRun, bool kVec>
+__global__ void __launch_bounds__(128) page_write_kernel(const __grid_constant__ Write p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, chunks = p.d >> 3;
+    const int64_t t0 = (blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5)) * kRun;
+    uint4 in[kRun][kPer];
+#pragma unroll
+    for (int r = 0; r < kRun; ++r)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = lane + 32 * i;
+            in[r][i] = c < chunks && t0 + r < p.n ? load8<kVec>(p.x + (t0 + r) * p.xs + 8 * c)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+        }
+    paged::Token k = {0, 0, -1};
+#pragma unroll
+    for (int r = 0; r < kRun; ++r) {
+        const int64_t t = t0 + r;
+        if (t >= p.n) break;
+        if (r > 0 && t < k.end && k.pos >= -1) {
+            ++k.pos;
+        } else {
+            k = paged::token_of(p.a, t);
+        }
+        if (k.pos < 0) continue;
+        const int64_t row = paged::row_of(p.a, k.seq, (uint32_t)k.pos);
+        if (row < 0 || (p.rot && k.pos >= p.npos)) {
+            if (p.status && lane == 0) atomicOr(p.status, kStatusBadIndex);
+            continue;
+        }
+        const int64_t g = row / p.a.page, off = row - g * p.a.page;
+        float v[kPer][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            unpacked8(in[r][i], v[i]);
+            float s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = fmaf(v[i][2 * j], v[i][2 * j], v[i][2 * j + 1] * v[i][2 * j + 1]);
+            sum += (s[0] + s[1]) + (s[2] + s[3]);
+        }
+        Two f = {1.f, 0.f};
+        if (p.weight) f = inverse_rms(warp_sum({sum, 0.f}), (float)p.d, p.eps);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = lane + 32 * i;
+            if (32 * i >= chunks) break;
+            const bool mine = c < chunks;
+            Two y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[j] = {v[i][j], 0.f};
+                if (p.weight) y[j] = mul(mul(v[i][j], f), mine ? __ldg(p.weight + 8 * c + j) : 0.f);
+            }
+            const int first = p.d - p.rope_dim;
+            if (p.rot && mine && 8 * c + 8 > first) {
+                const float2* turn = reinterpret_cast<const float2*>(p.rot) + k.pos * (p.rope_dim >> 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int e = 8 * c + 2 * j - first;
+                    if (e < 0) continue;
+                    const float2 w = __ldg(turn + (e >> 1));
+                    const Two a = y[2 * j], b = y[2 * j + 1], bs = mul(b, w.y), bc = mul(b, w.x);
+                    y[2 * j] = add(mul(a, w.x), {-bs.h, -bs.l});
+                    y[2 * j + 1] = add(mul(a, w.y), bc);
+                }
+            }
+            float out[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = rounded(y[j]);
+            uint4 values;
+            if constexpr (kQuant == SA_KV_BF16) {
+                values = packed8(out);
+            } else {
+                constexpr bool kFp4 = kQuant == SA_KV_FP4_E2M1;
+                uint2 codes;
+                uint32_t se;
+                quantise8<kFp4>(out, codes, se);
+                values = values8<kFp4>(codes, se);
+                if (p.codes && mine) {
+                    store_codes8<kVec, kFp4>(p.codes + g * p.cp + off * p.cs + (kFp4 ? 4 : 8) * c, codes);
+                    if ((c & 3) == 0) p.scales[g * p.sp + off * p.ss + (c >> 2)] = (uint8_t)se;
+                }
+            }
+            if (p.pages && mine) store8<kVec>(p.pages + g * p.pp + off * p.ps + 8 * c, values);
+        }
+    }
+}
+
+template <int kQuant, int kPer, bool kVec>
+cudaError_t write_run(const Write& p, cudaStream_t st) {
+    // a wave of 128-thread blocks holds 64 tokens a SM: below that, a token a warp; beyond, several
+    constexpr int kRun = kPer == 4 ? 2 : 4;
+    const bool few = p.n <= 64 * (int64_t)device_sm_count();
+    const int64_t per = few ? 4 : 4 * kRun, grid = (p.n + per - 1) / per;
+    return few ? launch_pdl(page_write_kernel<kQuant, kPer, 1, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p)
+               : launch_pdl(page_write_kernel<kQuant, kPer, kRun, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p);
+}
+
+template <int kQuant>
+cudaError_t write_launch(const Write& p, bool vec, cudaStream_t st) {
+    if (!vec) return write_run<kQuant, 4, false>(p, st);
+    if (p.d <= 256) return write_run<kQuant, 1, true>(p, st);
+    if (p.d <= 512) return write_run<kQuant, 2, true>(p, st);
+    return write_run<kQuant, 4, true>(p, st);
+}
+
+// ---------------------------------------------------------------------------------------------
+// window_attn by an index table
+// ---------------------------------------------------------------------------------------------
+
+// The pool's row of each position that a token may see: entry c < first of a token's row is position c,
+// entry first + c position p - window + 1 + c where that is not below first; -1 where there is none.  pos: each
+// token's position in the rotation's table.  A warp per 128 entries, four a lane.
+__global__ void __launch_bounds__(128) window_rows_kernel(Batch a, int64_t n, int window, int first, int topk,
+                                                          int32_t* idx, int32_t* pos, int64_t npos,
+                                                          uint32_t* status) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t = blockIdx.x;
+    const paged::Token k = paged::token_of(a, t);
+    bool bad = false;
+    if (pos && blockIdx.y == 0 && threadIdx.x == 0) {
+        bad = k.pos >= npos;
+        pos[t] = (int32_t)(k.pos < 0 ? 0 : bad ? npos - 1 : k.pos);
+    }
+    for (int c = (int)(blockIdx.y * blockDim.x + threadIdx.x); c < topk; c += (int)(gridDim.y * blockDim.x)) {
+        int32_t row = -1;
+        const int64_t j = c < first ? c : k.pos - window + 1 + (c - first);
+        if (j >= 0 && j <= k.pos && (c < first || j >= first)) {
+            row = (int32_t)paged::row_of(a, k.seq, (uint32_t)j);
+            bad |= row < 0;
+        }
+        idx[t * topk + c] = row;
+    }
+    if (bad) atomicOr(status, kStatusBadIndex);
+}
+
+// A pool of rows: their bytes, and how far apart rows and pages are.
+struct Pool {
+    const void* at;
+    int64_t width, row, page;
+};
+
+// Whether pieces of aw and bw bytes, each repeated every s bytes, never share one.
+bool apart(const void* a, int64_t aw, const void* b, int64_t bw, int64_t s) {
+    if (aw > s || bw > s) return false;
+    const uintptr_t u = (uintptr_t)s, at = (reinterpret_cast<uintptr_t>(b) % u + u - reinterpret_cast<uintptr_t>(a) % u) % u;
+    return at >= (uintptr_t)aw && at + (uintptr_t)bw <= u;
+}
+
+// Whether two pools share a byte.  Pages, or rows, equally far apart may lie between one another (codes and
+// scales side by side in a row, or in a page); of others the whole spans count.
+bool pools_overlap(const Pool& a, const Pool& b, int64_t n_pages, int64_t rows) {
+    const int64_t as = (rows - 1) * a.row + a.width, bs = (rows - 1) * b.row + b.width;
+    if (!overlap(a.at, (n_pages - 1) * a.page + as, b.at, (n_pages - 1) * b.page + bs)) return false;
+    if (n_pages > 1 && a.page != b.page) return true;
+    if (n_pages > 1 && apart(a.at, as, b.at, bs, a.page)) return false;
+    return !(rows > 1 && a.row == b.row && (n_pages == 1 || a.page % a.row == 0) &&
+             apart(a.at, a.width, b.at, b.width, a.row));
+}
+
+bool window_shape(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page) {
+    return n >= 0 && b >= 0 && h >= 1 && d >= 1 && window >= 1 && first >= 0 && page >= 1 &&
+           window < (int64_t(1) << 30) && first < (int64_t(1) << 30) && first + window < (int64_t(1) << 30);
+}
+
+bool window_supported(int64_t n, int h, int d) {
+    return h <= 128 && d >= 64 && d <= 512 && d % 64 == 0 && n * (int64_t)h < (int64_t(1) << 31);
+}
+
+// The workspace: the status word and the scratch of the family that the call is routed to, then its index
+// table and positions.
+struct Parts {
+    size_t idx, pos, all;
+};
+
+Parts parts_of(int64_t n, int h, int d, int topk, int kv_format) {
+    if (n < 1) n = 1;
+    const int fam = routed_family(SA_FAMILY_AUTO, h, d, kv_format, 1, 0);
+    Parts s;
+    s.idx = align_up(routed_workspace_bytes(fam, 1, n, h, d, 0, topk), 256);
+    s.pos = s.idx + align_up((size_t)n * topk * sizeof(int32_t), 256);
+    s.all = s.pos + align_up((size_t)n * sizeof(int32_t), 256);
+    return s;
+}
+
+}  // namespace
+}  // namespace sa
+
+extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const int32_t* page_table,
+                                   int64_t max_pages, int64_t table_stride, const int32_t* q_start,
+                                   const int32_t* kv_len, int64_t b, int64_t n_pages, int page, int quant,
+                                   void* pages, int64_t pages_stride, int64_t pages_page_stride, uint8_t* codes,
+                                   int64_t codes_stride, int64_t codes_page_stride, uint8_t* scales,
+                                   int64_t scales_stride, int64_t scales_page_stride, const float* weight,
+                                   float eps, const float* rot, int64_t npos, int rope_dim, void* status,
+                                   void* stream) {
+    using namespace sa;
+    if (n < 0 || d < 32 || d % 32 != 0 || b < 0 || n_pages < 0 || page < 1 || max_pages < 0) return SA_ERR_INVALID_ARG;
+    if (!kv_format_known(quant) || (!pages && !codes) || !codes != !scales) return SA_ERR_INVALID_ARG;
+    if (codes && quant == SA_KV_BF16) return SA_ERR_INVALID_ARG;
+    if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 0)) return SA_ERR_INVALID_ARG;
+    if (weight && !(eps >= 0.f)) return SA_ERR_INVALID_ARG;
+    if (d > 1024 || n >= (int64_t(1) << 31) || n_pages * (int64_t)page >= (int64_t(1) << 40)) return SA_ERR_UNSUPPORTED;
+    if (n == 0 || b == 0) return SA_OK;
+    if (!x || !aligned(x, 2) || x_stride < d) return SA_ERR_INVALID_ARG;
+    if (!q_start || !aligned(q_start, 4) || !kv_len || !aligned(kv_len, 4)) return SA_ERR_INVALID_ARG;
+    if ((max_pages > 0 && !page_table) || !aligned(page_table, 4) || (b > 1 && table_stride < max_pages))
+        return SA_ERR_INVALID_ARG;
+    if (!aligned(weight, 4) || !aligned(rot, 8) || !aligned(status, 4)) return SA_ERR_INVALID_ARG;
+    const int64_t cw = quant == SA_KV_FP4_E2M1 ? d / 2 : d, sw = d / 32, r1 = page - 1, g1 = n_pages > 0 ? n_pages - 1 : 0;
+    const int64_t p1 = r1 * pages_stride + d, c1 = r1 * codes_stride + cw, s1 = r1 * scales_stride + sw;  // a page's
+    if (pages && (!aligned(pages, 2) || pages_stride < d || (n_pages > 1 && pages_page_stride < p1)))
+        return SA_ERR_INVALID_ARG;
+    if (codes && (codes_stride < cw || (n_pages > 1 && codes_page_stride < c1) || scales_stride < sw ||
+                  (n_pages > 1 && scales_page_stride < s1)))
+        return SA_ERR_INVALID_ARG;
+    const struct {
+        const void* at;
+        int64_t bytes;
+        bool written;
+    } t[] = {{n_pages ? pages : nullptr, 2 * (g1 * pages_page_stride + p1), true},
+             {n_pages ? codes : nullptr, g1 * codes_page_stride + c1, true},
+             {n_pages ? scales : nullptr, g1 * scales_page_stride + s1, true},
+             {status, 4, true},
+             {x, 2 * ((n - 1) * x_stride + d), false},
+             {weight, 4 * (int64_t)d, false},
+             {rot, 4 * npos * rope_dim, false},
+             {q_start, 4 * (b + 1), false},
+             {kv_len, 4 * b, false},
+             {page_table, 4 * ((b - 1) * table_stride + max_pages), false}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 10; ++j)
+            if (j >= 3 && overlap(t[i].at, t[i].bytes, t[j].at, t[j].bytes)) return SA_ERR_INVALID_ARG;
+    const Pool pools[] = {{n_pages ? pages : nullptr, 2 * (int64_t)d, 2 * pages_stride, 2 * pages_page_stride},
+                          {n_pages ? codes : nullptr, cw, codes_stride, codes_page_stride},
+                          {n_pages ? scales : nullptr, sw, scales_stride, scales_page_stride}};
+    if (pools_overlap(pools[0], pools[1], n_pages, page) || pools_overlap(pools[0], pools[2], n_pages, page) ||
+        pools_overlap(pools[1], pools[2], n_pages, page))
+        return SA_ERR_INVALID_ARG;
+    Write p = {};
+    p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+    p.xs = x_stride;
+    p.n = n;
+    p.d = d;
+    p.a = {page_table, max_pages, table_stride, b, n_pages, q_start, kv_len, page};
+    p.pages = reinterpret_cast<__nv_bfloat16*>(pages);
+    p.ps = pages_stride;
+    p.pp = pages_page_stride;
+    p.codes = codes;
+    p.cs = codes_stride;
+    p.cp = codes_page_stride;
+    p.scales = scales;
+    p.ss = scales_stride;
+    p.sp = scales_page_stride;
+    p.weight = weight;
+    p.eps = eps;
+    p.rot = rot;
+    p.npos = npos;
+    p.rope_dim = rot ? rope_dim : 0;
+    p.status = reinterpret_cast<uint32_t*>(status);
+    const int ca = quant == SA_KV_FP4_E2M1 ? 4 : 8;
+    const bool vec = aligned(x, 16) && x_stride % 8 == 0 &&
+                     (!pages || (aligned(pages, 16) && pages_stride % 8 == 0 && pages_page_stride % 8 == 0)) &&
+                     (!codes || (aligned(codes, ca) && codes_stride % ca == 0 && codes_page_stride % ca == 0));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = quant == SA_KV_BF16       ? write_launch<SA_KV_BF16>(p, vec, st)
+                          : quant == SA_KV_FP8_E4M3 ? write_launch<SA_KV_FP8_E4M3>(p, vec, st)
+                                                    : write_launch<SA_KV_FP4_E2M1>(p, vec, st);
+    return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+extern "C" size_t sa_window_attn_workspace_size(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first,
+                                                int page, int kv_format) {
+    using namespace sa;
+    if (!kv_format_known(kv_format) || !window_shape(n, b, h, d, window, first, page) || !window_supported(n, h, d))
+        return 0;
+    return parts_of(n, h, d, (int)(first + window), kv_format).all;
+}
+
+extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,
+                                    const float* sink, const int32_t* page_table, int64_t max_pages,
+                                    int64_t table_stride, const int32_t* q_start, const int32_t* kv_len,
+                                    float softmax_scale, int64_t n, int64_t b, int h, int d, int64_t n_pages,
+                                    int page, int64_t window, int64_t first, void* o, float* lse, const float* rot,
+                                    int64_t npos, int rope_dim, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+    using namespace sa;
+    if (!kv_format_known(kv_format) || !window_shape(n, b, h, d, window, first, page) || n_pages < 0 || max_pages < 0)
+        return SA_ERR_INVALID_ARG;
+    if (!window_supported(n, h, d) || n_pages >= (int64_t(1) << 31) || n_pages * page >= (int64_t(1) << 31))
+        return SA_ERR_UNSUPPORTED;
+    if (kv_format == SA_KV_BF16 && kv_scale) return SA_ERR_INVALID_ARG;
+    if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 1)) return SA_ERR_INVALID_ARG;
+    const bool tc = attn_tc_supports(h, d, kv_format, 1, 0);
+    if (rot && !tc) return SA_ERR_UNSUPPORTED;
+    if (n == 0 || b == 0) return SA_OK;
+    const bool codes = kv_format != SA_KV_BF16;
+    if (!q || !sink || !o || !q_start || !kv_len || (max_pages > 0 && !page_table)) return SA_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!kv || (codes && !kv_scale))) return SA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) || !aligned(lse, 4) ||
+        !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
+        !aligned(kv_scale, tc ? 16 : 4) || (b > 1 && table_stride < max_pages))
+        return SA_ERR_INVALID_ARG;
+    const Parts parts = parts_of(n, h, d, (int)(first + window), kv_format);
+    const int64_t ob = 2 * n * h * d, rows = n_pages * page;
+    const struct {
+        const void* at;
+        int64_t bytes;
+    } t[] = {{o, ob},
+             {lse, 4 * n * h},
+             {workspace, (int64_t)parts.all},
+             {q, ob},
+             {kv, rows * kv_row_bytes(kv_format, d)},
+             {kv_scale, rows * (d / 32)},
+             {sink, 4 * (int64_t)h},
+             {rot, 4 * npos * rope_dim},
+             {q_start, 4 * (b + 1)},
+             {kv_len, 4 * b},
+             {page_table, 4 * ((b - 1) * table_stride + max_pages)}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = i + 1; j < 11; ++j)
+            if (j != 2 && overlap(t[i].at, t[i].bytes, t[j].at, t[j].bytes)) return SA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < parts.all) return SA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SA_ERR_INVALID_ARG;
+    for (int j = 0; j < 11; ++j)
+        if (j != 2 && overlap(t[2].at, t[2].bytes, t[j].at, t[j].bytes)) return SA_ERR_INVALID_ARG;
+
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    int32_t* idx = reinterpret_cast<int32_t*>(ws + parts.idx);
+    int32_t* pos = rot ? reinterpret_cast<int32_t*>(ws + parts.pos) : nullptr;
+    const int topk = (int)(first + window);
+    const Batch a = {page_table, max_pages, table_stride, b, n_pages, q_start, kv_len, page};
+    const int cols = (topk + 511) / 512 < 64 ? (topk + 511) / 512 : 64;
+    cudaError_t e = launch_pdl(window_rows_kernel, dim3((unsigned)n, cols), dim3(128), 0, st, a, n, (int)window,
+                               (int)first, topk, idx, pos, npos, reinterpret_cast<uint32_t*>(ws));
+    if (e != cudaSuccess) return SA_ERR_CUDA;
+    AttnCall c;
+    c.q = q;
+    c.kv = kv;
+    c.kv_scale = kv_scale;
+    c.kv_format = kv_format;
+    c.sink = sink;
+    c.idx = idx;
+    c.softmax_scale = softmax_scale;
+    c.b = 1;
+    c.s = n;
+    c.h = h;
+    c.d = d;
+    c.rows = rows;
+    c.topk = topk;
+    c.o = o;
+    c.status = reinterpret_cast<uint32_t*>(ws);
+    c.scratch = ws + SA_STATUS_BYTES;
+    c.scratch_bytes = parts.idx - SA_STATUS_BYTES;
+    c.stream = st;
+    c.rope = rot;
+    c.rope_dim = rot ? rope_dim : 0;
+    c.rope_at = pos;
+    c.n_live = q_start + b;
+    c.lse = lse;
+    e = tc ? attn_tc_launch(c) : attn_mma_launch(c);
+    return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}

@@ -1,0 +1,409 @@
+"""page_write and window_attn on the GPU, against their formulas in 64 bits."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sparse_latent_attention_gb300 as sa
+from sparse_latent_attention_gb300._lib import SA_ERR_INDEX, SA_STATUS_BYTES
+from tests import _cache, _paged
+from tests.test_gpu_cache import dev  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+MIX = ([1, 4, 0, 37, 1], [0, 90, 5, 0, 700])  # sequences' new tokens and what their caches held
+
+
+def _rows(dev, n, d, seed, pad=0):  # noqa: F811
+    g = torch.Generator(device=dev).manual_seed(seed)
+    x = torch.randn(n, d + pad, device=dev, generator=g) * torch.exp(torch.randn(n, 1, device=dev, generator=g))
+    return x.to(torch.bfloat16)[:, :d]
+
+
+def _pools(dev, bt, d, fmt, seed, pad=0):  # noqa: F811
+    """pages, codes, scales with arbitrary contents (pad: rows that lie apart)."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    shape = (bt.n_pages, bt.page)
+    pages = torch.randn(*shape, d + pad, device=dev, generator=g).to(torch.bfloat16)[..., :d]
+    if not fmt:
+        return pages, None, None
+    both = torch.randint(0, 256, (*shape, (d if fmt == "fp8" else d // 2) + d // 32 + pad), device=dev, generator=g,
+                         dtype=torch.uint8)
+    w = d if fmt == "fp8" else d // 2
+    codes, scales = both[..., :w], both[..., w:w + d // 32]   # side by side in a row
+    return (pages, codes, scales) if pad else (pages, codes.contiguous(), scales.contiguous())
+
+
+def _want(bt, x, weight, rot):
+    y = x[:bt.live].double() if weight is None else _paged.norm(x[:bt.live], weight, EPS)
+    return y if rot is None else _paged.turned(y, rot, bt.positions().to(y.device))
+
+
+def _check_rows(bt, y, pages, codes, scales, quant, before, rel):
+    rows = bt.rows().to(y.device)
+    for t, old in zip((pages, codes, scales), before):  # every other row is as it was
+        if t is not None:
+            other = torch.ones(bt.n_pages * bt.page, dtype=torch.bool, device=y.device)
+            other[rows] = False
+            assert torch.equal(t.flatten(0, 1)[other].view(torch.uint8), old.flatten(0, 1)[other].view(torch.uint8))
+    # y's parts may cancel in a rotation: its error is relative to the pair's length
+    if codes is not None:
+        c, s = codes.flatten(0, 1)[rows], scales.flatten(0, 1)[rows]
+        v = c.view(torch.float8_e4m3fn).double() if quant == "fp8" else _paged.fp4_values(c)
+        _paged.check_codes(v, s, y, quant, rel)
+        if pages is not None:
+            rt = v * _paged.pow2(s.long() - 127).repeat_interleave(32, -1)
+            assert torch.equal(pages.flatten(0, 1)[rows].double(), rt)
+    elif quant is None:
+        got = pages.flatten(0, 1)[rows].double()
+        assert ((got - y).abs() <= (2.0 ** -8 + rel) * y.abs() + 2.0 ** -135).all()
+    return rows
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("d,page,norm,rope,pad", [
+    (512, 64, True, 64, 0), (512, 1, False, 0, 0), (512, 100, True, 512, 0), (64, 16, True, 2, 0), (32, 3, False, 32, 0),
+    (448, 64, True, 64, 32), (1024, 48, True, 128, 0), (544, 64, True, 6, 0), (512, 64, True, 64, 1), (96, 5, True, 10, 3),
+])
+def test_page_write(dev, fmt, d, page, norm, rope, pad):  # noqa: F811
+    bt = _paged.Batch(*MIX, page, d + page, spare=3)
+    x = _rows(dev, bt.n, d, d, pad)
+    w = 1 + 0.3 * torch.randn(d, device=dev) if norm else None
+    rot = _paged.rotations(800, rope).to(dev) if rope else None
+    quant = None if fmt == "bf16" else fmt
+    pages, codes, scales = _pools(dev, bt, d, quant, 3, pad)
+    before = [None if t is None else t.clone() for t in (pages, codes, scales)]
+    ws = sa.new_window_workspace(bt.n, bt.b, 1, 64, 1, 0, page)
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, codes=codes, scales=scales, weight=w, eps=EPS,
+                  rope=rot, workspace=ws)
+    # (a rotation keeps what f32 loses: the error stays relative to the turned value but for a full cancellation)
+    rows = _check_rows(bt, _want(bt, x, w, rot), pages, codes, scales, quant, before, _paged.NORM_REL)
+    assert sa.read_status(ws) == 0
+    # codes alone, and the round trip alone, are the same rows
+    if quant:
+        c2, s2 = before[1].clone(), before[2].clone()
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, codes=c2, scales=s2, weight=w, eps=EPS, rope=rot)
+        assert torch.equal(c2, codes) and torch.equal(s2, scales)
+        p2 = before[0].clone()
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=p2, quant=quant, weight=w, eps=EPS, rope=rot)
+        assert torch.equal(p2.flatten(0, 1)[rows], pages.flatten(0, 1)[rows])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_page_write_quantises_as_act_quant(dev, fmt):  # noqa: F811
+    """Without norm and rotation the codes are those of the library's quantisers, bit for bit."""
+    bt = _paged.Batch([300], [13], 64, 1)
+    x = _rows(dev, 300, 512, 2)
+    _, codes, scales = _pools(dev, bt, 512, fmt, 3)
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, codes=codes, scales=scales)
+    c = torch.empty(300, codes.shape[2], dtype=torch.uint8, device=dev)
+    s = torch.empty(300, 16, dtype=torch.uint8, device=dev)
+    (sa.act_quant_fp8 if fmt == "fp8" else sa.act_quant_fp4)(x, codes=c, scales=s)
+    rows = bt.rows().to(dev)
+    assert torch.equal(codes.flatten(0, 1)[rows], c) and torch.equal(scales.flatten(0, 1)[rows], s)
+
+
+@pytest.mark.parametrize("b", [1, 31, 32, 33, 1000, 1100])
+@pytest.mark.parametrize("each", [1, 17])
+def test_page_write_many_sequences(dev, b, each):  # noqa: F811
+    """A token's sequence among many, some without tokens, with few tokens a warp and with several."""
+    new = [each if i % 5 != 3 or b == 1 else 0 for i in range(b)]
+    bt = _paged.Batch(new, [(7 * i) % 50 for i in range(b)], 16, b)
+    x = _rows(dev, bt.n, 64, b)
+    pages, _, _ = _pools(dev, bt, 64, None, 4)
+    before = pages.clone()
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages)
+    _check_rows(bt, x.double(), pages, None, None, None, (before, None, None), 0.0)
+
+
+def test_page_write_bad_pages(dev):  # noqa: F811
+    """Positions without a page, past the table, below zero or past the rotations are not written."""
+    bt = _paged.Batch([8, 8, 8, 8], [0, 60, 0, 90], 16, 5)
+    x = _rows(dev, bt.n, 128, 6)
+    pages, _, _ = _pools(dev, bt, 128, None, 7)
+    before, rot = pages.clone(), _paged.rotations(95, 64).to(dev)
+    bt.table[0, 0] = bt.n_pages            # no such page
+    bt.table[1, 4] = -1                    # positions 64 .. 67
+    bt.kv_len[2] = 3                       # its first five tokens have no position
+    ws = sa.new_window_workspace(bt.n, 4, 1, 64, 1, 0, 16)
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, rope=rot, workspace=ws)
+    assert sa.read_status(ws, clear=True) == SA_ERR_INDEX
+    written = (pages != before).flatten(0, 1).any(-1).nonzero().flatten().tolist()
+    want = [bt.row(1, p) for p in range(60, 64)] + [bt.row(2, p) for p in range(3)] + [bt.row(3, p) for p in range(90, 95)]
+    assert sorted(written) == sorted(want)
+    bt.kv_len[2], bt.kv_len[0] = 1 << 30, 8   # far past the table
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, workspace=ws)
+    assert sa.read_status(ws, clear=True) == SA_ERR_INDEX
+    # negative positions alone are no error
+    few = _paged.Batch([4], [0], 16, 5)
+    few.kv_len[0] = 2
+    sa.page_write(x[:4], few.table, few.q_start, few.kv_len, pages=pages[:few.n_pages], workspace=ws)
+    assert sa.read_status(ws) == 0
+
+
+def test_page_write_nan_and_inf(dev):  # noqa: F811
+    bt = _paged.Batch([3], [0], 16, 5)
+    x = _rows(dev, 3, 64, 6)
+    x[0, 3], x[1, 40] = float("nan"), float("inf")
+    for fmt in ("fp8", "fp4"):
+        _, codes, scales = _pools(dev, bt, 64, fmt, 3)
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, codes=codes, scales=scales)
+        c, s = codes.flatten(0, 1)[bt.rows().to(dev)], scales.flatten(0, 1)[bt.rows().to(dev)]
+        v = c.view(torch.float8_e4m3fn).double() if fmt == "fp8" else _paged.fp4_values(c)
+        y = x.double()
+        assert v[0, 3].isnan() if fmt == "fp8" else v[0, 3] == 0
+        assert v[1, 40] == (448 if fmt == "fp8" else 6) and int(s[1, 1]) < 255
+        v[0, 3] = y[0, 3] = 0.0
+        _paged.check_codes(v[[0, 2]], s[[0, 2]], y[[0, 2]], fmt, 0.0)
+        _paged.check_codes(v[1:2, :32], s[1:2, :1], y[1:2, :32], fmt, 0.0)
+
+
+# ---------------------------------------------------------------------------------------------
+# window_attn
+# ---------------------------------------------------------------------------------------------
+
+def _attn_inputs(dev, bt, h, d, fmt, window, first, seed, peak=1.0):  # noqa: F811
+    """q, sink, and a pool whose rows that no token sees hold NaN and infinities."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    q = (peak * torch.randn(bt.n, h, d, device=dev, generator=g)).to(torch.bfloat16)
+    sink = torch.randn(h, device=dev, generator=g)
+    rows = torch.randn(bt.n_pages * bt.page, d, device=dev, generator=g).to(torch.bfloat16)
+    seen = torch.zeros(bt.n_pages * bt.page, dtype=torch.bool, device=dev)
+    idx = bt.visible(window, first).to(dev)
+    seen[idx[idx >= 0].long()] = True
+    if fmt == "bf16":
+        odd = torch.arange(len(rows), device=dev)[:, None] + torch.arange(d, device=dev)
+        trash = torch.where(odd % 3 == 0, float("nan"), torch.where(odd % 3 == 1, float("inf"), -float("inf")))
+        rows = torch.where(seen[:, None], rows, trash.to(torch.bfloat16))
+        return q, sink, rows.view(bt.n_pages, bt.page, d), None
+    codes = torch.empty(len(rows), d if fmt == "fp8" else d // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty(len(rows), d // 32, dtype=torch.uint8, device=dev)
+    (sa.act_quant_fp8 if fmt == "fp8" else sa.act_quant_fp4)(rows, codes=codes, scales=scales)
+    codes[~seen], scales[~seen] = 0x7F, 255   # (e4m3's NaN; the largest scale)
+    return q, sink, codes.view(bt.n_pages, bt.page, -1), scales.view(bt.n_pages, bt.page, -1)
+
+
+def _attend(bt, q, pool, kv_scale, sink, scale, window, first, rot=None, with_lse=True):
+    lse = torch.full(q.shape[:2], 77.0, device=q.device) if with_lse else None
+    out = torch.full_like(q, 55.0)
+    ws = sa.new_window_workspace(bt.n, bt.b, q.shape[1], q.shape[2], window, first, bt.page,
+                                 sa.SA_KV_BF16 if kv_scale is None else
+                                 sa.SA_KV_FP8_E4M3 if pool.shape[2] == q.shape[2] else sa.SA_KV_FP4_E2M1)
+    ws[SA_STATUS_BYTES:].fill_(0xFF)   # (NaN wherever it is read unwritten)
+    got = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, scale, window, first=first,
+                         kv_scale=kv_scale, out=out, lse=lse, rope=rot, workspace=ws)
+    assert got is out
+    assert sa.read_status(ws) == 0
+    assert (out[bt.live:] == 55.0).all() and (lse is None or (lse[bt.live:] == 77.0).all())
+    return out[:bt.live], None if lse is None else lse[:bt.live]
+
+
+def _check_attn(bt, q, pool, kv_scale, sink, window, first, rot=None, scale=None):
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    o, lse = _attend(bt, q, pool, kv_scale, sink, scale, window, first, rot)
+    want, lse_w, tol, lse_tol = _paged.attention(bt, q, pool, kv_scale, sink, scale, window, first, rot)
+    off = (o.double() - want).abs() > tol
+    assert not off.any(), f"{int(off.sum())} of {off.numel()} off, first {off.nonzero()[0].tolist()}: " \
+                          f"{o[off][:4].tolist()} {want[off][:4].tolist()}"
+    assert ((lse.double() - lse_w).abs() <= lse_tol)[lse_w.isfinite()].all()
+    assert torch.equal(lse[lse_w.isinf()].double(), lse_w[lse_w.isinf()])
+    alone, _ = _attend(bt, q, pool, kv_scale, sink, scale, window, first, rot, with_lse=False)
+    assert torch.equal(alone, o)
+    return o
+
+
+ATTN = [  # new, held, page, h, d, window, first, spare
+    ([1], [0], 64, 64, 512, 128, 4, 0),                    # a cache of one row
+    ([1], [5000], 64, 64, 512, 128, 4, 0),                 # one token, its rows split over the GPU
+    ([1] * 20, [37 * i for i in range(20)], 64, 64, 512, 100, 16, 3),
+    ([1] * 5, [3000, 0, 64, 63, 9000], 32, 128, 512, 1024, 64, 0),
+    ([130, 0, 1, 64], [0, 9, 700, 33], 64, 64, 512, 128, 4, 5),
+    ([300], [0], 64, 64, 512, 128, 0, 0),
+    ([70, 3], [1000, 100], 64, 128, 512, 300, 40, 0),
+    ([257], [123], 32, 16, 512, 64, 7, 1),                 # eight tokens a tile
+    ([200, 90], [0, 77], 64, 1, 512, 33, 2, 0),            # 128 tokens a tile
+    ([33], [500], 64, 40, 512, 200, 0, 0),                 # a tile's edge inside a token
+    ([50], [64], 64, 100, 512, 1, 0, 0),                   # itself alone
+    ([9], [20], 64, 64, 512, 1, 12, 0),
+    ([40], [300], 64, 64, 512, 4000, 500, 0),              # everything before it
+    ([20], [300], 16, 64, 512, 128, 4, 0),                 # pages that end inside a tile
+    ([20], [300], 100, 64, 512, 128, 4, 0),
+    ([20], [300], 1, 64, 512, 128, 4, 0),
+    ([30, 1], [0, 400], 64, 64, 64, 128, 4, 2),            # other head dims
+    ([30, 1], [0, 400], 48, 40, 192, 100, 9, 0),
+    ([5, 1], [0, 4000], 64, 128, 448, 2000, 0, 0),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("case", ATTN, ids=[str(i) for i in range(len(ATTN))])
+def test_window_attn(dev, case, fmt):  # noqa: F811
+    new, held, page, h, d, window, first, spare = case
+    bt = _paged.Batch(new, held, page, 11, spare)
+    q, sink, pool, sc = _attn_inputs(dev, bt, h, d, fmt, window, first, 12, peak=2.0)
+    _check_attn(bt, q, pool, sc, sink, window, first)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("rope", [2, 64, 512])
+@pytest.mark.parametrize("new,held", [([40, 0, 70], [0, 3, 600]), ([1, 1], [5000, 10])])
+def test_window_attn_turned_back(dev, fmt, rope, new, held):  # noqa: F811
+    bt = _paged.Batch(new, held, 64, 13, 2)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 14)
+    _check_attn(bt, q, pool, sc, sink, 128, 4, rot=_paged.rotations(5001, rope).to(dev))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_sinks_and_scales(dev, fmt):  # noqa: F811
+    bt = _paged.Batch([20, 1], [0, 300], 64, 15)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 64, 4, 16)
+    sink[0], sink[1], sink[2], sink[3] = -float("inf"), 80.0, -80.0, float("inf")
+    for scale in (512 ** -0.5, -0.1, 0.0):
+        o = _check_attn(bt, q, pool, sc, sink, 64, 4, scale=scale)
+        assert (o[:, 3] == 0).all()
+
+
+def test_window_attn_peaks(dev):  # noqa: F811
+    """Logits that rise along the row, and far apart: the running maximum moves again and again."""
+    bt = _paged.Batch([64], [900], 64, 17)
+    q, sink, pool, _ = _attn_inputs(dev, bt, 64, 512, "bf16", 800, 32, 18, peak=8.0)
+    at = torch.tensor([bt.row(0, p) for p in range(964)], device=dev)
+    pool.view(-1, 512)[at] *= torch.linspace(0.1, 3.0, 964, device=dev)[:, None].to(torch.bfloat16)
+    _check_attn(bt, q, pool, None, sink, 800, 32)
+
+
+def test_window_attn_bad_pages(dev):  # noqa: F811
+    """A position without a page is not attended to, and noted; entries that no token meets are not looked at;
+    a token without a position attends to nothing."""
+    for fmt in ("bf16", "fp8"):
+        bt = _paged.Batch([3, 4], [500, 0], 64, 19)
+        q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 20)
+        want, _ = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+        bt.table[0, 1:5] = 1 << 30                       # positions 64 .. 319: out of everybody's sight
+        got, _ = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+        assert torch.equal(got, want)
+        hold = bt.table[0, 6].item()
+        bt.table[0, 6] = bt.n_pages                      # positions 384 .. 447
+        ws = sa.new_window_workspace(7, 2, 64, 512, 128, 4, 64, sa.SA_KV_FP8_E4M3 if sc is not None else 0)
+        got = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 128, first=4, kv_scale=sc,
+                             workspace=ws)
+        assert sa.read_status(ws, clear=True) == SA_ERR_INDEX
+        bt.table_cpu[0, 6] = hold
+        idx = bt.visible(128, 4).to(dev)
+        lost = (idx // 64) == hold
+        idx = torch.where(lost, -1, idx).to(torch.int32)
+        kv = _cache.rows_f64(torch.nan_to_num(pool.view(1, -1, 512).float(), 0, 0, 0).to(torch.bfloat16) if sc is None
+                             else pool.view(1, -1, 512), None if sc is None else sc.view(1, -1, 16).clamp(max=140), 512)
+        kv = torch.nan_to_num(kv)
+        o, _, tol, _ = _cache.attention(q[None], kv, sink, idx[None], 0.05)
+        assert ((got.double() - o[0]).abs() <= tol[0]).all()
+        bt.table[0, 6] = hold
+        bt.kv_len[1] = 2                                  # tokens 0 and 1 of the second have no position
+        got, lse = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+        assert (got[3:5] == 0).all() and torch.allclose(lse[3:5], sink.expand(2, -1)) and torch.equal(got[:3], want[:3])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_graph(dev, fmt):  # noqa: F811
+    """A captured step replayed with other lengths, pages and contents: the write, then the attention."""
+    bt = _paged.Batch([1, 1, 2], [100, 400, 40], 64, 21)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 22)
+    x = _rows(dev, 4, 512, 23)
+    ws = sa.new_window_workspace(4, 3, 64, 512, 128, 4, 64, sa.SA_KV_FP8_E4M3 if sc is not None else 0)
+    put = dict(pages=pool) if sc is None else dict(codes=pool, scales=sc)
+
+    def step():
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, workspace=ws, **put)
+        return sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 128, first=4, kv_scale=sc,
+                              workspace=ws)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = step()
+    for k in range(3):
+        nxt = _paged.Batch([1, 1, 2], [100 + 30 * k, 300 - k, 64 * k], 64, 30 + k)
+        m = min(nxt.max_pages, bt.max_pages)
+        bt.table.fill_(-1)
+        bt.table[:, :m] = nxt.table[:, :m] % pool.shape[0]
+        bt.table_cpu, bt.held = bt.table.cpu(), nxt.held
+        # (distinct pages: the pool is smaller than the new batch may ask for)
+        free = iter(torch.randperm(pool.shape[0], generator=torch.Generator().manual_seed(k)).tolist())
+        for i in range(3):
+            for j in range(-(-(nxt.held[i] + bt.new[i]) // 64)):
+                bt.table_cpu[i, j] = next(free)
+        bt.table.copy_(bt.table_cpu)
+        bt.kv_len.copy_(nxt.kv_len)
+        q2, _, pool2, sc2 = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 40 + k)
+        for a, b in ((q, q2), (pool, pool2), (sc, sc2)):
+            if a is not None:
+                a.copy_(b)
+        x.copy_(_rows(dev, 4, 512, 50 + k))
+        graph.replay()
+        assert sa.read_status(ws) == 0
+        want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 128, 4)
+        assert ((o.double() - want).abs() <= tol).all()
+
+
+def test_a_decode_loop(dev):  # noqa: F811
+    """Norm, write and attention as a program uses them: a prompt in pieces, then tokens one by one, against the
+    whole sequence at once; the window's pages behind it are given back on the way."""
+    d, h, window, first, page, total = 512, 64, 100, 4, 32, 230
+    g = torch.Generator(device=dev).manual_seed(60)
+    raw = torch.randn(total, d, device=dev, generator=g).to(torch.bfloat16)
+    q = torch.randn(total, h, d, device=dev, generator=g).to(torch.bfloat16)
+    w, sink = 1 + 0.1 * torch.randn(d, device=dev, generator=g), torch.randn(h, device=dev, generator=g)
+    rot = _paged.rotations(total, 64).to(dev)
+    one = _paged.Batch([total], [0], page, 61)
+    pool = torch.zeros(one.n_pages, page, d, dtype=torch.bfloat16, device=dev)
+    x = sa.add_rms_norm(raw, w)
+    sa.page_write(x, one.table, one.q_start, one.kv_len, pages=pool, rope=rot, quant="fp8")
+    whole = sa.window_attn(q, pool, sink, one.table, one.q_start, one.kv_len, d ** -0.5, window, first=first, rope=rot)
+    fresh, outs, at = torch.zeros_like(pool), [], 0
+    for n in [90, 33, 64] + [1] * 43:
+        bt = _paged.Batch([n], [at], page, 61, extra_pages=one.n_pages)
+        table = one.table.clone()
+        behind = max(0, at - window) // page      # pages that nobody sees any more, but the first
+        table[0, 1:behind] = -1
+        xs = sa.add_rms_norm(raw[at:at + n], w)
+        sa.page_write(xs, table, bt.q_start, bt.kv_len, pages=fresh, rope=rot, quant="fp8")
+        ws = sa.new_window_workspace(n, 1, h, d, window, first, page)
+        outs.append(sa.window_attn(q[at:at + n], fresh, sink, table, bt.q_start, bt.kv_len, d ** -0.5, window,
+                                   first=first, rope=rot, workspace=ws))
+        assert sa.read_status(ws) == 0
+        at += n
+    want, _, tol, _ = _paged.attention(one, q, pool, None, sink, d ** -0.5, window, first, rot)
+    assert torch.equal(fresh.flatten(0, 1)[one.rows().to(dev)], pool.flatten(0, 1)[one.rows().to(dev)])
+    for got in (whole, torch.cat(outs)):
+        assert ((got.double() - want).abs() <= tol).all()
+
+
+def test_streams_and_workspaces(dev):  # noqa: F811
+    """Two calls at once on streams of their own, each with its own workspace, and outputs made on the stream."""
+    bts = [_paged.Batch([1] * 9, [200 * i for i in range(9)], 64, 70 + k) for k in range(2)]
+    ins = [_attn_inputs(dev, bt, 64, 512, "fp8" if k else "bf16", 256, 8, 72 + k) for k, bt in enumerate(bts)]
+    streams = [torch.cuda.Stream() for _ in bts]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got = [sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 256, first=8, kv_scale=sc, stream=st)
+               for bt, (q, sink, pool, sc), st in zip(bts, ins, streams)]
+    torch.cuda.synchronize()
+    for bt, (q, sink, pool, sc), o in zip(bts, ins, got):
+        want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 256, 8)
+        assert ((o.double() - want).abs() <= tol).all()
+
+
+def test_nothing_to_do(dev):  # noqa: F811
+    z = dict(dtype=torch.int32, device=dev)
+    q = torch.empty(0, 64, 512, dtype=torch.bfloat16, device=dev)
+    pool, sink = torch.zeros(2, 64, 512, dtype=torch.bfloat16, device=dev), torch.zeros(64, device=dev)
+    assert sa.window_attn(q, pool, sink, torch.zeros(1, 2, **z), torch.zeros(2, **z), torch.zeros(1, **z), 1.0, 8).shape == q.shape
+    sa.page_write(q[:, 0], torch.zeros(1, 2, **z), torch.zeros(2, **z), torch.zeros(1, **z), pages=pool)
+    # no sequence: everything is left as it was
+    out = torch.full((3, 64, 512), 5.0, dtype=torch.bfloat16, device=dev)
+    sa.window_attn(torch.zeros_like(out), pool, sink, torch.zeros(0, 2, **z), torch.zeros(1, **z), torch.zeros(0, **z),
+                   1.0, 8, out=out)
+    assert (out == 5.0).all()

@@ -1,0 +1,147 @@
+"""The paged cache, its window attention and the residual norm without a GPU: exported symbols, workspace sizes,
+and every refusal before anything is enqueued."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import sparse_latent_attention_gb300 as sa
+from sparse_latent_attention_gb300 import _lib, build
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = (_lib.SA_OK, _lib.SA_ERR_INVALID_ARG, _lib.SA_ERR_UNSUPPORTED,
+                                       _lib.SA_ERR_WORKSPACE)
+
+
+def at(n, off=0):
+    """A made-up device address (never dereferenced), far from those of other n."""
+    return ctypes.c_void_p((n << 40) + off)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def test_exports_every_declared_symbol(lib):
+    names = _lib.declared_symbols("serve")
+    assert set(names) == {"sa_add_rms_norm", "sa_page_write", "sa_window_attn", "sa_window_attn_workspace_size"}
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(n=0, x=None), OK), (dict(n=-1), INVALID), (dict(d=0), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(kind=3), INVALID), (dict(kind=0), INVALID), (dict(res=None), INVALID),
+    (dict(out=None, codes=None, scales=None), INVALID), (dict(scales=None), INVALID), (dict(codes=None), INVALID),
+    (dict(d=63), INVALID), (dict(d=32800, xs=32800, rs=32800, os=32800, cs=32800, ss=1025), UNSUPPORTED),
+    (dict(x=None), INVALID), (dict(x=at(1, 1)), INVALID), (dict(xs=63), INVALID), (dict(w=None), INVALID),
+    (dict(w=at(2, 2)), INVALID), (dict(res=at(3, 1)), INVALID), (dict(kind=2, res=at(3, 2)), INVALID),
+    (dict(rs=63), INVALID), (dict(os=63), INVALID), (dict(out=at(4, 1)), INVALID), (dict(cs=63), INVALID),
+    (dict(ss=1), INVALID), (dict(out=at(1), os=72), INVALID), (dict(out=at(1, 128)), INVALID),
+    (dict(out=at(3)), INVALID), (dict(res=at(1, 2)), INVALID), (dict(codes=at(1, 383)), INVALID),
+    (dict(codes=at(4, 10)), INVALID), (dict(scales=at(5, 191)), INVALID), (dict(scales=at(3, 383)), INVALID),
+    (dict(out=at(2, 254)), INVALID), (dict(kind=2, scales=at(3, 767)), INVALID),
+])
+def test_add_rms_norm_refuses(lib, change, code):
+    a = dict(x=at(1), n=3, d=64, xs=64, w=at(2), eps=1e-6, res=at(3), kind=1, rs=64, out=at(4), os=64, codes=at(5),
+             cs=64, scales=at(6), ss=2)
+    a.update(change)
+    assert lib.sa_add_rms_norm(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(n=0, x=None), OK), (dict(b=0, q_start=None), OK), (dict(n=-1), INVALID), (dict(d=40), INVALID),
+    (dict(d=0), INVALID), (dict(d=1056, xs=1056, pgs=1056, pgp=1 << 20, cs=1056, ss=40), UNSUPPORTED),
+    (dict(n=1 << 31), UNSUPPORTED), (dict(n_pages=1 << 38), UNSUPPORTED), (dict(b=-1), INVALID),
+    (dict(n_pages=-1), INVALID), (dict(page=0), INVALID), (dict(max_pages=-1), INVALID), (dict(quant=3), INVALID),
+    (dict(quant=0), INVALID), (dict(codes=None, scales=None, pages=None), INVALID), (dict(scales=None), INVALID),
+    (dict(x=None), INVALID), (dict(x=at(1, 1)), INVALID), (dict(xs=63), INVALID), (dict(q_start=None), INVALID),
+    (dict(kv_len=None), INVALID), (dict(table=None), INVALID), (dict(table=at(2, 2)), INVALID),
+    (dict(ts=3), INVALID), (dict(pages=at(5, 1)), INVALID), (dict(pgs=63), INVALID), (dict(pgp=511), INVALID),
+    (dict(cs=63), INVALID), (dict(cp=511), INVALID), (dict(ss=1), INVALID), (dict(sp=15), INVALID),
+    (dict(w=at(8, 2)), INVALID), (dict(w=at(8), eps=-1.0), INVALID), (dict(rot=at(9, 4)), INVALID),
+    (dict(rot=at(9), rope=63), INVALID), (dict(rot=at(9), rope=66), INVALID), (dict(rot=at(9), rope=0), INVALID),
+    (dict(rot=at(9), npos=-1), INVALID), (dict(status=at(10, 2)), INVALID),
+    (dict(pages=at(1, 64)), INVALID), (dict(codes=at(1, 64)), INVALID), (dict(scales=at(1, 64)), INVALID),
+    (dict(codes=at(5, 64)), INVALID), (dict(scales=at(6, 64)), INVALID), (dict(codes=at(2, 4)), INVALID),
+    (dict(codes=at(3, 4)), INVALID), (dict(codes=at(4, 4)), INVALID), (dict(w=at(5, 64)), INVALID),
+    (dict(rot=at(5, 64)), INVALID), (dict(status=at(6, 64)), INVALID),
+])
+def test_page_write_refuses(lib, change, code):
+    a = dict(x=at(1), n=3, d=64, xs=64, table=at(2), max_pages=4, ts=4, q_start=at(3), kv_len=at(4), b=2, n_pages=10,
+             page=8, quant=1, pages=at(5), pgs=64, pgp=512, codes=at(6), cs=64, cp=512, scales=at(7), ss=2, sp=16, w=None,
+             eps=1e-6, rot=None, npos=100, rope=64, status=None)
+    a.update(change)
+    assert lib.sa_page_write(*a.values(), None) == code
+
+
+def test_page_write_takes_rows_between_one_another(lib):
+    """Codes and scales side by side in a row or in a page are no overlap; a byte further they are one.  (The calls
+    stop at a misaligned status word, which is looked at first, or at the overlap: neither is enqueued.)"""
+    a = dict(x=at(1), n=3, d=64, xs=64, table=at(2), max_pages=4, ts=4, q_start=at(3), kv_len=at(4), b=2, n_pages=10,
+             page=8, quant=1, pages=None, pgs=0, pgp=0, codes=at(6), cs=66, cp=528, scales=at(6, 63), ss=66, sp=528,
+             w=None, eps=1e-6, rot=None, npos=0, rope=0, status=None)
+    assert lib.sa_page_write(*a.values(), None) == INVALID           # the row's last code
+    a.update(cs=64, scales=at(6, 511), ss=2)
+    assert lib.sa_page_write(*a.values(), None) == INVALID           # the page's last code
+    a.update(scales=at(6, 513))
+    assert lib.sa_page_write(*a.values(), None) == INVALID           # the next page's first
+
+
+@pytest.mark.parametrize("change,code", [
+    ({}, WORKSPACE), (dict(n=0, q=None), OK), (dict(b=0), OK), (dict(fmt=3), INVALID), (dict(fmt=1), INVALID),
+    (dict(scale_ptr=at(9)), INVALID), (dict(fmt=1, scale_ptr=at(9, 4)), INVALID), (dict(fmt=1, scale_ptr=at(9)), WORKSPACE),
+    (dict(n=-1), INVALID), (dict(h=0), INVALID), (dict(h=129), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
+    (dict(d=576), UNSUPPORTED), (dict(window=0), INVALID), (dict(window=1 << 30), INVALID), (dict(first=-1), INVALID),
+    (dict(first=(1 << 30) - 128), INVALID), (dict(page=0), INVALID), (dict(n_pages=-1), INVALID),
+    (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED), (dict(max_pages=-1), INVALID),
+    (dict(ts=3), INVALID), (dict(q=None), INVALID), (dict(q=at(1, 8)), INVALID), (dict(kv=None), INVALID),
+    (dict(kv=at(2, 8)), INVALID), (dict(sink=None), INVALID), (dict(sink=at(3, 2)), INVALID), (dict(o=None), INVALID),
+    (dict(o=at(7, 8)), INVALID), (dict(table=None), INVALID), (dict(q_start=None), INVALID), (dict(kv_len=None), INVALID),
+    (dict(q_start=at(5, 2)), INVALID), (dict(lse=at(8, 2)), INVALID), (dict(rot=at(10)), WORKSPACE),
+    (dict(rot=at(10, 4)), INVALID), (dict(rot=at(10), rope=63), INVALID), (dict(rot=at(10), npos=0), INVALID),
+    (dict(rot=at(10), d=256), UNSUPPORTED), (dict(o=at(1)), INVALID), (dict(o=at(2, 64)), INVALID), (dict(o=at(4)), INVALID),
+    (dict(o=at(5)), INVALID), (dict(o=at(6)), INVALID), (dict(o=at(3)), INVALID), (dict(lse=at(7, 64)), INVALID),
+    (dict(lse=at(1, 64)), INVALID), (dict(lse=at(2, 64)), INVALID), (dict(rot=at(10), lse=at(10)), INVALID),
+    (dict(ws=at(11), ws_bytes=255), WORKSPACE), (dict(ws=at(11, 64), ws_bytes=1 << 30), INVALID),
+    (dict(ws=at(7), ws_bytes=1 << 30), INVALID), (dict(ws=at(2), ws_bytes=1 << 30), INVALID),
+    (dict(lse=at(11, 1024), ws=at(11), ws_bytes=1 << 30), INVALID),
+])
+def test_window_attn_refuses(lib, change, code):
+    a = dict(q=at(1), kv=at(2), scale_ptr=None, fmt=0, sink=at(3), table=at(4), max_pages=4, ts=4, q_start=at(5),
+             kv_len=at(6), scale=0.1, n=3, b=2, h=64, d=512, n_pages=10, page=64, window=128, first=4, o=at(7), lse=at(8),
+             rot=None, npos=100, rope=64, ws=None, ws_bytes=0)
+    a.update(change)
+    assert lib.sa_window_attn(*a.values(), None) == code
+
+
+def test_window_attn_workspace_size(lib):
+    f = lib.sa_window_attn_workspace_size
+    for fmt in (0, 1, 2):
+        assert f(0, 0, 64, 512, 128, 4, 64, fmt) >= _lib.SA_STATUS_BYTES
+        assert f(8192, 3, 64, 512, 128, 4, 64, fmt) >= _lib.SA_STATUS_BYTES
+    for bad in ((-1, 1, 64, 512, 128, 4, 64, 0), (1, 1, 0, 512, 128, 4, 64, 0), (1, 1, 64, 500, 128, 4, 64, 0),
+                (1, 1, 64, 512, 0, 4, 64, 0), (1, 1, 64, 512, 128, -1, 64, 0), (1, 1, 64, 512, 128, 4, 0, 0),
+                (1, 1, 64, 512, 128, 4, 64, 3), (1 << 25, 1, 64, 512, 128, 4, 64, 0)):
+        assert f(*bad) == 0
+    with pytest.raises(sa.SparseAttnError):
+        sa.window_workspace_size(1, 1, 64, 500, 128, 4, 64)
+
+
+def test_host_tensors_are_refused():
+    """Tensors that are not on a GPU, or of another type, are refused before the library is called."""
+    i = dict(dtype=torch.int32)
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64)
+    with pytest.raises(TypeError):
+        sa.add_rms_norm(x, w)
+    with pytest.raises(TypeError):
+        sa.page_write(x, torch.zeros(1, 1, **i), torch.zeros(2, **i), torch.zeros(1, **i), pages=torch.zeros(1, 8, 64))
+    with pytest.raises(TypeError):
+        sa.window_attn(x[:, None], torch.zeros(1, 8, 64, dtype=torch.bfloat16), torch.zeros(1), torch.zeros(1, 1, **i),
+                       torch.zeros(2, **i), torch.zeros(1, **i), 1.0, 8)
+    with pytest.raises(TypeError):
+        sa.add_rms_norm(None, w)
