@@ -1373,6 +1373,30 @@ bool encode_rows_map(CUtensorMap& map, const void* rows, int d, int64_t n, int b
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_blocks_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows, int blocks) {
+    auto encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t gdim[3] = {64, (cuuint64_t)n, (cuuint64_t)d / 64};
+    const cuuint64_t gstride[2] = {(cuuint64_t)d * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), gdim, gstride, box,
+                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_groups_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows, int blocks) {
+    auto encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t gdim[4] = {64, 8, (cuuint64_t)d / 64, (cuuint64_t)n / 8};
+    const cuuint64_t gstride[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 16};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)blocks, (cuuint32_t)box_rows / 8};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), gdim, gstride, box,
+                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows) {
     (void)h;
     (void)b;

@@ -90,6 +90,11 @@ cudaError_t attn_tc_launch(const AttnCall& c);
 // The TMA map of n bf16 rows of d, in boxes of [box_rows x 64] with the 128-byte swizzle; false when the
 // driver has no encoder or refuses it (sa_attn_tc.cu).
 bool encode_rows_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows);
+// The same rows as (64 elements, row, 64-element block), in boxes of [blocks][box_rows x 64].
+bool encode_blocks_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows, int blocks);
+// The same as (64 elements, row mod 8, 64-element block, row / 8), n a multiple of 8, in boxes of
+// [box_rows / 8][blocks][8 x 64].
+bool encode_groups_map(CUtensorMap& map, const void* rows, int d, int64_t n, int box_rows, int blocks);
 
 // helpers (sa_helpers.cu)
 cudaError_t window_idxs_launch(int64_t start_pos, int64_t seqlen, int window, int32_t* idx,

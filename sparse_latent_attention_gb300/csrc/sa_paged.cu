@@ -214,14 +214,19 @@ bool window_supported(int64_t n, int h, int d) {
     return h <= 128 && d >= 64 && d <= 512 && d % 64 == 0 && n * (int64_t)h < (int64_t(1) << 31);
 }
 
-// The workspace: the status word and the scratch of the family that the call is routed to, then its index
-// table and positions.
+// The workspace: the status word and the scratch of the kernels that the call is routed to, then, of those that
+// gather by row, the index table and positions.
 struct Parts {
     size_t idx, pos, all;
 };
 
-Parts parts_of(int64_t n, int h, int d, int topk, int kv_format) {
+Parts parts_of(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page, int kv_format) {
     if (n < 1) n = 1;
+    if (window_tc_supports(d, kv_format, page)) {
+        const size_t all = SA_STATUS_BYTES + align_up(window_tc_scratch_bytes(n, b, h, window, first), 256);
+        return {all, all, all};
+    }
+    const int topk = (int)(first + window);
     const int fam = routed_family(SA_FAMILY_AUTO, h, d, kv_format, 1, 0);
     Parts s;
     s.idx = align_up(routed_workspace_bytes(fam, 1, n, h, d, 0, topk), 256);
@@ -321,7 +326,7 @@ extern "C" size_t sa_window_attn_workspace_size(int64_t n, int64_t b, int h, int
     using namespace sa;
     if (!kv_format_known(kv_format) || !window_shape(n, b, h, d, window, first, page) || !window_supported(n, h, d))
         return 0;
-    return parts_of(n, h, d, (int)(first + window), kv_format).all;
+    return parts_of(n, b, h, d, window, first, page, kv_format).all;
 }
 
 extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,
@@ -348,7 +353,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
         !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
         !aligned(kv_scale, tc ? 16 : 4) || (b > 1 && table_stride < max_pages))
         return SA_ERR_INVALID_ARG;
-    const Parts parts = parts_of(n, h, d, (int)(first + window), kv_format);
+    const Parts parts = parts_of(n, b, h, d, window, first, page, kv_format);
     const int64_t ob = 2 * n * h * d, rows = n_pages * page;
     const struct {
         const void* at;
@@ -374,10 +379,31 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
 
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    const Batch a = {page_table, max_pages, table_stride, b, n_pages, q_start, kv_len, page};
+    if (window_tc_supports(d, kv_format, page)) {
+        WindowCall c;
+        c.q = q;
+        c.kv = kv;
+        c.sink = sink;
+        c.a = a;
+        c.softmax_scale = softmax_scale;
+        c.n = n;
+        c.h = h;
+        c.window = window;
+        c.first = first;
+        c.o = o;
+        c.lse = lse;
+        c.rope = rot;
+        c.npos = npos;
+        c.rope_dim = rope_dim;
+        c.status = reinterpret_cast<uint32_t*>(ws);
+        c.scratch = ws + SA_STATUS_BYTES;
+        c.stream = st;
+        return window_tc_launch(c) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+    }
     int32_t* idx = reinterpret_cast<int32_t*>(ws + parts.idx);
     int32_t* pos = rot ? reinterpret_cast<int32_t*>(ws + parts.pos) : nullptr;
     const int topk = (int)(first + window);
-    const Batch a = {page_table, max_pages, table_stride, b, n_pages, q_start, kv_len, page};
     const int cols = (topk + 511) / 512 < 64 ? (topk + 511) / 512 : 64;
     cudaError_t e = launch_pdl(window_rows_kernel, dim3((unsigned)n, cols), dim3(128), 0, st, a, n, (int)window,
                                (int)first, topk, idx, pos, npos, reinterpret_cast<uint32_t*>(ws));

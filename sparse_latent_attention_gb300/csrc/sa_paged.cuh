@@ -57,4 +57,30 @@ __device__ __forceinline__ int64_t row_of(const Batch& a, int64_t seq, uint32_t 
 }
 
 }  // namespace paged
+
+// A window_attn call, already validated.
+struct WindowCall {
+    const void* q;
+    const void* kv;
+    const float* sink;
+    paged::Batch a;
+    float softmax_scale;
+    int64_t n;
+    int h;
+    int64_t window, first;
+    void* o;
+    float* lse;
+    const float* rope;
+    int64_t npos;
+    int rope_dim;
+    uint32_t* status;
+    void* scratch;
+    cudaStream_t stream;
+};
+
+// Pairs of SMs over whole blocks of positions (sa_window_tc.cu): d = 512, bf16, pages of a multiple of 32 rows.
+bool window_tc_supports(int d, int kv_format, int page);
+size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int64_t first);
+cudaError_t window_tc_launch(const WindowCall& c);
+
 }  // namespace sa

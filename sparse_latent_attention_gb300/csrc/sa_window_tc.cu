@@ -1,0 +1,867 @@
+// Window attention over a paged bf16 cache, head_dim 512, on pairs of SMs (tcgen05 with cta_group::2).
+//
+// Formulation.  Every query row of a sequence (token x head) attends to rows that its neighbours attend to
+// too, so a task is 128 query rows: consecutive (token, head) rows of one sequence (two tokens of 64 heads,
+// one of 128, eight of 16).  A pair of SMs shares the task, 64 rows each:
+//   S[128 x 128] = Q[128 x 512] . K^T      a tile: four blocks of 32 positions; each SM holds 64 rows of Q and
+//                                          the 512-wide rows of two of the blocks
+//   O[128 x 512] += P[128 x 128] . V       each SM holds its 64 rows of P and all four blocks' rows in its half
+//                                          of d
+// Both are M = 128 products of the pair: an SM's 64 rows fill its 128 TMEM lanes, lanes 0-63 with the first
+// half of the columns and 64-127 with the second.  One SM alone would have O of 128 rows x 512 in all of its
+// TMEM, and M = 64 products run at half the rate (64 rows x N 256 x K 16 take 64 cycles a SM here, measured).
+// TMEM: O in 256 columns, two S buffers of 64.
+//
+// Blocks, not rows, are loaded: 32 positions lie in one page (a page is a multiple of 32 rows), so a block is a TMA
+// box and there is no gather.  K (stages of 64 rows x 128 of d, 16 KB) and V (of a block x 256 of d) go through a ring
+// each, five and four stages, and a tile's softmax runs behind the next tile's logits.
+//
+// Masked positions.  A block is loaded whole, so rows that some or all of the task's tokens do not see come
+// with it, and they may hold anything.  Their p is set to zero, but 0 x NaN is NaN: a logit that is not finite in
+// a column that not every token sees makes the softmax warps clear that row of V (in their half of d) before the
+// product; a row that is not finite gives every query row such a logit.  Rows that see the row have a NaN there
+// anyway.
+//
+// Roles (each CTA of the pair, 448 threads): warps 0 and 13 issue the pair's logits and P.V (rank 0) or pass on that
+// this CTA's stages have landed (rank 1); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 12 V,
+// warp 3 Q; warps 4-7 softmax; warps 8-11 epilogue.  Every wait is bounded; one that gives up raises the timeout bit
+// and every role unwinds.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "sa_internal.cuh"
+#include "sa_paged.cuh"
+#include "sa_tc.cuh"
+
+namespace sa {
+namespace {
+
+using namespace tc;
+
+constexpr int kD = 512;
+constexpr int kM = 128;            // query rows of a task
+constexpr int kBlock = 32;         // positions of a block
+constexpr int kTileBlocks = 4;     // blocks of a tile
+constexpr int kKStages = 5, kVStages = 4;  // of the two rings
+constexpr int kThreads = 448;
+constexpr int kInfos = 4;          // tiles, and tasks, described ahead
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr uint32_t kColO = 0, kColS = 256;
+
+constexpr uint32_t kStageBytes = 16384;
+constexpr uint32_t kQBytes = 65536;  // [8 blocks of 64 d][64 rows][128 B]
+constexpr uint32_t kPBytes = 16384;  // [2 halves of the columns][64 rows][128 B]
+constexpr uint32_t kOffK = 0;
+constexpr uint32_t kOffV = kOffK + kKStages * kStageBytes;
+constexpr uint32_t kOffQ = kOffV + kVStages * kStageBytes;
+constexpr uint32_t kOffP = kOffQ + kQBytes;
+constexpr uint32_t kOffMisc = kOffP + kPBytes;
+
+struct Task {
+    int row0, rows;   // its first row among all of q's, and how many are its own
+    int tok0, off0;   // that row's token and head
+    int pos0;         // that token's position
+    int pmax;         // its last token's
+    int seq, split;
+    int k0, nb;       // the unit's blocks: k0 .. k0 + nb - 1 of the task's
+    int fb, wb;       // block k of the task is k < fb ? k : k - fb + wb of the sequence
+    int more;         // 0: no further task
+};
+
+struct Misc {
+    // full: this CTA's part has landed, and in rank 0 the other's too, which passes it on
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t q_full[4], q_empty[4];          // (the same for a quarter of Q)
+    uint64_t s_full[2], s_empty[2];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
+    uint64_t p_full, p_empty, o_full, o_empty;
+    uint64_t info_full[kInfos];
+    uint64_t task_full[kInfos], task_empty[kInfos];
+    uint64_t stats_full, stats_empty;
+    uint64_t pair_bar[2], done;
+    uint32_t tmem_base;
+    int abort;
+    int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
+    Task task[kInfos];
+    float mx[2][128];
+    float stats_m[64], stats_l[128];
+};
+constexpr uint32_t kSmem = kOffMisc + sizeof(Misc);
+static_assert(kSmem <= 232448, "shared memory budget");
+
+struct Params {
+    paged::Batch a;
+    const float* sink;
+    __nv_bfloat16* o;
+    float* lse;
+    float* part_ml;
+    float* part_o;
+    uint32_t* status;
+    const float* rope;
+    int64_t npos;
+    int rope_dim;
+    float scale_log2;
+    int n;               // tokens
+    int h;
+    int window, first;
+    int n_splits;
+    int64_t n_units;
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An address of this CTA's shared memory in rank 0's.
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+// An arrival at a barrier of either CTA.  What it announces is in shared memory or TMEM, for the tensor core to read
+// (behind a proxy or tcgen05 fence) or to overwrite, so that the default scope does: arrivals and waits of
+// cluster scope wait for a thread's global writes too, and made a tile take 10 k cycles.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
+    return warp_wait(smem_addr(&bar), parity & 1, abort);
+}
+// One arrival for a converged warp, after what every lane did.
+__device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&bar));
+}
+__device__ __forceinline__ void warp_arrive_leader(uint64_t& bar, int lane) {
+    __syncwarp();
+    if (lane == 0) arrive_at(at_leader(smem_addr(&bar)));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                            int32_t w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// The pair's product, from the words of its descriptors (the same in both CTAs); one elected lane issues.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .b64 da, db;\n .reg .pred p, e;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+        " setp.ne.b32 p, %6, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at a barrier in both CTAs once every product issued so far has completed.
+__device__ __forceinline__ void commit_pair(uint64_t& bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(
+            smem_addr(&bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3f(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// 32 bytes at a 32-byte aligned address
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Bits lo .. hi of a word (none where hi < lo).
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 31);
+    return hi < lo ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+}
+// The positions base .. base + 31 that every token from position p0 to p1 sees.
+__device__ __forceinline__ uint32_t seen(const Params& p, int base, int p0, int p1) {
+    return base < 0 ? 0u : bits(p1 - p.window + 1 - base, p0 - base) | bits(0, min(p.first - 1, p0) - base);
+}
+
+// Unit u -> its task (the whole warp calls); false: nothing there.  Sequence i's tiles of 128 rows are numbered
+// from q_start[i] h / 128 + i on: more numbers than tiles, but the same on every CTA without a list of them.
+__device__ __forceinline__ bool task_of(const Params& p, int64_t u, Task& t) {
+    const int64_t tile = u / p.n_splits;
+    const auto first_tile = [&](int64_t i) {
+        const int64_t s = min(max(__ldg(p.a.q_start + i), 0), p.n);
+        return s * p.h / kM + i;
+    };
+    const int64_t seq = paged::last_at_most(p.a.b, tile, first_tile);
+    const int q0 = min(max(__ldg(p.a.q_start + seq), 0), p.n), q1 = min(max(__ldg(p.a.q_start + seq + 1), 0), p.n);
+    const int64_t r0 = (tile - first_tile(seq)) * kM, rows = (int64_t)(q1 - q0) * p.h - r0;
+    if (r0 < 0 || rows <= 0) return false;
+    t.seq = (int)seq;
+    t.split = (int)(u - tile * p.n_splits);
+    t.rows = (int)min(rows, (int64_t)kM);
+    const int tok = (int)(r0 / p.h);
+    t.off0 = (int)(r0 - (int64_t)tok * p.h);
+    t.tok0 = q0 + tok;
+    t.row0 = (int)((int64_t)q0 * p.h + r0);
+    // (lengths far outside the table's range, which are errors, are held where 32 bits do)
+    const int64_t pos = (int64_t)__ldg(p.a.kv_len + seq) - (q1 - q0) + tok;
+    t.pos0 = (int)min(max(pos, -(int64_t(1) << 30)), (int64_t(1) << 31) - 1 - kM);
+    t.pmax = t.pos0 + (t.off0 + t.rows - 1) / p.h;
+    // blocks: the first positions' and the window's, those of both once; none past the table's last page
+    const int last = (int)min((int64_t)t.pmax, p.a.max_pages * p.a.page - 1);
+    if (last < t.pmax) atomicOr(p.status, kStatusBadIndex);
+    t.fb = t.wb = t.k0 = t.nb = 0;
+    if (last >= 0) {
+        t.fb = (min(p.first, last + 1) + kBlock - 1) / kBlock;
+        t.wb = max(max(0, t.pos0 - p.window + 1) / kBlock, t.fb);
+        const int n = t.fb + max(0, last / kBlock - t.wb + 1);
+        const int per = (n + kTileBlocks * p.n_splits - 1) / (kTileBlocks * p.n_splits) * kTileBlocks;
+        t.k0 = min(t.split * per, n);
+        t.nb = min(n, t.k0 + per) - t.k0;
+    }
+    return true;
+}
+
+template <bool kRope>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Misc& M = *reinterpret_cast<Misc*>(smem + kOffMisc);
+    const uint32_t s_k = smem_addr(smem + kOffK), s_v = smem_addr(smem + kOffV), s_q = smem_addr(smem + kOffQ), s_p = smem_addr(smem + kOffP);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t rank = __shfl_sync(0xffffffffu, cta_rank(), 0);  // (warp-uniform for the compiler too)
+    volatile int* abort = &M.abort;
+    pdl_trigger();
+    if (smem_addr(smem) & 1023u) {  // (the swizzle's alignment, which leaves no room to be rounded to)
+        if (tid == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
+
+    if (tid == 0) {
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(smem_addr(&M.k_full[s]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.k_empty[s]), 1);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(smem_addr(&M.v_full[s]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.v_empty[s]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&M.q_full[i]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.q_empty[i]), 1);
+        }
+        for (int i = 0; i < kInfos; ++i) {
+            mbar_init(smem_addr(&M.info_full[i]), 1);
+            mbar_init(smem_addr(&M.task_full[i]), 1);
+            mbar_init(smem_addr(&M.task_empty[i]), 13);  // warps 0 and 2-13
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&M.s_full[b]), 1);
+            mbar_init(smem_addr(&M.s_empty[b]), 8);
+            mbar_init(smem_addr(&M.pair_bar[b]), 2);
+        }
+        mbar_init(smem_addr(&M.p_full), 8);
+        mbar_init(smem_addr(&M.p_empty), 1);
+        mbar_init(smem_addr(&M.o_full), 1);
+        mbar_init(smem_addr(&M.o_empty), 8);
+        mbar_init(smem_addr(&M.stats_full), 4);
+        mbar_init(smem_addr(&M.stats_empty), 4);
+        mbar_init(smem_addr(&M.done), 2);
+        M.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&M.tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == 2 && lane == 0) {
+        tma_prefetch_desc(&k_map);
+        tma_prefetch_desc(&v_map);
+    }
+    if (warp == 3 && lane == 0) tma_prefetch_desc(&q_map);
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();  // the other CTA's barriers and TMEM are there
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, M.tmem_base, 0);
+    // the set-up above touches no global memory; everything below may read what the work queued before this launch
+    // writes
+    pdl_wait();
+
+    // The tasks, in turn: fetch(t) waits for the next one's description; false: none is left (or a wait gave up).
+    uint32_t nth = 0;
+    bool ok = true;
+    auto fetch = [&](Task& t) {
+        const uint32_t i = nth % kInfos;
+        ok = ok && wait(M.task_full[i], nth / kInfos, abort);
+        if (!ok) return false;
+        t = M.task[i];
+        warp_arrive(M.task_empty[i], lane);
+        ++nth;
+        // (uniform for the compiler too, so that the loops over them are)
+        t.nb = __shfl_sync(0xffffffffu, t.nb, 0);
+        return __shfl_sync(0xffffffffu, t.more, 0) != 0;
+    };
+
+    if (warp == 1) {
+        // ------------------------------------------------------------------ tasks
+        const int64_t pairs = gridDim.x >> 1;
+        for (int64_t u = blockIdx.x >> 1; ok; u += pairs) {
+            Task t = {};
+            const bool more = u < p.n_units;
+            if (more && !task_of(p, u, t)) continue;
+            t.more = more;
+            const uint32_t i = nth % kInfos;
+            if (!(ok = wait(M.task_empty[i], (nth / kInfos) ^ 1u, abort))) break;
+            if (lane == 0) M.task[i] = t;
+            warp_arrive(M.task_full[i], lane);
+            ++nth;
+            if (!more) break;
+        }
+    } else if (warp == 0 || warp == 13) {
+        // ------------------------------------------------------------------ the pair's products
+        // Warp 0 issues the logits, warp 13 P.V (rank 1: they pass on that K, and V, have landed).  One warp for both
+        // spent 600 cycles a stage of 256 cycles of products (a wait for a barrier that has long completed takes
+        // 130, a commit 75, and the tensor pipe holds too few products to bridge them); of two, one's products run
+        // behind the other's barriers.
+        constexpr uint32_t id_s = idesc_bf16_f32(kM, 128, false, false);
+        constexpr uint32_t id_o = idesc_bf16_f32(kM, 256, false, true);
+        const uint64_t a_s = smem_desc_sw128(s_q, 16, 1024), b_s = smem_desc_sw128(s_k, 16, 2048);
+        const uint64_t a_o = smem_desc_sw128(s_p, 16, 1024), b_o = smem_desc_sw128(s_v, 4096, 1024);
+        const bool leader = rank == 0;
+        uint32_t st = 0, st_use = 0, g = 0, c = 0;
+        bool landed = false;  // stage st has: its barrier was looked at while the stage before it was issued
+        auto stage_in = [&](uint64_t* full) {
+            if (!landed) ok = ok && wait(full[st], st_use, abort);
+            if (!leader && ok) warp_arrive_leader(full[st], lane);
+            return ok;
+        };
+        auto peek = [&](uint64_t* full, uint32_t stages) {
+            const uint32_t n = st + 1 == stages ? 0 : st + 1;
+            return mbar_test_wait(smem_addr(&full[n]), (st_use + (n == 0)) & 1);
+        };
+        auto stage_out = [&](uint64_t* empty, uint32_t stages, bool next) {
+            if (leader) {
+                commit_pair(empty[st]);
+                landed = __all_sync(0xffffffffu, next);
+            }
+            if (++st == stages) {
+                st = 0;
+                ++st_use;
+            }
+        };
+        Task t;
+        if (warp == 0) {
+            while (fetch(t)) {
+                if (t.nb == 0) continue;
+                const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks;
+                for (int i = 0; i < nt && ok; ++i, ++g) {
+                    const uint32_t b = g & 1;
+                    if (leader) ok = wait(M.s_empty[b], (g >> 1) ^ 1u, abort);
+                    for (int q = 0; q < 4 && ok; ++q) {
+                        if (i == 0) {
+                            ok = wait(M.q_full[q], c, abort);
+                            if (!leader && ok) warp_arrive_leader(M.q_full[q], lane);
+                        }
+                        if (!ok || !stage_in(M.k_full)) break;
+                        bool next = false;
+                        if (leader) {
+                            tc_fence_after();
+                            next = peek(M.k_full, kKStages);
+                            const uint32_t alo = (uint32_t)a_s + q * (16384 >> 4);
+                            const uint32_t blo = (uint32_t)b_s + st * (kStageBytes >> 4);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t at = (k & 3) * (32 >> 4);
+                                mma_pair(tmem + kColS + 64 * b, alo + (k >> 2) * (8192 >> 4) + at,
+                                         (uint32_t)(a_s >> 32), blo + (k >> 2) * (1024 >> 4) + at,
+                                         (uint32_t)(b_s >> 32), id_s, (q | k) != 0);
+                            }
+                            if (i == nt - 1) commit_pair(M.q_empty[q]);
+                        }
+                        stage_out(M.k_empty, kKStages, next);
+                    }
+                    if (leader && ok) commit_pair(M.s_full[b]);
+                }
+                ++c;
+            }
+        } else {
+            while (fetch(t)) {
+                if (t.nb == 0) continue;
+                for (int i = 0; 4 * i < t.nb && ok; ++i, ++g) {
+                    if (leader) {
+                        ok = wait(M.p_full, g, abort);
+                        if (i == 0) ok = ok && wait(M.o_empty, c ^ 1u, abort);
+                        tc_fence_after();
+                    }
+                    const int nb = min(kTileBlocks, t.nb - kTileBlocks * i);
+                    for (int j = 0; j < nb && ok; ++j) {
+                        if (!stage_in(M.v_full)) break;
+                        bool next = false;
+                        if (leader) {
+                            tc_fence_after();
+                            next = peek(M.v_full, kVStages);
+                            const uint32_t alo = (uint32_t)a_o + (j & 1) * (8192 >> 4) + (j >> 1) * (64 >> 4);
+                            const uint32_t blo = (uint32_t)b_o + st * (kStageBytes >> 4);
+#pragma unroll
+                            for (int dh = 0; dh < 2; ++dh)
+#pragma unroll
+                                for (int ks = 0; ks < 2; ++ks)
+                                    mma_pair(tmem + kColO + 128 * dh, alo + ks * (32 >> 4), (uint32_t)(a_o >> 32),
+                                             blo + ks * (2048 >> 4) + dh * (8192 >> 4), (uint32_t)(b_o >> 32), id_o,
+                                             (i | j | ks) != 0);
+                        }
+                        stage_out(M.v_empty, kVStages, next);
+                    }
+                    if (leader && ok) {
+                        commit_pair(M.p_empty);
+                        if (kTileBlocks * (i + 1) >= t.nb) commit_pair(M.o_full);
+                    }
+                }
+                ++c;
+            }
+        }
+        // every product has completed, and every arrival at either CTA's barriers, before the accumulators are
+        // released (an abandoned one too)
+        if (leader) commit_pair(M.done);
+        wait(M.done, 0, abort);
+    } else if (warp == 2 || warp == 12) {
+        // ------------------------------------------------------------------ K (warp 2) and V (warp 12)
+        const bool is_v = warp == 12;
+        const uint32_t stages = is_v ? kVStages : kKStages, ring = is_v ? s_v : s_k;
+        uint64_t* const full = is_v ? M.v_full : M.k_full;
+        uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
+        uint32_t st = 0, st_use = 0, g = 0;
+        auto load = [&](uint32_t bytes, auto issue) {
+            if (!(ok = ok && wait(empty[st], st_use ^ 1u, abort))) return;
+            if (lane == 0) {
+                const uint32_t bar = smem_addr(&full[st]);
+                mbar_arrive_expect_tx(bar, bytes);
+                issue(ring + st * kStageBytes, bar);
+            }
+            if (++st == stages) {
+                st = 0;
+                ++st_use;
+            }
+        };
+        Task t;
+        while (fetch(t)) {
+            int rows32 = 0, base32 = -2;  // lane l: the blocks 32 at a time
+            for (int i = 0; 4 * i < t.nb && ok; ++i, ++g) {
+                if ((i & 7) == 0) {
+                    const int k = t.k0 + 4 * i + lane;
+                    base32 = -2;
+                    rows32 = 0;
+                    if (4 * i + lane < t.nb) {
+                        const int blk = k < t.fb ? k : k - t.fb + t.wb;
+                        const int64_t row = paged::row_of(p.a, t.seq, (uint32_t)blk * kBlock);
+                        // (a block without a page: some rows that are there, which no token sees)
+                        base32 = row < 0 ? -1 : blk * kBlock;
+                        rows32 = row < 0 ? 0 : (int)row;
+                        if (row < 0 && !is_v && rank == 0) atomicOr(p.status, kStatusBadIndex);
+                    }
+                }
+                const int src = 4 * (i & 7) + (lane & 3);
+                const int row = __shfl_sync(0xffffffffu, rows32, src), base = __shfl_sync(0xffffffffu, base32, src);
+                const int nb = min(kTileBlocks, t.nb - 4 * i);
+                if (is_v) {
+                    for (int j = 0; j < nb && ok; ++j) {
+                        const int at = __shfl_sync(0xffffffffu, row, j);
+                        load(kStageBytes, [&](uint32_t dst, uint32_t bar) {
+                            tma_load_3d(dst, &v_map, 0, at, 4 * (int)rank, bar);
+                        });
+                    }
+                    continue;
+                }
+                if (lane < kTileBlocks) M.base[g % kInfos][lane] = lane < nb ? base : -2;
+                warp_arrive(M.info_full[g % kInfos], lane);
+                const int own = (nb - (int)rank + 1) / 2;  // this CTA's blocks: rank, rank + 2
+                const int g0 = __shfl_sync(0xffffffffu, row, (int)rank) >> 3,
+                          g1 = __shfl_sync(0xffffffffu, row, (int)rank + 2) >> 3;
+                for (int q = 0; q < 4 && ok; ++q)
+                    load((uint32_t)own * 8192u, [&](uint32_t dst, uint32_t bar) {
+                        if (own > 0) tma_load_4d(dst, &k_map, 0, 0, 2 * q, g0, bar);
+                        if (own > 1) tma_load_4d(dst + 8192, &k_map, 0, 0, 2 * q, g1, bar);
+                    });
+            }
+        }
+        // after a failed wait, the copies under way land before the CTA exits
+        if (!ok && lane == 0) {
+            const uint32_t n = st_use * stages + st;
+            for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
+                mbar_drain(smem_addr(&full[k % stages]), (k / stages) & 1);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------------ Q
+        uint32_t c = 0, sent = 0;
+        Task t;
+        while (fetch(t)) {
+            if (t.nb == 0) continue;
+            for (int q = 0; q < 4 && ok; ++q) {
+                if (!(ok = wait(M.q_empty[q], c ^ 1u, abort))) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_addr(&M.q_full[q]);
+                    mbar_arrive_expect_tx(bar, 16384);
+                    tma_load_3d(s_q + q * 16384, &q_map, 0, t.row0 + 64 * (int)rank, 2 * q, bar);
+                }
+                ++sent;
+            }
+            ++c;
+        }
+        if (!ok && lane == 0)
+            for (uint32_t k = sent > 4 ? sent - 4 : 0; k < sent; ++k) mbar_drain(smem_addr(&M.q_full[k % 4]), (k / 4) & 1);
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------------ softmax
+        // A thread has one row of the CTA's 64 and half of a tile's columns (64: blocks `half` and half + 2); the
+        // thread 64 further has the other half, and the two trade their maxima.
+        const int w = warp & 3, half = w >> 1, row = 32 * (w & 1) + lane, me = 32 * w + lane;
+        const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+        uint32_t g = 0, c = 0, v_seq = 0;
+        Task t;
+        while (fetch(t)) {
+            // (a row that is not the task's own has the last one's mask; it is not stored)
+            const int pos = t.pos0 + (t.off0 + min(64 * (int)rank + row, t.rows - 1)) / p.h;
+            float m = -INFINITY, mu = 0.f, l = 0.f;
+            const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks;
+            for (int i = 0; i < nt && ok; ++i, ++g) {
+                const uint32_t b = g & 1, gi = g % kInfos;
+                const bool first = i == 0;
+                ok = wait(M.info_full[gi], g / kInfos, abort) && wait(M.s_full[b], g >> 1, abort);
+                if (!ok) break;
+                const int b0 = M.base[gi][half], b1 = M.base[gi][half + 2];
+                tc_fence_after();
+                uint32_t r[64];
+                tmem_ld_32x32b_x64(tmem + lane_base + kColS + 64 * b, r);
+                tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive_leader(M.s_empty[b], lane);
+                const uint32_t v0 = seen(p, b0, pos, pos), v1 = seen(p, b1, pos, pos);
+                const uint32_t e0 = seen(p, b0, t.pos0, t.pmax), e1 = seen(p, b1, t.pos0, t.pmax);
+                uint32_t bad0 = 0, bad1 = 0;
+                float mt, sc = p.scale_log2;
+                if ((e0 & e1) == 0xffffffffu) {
+                    // every column seen by every row: the maximum of the raw logits (the minimum for a negative
+                    // scale), and p = 2^(s scale - m) in one FMA
+                    float x[22];
+                    if (sc >= 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 21; ++k)
+                            x[k] = max3f(__uint_as_float(r[3 * k]), __uint_as_float(r[3 * k + 1]), __uint_as_float(r[3 * k + 2]));
+                        x[21] = __uint_as_float(r[63]);
+#pragma unroll
+                        for (int k = 0; k < 7; ++k) x[k] = max3f(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
+                        mt = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]), fmaxf(x[6], x[21]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 21; ++k)
+                            x[k] = min3f(__uint_as_float(r[3 * k]), __uint_as_float(r[3 * k + 1]), __uint_as_float(r[3 * k + 2]));
+                        x[21] = __uint_as_float(r[63]);
+#pragma unroll
+                        for (int k = 0; k < 7; ++k) x[k] = min3f(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
+                        mt = min3f(min3f(x[0], x[1], x[2]), min3f(x[3], x[4], x[5]), fminf(x[6], x[21]));
+                    }
+                    mt *= sc;
+                } else {
+                    mt = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        const uint32_t v = k < 32 ? v0 : v1, e = k < 32 ? e0 : e1;
+                        const float s = __uint_as_float(r[k]);
+                        if (!((e >> (k & 31)) & 1u) && !(fabsf(s) < INFINITY)) (k < 32 ? bad0 : bad1) |= 1u << (k & 31);
+                        const float x = ((v >> (k & 31)) & 1u) ? s * sc : -INFINITY;
+                        r[k] = __float_as_uint(x);
+                        mt = fmaxf(mt, x);
+                    }
+                    sc = 1.f;
+                    // (a block that is not there has no V)
+                    if (b0 == -2) bad0 = 0;
+                    if (b1 == -2) bad1 = 0;
+                }
+                M.mx[b][me] = mt;
+                warp_arrive(M.pair_bar[w & 1], lane);
+                if (!(ok = wait(M.pair_bar[w & 1], g, abort))) break;
+                mt = fmaxf(mt, M.mx[b][me ^ 64]);
+                float al = 1.f, mn = mt;
+                if (!first) {
+                    mn = mt > m + kRescaleThreshold ? mt : m;
+                    if (mn != m) al = fast_exp2(m - mn);  // 0 when m = -inf (nothing summed yet)
+                }
+                const bool corr = !first && mn != m;
+                m = mn;
+                mu = mn == -INFINITY ? 0.f : mn;
+                uint32_t pk[32];
+                const uint64_t sc2 = f2(sc, sc), nm2 = f2(-mu, -mu);
+                uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float x0, x1;
+                    f2_split(ffma2(f2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), x0, x1);
+                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                    acc[k & 1] = fadd2(acc[k & 1], f2(p0, p1));
+                    pk[k] = pack_bf16(p0, p1);
+                }
+                float a0, a1, a2, a3;
+                f2_split(acc[0], a0, a1);
+                f2_split(acc[1], a2, a3);
+                const float ps = (a0 + a1) + (a2 + a3);
+                l = first ? ps : fmaf(al, l, ps);
+                // P is free, and O whole, once the previous tile's P.V has completed
+                if (!(ok = wait(M.p_empty, g ^ 1u, abort))) break;
+                const uint32_t prow = s_p + half * 8192 + (uint32_t)row * 128;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    st_shared_v4(prow + (((uint32_t)u ^ ((uint32_t)row & 7)) << 4), pk[4 * u], pk[4 * u + 1],
+                                 pk[4 * u + 2], pk[4 * u + 3]);
+                if (__any_sync(0xffffffffu, corr)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t o[32];
+                        const uint32_t ta = tmem + lane_base + kColO + 32 * k;
+                        tmem_ld_32x32b_x32(ta, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                        tmem_st_32x32b_x32(ta, o);
+                    }
+                    tmem_wait_st();
+                }
+                if (__any_sync(0xffffffffu, (bad0 | bad1) != 0)) {
+                    // rows of V to clear (the stage's last use was the tile before's, which has completed)
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
+                        uint32_t rows = __reduce_or_sync(0xffffffffu, s ? bad1 : bad0);
+                        if (!rows) continue;
+                        const uint32_t vs = v_seq + half + 2 * s;
+                        if (!(ok = wait(M.v_full[vs % kVStages], vs / kVStages, abort))) break;
+                        const uint32_t at = s_v + (vs % kVStages) * kStageBytes + (uint32_t)lane * 16;
+                        for (; rows; rows &= rows - 1) {  // 4 pieces of 128 bytes: a lane 16 of them
+                            const uint32_t ra = at - (lane & 24) * 16 + (lane >> 3) * 4096 + (__ffs(rows) - 1) * 128;
+                            st_shared_v4(ra, 0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                warp_arrive_leader(M.p_full, lane);
+                v_seq += min(kTileBlocks, t.nb - kTileBlocks * i);
+            }
+            if (!ok) break;
+            if (!(ok = wait(M.stats_empty, c ^ 1u, abort))) break;
+            M.stats_l[me] = l;
+            if (half == 0) M.stats_m[row] = mu;
+            warp_arrive(M.stats_full, lane);
+            ++c;
+        }
+    } else {
+        // ------------------------------------------------------------------ epilogue
+        // A thread has one row and 256 of its d: 128 dh + 0..127 of its half.
+        const int w = warp & 3, half = w >> 1, row = 32 * (w & 1) + lane;
+        const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+        const bool split = p.n_splits > 1;
+        uint32_t c = 0, c_o = 0;
+        Task t;
+        while (fetch(t)) {
+            const int r = 64 * (int)rank + row;
+            const bool mine = r < t.rows;
+            const int tok = (t.off0 + r) / p.h, head = t.off0 + r - tok * p.h;
+            const float2* turn = nullptr;
+            if constexpr (kRope) {
+                int64_t pos = t.pos0 + min(tok, t.pmax - t.pos0);
+                if (pos >= p.npos) {
+                    if (mine && half == 0) atomicOr(p.status, kStatusBadIndex);
+                    pos = p.npos - 1;
+                }
+                turn = reinterpret_cast<const float2*>(p.rope) + max(pos, (int64_t)0) * (p.rope_dim >> 1);
+            }
+            const float sink = __ldg(p.sink + head);
+            ok = wait(M.stats_full, c, abort);
+            if (ok && t.nb) ok = wait(M.o_full, c_o, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const float l = M.stats_l[row] + M.stats_l[row + 64], mu = M.stats_m[row];
+            warp_arrive(M.stats_empty, lane);
+            ++c;
+            const int64_t flat = (int64_t)t.row0 + r;
+            const int64_t part = ((int64_t)(t.tok0 + tok) * p.n_splits + t.split) * p.h + head;
+            float inv = 0.f;
+            if (!split) {
+                if (l > 0.f) inv = 1.f / (l + fast_exp2(sink * kLog2e - mu));
+                if (p.lse && mine && half == 0) p.lse[flat] = log_sum_exp(l, mu, sink);
+            } else if (mine && half == 0) {
+                *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(mu, l);
+            }
+            if (t.nb == 0 && split) continue;  // (its sum is 0: O is not looked at)
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {  // 32 d at a time
+                const int d0 = 256 * half + 32 * k;
+                uint32_t o[32];
+                __syncwarp();
+                if (t.nb) {
+                    tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * k, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+                if (t.nb && k == 7) {
+                    tc_fence_before();
+                    warp_arrive_leader(M.o_empty, lane);
+                }
+                if constexpr (kRope) {
+                    // (a + i b)(c - i s), on the f32 sums (partials too: the merge is linear)
+                    const int e0 = d0 - (kD - p.rope_dim);
+                    if (e0 + 32 > 0) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int e = e0 + 2 * j;
+                            if (e < 0) continue;
+                            const float2 cs = __ldg(turn + (e >> 1));
+                            const float a = __uint_as_float(o[2 * j]), b = __uint_as_float(o[2 * j + 1]);
+                            o[2 * j] = __float_as_uint(fmaf(a, cs.x, b * cs.y));
+                            o[2 * j + 1] = __float_as_uint(fmaf(b, cs.x, -a * cs.y));
+                        }
+                    }
+                }
+                uint32_t out[8];
+                if (split && mine) {
+                    float* at = p.part_o + part * kD + d0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) out[j] = o[8 * q + j];
+                        store32(at + 8 * q, out);
+                    }
+                } else if (mine) {
+                    __nv_bfloat16* at = p.o + flat * kD + d0;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            out[j] = pack_bf16(__uint_as_float(o[16 * q + 2 * j]) * inv,
+                                               __uint_as_float(o[16 * q + 2 * j + 1]) * inv);
+                        store32(at + 16 * q, out);
+                    }
+                }
+            }
+            if (t.nb) ++c_o;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && M.abort) atomicOr(p.status, kStatusTimeout);
+    __syncwarp();
+    cluster_barrier();  // nobody reads this CTA's shared memory, or arrives at its barriers, any more
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// How many parts a task's blocks are cut into: more than one only where the tasks (about: a token's tile or the
+// rows' tiles, whichever are more) leave pairs of SMs without work, and at most one a tile.
+int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, int sms) {
+    const int64_t tiles = std::max<int64_t>(std::max<int64_t>((n * h + kM - 1) / kM, std::min(b, n)), 1);
+    const int64_t keys = first + kBlock + window + kM / h + 2 * kBlock;
+    const int64_t most = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / 2 / tiles, most), 64));
+}
+
+}  // namespace
+
+bool window_tc_supports(int d, int kv_format, int page) {
+    return d == kD && kv_format == SA_KV_BF16 && page % kBlock == 0;
+}
+
+size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int64_t first) {
+    const size_t s = window_splits(n, b, h, window, first, kMaxSmCount);
+    return s == 1 ? 0 : align_up((size_t)n * s * h * 2 * sizeof(float), 256) + (size_t)n * s * h * kD * sizeof(float);
+}
+
+cudaError_t window_tc_launch(const WindowCall& c) {
+    const int sms = device_sm_count();
+    // Q: 64 rows x two blocks of 64 d, block by block.  V: 32 rows x four blocks of 64 d, block by block.  K: 32
+    // rows x two blocks of 64 d, eight rows of one block behind those of the other (so that a stage's 64 rows,
+    // two boxes, are 2 KB a step of eight in either block).
+    CUtensorMap q_map, k_map, v_map;
+    const int64_t rows = c.a.n_pages * c.a.page;
+    if (!encode_blocks_map(q_map, c.q, kD, c.n * c.h, 64, 2) || !encode_blocks_map(v_map, c.kv, kD, rows, kBlock, 4) ||
+        !encode_groups_map(k_map, c.kv, kD, rows, kBlock, 2))
+        return cudaErrorInvalidValue;
+    Params p = {};
+    p.a = c.a;
+    p.sink = c.sink;
+    p.o = reinterpret_cast<__nv_bfloat16*>(c.o);
+    p.lse = c.lse;
+    p.status = c.status;
+    p.rope = c.rope;
+    p.npos = c.npos;
+    p.rope_dim = c.rope_dim;
+    p.scale_log2 = c.softmax_scale * kLog2e;
+    p.n = (int)c.n;
+    p.h = c.h;
+    p.window = (int)c.window;
+    p.first = (int)c.first;
+    p.n_splits = window_splits(c.n, c.a.b, c.h, c.window, c.first, sms);
+    p.n_units = (c.n * c.h / kM + c.a.b) * p.n_splits;
+    if (p.n_splits > 1) {
+        p.part_ml = reinterpret_cast<float*>(c.scratch);
+        p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(c.scratch) +
+                                            align_up((size_t)c.n * p.n_splits * c.h * 2 * sizeof(float), 256));
+    }
+    auto kernel = c.rope ? window_tc_kernel<true> : window_tc_kernel<false>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        for (auto fn : {window_tc_kernel<true>, window_tc_kernel<false>}) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+            if (e != cudaSuccess) return e;
+        }
+        if (dev < 64) configured[dev] = true;
+    }
+    int64_t pairs = sms / 2;
+    if (pairs > p.n_units) pairs = p.n_units;
+    e = launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, c.stream, q_map, k_map, v_map, p);
+    if (e != cudaSuccess || p.n_splits == 1) return e;
+    return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, c.n, c.h, kD, p.n_splits,
+                               c.a.q_start + c.a.b, c.stream);
+}
+
+}  // namespace sa
