@@ -47,7 +47,7 @@ constexpr int kD = 512;
 constexpr int kM = 128;            // query rows of a task
 constexpr int kBlock = 32;         // positions of a block
 constexpr int kTileBlocks = 4;     // blocks of a tile
-constexpr int kKStages = 5, kVStages = 4;  // of the two rings
+constexpr int kKStages = 4, kVStages = 4;  // of the two rings
 constexpr int kThreads = 448;
 constexpr int kInfos = 4;          // tiles, and tasks, described ahead
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,12 +56,12 @@ constexpr uint32_t kColO = 0, kColS = 256;
 
 constexpr uint32_t kStageBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [8 blocks of 64 d][64 rows][128 B]
-constexpr uint32_t kPBytes = 16384;  // [2 halves of the columns][64 rows][128 B]
+constexpr uint32_t kPBytes = 16384;  // [2 halves of the columns][64 rows][128 B], two buffers
 constexpr uint32_t kOffK = 0;
 constexpr uint32_t kOffV = kOffK + kKStages * kStageBytes;
 constexpr uint32_t kOffQ = kOffV + kVStages * kStageBytes;
 constexpr uint32_t kOffP = kOffQ + kQBytes;
-constexpr uint32_t kOffMisc = kOffP + kPBytes;
+constexpr uint32_t kOffMisc = kOffP + 2 * kPBytes;
 
 struct Task {
     int row0, rows;   // its first row among all of q's, and how many are its own
@@ -79,7 +79,7 @@ struct Misc {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t q_full[4], q_empty[4];          // (the same for a quarter of Q)
     uint64_t s_full[2], s_empty[2];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
-    uint64_t p_full, p_empty, o_full, o_empty;
+    uint64_t p_full[2], p_empty[2], o_full, o_empty;
     uint64_t info_full[kInfos];
     uint64_t task_full[kInfos], task_empty[kInfos];
     uint64_t stats_full, stats_empty;
@@ -87,6 +87,7 @@ struct Misc {
     uint32_t tmem_base;
     int abort;
     int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
+    int whole[kInfos];                // every token of the task sees every position of the tile's blocks
     Task task[kInfos];
     float mx[2][128];
     float stats_m[64], stats_l[128];
@@ -110,7 +111,7 @@ struct Params {
     int h;
     int window, first;
     int n_splits;
-    int64_t n_units;
+    int n_units;         // below 2^31: at most 2^24 tiles and b, 64 splits only of few tiles
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -133,8 +134,25 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A wait by a converged warp, with a warp-uniform result.  The hardware suspends the warp until the phase completes or
+// a millisecond has passed (a poll that returns at once takes issue slots from the warps that work); bounded to
+// some two seconds, and left as soon as another role has given up.  (Out of line: see the note on code below.)
+static __device__ __noinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+    for (int i = 0; i < 2000; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity & 1), "r"(1000000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    return false;
+}
 __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
-    return warp_wait(smem_addr(&bar), parity & 1, abort);
+    return __all_sync(0xffffffffu, wait_for(smem_addr(&bar), parity, abort));
 }
 // One arrival for a converged warp, after what every lane did.
 __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane) {
@@ -192,9 +210,9 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float min3f(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 // 32 bytes at a 32-byte aligned address
@@ -211,29 +229,28 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi) {
     return hi < lo ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
 }
 // The positions base .. base + 31 that every token from position p0 to p1 sees.
-__device__ __forceinline__ uint32_t seen(const Params& p, int base, int p0, int p1) {
-    return base < 0 ? 0u : bits(p1 - p.window + 1 - base, p0 - base) | bits(0, min(p.first - 1, p0) - base);
+static __device__ __noinline__ uint32_t seen(int window, int first, int base, int p0, int p1) {
+    return base < 0 ? 0u : bits(p1 - window + 1 - base, p0 - base) | bits(0, min(first - 1, p0) - base);
 }
 
 // Unit u -> its task (the whole warp calls); false: nothing there.  Sequence i's tiles of 128 rows are numbered
 // from q_start[i] h / 128 + i on: more numbers than tiles, but the same on every CTA without a list of them.
-__device__ __forceinline__ bool task_of(const Params& p, int64_t u, Task& t) {
-    const int64_t tile = u / p.n_splits;
-    const auto first_tile = [&](int64_t i) {
-        const int64_t s = min(max(__ldg(p.a.q_start + i), 0), p.n);
-        return s * p.h / kM + i;
-    };
-    const int64_t seq = paged::last_at_most(p.a.b, tile, first_tile);
+__device__ __forceinline__ int first_tile(const Params& p, int64_t i) {
+    return (int)((uint32_t)(min(max(__ldg(p.a.q_start + i), 0), p.n) * p.h) / kM) + (int)i;  // (n h < 2^31)
+}
+__device__ __forceinline__ bool task_of(const Params& p, int u, Task& t) {
+    const int tile = u / p.n_splits;
+    const int seq = (int)paged::last_at_most(p.a.b, tile, [&](int64_t i) { return first_tile(p, i); });
     const int q0 = min(max(__ldg(p.a.q_start + seq), 0), p.n), q1 = min(max(__ldg(p.a.q_start + seq + 1), 0), p.n);
-    const int64_t r0 = (tile - first_tile(seq)) * kM, rows = (int64_t)(q1 - q0) * p.h - r0;
+    const int r0 = (tile - first_tile(p, seq)) * kM, rows = (q1 - q0) * p.h - r0;
     if (r0 < 0 || rows <= 0) return false;
-    t.seq = (int)seq;
-    t.split = (int)(u - tile * p.n_splits);
-    t.rows = (int)min(rows, (int64_t)kM);
-    const int tok = (int)(r0 / p.h);
-    t.off0 = (int)(r0 - (int64_t)tok * p.h);
+    t.seq = seq;
+    t.split = u - tile * p.n_splits;
+    t.rows = min(rows, kM);
+    const int tok = r0 / p.h;
+    t.off0 = r0 - tok * p.h;
     t.tok0 = q0 + tok;
-    t.row0 = (int)((int64_t)q0 * p.h + r0);
+    t.row0 = q0 * p.h + r0;
     // (lengths far outside the table's range, which are errors, are held where 32 bits do)
     const int64_t pos = (int64_t)__ldg(p.a.kv_len + seq) - (q1 - q0) + tok;
     t.pos0 = (int)min(max(pos, -(int64_t(1) << 30)), (int64_t(1) << 31) - 1 - kM);
@@ -243,9 +260,9 @@ __device__ __forceinline__ bool task_of(const Params& p, int64_t u, Task& t) {
     if (last < t.pmax) atomicOr(p.status, kStatusBadIndex);
     t.fb = t.wb = t.k0 = t.nb = 0;
     if (last >= 0) {
-        t.fb = (min(p.first, last + 1) + kBlock - 1) / kBlock;
-        t.wb = max(max(0, t.pos0 - p.window + 1) / kBlock, t.fb);
-        const int n = t.fb + max(0, last / kBlock - t.wb + 1);
+        t.fb = (int)((uint32_t)(min(p.first, last + 1) + kBlock - 1) / kBlock);
+        t.wb = max((int)((uint32_t)max(0, t.pos0 - p.window + 1) / kBlock), t.fb);
+        const int n = t.fb + max(0, (int)((uint32_t)last / kBlock) - t.wb + 1);
         const int per = (n + kTileBlocks * p.n_splits - 1) / (kTileBlocks * p.n_splits) * kTileBlocks;
         t.k0 = min(t.split * per, n);
         t.nb = min(n, t.k0 + per) - t.k0;
@@ -291,9 +308,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&M.s_full[b]), 1);
             mbar_init(smem_addr(&M.s_empty[b]), 8);
             mbar_init(smem_addr(&M.pair_bar[b]), 2);
+            mbar_init(smem_addr(&M.p_full[b]), 8);
+            mbar_init(smem_addr(&M.p_empty[b]), 1);
         }
-        mbar_init(smem_addr(&M.p_full), 8);
-        mbar_init(smem_addr(&M.p_empty), 1);
         mbar_init(smem_addr(&M.o_full), 1);
         mbar_init(smem_addr(&M.o_empty), 8);
         mbar_init(smem_addr(&M.stats_full), 4);
@@ -338,11 +355,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 1) {
         // ------------------------------------------------------------------ tasks
-        const int64_t pairs = gridDim.x >> 1;
-        for (int64_t u = blockIdx.x >> 1; ok; u += pairs) {
+        // In every round of `pairs` units a pair takes the place behind its last: the units that are nothing lie evenly
+        // among the others (every second one where a token is a tile), and would fall to the same pairs.
+        const int pairs = gridDim.x >> 1;
+        int place = blockIdx.x >> 1;
+        for (int u0 = 0; ok; u0 += pairs) {
+            const int u = u0 + place;
+            if (++place == pairs) place = 0;
             Task t = {};
-            const bool more = u < p.n_units;
-            if (more && !task_of(p, u, t)) continue;
+            const bool more = u0 < p.n_units;
+            if (more && (u >= p.n_units || !task_of(p, u, t))) continue;
             t.more = more;
             const uint32_t i = nth % kInfos;
             if (!(ok = wait(M.task_empty[i], (nth / kInfos) ^ 1u, abort))) break;
@@ -403,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             next = peek(M.k_full, kKStages);
                             const uint32_t alo = (uint32_t)a_s + q * (16384 >> 4);
                             const uint32_t blo = (uint32_t)b_s + st * (kStageBytes >> 4);
-#pragma unroll
+#pragma unroll 4
                             for (int k = 0; k < 8; ++k) {
                                 const uint32_t at = (k & 3) * (32 >> 4);
                                 mma_pair(tmem + kColS + 64 * b, alo + (k >> 2) * (8192 >> 4) + at,
@@ -423,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (t.nb == 0) continue;
                 for (int i = 0; 4 * i < t.nb && ok; ++i, ++g) {
                     if (leader) {
-                        ok = wait(M.p_full, g, abort);
+                        ok = wait(M.p_full[g & 1], g >> 1, abort);
                         if (i == 0) ok = ok && wait(M.o_empty, c ^ 1u, abort);
                         tc_fence_after();
                     }
@@ -434,7 +456,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (leader) {
                             tc_fence_after();
                             next = peek(M.v_full, kVStages);
-                            const uint32_t alo = (uint32_t)a_o + (j & 1) * (8192 >> 4) + (j >> 1) * (64 >> 4);
+                            const uint32_t alo =
+                                (uint32_t)a_o + (g & 1) * (kPBytes >> 4) + (j & 1) * (8192 >> 4) + (j >> 1) * (64 >> 4);
                             const uint32_t blo = (uint32_t)b_o + st * (kStageBytes >> 4);
 #pragma unroll
                             for (int dh = 0; dh < 2; ++dh)
@@ -447,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         stage_out(M.v_empty, kVStages, next);
                     }
                     if (leader && ok) {
-                        commit_pair(M.p_empty);
+                        commit_pair(M.p_empty[g & 1]);
                         if (kTileBlocks * (i + 1) >= t.nb) commit_pair(M.o_full);
                     }
                 }
@@ -506,7 +529,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
+                const bool all = lane < nb && seen(p.window, p.first, base, t.pos0, t.pmax) == 0xffffffffu;
+                const bool whole = __all_sync(0xffffffffu, lane >= kTileBlocks || all);
                 if (lane < kTileBlocks) M.base[g % kInfos][lane] = lane < nb ? base : -2;
+                if (lane == 0) M.whole[g % kInfos] = whole;
                 warp_arrive(M.info_full[g % kInfos], lane);
                 const int own = (nb - (int)rank + 1) / 2;  // this CTA's blocks: rank, rank + 2
                 const int g0 = __shfl_sync(0xffffffffu, row, (int)rank) >> 3,
@@ -546,69 +572,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------------ softmax
         // A thread has one row of the CTA's 64 and half of a tile's columns (64: blocks `half` and half + 2); the
-        // thread 64 further has the other half, and the two trade their maxima.
+        // thread 64 further has the other half, and the two trade their maxima.  A block's logits are read from TMEM
+        // twice, for the maximum and for p, by loops: with both blocks in registers and the loops unrolled, the
+        // warps of a SM waited for instructions (4.2 warps at every issue, over a sliding window's prefill).
         const int w = warp & 3, half = w >> 1, row = 32 * (w & 1) + lane, me = 32 * w + lane;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+        const uint32_t prow = s_p + half * 8192 + (uint32_t)row * 128;
+        const float sc = p.scale_log2;
         uint32_t g = 0, c = 0, v_seq = 0;
         Task t;
         while (fetch(t)) {
             // (a row that is not the task's own has the last one's mask; it is not stored)
             const int pos = t.pos0 + (t.off0 + min(64 * (int)rank + row, t.rows - 1)) / p.h;
             float m = -INFINITY, mu = 0.f, l = 0.f;
-            const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks;
-            for (int i = 0; i < nt && ok; ++i, ++g) {
+            for (int i = 0; kTileBlocks * i < t.nb && ok; ++i, ++g) {
                 const uint32_t b = g & 1, gi = g % kInfos;
                 const bool first = i == 0;
                 ok = wait(M.info_full[gi], g / kInfos, abort) && wait(M.s_full[b], g >> 1, abort);
                 if (!ok) break;
-                const int b0 = M.base[gi][half], b1 = M.base[gi][half + 2];
+                const bool whole = __shfl_sync(0xffffffffu, M.whole[gi], 0) != 0;
+                const uint32_t sa = tmem + lane_base + kColS + 64 * b;
                 tc_fence_after();
-                uint32_t r[64];
-                tmem_ld_32x32b_x64(tmem + lane_base + kColS + 64 * b, r);
-                tmem_wait_ld();
-                tc_fence_before();
-                warp_arrive_leader(M.s_empty[b], lane);
-                const uint32_t v0 = seen(p, b0, pos, pos), v1 = seen(p, b1, pos, pos);
-                const uint32_t e0 = seen(p, b0, t.pos0, t.pmax), e1 = seen(p, b1, t.pos0, t.pmax);
-                uint32_t bad0 = 0, bad1 = 0;
-                float mt, sc = p.scale_log2;
-                if ((e0 & e1) == 0xffffffffu) {
-                    // every column seen by every row: the maximum of the raw logits (the minimum for a negative
-                    // scale), and p = 2^(s scale - m) in one FMA
-                    float x[22];
-                    if (sc >= 0.f) {
+                uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu, bad0 = 0, bad1 = 0;  // by block: seen, and to be cleared
+                if (!whole) {
+                    v0 = seen(p.window, p.first, M.base[gi][half], pos, pos);
+                    v1 = seen(p.window, p.first, M.base[gi][half + 2], pos, pos);
+                }
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(sa + 16 * k, r);
+                    tmem_wait_ld();
+                    if (!whole) {
+                        // A logit that is not finite makes the sum of their products with zero a NaN
+                        uint64_t z = f2(0.f, 0.f);
 #pragma unroll
-                        for (int k = 0; k < 21; ++k)
-                            x[k] = max3f(__uint_as_float(r[3 * k]), __uint_as_float(r[3 * k + 1]), __uint_as_float(r[3 * k + 2]));
-                        x[21] = __uint_as_float(r[63]);
+                        for (int j = 0; j < 8; ++j)
+                            z = ffma2(f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(0.f, 0.f), z);
+                        float z0, z1;
+                        f2_split(z, z0, z1);
+                        if (!(z0 + z1 == 0.f)) {
+                            uint32_t odd = 0;
 #pragma unroll
-                        for (int k = 0; k < 7; ++k) x[k] = max3f(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
-                        mt = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]), fmaxf(x[6], x[21]));
+                            for (int j = 0; j < 16; ++j)
+                                odd |= (uint32_t)!(fabsf(__uint_as_float(r[j])) < INFINITY) << j;
+                            (k & 2 ? bad1 : bad0) |= odd << (16 * (k & 1));
+                        }
+                        const uint32_t v = (k & 2 ? v1 : v0) >> (16 * (k & 1));
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            r[j] = v & (1u << j) ? __float_as_uint(__uint_as_float(r[j]) * sc) : 0xff800000u;
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 21; ++k)
-                            x[k] = min3f(__uint_as_float(r[3 * k]), __uint_as_float(r[3 * k + 1]), __uint_as_float(r[3 * k + 2]));
-                        x[21] = __uint_as_float(r[63]);
-#pragma unroll
-                        for (int k = 0; k < 7; ++k) x[k] = min3f(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
-                        mt = min3f(min3f(x[0], x[1], x[2]), min3f(x[3], x[4], x[5]), fminf(x[6], x[21]));
+                        for (int j = 0; j < 8; ++j) {
+                            float x0, x1;
+                            f2_split(fmul2(f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(sc, sc)), x0, x1);
+                            r[2 * j] = __float_as_uint(x0);
+                            r[2 * j + 1] = __float_as_uint(x1);
+                        }
                     }
-                    mt *= sc;
-                } else {
-                    mt = -INFINITY;
+                    float x[5];
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        const uint32_t v = k < 32 ? v0 : v1, e = k < 32 ? e0 : e1;
-                        const float s = __uint_as_float(r[k]);
-                        if (!((e >> (k & 31)) & 1u) && !(fabsf(s) < INFINITY)) (k < 32 ? bad0 : bad1) |= 1u << (k & 31);
-                        const float x = ((v >> (k & 31)) & 1u) ? s * sc : -INFINITY;
-                        r[k] = __float_as_uint(x);
-                        mt = fmaxf(mt, x);
-                    }
-                    sc = 1.f;
-                    // (a block that is not there has no V)
-                    if (b0 == -2) bad0 = 0;
-                    if (b1 == -2) bad1 = 0;
+                    for (int j = 0; j < 5; ++j)
+                        x[j] = max3f(__uint_as_float(r[3 * j]), __uint_as_float(r[3 * j + 1]), __uint_as_float(r[3 * j + 2]));
+                    mt = max3f(max3f(mt, __uint_as_float(r[15]), x[0]), x[1], max3f(x[2], x[3], x[4]));
+                }
+                if (bad0 | bad1) {  // in columns that not every row sees (a block that is not there has no V)
+                    const int base0 = M.base[gi][half], base1 = M.base[gi][half + 2];
+                    bad0 = base0 == -2 ? 0u : bad0 & ~seen(p.window, p.first, base0, t.pos0, t.pmax);
+                    bad1 = base1 == -2 ? 0u : bad1 & ~seen(p.window, p.first, base1, t.pos0, t.pmax);
                 }
                 M.mx[b][me] = mt;
                 warp_arrive(M.pair_bar[w & 1], lane);
@@ -622,62 +655,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool corr = !first && mn != m;
                 m = mn;
                 mu = mn == -INFINITY ? 0.f : mn;
-                uint32_t pk[32];
-                const uint64_t sc2 = f2(sc, sc), nm2 = f2(-mu, -mu);
-                uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float x0, x1;
-                    f2_split(ffma2(f2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), x0, x1);
-                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                    acc[k & 1] = fadd2(acc[k & 1], f2(p0, p1));
-                    pk[k] = pack_bf16(p0, p1);
-                }
-                float a0, a1, a2, a3;
-                f2_split(acc[0], a0, a1);
-                f2_split(acc[1], a2, a3);
-                const float ps = (a0 + a1) + (a2 + a3);
-                l = first ? ps : fmaf(al, l, ps);
-                // P is free, and O whole, once the previous tile's P.V has completed
-                if (!(ok = wait(M.p_empty, g ^ 1u, abort))) break;
-                const uint32_t prow = s_p + half * 8192 + (uint32_t)row * 128;
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    st_shared_v4(prow + (((uint32_t)u ^ ((uint32_t)row & 7)) << 4), pk[4 * u], pk[4 * u + 1],
-                                 pk[4 * u + 2], pk[4 * u + 3]);
-                if (__any_sync(0xffffffffu, corr)) {
-                    tc_fence_after();
+                // P's buffer is free once the P.V two tiles back has completed
+                if (!(ok = wait(M.p_empty[b], (g >> 1) ^ 1u, abort))) break;
+                uint64_t acc = f2(0.f, 0.f);
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t o[32];
-                        const uint32_t ta = tmem + lane_base + kColO + 32 * k;
-                        tmem_ld_32x32b_x32(ta, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-                        tmem_st_32x32b_x32(ta, o);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(sa + 16 * k, r);
+                    tmem_wait_ld();
+                    if (k == 3) {
+                        tc_fence_before();
+                        warp_arrive_leader(M.s_empty[b], lane);
                     }
-                    tmem_wait_st();
-                }
-                if (__any_sync(0xffffffffu, (bad0 | bad1) != 0)) {
-                    // rows of V to clear (the stage's last use was the tile before's, which has completed)
-#pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-                        uint32_t rows = __reduce_or_sync(0xffffffffu, s ? bad1 : bad0);
-                        if (!rows) continue;
-                        const uint32_t vs = v_seq + half + 2 * s;
-                        if (!(ok = wait(M.v_full[vs % kVStages], vs / kVStages, abort))) break;
-                        const uint32_t at = s_v + (vs % kVStages) * kStageBytes + (uint32_t)lane * 16;
-                        for (; rows; rows &= rows - 1) {  // 4 pieces of 128 bytes: a lane 16 of them
-                            const uint32_t ra = at - (lane & 24) * 16 + (lane >> 3) * 4096 + (__ffs(rows) - 1) * 128;
-                            st_shared_v4(ra, 0u, 0u, 0u, 0u);
+                    const uint32_t v = (k & 2 ? v1 : v0) >> (16 * (k & 1));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = 8 * u + 2 * j;
+                            float x0, x1;
+                            f2_split(ffma2(f2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f2(sc, sc), f2(-mu, -mu)), x0, x1);
+                            if (!whole) {
+                                x0 = v & (1u << at) ? x0 : -INFINITY;
+                                x1 = v & (2u << at) ? x1 : -INFINITY;
+                            }
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            acc = fadd2(acc, f2(p0, p1));
+                            pk[j] = pack_bf16(p0, p1);
                         }
+                        st_shared_v4(prow + b * kPBytes + (((uint32_t)(2 * k + u) ^ ((uint32_t)row & 7)) << 4), pk[0], pk[1],
+                                     pk[2], pk[3]);
+                    }
+                }
+                float a0, a1;
+                f2_split(acc, a0, a1);
+                l = first ? a0 + a1 : fmaf(al, l, a0 + a1);
+                if (__any_sync(0xffffffffu, corr || (bad0 | bad1) != 0)) {
+                    // O is whole, and V's stages have been left, once the previous tile's P.V has completed
+                    if (g > 0 && !(ok = wait(M.p_empty[b ^ 1], (g - 1) >> 1, abort))) break;
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, corr)) {
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t o[32];
+                            const uint32_t ta = tmem + lane_base + kColO + 32 * k;
+                            tmem_ld_32x32b_x32(ta, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                            tmem_st_32x32b_x32(ta, o);
+                        }
+                        tmem_wait_st();
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {  // rows of V to clear
+                        uint32_t rows = __reduce_or_sync(0xffffffffu, k ? bad1 : bad0);
+                        if (!rows) continue;
+                        const uint32_t vs = v_seq + half + 2 * k;
+                        if (!(ok = wait(M.v_full[vs % kVStages], vs / kVStages, abort))) break;
+                        // (4 pieces of 128 bytes: a lane 16 of them)
+                        const uint32_t at = s_v + (vs % kVStages) * kStageBytes + (lane >> 3) * 4096 + (lane & 7) * 16;
+                        for (; rows; rows &= rows - 1) st_shared_v4(at + (__ffs(rows) - 1) * 128, 0u, 0u, 0u, 0u);
                     }
                     if (!ok) break;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                warp_arrive_leader(M.p_full, lane);
+                warp_arrive_leader(M.p_full[b], lane);
                 v_seq += min(kTileBlocks, t.nb - kTileBlocks * i);
             }
             if (!ok) break;
@@ -727,27 +772,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (t.nb == 0 && split) continue;  // (its sum is 0: O is not looked at)
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k) {  // 32 d at a time
-                const int d0 = 256 * half + 32 * k;
-                uint32_t o[32];
+            for (int k = 0; k < 16; ++k) {  // 16 d at a time
+                const int d0 = 256 * half + 16 * k;
+                uint32_t o[16];
                 __syncwarp();
                 if (t.nb) {
-                    tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * k, o);
+                    tmem_ld_32x32b_x16(tmem + lane_base + kColO + 16 * k, o);
                     tmem_wait_ld();
+                    if (k == 15) {
+                        tc_fence_before();
+                        warp_arrive_leader(M.o_empty, lane);
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-                if (t.nb && k == 7) {
-                    tc_fence_before();
-                    warp_arrive_leader(M.o_empty, lane);
+                    for (int j = 0; j < 16; ++j) o[j] = 0u;
                 }
                 if constexpr (kRope) {
                     // (a + i b)(c - i s), on the f32 sums (partials too: the merge is linear)
                     const int e0 = d0 - (kD - p.rope_dim);
-                    if (e0 + 32 > 0) {
+                    if (e0 + 16 > 0) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 8; ++j) {
                             const int e = e0 + 2 * j;
                             if (e < 0) continue;
                             const float2 cs = __ldg(turn + (e >> 1));
@@ -761,21 +806,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (split && mine) {
                     float* at = p.part_o + part * kD + d0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) out[j] = o[8 * q + j];
                         store32(at + 8 * q, out);
                     }
                 } else if (mine) {
-                    __nv_bfloat16* at = p.o + flat * kD + d0;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            out[j] = pack_bf16(__uint_as_float(o[16 * q + 2 * j]) * inv,
-                                               __uint_as_float(o[16 * q + 2 * j + 1]) * inv);
-                        store32(at + 16 * q, out);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        out[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    store32(p.o + flat * kD + d0, out);
                 }
             }
             if (t.nb) ++c_o;
@@ -838,7 +878,9 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     p.window = (int)c.window;
     p.first = (int)c.first;
     p.n_splits = window_splits(c.n, c.a.b, c.h, c.window, c.first, sms);
-    p.n_units = (c.n * c.h / kM + c.a.b) * p.n_splits;
+    const int64_t units = (c.n * c.h / kM + c.a.b) * p.n_splits;
+    if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;
+    p.n_units = (int)units;
     if (p.n_splits > 1) {
         p.part_ml = reinterpret_cast<float*>(c.scratch);
         p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(c.scratch) +
@@ -857,7 +899,7 @@ cudaError_t window_tc_launch(const WindowCall& c) {
         if (dev < 64) configured[dev] = true;
     }
     int64_t pairs = sms / 2;
-    if (pairs > p.n_units) pairs = p.n_units;
+    if (pairs > units) pairs = units;
     e = launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, c.stream, q_map, k_map, v_map, p);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, c.n, c.h, kD, p.n_splits,

@@ -107,7 +107,7 @@ def check_codes(values, scale_bytes, y, fmt, rel):
     a = y / s.repeat_interleave(32, -1)
     # (half a step of the larger neighbour's, where the value lies at a power of two)
     tol = torch.maximum(half_step(a, fmt), half_step(values, fmt)) + rel * a.abs()
-    bad = (values - a).abs() > tol
+    bad = ~((values - a).abs() <= tol)
     assert not bad.any(), f"{int(bad.sum())} codes off, first {bad.nonzero()[0].tolist()}"
 
 

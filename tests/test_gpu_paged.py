@@ -204,7 +204,7 @@ def _check_attn(bt, q, pool, kv_scale, sink, window, first, rot=None, scale=None
     scale = q.shape[-1] ** -0.5 if scale is None else scale
     o, lse = _attend(bt, q, pool, kv_scale, sink, scale, window, first, rot)
     want, lse_w, tol, lse_tol = _paged.attention(bt, q, pool, kv_scale, sink, scale, window, first, rot)
-    off = (o.double() - want).abs() > tol
+    off = ~((o.double() - want).abs() <= tol)
     assert not off.any(), f"{int(off.sum())} of {off.numel()} off, first {off.nonzero()[0].tolist()}: " \
                           f"{o[off][:4].tolist()} {want[off][:4].tolist()}"
     assert ((lse.double() - lse_w).abs() <= lse_tol)[lse_w.isfinite()].all()
