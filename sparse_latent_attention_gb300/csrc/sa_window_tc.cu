@@ -22,9 +22,9 @@
 // product; a row that is not finite gives every query row such a logit.  Rows that see the row have a NaN there
 // anyway.
 //
-// Roles (each CTA of the pair, 448 threads): warps 0 and 13 issue the pair's logits and P.V (rank 0) or pass on that
-// this CTA's stages have landed (rank 1); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 12 V,
-// warp 3 Q; warps 4-7 softmax; warps 8-11 epilogue.  Every wait is bounded; one that gives up raises the timeout bit
+// Roles (each CTA of the pair, 704 threads): warps 0 and 21 issue the pair's logits and P.V (rank 0; rank 1's warp 21
+// passes on that its V has landed); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 20 V,
+// warp 3 Q; warps 4-7 and 8-11 softmax, every second tile each; warps 12-15 and 16-19 epilogue, half of d each.  Every wait is bounded; one that gives up raises the timeout bit
 // and every role unwinds.
 
 #include <cuda.h>
@@ -48,11 +48,13 @@ constexpr int kM = 128;            // query rows of a task
 constexpr int kBlock = 32;         // positions of a block
 constexpr int kTileBlocks = 4;     // blocks of a tile
 constexpr int kKStages = 4, kVStages = 4;  // of the two rings
-constexpr int kThreads = 448;
+constexpr int kThreads = 704;
 constexpr int kInfos = 4;          // tiles, and tasks, described ahead
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr uint32_t kColO = 0, kColS = 256;
+// TMEM columns: O, two S buffers, a row's running maximum after the last two tiles, and the softmax groups' final
+// maxima and sums
+constexpr uint32_t kColO = 0, kColS = 256, kColM = 384, kColT = 388;
 
 constexpr uint32_t kStageBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [8 blocks of 64 d][64 rows][128 B]
@@ -75,22 +77,23 @@ struct Task {
 };
 
 struct Misc {
-    // full: this CTA's part has landed, and in rank 0 the other's too, which passes it on
+    // full: of K and Q both CTAs' parts have landed (rank 0's); of V this CTA's, in rank 0 the other's too, which
+    // passes it on
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t q_full[4], q_empty[4];          // (the same for a quarter of Q)
+    uint64_t q_full[4], q_empty[4];          // (a quarter of Q)
     uint64_t s_full[2], s_empty[2];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
     uint64_t p_full[2], p_empty[2], o_full, o_empty;
     uint64_t info_full[kInfos];
     uint64_t task_full[kInfos], task_empty[kInfos];
     uint64_t stats_full, stats_empty;
-    uint64_t pair_bar[2], done;
+    uint64_t pair_bar[2][2], m_full[4], sum_full[2][2], sum_empty[2][2], done;
     uint32_t tmem_base;
     int abort;
     int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
     int whole[kInfos];                // every token of the task sees every position of the tile's blocks
     Task task[kInfos];
     float mx[2][128];
-    float stats_m[64], stats_l[128];
+    float sum[2][128];
 };
 constexpr uint32_t kSmem = kOffMisc + sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory budget");
@@ -173,10 +176,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+// The same, and (cta_group::2) into this CTA with the barrier in either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
                                             int32_t w, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(
             dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
@@ -214,6 +227,35 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// One, two and four 32-bit words of a thread's own TMEM lane.
+__device__ __forceinline__ float tmem_ld_x1(uint32_t at) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(at) : "memory");
+    tmem_wait_ld();
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_ld_x4(uint32_t at, float& a, float& b, float& c, float& d) {
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+    tmem_wait_ld();
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+    c = __uint_as_float(r[2]);
+    d = __uint_as_float(r[3]);
+}
+__device__ __forceinline__ void tmem_st_x1(uint32_t at, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(__float_as_uint(v)) : "memory");
+    tmem_wait_st();
+}
+__device__ __forceinline__ void tmem_st_x2(uint32_t at, float a, float b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "r"(__float_as_uint(a)),
+                 "r"(__float_as_uint(b))
+                 : "memory");
+    tmem_wait_st();
 }
 // 32 bytes at a 32-byte aligned address
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
@@ -288,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kKStages; ++s) {
-            mbar_init(smem_addr(&M.k_full[s]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.k_full[s]), 1);
             mbar_init(smem_addr(&M.k_empty[s]), 1);
         }
         for (int s = 0; s < kVStages; ++s) {
@@ -296,25 +338,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&M.v_empty[s]), 1);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_addr(&M.q_full[i]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.q_full[i]), 1);
             mbar_init(smem_addr(&M.q_empty[i]), 1);
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_addr(&M.info_full[i]), 1);
             mbar_init(smem_addr(&M.task_full[i]), 1);
-            mbar_init(smem_addr(&M.task_empty[i]), 13);  // warps 0 and 2-13
+            mbar_init(smem_addr(&M.task_empty[i]), 21);  // all warps but the one that fills it
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&M.s_full[b]), 1);
             mbar_init(smem_addr(&M.s_empty[b]), 8);
-            mbar_init(smem_addr(&M.pair_bar[b]), 2);
+            mbar_init(smem_addr(&M.pair_bar[b][0]), 2);
+            mbar_init(smem_addr(&M.pair_bar[b][1]), 2);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&M.sum_full[b][i]), 2);
+                mbar_init(smem_addr(&M.sum_empty[b][i]), 2);
+            }
             mbar_init(smem_addr(&M.p_full[b]), 8);
             mbar_init(smem_addr(&M.p_empty[b]), 1);
         }
         mbar_init(smem_addr(&M.o_full), 1);
-        mbar_init(smem_addr(&M.o_empty), 8);
-        mbar_init(smem_addr(&M.stats_full), 4);
-        mbar_init(smem_addr(&M.stats_empty), 4);
+        mbar_init(smem_addr(&M.o_empty), 16);
+        for (int w = 0; w < 4; ++w) mbar_init(smem_addr(&M.m_full[w]), 1);
+        mbar_init(smem_addr(&M.stats_full), 8);
+        mbar_init(smem_addr(&M.stats_empty), 8);
         mbar_init(smem_addr(&M.done), 2);
         M.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -373,9 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++nth;
             if (!more) break;
         }
-    } else if (warp == 0 || warp == 13) {
+    } else if (warp == 0 || warp == 21) {
         // ------------------------------------------------------------------ the pair's products
-        // Warp 0 issues the logits, warp 13 P.V (rank 1: they pass on that K, and V, have landed).  One warp for both
+        // Warp 0 issues the logits, warp 21 P.V (rank 1: they pass on that K, and V, have landed).  One warp for both
         // spent 600 cycles a stage of 256 cycles of products (a wait for a barrier that has long completed takes
         // 130, a commit 75, and the tensor pipe holds too few products to bridge them); of two, one's products run
         // behind the other's barriers.
@@ -388,7 +436,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool landed = false;  // stage st has: its barrier was looked at while the stage before it was issued
         auto stage_in = [&](uint64_t* full) {
             if (!landed) ok = ok && wait(full[st], st_use, abort);
-            if (!leader && ok) warp_arrive_leader(full[st], lane);
             return ok;
         };
         auto peek = [&](uint64_t* full, uint32_t stages) {
@@ -406,37 +453,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         };
         Task t;
-        if (warp == 0) {
+        if (warp == 0 && !leader) {
+            while (fetch(t)) {
+            }
+        } else if (warp == 0) {
             while (fetch(t)) {
                 if (t.nb == 0) continue;
                 const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks;
                 for (int i = 0; i < nt && ok; ++i, ++g) {
                     const uint32_t b = g & 1;
-                    if (leader) ok = wait(M.s_empty[b], (g >> 1) ^ 1u, abort);
+                    ok = wait(M.s_empty[b], (g >> 1) ^ 1u, abort);
                     for (int q = 0; q < 4 && ok; ++q) {
                         if (i == 0) {
                             ok = wait(M.q_full[q], c, abort);
-                            if (!leader && ok) warp_arrive_leader(M.q_full[q], lane);
                         }
                         if (!ok || !stage_in(M.k_full)) break;
-                        bool next = false;
-                        if (leader) {
-                            tc_fence_after();
-                            next = peek(M.k_full, kKStages);
-                            const uint32_t alo = (uint32_t)a_s + q * (16384 >> 4);
-                            const uint32_t blo = (uint32_t)b_s + st * (kStageBytes >> 4);
+                        tc_fence_after();
+                        const bool next = peek(M.k_full, kKStages);
+                        const uint32_t alo = (uint32_t)a_s + q * (16384 >> 4);
+                        const uint32_t blo = (uint32_t)b_s + st * (kStageBytes >> 4);
 #pragma unroll 4
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t at = (k & 3) * (32 >> 4);
-                                mma_pair(tmem + kColS + 64 * b, alo + (k >> 2) * (8192 >> 4) + at,
-                                         (uint32_t)(a_s >> 32), blo + (k >> 2) * (1024 >> 4) + at,
-                                         (uint32_t)(b_s >> 32), id_s, (q | k) != 0);
-                            }
-                            if (i == nt - 1) commit_pair(M.q_empty[q]);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t at = (k & 3) * (32 >> 4);
+                            mma_pair(tmem + kColS + 64 * b, alo + (k >> 2) * (8192 >> 4) + at, (uint32_t)(a_s >> 32),
+                                     blo + (k >> 2) * (1024 >> 4) + at, (uint32_t)(b_s >> 32), id_s, (q | k) != 0);
                         }
+                        if (i == nt - 1) commit_pair(M.q_empty[q]);
                         stage_out(M.k_empty, kKStages, next);
                     }
-                    if (leader && ok) commit_pair(M.s_full[b]);
+                    if (ok) commit_pair(M.s_full[b]);
                 }
                 ++c;
             }
@@ -452,6 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int nb = min(kTileBlocks, t.nb - kTileBlocks * i);
                     for (int j = 0; j < nb && ok; ++j) {
                         if (!stage_in(M.v_full)) break;
+                        if (!leader) warp_arrive_leader(M.v_full[st], lane);
                         bool next = false;
                         if (leader) {
                             tc_fence_after();
@@ -481,19 +527,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // released (an abandoned one too)
         if (leader) commit_pair(M.done);
         wait(M.done, 0, abort);
-    } else if (warp == 2 || warp == 12) {
-        // ------------------------------------------------------------------ K (warp 2) and V (warp 12)
-        const bool is_v = warp == 12;
+    } else if (warp == 2 || warp == 20) {
+        // ------------------------------------------------------------------ K (warp 2) and V (warp 20)
+        const bool is_v = warp == 20;
         const uint32_t stages = is_v ? kVStages : kKStages, ring = is_v ? s_v : s_k;
         uint64_t* const full = is_v ? M.v_full : M.k_full;
         uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
         uint32_t st = 0, st_use = 0, g = 0;
+        // (V's copies complete at this CTA's barrier, K's of both CTAs at rank 0's, which expects them all)
         auto load = [&](uint32_t bytes, auto issue) {
             if (!(ok = ok && wait(empty[st], st_use ^ 1u, abort))) return;
             if (lane == 0) {
                 const uint32_t bar = smem_addr(&full[st]);
-                mbar_arrive_expect_tx(bar, bytes);
-                issue(ring + st * kStageBytes, bar);
+                if (is_v || rank == 0) mbar_arrive_expect_tx(bar, bytes);
+                issue(ring + st * kStageBytes, is_v ? bar : at_leader(bar));
             }
             if (++st == stages) {
                 st = 0;
@@ -538,14 +585,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int g0 = __shfl_sync(0xffffffffu, row, (int)rank) >> 3,
                           g1 = __shfl_sync(0xffffffffu, row, (int)rank + 2) >> 3;
                 for (int q = 0; q < 4 && ok; ++q)
-                    load((uint32_t)own * 8192u, [&](uint32_t dst, uint32_t bar) {
-                        if (own > 0) tma_load_4d(dst, &k_map, 0, 0, 2 * q, g0, bar);
-                        if (own > 1) tma_load_4d(dst + 8192, &k_map, 0, 0, 2 * q, g1, bar);
+                    load((uint32_t)nb * 8192u, [&](uint32_t dst, uint32_t bar) {
+                        if (own > 0) tma_load_4d_pair(dst, &k_map, 0, 0, 2 * q, g0, bar);
+                        if (own > 1) tma_load_4d_pair(dst + 8192, &k_map, 0, 0, 2 * q, g1, bar);
                     });
             }
         }
-        // after a failed wait, the copies under way land before the CTA exits
-        if (!ok && lane == 0) {
+        // after a failed wait, the copies under way land before the CTA exits (K's: rank 0 sees those of both, and
+        // rank 1 gives its own the time)
+        if (!ok && lane == 0 && !is_v && rank != 0)
+            for (int i = 0; i < 100; ++i) __nanosleep(1000);
+        if (!ok && lane == 0 && (is_v || rank == 0)) {
             const uint32_t n = st_use * stages + st;
             for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
                 mbar_drain(smem_addr(&full[k % stages]), (k / stages) & 1);
@@ -560,32 +610,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(M.q_empty[q], c ^ 1u, abort))) break;
                 if (lane == 0) {
                     const uint32_t bar = smem_addr(&M.q_full[q]);
-                    mbar_arrive_expect_tx(bar, 16384);
-                    tma_load_3d(s_q + q * 16384, &q_map, 0, t.row0 + 64 * (int)rank, 2 * q, bar);
+                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 16384);
+                    tma_load_3d_pair(s_q + q * 16384, &q_map, 0, t.row0 + 64 * (int)rank, 2 * q, at_leader(bar));
                 }
                 ++sent;
             }
             ++c;
         }
-        if (!ok && lane == 0)
+        if (!ok && lane == 0 && rank == 0)
             for (uint32_t k = sent > 4 ? sent - 4 : 0; k < sent; ++k) mbar_drain(smem_addr(&M.q_full[k % 4]), (k / 4) & 1);
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------------ softmax
         // A thread has one row of the CTA's 64 and half of a tile's columns (64: blocks `half` and half + 2); the
-        // thread 64 further has the other half, and the two trade their maxima.  A block's logits are read from TMEM
+        // thread 64 further has the other half, and the two trade their maxima.  Two groups of four warps take the
+        // tiles in turn: a tile's chain of steps is longer than its products, and of two tiles' chains only the
+        // running maximum is passed from one to the next (through TMEM, which the same lanes of either group read).
+        // Each group sums its own tiles' p.  A block's logits are read from TMEM
         // twice, for the maximum and for p, by loops: with both blocks in registers and the loops unrolled, the
         // warps of a SM waited for instructions (4.2 warps at every issue, over a sliding window's prefill).
         const int w = warp & 3, half = w >> 1, row = 32 * (w & 1) + lane, me = 32 * w + lane;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const uint32_t prow = s_p + half * 8192 + (uint32_t)row * 128;
         const float sc = p.scale_log2;
+        const uint32_t grp = (uint32_t)(warp - 4) >> 2;
         uint32_t g = 0, c = 0, v_seq = 0;
         Task t;
         while (fetch(t)) {
             // (a row that is not the task's own has the last one's mask; it is not stored)
             const int pos = t.pos0 + (t.off0 + min(64 * (int)rank + row, t.rows - 1)) / p.h;
-            float m = -INFINITY, mu = 0.f, l = 0.f;
+            float m = -INFINITY, l = 0.f;  // of this group's tiles: the maximum that l is relative to
             for (int i = 0; kTileBlocks * i < t.nb && ok; ++i, ++g) {
+                const uint32_t v_at = v_seq;
+                v_seq += min(kTileBlocks, t.nb - kTileBlocks * i);
+                if ((g & 1) != grp) continue;
                 const uint32_t b = g & 1, gi = g % kInfos;
                 const bool first = i == 0;
                 ok = wait(M.info_full[gi], g / kInfos, abort) && wait(M.s_full[b], g >> 1, abort);
@@ -644,19 +701,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bad1 = base1 == -2 ? 0u : bad1 & ~seen(p.window, p.first, base1, t.pos0, t.pmax);
                 }
                 M.mx[b][me] = mt;
-                warp_arrive(M.pair_bar[w & 1], lane);
-                if (!(ok = wait(M.pair_bar[w & 1], g, abort))) break;
+                warp_arrive(M.pair_bar[grp][w & 1], lane);
+                if (!(ok = wait(M.pair_bar[grp][w & 1], g >> 1, abort))) break;
                 mt = fmaxf(mt, M.mx[b][me ^ 64]);
-                float al = 1.f, mn = mt;
-                if (!first) {
-                    mn = mt > m + kRescaleThreshold ? mt : m;
-                    if (mn != m) al = fast_exp2(m - mn);  // 0 when m = -inf (nothing summed yet)
-                }
-                const bool corr = !first && mn != m;
-                m = mn;
-                mu = mn == -INFINITY ? 0.f : mn;
                 // P's buffer is free once the P.V two tiles back has completed
                 if (!(ok = wait(M.p_empty[b], (g >> 1) ^ 1u, abort))) break;
+                // the running maximum before this tile, and after it: raised only where a logit exceeds it by more
+                // than the threshold
+                if (g > 0 && !(ok = wait(M.m_full[w], g - 1, abort))) break;
+                float before = -INFINITY, mn = mt;
+                if (!first) {
+                    tc_fence_after();
+                    before = tmem_ld_x1(tmem + lane_base + kColM + (b ^ 1));
+                    mn = mt > before + kRescaleThreshold ? mt : before;
+                }
+                tmem_st_x1(tmem + lane_base + kColM + b, mn);
+                tc_fence_before();
+                warp_arrive(M.m_full[w], lane);
+                const bool corr = !first && mn != before;
+                const float mu = mn == -INFINITY ? 0.f : mn;
                 uint64_t acc = f2(0.f, 0.f);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
@@ -690,12 +753,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 float a0, a1;
                 f2_split(acc, a0, a1);
-                l = first ? a0 + a1 : fmaf(al, l, a0 + a1);
+                l = fmaf(mn == m ? 1.f : fast_exp2(m - mn), l, a0 + a1);  // (0 l where nothing was summed yet)
+                m = mn;
                 if (__any_sync(0xffffffffu, corr || (bad0 | bad1) != 0)) {
                     // O is whole, and V's stages have been left, once the previous tile's P.V has completed
+                    // (the other group's barrier: the phase before had completed when that group passed its maximum on)
                     if (g > 0 && !(ok = wait(M.p_empty[b ^ 1], (g - 1) >> 1, abort))) break;
                     tc_fence_after();
                     if (__any_sync(0xffffffffu, corr)) {
+                        const float al = corr ? fast_exp2(before - mn) : 1.f;
 #pragma unroll 1
                         for (int k = 0; k < 8; ++k) {
                             uint32_t o[32];
@@ -712,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 2; ++k) {  // rows of V to clear
                         uint32_t rows = __reduce_or_sync(0xffffffffu, k ? bad1 : bad0);
                         if (!rows) continue;
-                        const uint32_t vs = v_seq + half + 2 * k;
+                        const uint32_t vs = v_at + half + 2 * k;
                         if (!(ok = wait(M.v_full[vs % kVStages], vs / kVStages, abort))) break;
                         // (4 pieces of 128 bytes: a lane 16 of them)
                         const uint32_t at = s_v + (vs % kVStages) * kStageBytes + (lane >> 3) * 4096 + (lane & 7) * 16;
@@ -723,19 +789,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive_leader(M.p_full[b], lane);
-                v_seq += min(kTileBlocks, t.nb - kTileBlocks * i);
             }
             if (!ok) break;
             if (!(ok = wait(M.stats_empty, c ^ 1u, abort))) break;
-            M.stats_l[me] = l;
-            if (half == 0) M.stats_m[row] = mu;
+            tmem_st_x2(tmem + lane_base + kColT + 2 * grp, m, l);
+            tc_fence_before();
             warp_arrive(M.stats_full, lane);
             ++c;
         }
     } else {
         // ------------------------------------------------------------------ epilogue
-        // A thread has one row and 256 of its d: 128 dh + 0..127 of its half.
-        const int w = warp & 3, half = w >> 1, row = 32 * (w & 1) + lane;
+        // A thread has one row and 128 of its d: of the half that its lane holds, those of its group of four warps.
+        const int w = warp & 3, grp = (warp - 12) >> 2, half = w >> 1, row = 32 * (w & 1) + lane;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const bool split = p.n_splits > 1;
         uint32_t c = 0, c_o = 0;
@@ -748,7 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kRope) {
                 int64_t pos = t.pos0 + min(tok, t.pmax - t.pos0);
                 if (pos >= p.npos) {
-                    if (mine && half == 0) atomicOr(p.status, kStatusBadIndex);
+                    if (mine && half + grp == 0) atomicOr(p.status, kStatusBadIndex);
                     pos = p.npos - 1;
                 }
                 turn = reinterpret_cast<const float2*>(p.rope) + max(pos, (int64_t)0) * (p.rope_dim >> 1);
@@ -758,28 +823,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (ok && t.nb) ok = wait(M.o_full, c_o, abort);
             if (!ok) break;
             tc_fence_after();
-            const float l = M.stats_l[row] + M.stats_l[row + 64], mu = M.stats_m[row];
+            // the two groups' sums, relative to the larger maximum (the last tile's), then the two halves'
+            float m0, l0, m1, l1;
+            tmem_ld_x4(tmem + lane_base + kColT, m0, l0, m1, l1);
+            tc_fence_before();
             warp_arrive(M.stats_empty, lane);
+            const float top = fmaxf(m0, m1), mu = top == -INFINITY ? 0.f : top;
+            const float mine_l = l0 * fast_exp2(m0 - mu) + l1 * fast_exp2(m1 - mu);
+            if (!(ok = wait(M.sum_empty[grp][w & 1], c ^ 1u, abort))) break;  // (the last task's have been read)
+            M.sum[grp][32 * w + lane] = mine_l;
+            warp_arrive(M.sum_full[grp][w & 1], lane);
+            if (!(ok = wait(M.sum_full[grp][w & 1], c, abort))) break;
+            const float l = mine_l + M.sum[grp][(32 * w + lane) ^ 64];
+            warp_arrive(M.sum_empty[grp][w & 1], lane);
             ++c;
             const int64_t flat = (int64_t)t.row0 + r;
             const int64_t part = ((int64_t)(t.tok0 + tok) * p.n_splits + t.split) * p.h + head;
             float inv = 0.f;
             if (!split) {
                 if (l > 0.f) inv = 1.f / (l + fast_exp2(sink * kLog2e - mu));
-                if (p.lse && mine && half == 0) p.lse[flat] = log_sum_exp(l, mu, sink);
-            } else if (mine && half == 0) {
+                if (p.lse && mine && half + grp == 0) p.lse[flat] = log_sum_exp(l, mu, sink);
+            } else if (mine && half + grp == 0) {
                 *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(mu, l);
             }
             if (t.nb == 0 && split) continue;  // (its sum is 0: O is not looked at)
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {  // 16 d at a time
+            for (int k = 8 * grp; k < 8 * grp + 8; ++k) {  // 16 d at a time
                 const int d0 = 256 * half + 16 * k;
                 uint32_t o[16];
                 __syncwarp();
                 if (t.nb) {
                     tmem_ld_32x32b_x16(tmem + lane_base + kColO + 16 * k, o);
                     tmem_wait_ld();
-                    if (k == 15) {
+                    if (k == 8 * grp + 7) {
                         tc_fence_before();
                         warp_arrive_leader(M.o_empty, lane);
                     }
