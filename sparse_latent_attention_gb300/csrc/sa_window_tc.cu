@@ -49,12 +49,12 @@ constexpr int kBlock = 32;         // positions of a block
 constexpr int kTileBlocks = 4;     // blocks of a tile
 constexpr int kKStages = 4, kVStages = 4;  // of the two rings
 constexpr int kThreads = 704;
-constexpr int kInfos = 4;          // tiles, and tasks, described ahead
+constexpr int kInfos = 8, kTasks = 4;  // tiles and tasks described ahead
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// TMEM columns: O, two S buffers, a row's running maximum after the last two tiles, and the softmax groups' final
+// TMEM columns: O, three S buffers, a row's running maximum after the last two tiles, and the softmax groups' final
 // maxima and sums
-constexpr uint32_t kColO = 0, kColS = 256, kColM = 384, kColT = 388;
+constexpr uint32_t kColO = 0, kColS = 256, kColM = 448, kColT = 452;
 
 constexpr uint32_t kStageBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [8 blocks of 64 d][64 rows][128 B]
@@ -81,17 +81,17 @@ struct Misc {
     // passes it on
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t q_full[4], q_empty[4];          // (a quarter of Q)
-    uint64_t s_full[2], s_empty[2];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
+    uint64_t s_full[3], s_empty[3];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
     uint64_t p_full[2], p_empty[2], o_full, o_empty;
     uint64_t info_full[kInfos];
-    uint64_t task_full[kInfos], task_empty[kInfos];
+    uint64_t task_full[kTasks], task_empty[kTasks];
     uint64_t stats_full, stats_empty;
     uint64_t pair_bar[2][2], m_full[4], sum_full[2][2], sum_empty[2][2], done;
     uint32_t tmem_base;
     int abort;
     int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
     int whole[kInfos];                // every token of the task sees every position of the tile's blocks
-    Task task[kInfos];
+    Task task[kTasks];
     float mx[2][128];
     float sum[2][128];
 };
@@ -343,12 +343,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_addr(&M.info_full[i]), 1);
+        }
+        for (int i = 0; i < kTasks; ++i) {
             mbar_init(smem_addr(&M.task_full[i]), 1);
             mbar_init(smem_addr(&M.task_empty[i]), 21);  // all warps but the one that fills it
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 3; ++b) {
             mbar_init(smem_addr(&M.s_full[b]), 1);
             mbar_init(smem_addr(&M.s_empty[b]), 8);
+        }
+        for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&M.pair_bar[b][0]), 2);
             mbar_init(smem_addr(&M.pair_bar[b][1]), 2);
             for (int i = 0; i < 2; ++i) {
@@ -390,8 +394,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t nth = 0;
     bool ok = true;
     auto fetch = [&](Task& t) {
-        const uint32_t i = nth % kInfos;
-        ok = ok && wait(M.task_full[i], nth / kInfos, abort);
+        const uint32_t i = nth % kTasks;
+        ok = ok && wait(M.task_full[i], nth / kTasks, abort);
         if (!ok) return false;
         t = M.task[i];
         warp_arrive(M.task_empty[i], lane);
@@ -414,8 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool more = u0 < p.n_units;
             if (more && (u >= p.n_units || !task_of(p, u, t))) continue;
             t.more = more;
-            const uint32_t i = nth % kInfos;
-            if (!(ok = wait(M.task_empty[i], (nth / kInfos) ^ 1u, abort))) break;
+            const uint32_t i = nth % kTasks;
+            if (!(ok = wait(M.task_empty[i], (nth / kTasks) ^ 1u, abort))) break;
             if (lane == 0) M.task[i] = t;
             warp_arrive(M.task_full[i], lane);
             ++nth;
@@ -461,8 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (t.nb == 0) continue;
                 const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks;
                 for (int i = 0; i < nt && ok; ++i, ++g) {
-                    const uint32_t b = g & 1;
-                    ok = wait(M.s_empty[b], (g >> 1) ^ 1u, abort);
+                    const uint32_t b = g % 3;
+                    ok = wait(M.s_empty[b], (g / 3) ^ 1u, abort);
                     for (int q = 0; q < 4 && ok; ++q) {
                         if (i == 0) {
                             ok = wait(M.q_full[q], c, abort);
@@ -643,12 +647,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t v_at = v_seq;
                 v_seq += min(kTileBlocks, t.nb - kTileBlocks * i);
                 if ((g & 1) != grp) continue;
-                const uint32_t b = g & 1, gi = g % kInfos;
+                // (S's buffers go round in threes, from one group to the other: the use before this one had completed when
+                // that group passed its maximum on, a tile ago)
+                const uint32_t b = g & 1, sb = g % 3, gi = g % kInfos;
                 const bool first = i == 0;
-                ok = wait(M.info_full[gi], g / kInfos, abort) && wait(M.s_full[b], g >> 1, abort);
+                ok = wait(M.info_full[gi], g / kInfos, abort) && wait(M.s_full[sb], g / 3, abort);
                 if (!ok) break;
                 const bool whole = __shfl_sync(0xffffffffu, M.whole[gi], 0) != 0;
-                const uint32_t sa = tmem + lane_base + kColS + 64 * b;
+                const uint32_t sa = tmem + lane_base + kColS + 64 * sb;
                 tc_fence_after();
                 uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu, bad0 = 0, bad1 = 0;  // by block: seen, and to be cleared
                 if (!whole) {
@@ -728,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     if (k == 3) {
                         tc_fence_before();
-                        warp_arrive_leader(M.s_empty[b], lane);
+                        warp_arrive_leader(M.s_empty[sb], lane);
                     }
                     const uint32_t v = (k & 2 ? v1 : v0) >> (16 * (k & 1));
 #pragma unroll
@@ -847,28 +853,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(mu, l);
             }
             if (t.nb == 0 && split) continue;  // (its sum is 0: O is not looked at)
+            // Lanes 2 i and 2 i + 1 trade 32-byte pieces of their rows, so that each store writes 64 bytes of 16 rows (32
+            // of 32, a lane's own, take twice the time: a store's time is its pieces')
+            const bool odd = lane & 1;
+            const int at_row = mine ? (split ? (int)part : (int)flat) : -1;
+            const int even_row = __shfl_sync(0xffffffffu, at_row, lane & 30), odd_row = __shfl_sync(0xffffffffu, at_row, lane | 1);
 #pragma unroll 1
-            for (int k = 8 * grp; k < 8 * grp + 8; ++k) {  // 16 d at a time
-                const int d0 = 256 * half + 16 * k;
-                uint32_t o[16];
+            for (int k = 4 * grp; k < 4 * grp + 4; ++k) {  // 32 d at a time
+                const int d0 = 256 * half + 32 * k;
+                uint32_t o[32];
                 __syncwarp();
                 if (t.nb) {
-                    tmem_ld_32x32b_x16(tmem + lane_base + kColO + 16 * k, o);
+                    tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * k, o);
                     tmem_wait_ld();
-                    if (k == 8 * grp + 7) {
+                    if (k == 4 * grp + 3) {
                         tc_fence_before();
                         warp_arrive_leader(M.o_empty, lane);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
                 }
                 if constexpr (kRope) {
                     // (a + i b)(c - i s), on the f32 sums (partials too: the merge is linear)
                     const int e0 = d0 - (kD - p.rope_dim);
-                    if (e0 + 16 > 0) {
+                    if (e0 + 32 > 0) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+                        for (int j = 0; j < 16; ++j) {
                             const int e = e0 + 2 * j;
                             if (e < 0) continue;
                             const float2 cs = __ldg(turn + (e >> 1));
@@ -878,20 +889,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                uint32_t out[8];
-                if (split && mine) {
-                    float* at = p.part_o + part * kD + d0;
+                // two pieces, of even and odd lanes, into x[0..7] (the even row's) and x[8..15] (the odd row's)
+                auto trade_and_store = [&](uint32_t (&x)[16], char* base, int row_bytes, int at) {
+                    uint32_t e[8], f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[8 + j], 1);
+                        e[j] = odd ? got : x[j];
+                        f[j] = odd ? x[8 + j] : got;
+                    }
+                    if (even_row >= 0) store32(base + (int64_t)even_row * row_bytes + at + 32 * odd, e);
+                    if (odd_row >= 0) store32(base + (int64_t)odd_row * row_bytes + at + 32 * odd, f);
+                };
+                uint32_t x[16];
+                if (split) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) out[j] = o[8 * q + j];
-                        store32(at + 8 * q, out);
+                        for (int j = 0; j < 16; ++j) x[j] = o[16 * q + j];
+                        trade_and_store(x, reinterpret_cast<char*>(p.part_o), 4 * kD, 4 * (d0 + 16 * q));
                     }
-                } else if (mine) {
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        out[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                    store32(p.o + flat * kD + d0, out);
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    trade_and_store(x, reinterpret_cast<char*>(p.o), 2 * kD, 2 * d0);
                 }
             }
             if (t.nb) ++c_o;
