@@ -600,6 +600,36 @@ def read_status(workspace, clear=False, stream=None) -> int:
     return _status(workspace.get_device(), "sa_read_status", stream, _ptr(workspace), int(bool(clear)))
 
 
+# The calls below are made once a layer and token: their checks are one look at what is usual, and the precise ones, which
+# name what is wrong, only where that look finds something else.
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_functions = {}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(name, dev, stream, *args):
+    """_call for the functions that a step makes many calls of: the library's function looked up once."""
+    if stream is not None or dev != _current_device():
+        return _call(name, dev, stream, *args)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions.setdefault(name, getattr(load(), name))
+    st = f(*args, _raw_stream(dev))
+    if st:
+        _lib.check(st, name)
+
+
+def _check_rows(t, name, dtypes, shape, dev):
+    """Raises what is wrong with a tensor of strided rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA {' or '.join(map(str, dtypes))} tensor")
+    if tuple(t.shape) != shape or (t.numel() and shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have shape {shape} and unit column stride, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
 def add_rms_norm(x, weight, *, residual=None, eps=1e-6, out=None, codes=None, scales=None, stream=None):
     """residual += x (in place), and the root-mean-square norm of the sum (of x without a residual):
     y = h * rsqrt(mean(h^2) + eps) * weight, h as the residual holds it.
@@ -608,29 +638,33 @@ def add_rms_norm(x, weight, *, residual=None, eps=1e-6, out=None, codes=None, sc
     ``x`` itself and is made (and returned) when neither it nor ``codes`` is given, and, quantised as
     act_quant_fp8 quantises, to ``codes`` [n, d] and ``scales`` [n, d / 32] uint8.  All but the weight with
     unit column stride; rows may be strided.  Returns out (None when only codes were asked for)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _BF16:
         raise TypeError("x must be a CUDA bf16 tensor")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be a 2-D tensor with unit column stride")
-    n, d = x.shape
+    n, d = shape
+    xs, xc = x.stride()
+    if xc != 1 and d > 1:
+        raise ValueError("x must be a 2-D tensor with unit column stride")
     dev = x.get_device()
+    many = n > 1
 
     def rows_of(t, name, dtypes, width):
-        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-            raise TypeError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor")
-        if tuple(t.shape) != (n, width) or (width > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must have shape ({n}, {width}) and unit column stride")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-        return t.data_ptr(), t.stride(0) if n > 1 else width
+        """(address, distance of its rows) of a tensor of rows."""
+        if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (n, width) and t.get_device() == dev
+                and (t.stride(1) == 1 or width < 2)):
+            _check_rows(t, name, dtypes, (n, width), dev)
+        return t.data_ptr(), t.stride(0) if many else width
 
-    _need(weight, "weight", torch.float32, x.device)
-    if tuple(weight.shape) != (d,):
+    if not (isinstance(weight, torch.Tensor) and weight.dtype is _F32 and weight.shape == (d,)
+            and weight.get_device() == dev and weight.is_contiguous()):
+        _need(weight, "weight", _F32, x.device)
         raise ValueError(f"weight shape {tuple(weight.shape)} != ({d},)")
     kind, res, rs = _lib.SA_RESIDUAL_NONE, None, 0
     if residual is not None:
-        res, rs = rows_of(residual, "residual", (torch.bfloat16, torch.float32), d)
-        kind = _lib.SA_RESIDUAL_F32 if residual.dtype == torch.float32 else _lib.SA_RESIDUAL_BF16
+        res, rs = rows_of(residual, "residual", (_BF16, _F32), d)
+        kind = _lib.SA_RESIDUAL_F32 if residual.dtype is _F32 else _lib.SA_RESIDUAL_BF16
     if (codes is None) != (scales is None):
         raise ValueError("give codes and scales together")
     cd = sc = po = None
@@ -638,35 +672,46 @@ def add_rms_norm(x, weight, *, residual=None, eps=1e-6, out=None, codes=None, sc
     if codes is not None:
         if d % 32:
             raise ValueError(f"blocks of 32 need a row of a multiple of 32, got {d}")
-        cd, cs = rows_of(codes, "codes", (torch.uint8,), d)
-        sc, ss = rows_of(scales, "scales", (torch.uint8,), d // 32)
-    elif out is None:
-        out = _new(stream, lambda: torch.empty((n, d), dtype=torch.bfloat16, device=x.device))
+        cd, cs = rows_of(codes, "codes", (_U8,), d)
+        sc, ss = rows_of(scales, "scales", (_U8,), d // 32)
     if out is not None:
-        po, os_ = rows_of(out, "out", (torch.bfloat16,), d)
+        po, os_ = rows_of(out, "out", (_BF16,), d)
+    elif codes is None:
+        if stream is None and x.is_contiguous():
+            out = torch.empty_like(x)
+        else:
+            out = _new(stream, lambda: torch.empty(shape, dtype=_BF16, device=x.device))
+        po, os_ = out.data_ptr(), d
     if n and d:
-        _call("sa_add_rms_norm", dev, stream, x.data_ptr(), n, d, x.stride(0) if n > 1 else d, weight.data_ptr(),
-              float(eps), res, kind, rs, po, os_, cd, cs, sc, ss)
+        _launch("sa_add_rms_norm", dev, stream, x.data_ptr(), n, d, xs if many else d, weight.data_ptr(),
+                eps, res, kind, rs, po, os_, cd, cs, sc, ss)
     return out
 
 
 def _batch(page_table, q_start, kv_len, dev):
-    """The packed batch's tables: (b, the arguments they make)."""
+    """The packed batch's tables: (b, max_pages, distance of the table's rows)."""
+    try:
+        b, max_pages = page_table.shape
+        if (page_table.dtype is _I32 and q_start.dtype is _I32 and kv_len.dtype is _I32
+                and page_table.get_device() == q_start.get_device() == kv_len.get_device() == dev
+                and kv_len.shape == (b,) and q_start.shape == (b + 1,) and kv_len.is_contiguous()
+                and q_start.is_contiguous() and (page_table.is_contiguous() or page_table.stride(1) == 1)):
+            return b, max_pages, page_table.stride(0) if b > 1 else max_pages
+    except (AttributeError, ValueError):
+        pass
     for t, name, dim in ((page_table, "page_table", 2), (q_start, "q_start", 1), (kv_len, "kv_len", 1)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != _I32:
             raise TypeError(f"{name} must be a CUDA int32 tensor")
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-        if t.dim() != dim or (t.numel() and t.stride(-1) != 1):
+        if t.dim() != dim or (t.numel() > 1 and t.stride(-1) != 1):
             raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''} and unit column stride")
-    b = kv_len.shape[0]
-    if page_table.shape[0] != b or q_start.shape[0] != b + 1:
-        raise ValueError(f"page_table {tuple(page_table.shape)} and q_start {tuple(q_start.shape)} do not fit "
-                         f"the {b} sequences of kv_len")
-    return b, page_table.shape[1], page_table.stride(0) if b > 1 else page_table.shape[1]
+    raise ValueError(f"page_table {tuple(page_table.shape)} and q_start {tuple(q_start.shape)} do not fit "
+                     f"the {kv_len.shape[0]} sequences of kv_len")
 
 
-_QUANT = {"fp8": SA_KV_FP8_E4M3, "fp4": SA_KV_FP4_E2M1}
+_QUANT = {None: SA_KV_BF16, "fp8": SA_KV_FP8_E4M3, "fp4": SA_KV_FP4_E2M1}
+_NO_POOL = (None, 0, 0)
 
 
 def page_write(x, page_table, q_start, kv_len, *, pages=None, codes=None, scales=None, quant=None, weight=None,
@@ -684,71 +729,79 @@ def page_write(x, page_table, q_start, kv_len, *, pages=None, codes=None, scales
     and rows may be strided.
     workspace: one of new_workspace or new_window_workspace, whose status word notes a position without a page
     (or past the rotations); such a row is not written."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _BF16:
         raise TypeError("x must be a CUDA bf16 tensor")
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D tensor with unit column stride")
     n, d = x.shape
     dev = x.get_device()
     b, max_pages, table_stride = _batch(page_table, q_start, kv_len, dev)
-    shape = None
+    n_pages = page = None
 
-    def pool_of(t, name, dtype, widths):
-        nonlocal shape
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    def pool_of(t, name, dtype, width):
+        """(address, distance of rows, of pages) of a pool of rows of ``width``."""
+        nonlocal n_pages, page
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
             raise TypeError(f"{name} must be a {dtype} tensor")
-        if t.dim() != 3 or t.shape[2] not in widths or t.stride(2) != 1 or shape not in (None, t.shape[:2]):
-            raise ValueError(f"{name} shape {tuple(t.shape)} does not fit rows of {d}"
-                             f"{'' if shape is None else f' in {shape[0]} pages of {shape[1]}'}"
-                             " with unit column stride")
+        shape, (ps, rs, cs) = t.shape, t.stride() if t.dim() == 3 else (0, 0, 0)
+        if page is None and cs:
+            n_pages, page, _ = shape
+        if shape != (n_pages, page, width) or cs != 1:
+            raise ValueError(f"{name} shape {tuple(shape)} does not fit rows of {width}"
+                             f"{'' if page is None else f' in {n_pages} pages of {page}'} with unit column stride")
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-        shape = t.shape[:2]
-        return t.data_ptr(), t.stride(1) if t.shape[1] > 1 else t.shape[2], t.stride(0)
+        return t.data_ptr(), rs if page > 1 else width, ps
 
-    if quant is not None and quant not in _QUANT:
-        raise ValueError(f"quant must be one of {sorted(_QUANT)}")
-    fmt = _QUANT.get(quant, SA_KV_BF16)
+    fmt = _QUANT.get(quant)
+    if fmt is None:
+        raise ValueError("quant must be None, 'fp8' or 'fp4'")
     if (codes is None) != (scales is None):
         raise ValueError("give codes and scales together")
-    pg = cd = sc = (None, 0, 0)
+    pg = cd = sc = _NO_POOL
     if codes is not None:
-        cd = pool_of(codes, "codes", torch.uint8, (d, d // 2))
-        sc = pool_of(scales, "scales", torch.uint8, (d // 32,))
-        held = SA_KV_FP8_E4M3 if codes.shape[2] == d else SA_KV_FP4_E2M1
+        width = codes.shape[-1] if isinstance(codes, torch.Tensor) and codes.dim() else 0
+        held = SA_KV_FP4_E2M1 if 2 * width == d else SA_KV_FP8_E4M3
+        cd = pool_of(codes, "codes", _U8, width if held == SA_KV_FP4_E2M1 else d)
+        sc = pool_of(scales, "scales", _U8, d // 32)
         if quant is not None and held != fmt:
             raise ValueError(f"quant {quant} does not fit codes of shape {tuple(codes.shape)}")
         fmt = held
     if pages is not None:
-        pg = pool_of(pages, "pages", torch.bfloat16, (d,))
-    if shape is None:
+        pg = pool_of(pages, "pages", _BF16, d)
+    if page is None:
         raise ValueError("give pages, or codes and scales")
     w = turn = None
     npos = rope_dim = 0
     if weight is not None:
-        _need(weight, "weight", torch.float32, x.device)
-        if tuple(weight.shape) != (d,):
+        if not (isinstance(weight, torch.Tensor) and weight.dtype is _F32 and weight.shape == (d,)
+                and weight.get_device() == dev and weight.is_contiguous()):
+            _need(weight, "weight", _F32, x.device)
             raise ValueError(f"weight shape {tuple(weight.shape)} != ({d},)")
         w = weight.data_ptr()
     if rope is not None:
-        turn, npos, rope_dim = _rotation(rope, x.device)
+        turn, npos, rope_dim = _rotation(rope, dev, x)
+    status = None
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, x.device)
+        _need(workspace, "workspace", _U8, x.device)
         if workspace.numel() < SA_STATUS_BYTES:
             raise ValueError("workspace is too small")
-    _call("sa_page_write", dev, stream, x.data_ptr(), n, d, x.stride(0) if n > 1 else d, page_table.data_ptr(),
-          max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(), b, shape[0], shape[1], fmt, *pg, *cd, *sc,
-          w, float(eps), turn, npos, rope_dim, _ptr(workspace))
+        status = workspace.data_ptr()
+    _launch("sa_page_write", dev, stream, x.data_ptr(), n, d, x.stride(0) if n > 1 else d, page_table.data_ptr(),
+            max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(), b, n_pages, page, fmt, *pg, *cd, *sc,
+            w, eps, turn, npos, rope_dim, status)
 
 
-def _rotation(rope, device):
+def _rotation(rope, dev, like):
     """A table of rotations by position: (address, positions, rope_dim)."""
-    _need(rope, "rope", torch.float32, device)
-    if rope.dim() != 3 or rope.shape[2] != 2:
-        raise ValueError(f"rope shape {tuple(rope.shape)} is not [positions, rope_dim / 2, 2]")
-    if rope.numel() == 0:  # (its address would say: no rotation)
+    if not (isinstance(rope, torch.Tensor) and rope.dtype is _F32 and rope.get_device() == dev and rope.is_contiguous()):
+        _need(rope, "rope", _F32, like.device)
+    shape = rope.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise ValueError(f"rope shape {tuple(shape)} is not [positions, rope_dim / 2, 2]")
+    if not shape[0] or not shape[1]:  # (its address would say: no rotation)
         raise ValueError("rope is empty")
-    return rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+    return rope.data_ptr(), shape[0], 2 * shape[1]
 
 
 def window_workspace_size(n, b, h, d, window, first, page, kv_format=SA_KV_BF16) -> int:
@@ -778,37 +831,46 @@ def window_attn(q, pages, sink, page_table, q_start, kv_len, softmax_scale, wind
     q_start[b] on are left as they were.
     lse: an f32 tensor [n, h] that receives the log of each softmax's denominator (the sink's term included).
     rope [positions, rope_dim / 2, 2] f32: also turn o's last dims back by each token's position (d = 512)."""
-    _need(q, "q", torch.bfloat16)
-    device = q.device
-    if q.dim() != 3:
-        raise ValueError(f"q shape {tuple(q.shape)} is not [n, h, d]")
-    n, h, d = q.shape
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype is _BF16 and q.is_contiguous()):
+        _need(q, "q", _BF16)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q shape {tuple(shape)} is not [n, h, d]")
+    n, h, d = shape
     dev = q.get_device()
-    if pages.dim() != 3:
-        raise ValueError(f"pages shape {tuple(pages.shape)} is not [n_pages, page, .]")
-    n_pages, page = pages.shape[:2]
-    fmt = _kv_format(pages, kv_scale, n_pages, d, device)
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
+        raise ValueError("pages must be a tensor [n_pages, page, .]")
+    n_pages, page, _ = pages.shape
+    fmt = SA_KV_BF16
+    if not (kv_scale is None and pages.dtype is _BF16 and pages.get_device() == dev and pages.shape[2] == d
+            and pages.is_contiguous()):
+        fmt = _kv_format(pages, kv_scale, n_pages, d, q.device)
     b, max_pages, table_stride = _batch(page_table, q_start, kv_len, dev)
-    _need(sink, "sink", torch.float32, device)
-    if tuple(sink.shape) != (h,):
+    if not (isinstance(sink, torch.Tensor) and sink.dtype is _F32 and sink.shape == (h,) and sink.get_device() == dev
+            and sink.is_contiguous()):
+        _need(sink, "sink", _F32, q.device)
         raise ValueError(f"sink shape {tuple(sink.shape)} != ({h},)")
     if out is None:
-        out = _new(stream, lambda: torch.empty_like(q))
-    else:
-        _need(out, "out", torch.bfloat16, device)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+        out = torch.empty_like(q) if stream is None else _new(stream, lambda: torch.empty_like(q))
+    elif not (isinstance(out, torch.Tensor) and out.dtype is _BF16 and out.shape == shape and out.get_device() == dev
+              and out.is_contiguous()):
+        _need(out, "out", _BF16, q.device)
+        raise ValueError("out must have q's shape")
+    lp = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, device)
-        if tuple(lse.shape) != (n, h):
+        if not (isinstance(lse, torch.Tensor) and lse.dtype is _F32 and lse.shape == (n, h) and lse.get_device() == dev
+                and lse.is_contiguous()):
+            _need(lse, "lse", _F32, q.device)
             raise ValueError(f"lse shape {tuple(lse.shape)} != {(n, h)}")
-    turn, npos, rope_dim = (None, 0, 0) if rope is None else _rotation(rope, device)
+        lp = lse.data_ptr()
+    turn, npos, rope_dim = _NO_POOL if rope is None else _rotation(rope, dev, q)
     if workspace is None:
-        workspace = _new(stream, lambda: new_window_workspace(n, b, h, d, window, first, page, fmt, device))
-    else:
-        _need(workspace, "workspace", torch.uint8, device)
-    _call("sa_window_attn", dev, stream, q.data_ptr(), pages.data_ptr(), _ptr(kv_scale), fmt, sink.data_ptr(),
-          page_table.data_ptr(), max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(),
-          float(softmax_scale), n, b, h, d, n_pages, page, window, first, out.data_ptr(), _ptr(lse), turn, npos,
-          rope_dim, workspace.data_ptr(), workspace.numel())
+        workspace = _new(stream, lambda: new_window_workspace(n, b, h, d, window, first, page, fmt, q.device))
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and workspace.get_device() == dev
+              and workspace.is_contiguous()):
+        _need(workspace, "workspace", _U8, q.device)
+    _launch("sa_window_attn", dev, stream, q.data_ptr(), pages.data_ptr(), None if kv_scale is None else kv_scale.data_ptr(),
+            fmt, sink.data_ptr(), page_table.data_ptr(), max_pages, table_stride, q_start.data_ptr(), kv_len.data_ptr(),
+            softmax_scale, n, b, h, d, n_pages, page, window, first, out.data_ptr(), lp, turn, npos, rope_dim,
+            workspace.data_ptr(), workspace.numel())
     return out

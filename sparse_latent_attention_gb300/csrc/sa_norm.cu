@@ -23,7 +23,7 @@ struct Norm {
     int64_t xs, n;
     int d;
     const float* weight;
-    float eps;
+    RmsOf of;
     void* res;
     int64_t rs;
     __nv_bfloat16* out;
@@ -35,9 +35,9 @@ struct Norm {
 };
 
 // The sum over a block's warps of the pairs that they hold (every thread gets it).
-__device__ __forceinline__ Two block_sum(Two v, Two* part) {
+__device__ __forceinline__ Two block_sum(float x, Two* part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    v = warp_sum(v);
+    const Two v = warp_sum(x);
     if (lane == 0) part[warp] = v;
     __syncthreads();
     return warp_sum(lane < warps ? part[lane] : Two{0.f, 0.f});
@@ -121,8 +121,7 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
             sum += (s[0] + s[1]) + (s[2] + s[3]);
         }
     }
-    const Two all = kWarpRow ? warp_sum({sum, 0.f}) : block_sum({sum, 0.f}, part);
-    const Two r = inverse_rms(all, (float)p.d, p.eps);
+    const Two r = inverse_rms(kWarpRow ? warp_sum(sum) : block_sum(sum, part), p.of);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int c = me + i * width;
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
         if constexpr (kRes == SA_RESIDUAL_F32) res32[k] = h = h + res32[k];
         sum = fmaf(h, h, sum);
     }
-    const Two r = inverse_rms(block_sum({sum, 0.f}, part), (float)p.d, p.eps);
+    const Two r = inverse_rms(block_sum(sum, part), p.of);
     for (int k0 = threadIdx.x & ~31; k0 < p.d; k0 += blockDim.x) {  // (a warp's 32 elements)
         const int lane = threadIdx.x & 31, k = k0 + lane;
         float y = 0.f;
@@ -258,7 +257,7 @@ extern "C" sa_status sa_add_rms_norm(const void* x, int64_t n, int d, int64_t x_
     p.n = n;
     p.d = d;
     p.weight = weight;
-    p.eps = eps;
+    p.of = rms_of(d, eps);
     p.res = residual;
     p.rs = r_stride;
     p.out = reinterpret_cast<__nv_bfloat16*>(out);

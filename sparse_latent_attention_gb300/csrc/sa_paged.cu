@@ -32,7 +32,7 @@ struct Write {
     uint8_t* scales;
     int64_t ss, sp;
     const float* weight;
-    float eps;
+    RmsOf of;
     const float* rot;
     int64_t npos;
     int rope_dim;
@@ -41,9 +41,11 @@ struct Write {
 
 // A warp a token, eight consecutive elements a lane and chunk (kPer chunks of 256).  kRun tokens one behind the
 // other a warp: their rows are under way before the first one's sequence and page are known, and the sequence is
-// looked for once.
+// looked for once.  Bound by instructions, some 550 a row of 512 with norm, rotation and 4-bit codes (a third of them the
+// norm's products and what they lose, a third the codes and their round trip): 65536 such rows take 60 us with two
+// tokens a warp and six blocks a SM, 64 with four tokens or four blocks, 65 with one token.
 template <int kQuant, int kPer, int kRun, bool kVec>
-__global__ void __launch_bounds__(128) page_write_kernel(const __grid_constant__ Write p) {
+__global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(const __grid_constant__ Write p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, chunks = p.d >> 3;
@@ -57,45 +59,78 @@ __global__ void __launch_bounds__(128) page_write_kernel(const __grid_constant__
             in[r][i] = c < chunks && t0 + r < p.n ? load8<kVec>(p.x + (t0 + r) * p.xs + 8 * c)
                                                   : make_uint4(0u, 0u, 0u, 0u);
         }
+    // the weights of this lane's columns, for all of its tokens
+    uint64_t w[kPer][4];
+    if (p.weight) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = lane + 32 * i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[i][j] = c < chunks ? tc::f2(__ldg(p.weight + 8 * c + 2 * j), __ldg(p.weight + 8 * c + 2 * j + 1)) : 0ull;
+        }
+    }
     paged::Token k = {0, 0, -1};
 #pragma unroll
     for (int r = 0; r < kRun; ++r) {
         const int64_t t = t0 + r;
         if (t >= p.n) break;
-        if (r > 0 && t < k.end && k.pos >= -1) {
+        if (r > 0 && t < k.end) {
             ++k.pos;
         } else {
             k = paged::token_of(p.a, t);
         }
         if (k.pos < 0) continue;
-        const int64_t row = paged::row_of(p.a, k.seq, (uint32_t)k.pos);
-        if (row < 0 || (p.rot && k.pos >= p.npos)) {
+        uint32_t page, off;
+        if (!paged::place_of(p.a, k.seq, (uint32_t)k.pos, page, off) || (p.rot && k.pos >= p.npos)) {
             if (p.status && lane == 0) atomicOr(p.status, kStatusBadIndex);
             continue;
         }
-        const int64_t g = row / p.a.page, off = row - g * p.a.page;
-        float v[kPer][8];
-        float sum = 0.f;
+        uint64_t v[kPer][4];  // elements 2 j and 2 j + 1
+        uint64_t sum = 0ull;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            unpacked8(in[r][i], v[i]);
-            float s[4];
+            float e[8];
+            unpacked8(in[r][i], e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = fmaf(v[i][2 * j], v[i][2 * j], v[i][2 * j + 1] * v[i][2 * j + 1]);
-            sum += (s[0] + s[1]) + (s[2] + s[3]);
+            for (int j = 0; j < 4; ++j) {
+                v[i][j] = tc::f2(e[2 * j], e[2 * j + 1]);
+                sum = fma2(v[i][j], v[i][j], sum);
+            }
         }
         Two f = {1.f, 0.f};
-        if (p.weight) f = inverse_rms(warp_sum({sum, 0.f}), (float)p.d, p.eps);
+        if (p.weight) {
+            float s0, s1;
+            tc::f2_split(sum, s0, s1);
+            f = inverse_rms(warp_sum(s0 + s1), p.of);
+        }
+        const uint64_t fh = tc::f2(f.h, f.h), fn = tc::f2(-f.h, -f.h), fl = tc::f2(f.l, f.l);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = lane + 32 * i;
             if (32 * i >= chunks) break;
             const bool mine = c < chunks;
-            Two y[8];
+            float h[8], l[8], out[8];  // y in two parts, and rounded
+            if (p.weight) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y[j] = {v[i][j], 0.f};
-                if (p.weight) y[j] = mul(mul(v[i][j], f), mine ? __ldg(p.weight + 8 * c + j) : 0.f);
+                for (int j = 0; j < 4; ++j) {
+                    // x f as p + e + x fl, that times w: each product's rounding from the product again with the
+                    // rounded one, which the negative factor gives, taken away
+                    const uint64_t x = v[i][j], pr = mul2(x, fh), np = mul2(x, fn);
+                    const uint64_t pl = fma2(x, fl, fma2(x, fh, np));
+                    const uint64_t q = mul2(pr, w[i][j]), ql = fma2(pl, w[i][j], fma2(pr, w[i][j], mul2(np, w[i][j])));
+                    tc::f2_split(q, h[2 * j], h[2 * j + 1]);
+                    tc::f2_split(ql, l[2 * j], l[2 * j + 1]);
+                    tc::f2_split(add2(q, ql), out[2 * j], out[2 * j + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tc::f2_split(v[i][j], h[2 * j], h[2 * j + 1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    l[j] = 0.f;
+                    out[j] = h[j];
+                }
             }
             const int first = p.d - p.rope_dim;
             if (p.rot && mine && 8 * c + 8 > first) {
@@ -104,15 +139,23 @@ __global__ void __launch_bounds__(128) page_write_kernel(const __grid_constant__
                 for (int j = 0; j < 4; ++j) {
                     const int e = 8 * c + 2 * j - first;
                     if (e < 0) continue;
-                    const float2 w = __ldg(turn + (e >> 1));
-                    const Two a = y[2 * j], b = y[2 * j + 1], bs = mul(b, w.y), bc = mul(b, w.x);
-                    y[2 * j] = add(mul(a, w.x), {-bs.h, -bs.l});
-                    y[2 * j + 1] = add(mul(a, w.y), bc);
+                    // a c - b s: b s rounded to u, what that lost, a c - u in one rounding, and the parts' own
+                    const float2 cs = __ldg(turn + (e >> 1));
+                    const float a = h[2 * j], b = h[2 * j + 1], al = l[2 * j], bl = l[2 * j + 1];
+                    const float u = b * cs.y, ul = fmaf(bl, cs.y, fmaf(b, cs.y, -u));
+                    const float z = b * cs.x, zl = fmaf(bl, cs.x, fmaf(b, cs.x, -z));
+                    h[2 * j] = fmaf(a, cs.x, -u);
+                    l[2 * j] = fmaf(al, cs.x, -ul);
+                    h[2 * j + 1] = fmaf(a, cs.y, z);
+                    l[2 * j + 1] = fmaf(al, cs.y, zl);
+                    out[2 * j] = h[2 * j] + l[2 * j];
+                    out[2 * j + 1] = h[2 * j + 1] + l[2 * j + 1];
                 }
             }
-            float out[8];
+            if (!(largest8(out) < INFINITY)) {  // (an infinity has no second part)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) out[j] = rounded(y[j]);
+                for (int j = 0; j < 8; ++j) out[j] = rounded({h[j], l[j]});
+            }
             uint4 values;
             if constexpr (kQuant == SA_KV_BF16) {
                 values = packed8(out);
@@ -123,23 +166,22 @@ __global__ void __launch_bounds__(128) page_write_kernel(const __grid_constant__
                 quantise8<kFp4>(out, codes, se);
                 values = values8<kFp4>(codes, se);
                 if (p.codes && mine) {
-                    store_codes8<kVec, kFp4>(p.codes + g * p.cp + off * p.cs + (kFp4 ? 4 : 8) * c, codes);
-                    if ((c & 3) == 0) p.scales[g * p.sp + off * p.ss + (c >> 2)] = (uint8_t)se;
+                    store_codes8<kVec, kFp4>(p.codes + page * p.cp + off * p.cs + (kFp4 ? 4 : 8) * c, codes);
+                    if ((c & 3) == 0) p.scales[page * p.sp + off * p.ss + (c >> 2)] = (uint8_t)se;
                 }
             }
-            if (p.pages && mine) store8<kVec>(p.pages + g * p.pp + off * p.ps + 8 * c, values);
+            if (p.pages && mine) store8<kVec>(p.pages + page * p.pp + off * p.ps + 8 * c, values);
         }
     }
 }
 
 template <int kQuant, int kPer, bool kVec>
 cudaError_t write_run(const Write& p, cudaStream_t st) {
-    // a wave of 128-thread blocks holds 64 tokens a SM: below that, a token a warp; beyond, several
-    constexpr int kRun = kPer == 4 ? 2 : 4;
-    const bool few = p.n <= 64 * (int64_t)device_sm_count();
-    const int64_t per = few ? 4 : 4 * kRun, grid = (p.n + per - 1) / per;
+    // a wave of blocks holds 24 tokens a SM: below that, a token a warp; beyond, two
+    const bool few = p.n <= 24 * (int64_t)device_sm_count();
+    const int64_t per = few ? 4 : 8, grid = (p.n + per - 1) / per;
     return few ? launch_pdl(page_write_kernel<kQuant, kPer, 1, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p)
-               : launch_pdl(page_write_kernel<kQuant, kPer, kRun, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p);
+               : launch_pdl(page_write_kernel<kQuant, kPer, 2, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p);
 }
 
 template <int kQuant>
@@ -305,7 +347,7 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
     p.ss = scales_stride;
     p.sp = scales_page_stride;
     p.weight = weight;
-    p.eps = eps;
+    if (weight) p.of = rms_of(d, eps);
     p.rot = rot;
     p.npos = npos;
     p.rope_dim = rot ? rope_dim : 0;

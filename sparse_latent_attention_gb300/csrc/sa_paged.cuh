@@ -47,13 +47,19 @@ __device__ __forceinline__ Token token_of(const Batch& a, int64_t t) {
     return k;
 }
 
+// The page of a position and the row in it; false where the table has no page for it.
+__device__ __forceinline__ bool place_of(const Batch& a, int64_t seq, uint32_t pos, uint32_t& page, uint32_t& row) {
+    const uint32_t j = pos / (uint32_t)a.page;
+    if ((int64_t)j >= a.max_pages) return false;
+    page = (uint32_t)__ldg(a.table + seq * a.table_stride + j);
+    row = pos - j * (uint32_t)a.page;
+    return (int64_t)page < a.n_pages;  // (a negative entry is beyond 2^31)
+}
+
 // The pool's row of a position, or -1 where the table has no page for it.
 __device__ __forceinline__ int64_t row_of(const Batch& a, int64_t seq, uint32_t pos) {
-    const uint32_t j = pos / (uint32_t)a.page;
-    if ((int64_t)j >= a.max_pages) return -1;
-    const int32_t g = __ldg(a.table + seq * a.table_stride + j);
-    if (g < 0 || g >= a.n_pages) return -1;
-    return (int64_t)g * a.page + (pos - j * (uint32_t)a.page);
+    uint32_t page, row;
+    return place_of(a, seq, pos, page, row) ? (int64_t)page * a.page + row : -1;
 }
 
 }  // namespace paged

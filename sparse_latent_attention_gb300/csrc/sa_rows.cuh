@@ -10,10 +10,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "sa_fp4.cuh"
 #include "sa_fp8.cuh"
+#include "sa_tc.cuh"
 
 namespace sa {
 namespace rows {
@@ -31,7 +33,7 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
 
 __device__ __forceinline__ Two add(Two a, Two b) {
     const Two s = two_sum(a.h, b.h);
-    if (!(fabsf(s.h) < INFINITY)) return {s.h, 0.f};
+    if (!(fabsf(s.h) < INFINITY)) return {s.h, 0.f};  // (an infinity has no second part)
     const float l = s.l + (a.l + b.l), h = s.h + l;
     return {h, l - (h - s.h)};
 }
@@ -48,32 +50,56 @@ __device__ __forceinline__ Two mul(Two x, float w) {
 // (an infinity has no second part)
 __device__ __forceinline__ float rounded(Two v) { return fabsf(v.h) < INFINITY ? v.h + v.l : v.h; }
 
-// The sum of one f32 a lane over a warp, and over pairs: the rounding of a tree's last additions, which a
-// whole sum shares, is kept.
+// Two elements an instruction: the packed products and sums.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) { return tc::fadd2(a, b); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) { return tc::ffma2(a, b, c); }
+
+// The sum of one f32 a lane over a warp: of the additions of a tree, the last two, whose rounding the whole sum shares,
+// keep what they lose (that of the ones before, of 4 sums and more, averages out: some 2^-26).
+__device__ __forceinline__ Two warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m > 2; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    Two s = two_sum(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    s = add(s, {__shfl_xor_sync(0xffffffffu, s.h, 1), __shfl_xor_sync(0xffffffffu, s.l, 1)});
+    return s;
+}
+// The same of pairs, every addition's rounding kept.
 __device__ __forceinline__ Two warp_sum(Two v) {
 #pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        const Two o = {__shfl_xor_sync(0xffffffffu, v.h, m), __shfl_xor_sync(0xffffffffu, v.l, m)};
-        v = add(v, o);
-    }
+    for (int m = 16; m; m >>= 1)
+        v = add(v, {__shfl_xor_sync(0xffffffffu, v.h, m), __shfl_xor_sync(0xffffffffu, v.l, m)});
     return v;
 }
 
-// (sum / d + eps)^(-1/2): the hardware's estimate r0 and one step of Newton's iteration, whose correction
-// r0 (1 - v r0^2) / 2 is formed from exact products and kept as the second part.  A sum that overflowed or
-// is a NaN gives what the estimate gives (0, NaN).
-__device__ __forceinline__ Two inverse_rms(Two sum, float d, float eps) {
-    if (!(sum.h < INFINITY)) return {rsqrtf(sum.h), 0.f};
-    const float q = __fdiv_rn(sum.h, d);
-    const float ql = __fdiv_rn(fmaf(-q, d, sum.h) + sum.l, d);
-    Two v = two_sum(q, eps);
-    v.l += ql;
+// What a norm over d elements needs of d and eps: (sum / d + eps)^(-1/2) = d^(1/2) (sum + d eps)^(-1/2).
+struct RmsOf {
+    Two shift, root;  // d eps and d^(1/2)
+};
+inline RmsOf rms_of(int d, float eps) {
+    auto two = [](double v) {
+        const float h = (float)v;
+        return Two{h, (float)(v - (double)h)};
+    };
+    return {two((double)d * (double)eps), two(sqrt((double)d))};
+}
+
+// The factor of a row with this sum of squares: the hardware's estimate r0 of v^(-1/2) and one step of Newton's
+// iteration, whose correction r0 (1 - v r0^2) / 2 is formed from exact products and kept as the second part.  A sum
+// that overflowed or is a NaN gives what the estimate gives (0, NaN).
+__device__ __forceinline__ Two inverse_rms(Two sum, const RmsOf& of) {
+    const Two v = add(sum, of.shift);
     const float r0 = rsqrtf(v.h);
     if (!(r0 > 0.f && r0 < INFINITY)) return {r0, 0.f};
     const float t = r0 * r0, tl = fmaf(r0, r0, -t);
     const float p = v.h * t, pl = fmaf(v.h, t, -p);
     const float e = ((1.f - p) - pl) - fmaf(v.h, tl, v.l * t);
-    return {r0, 0.5f * r0 * e};
+    const Two r = mul(Two{r0, 0.5f * r0 * e}, of.root.h);
+    return {r.h, fmaf(r0, of.root.l, r.l)};
 }
 
 // The magnitude's bits, a NaN as 0 and an infinity as the largest finite value.
@@ -93,35 +119,55 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
     return kFp4 && e > fp4::kMaxScale ? fp4::kMaxScale : e;
 }
 
+// The largest magnitude of eight values; a NaN among them comes out as one.
+__device__ __forceinline__ float largest8(const float (&v)[8]) {
+    auto top = [](float a, float b) {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+        return r;
+    };
+    return top(top(top(v[0], v[1]), top(v[2], v[3])), top(top(v[4], v[5]), top(v[6], v[7])));
+}
+
 // Eight elements of a block of 32, the other 24 with the warp's three neighbouring lanes (lanes 4 k .. 4 k
 // + 3; the whole warp calls).  codes: eight e4m3 bytes, or eight e2m1 codes in the first word; se: the
-// scale byte.
+// scale byte.  A block with an infinity or a NaN, whose bits exceed every finite value's, is looked at again.
 template <bool kFp4>
-__device__ __forceinline__ void quantise8(const float (&v)[8], uint2& codes, uint32_t& se) {
-    uint32_t m = 0;
+__device__ __forceinline__ void quantise8(float (&v)[8], uint2& codes, uint32_t& se) {
+    auto block_max = [](uint32_t m) {
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    uint32_t m = block_max(__float_as_uint(largest8(v)));
+    if (__any_sync(0xffffffffu, m > 0x7F7FFFFFu)) {
+        m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(v[i]));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        for (int i = 0; i < 8; ++i) {
+            m = max(m, finite_magnitude(v[i]));
+            if (kFp4 && v[i] != v[i]) v[i] = 0.f;  // (the format has no NaN)
+        }
+        m = block_max(m);
+    }
     se = scale_byte<kFp4>(m);
     const float inv = __uint_as_float((254u - se) << 23);  // 1 / s, exact
-    uint32_t w[2] = {0u, 0u};
+    const uint64_t inv2 = tc::f2(inv, inv);
+    uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float lo = v[2 * i] * inv, hi = v[2 * i + 1] * inv;
+        float lo, hi;
+        tc::f2_split(mul2(tc::f2(v[2 * i], v[2 * i + 1]), inv2), lo, hi);
         if constexpr (kFp4) {
-            lo = lo != lo ? 0.f : lo;  // (the format has no NaN)
-            hi = hi != hi ? 0.f : hi;
-            uint32_t c;
-            asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n cvt.u32.u8 %0, b;\n}" : "=r"(c) : "f"(lo), "f"(hi));
-            w[0] |= c << (8 * i);
+            asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n cvt.u32.u8 %0, b;\n}" : "=r"(c[i]) : "f"(lo), "f"(hi));
         } else {
-            uint16_t c;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
-            w[i >> 1] |= (uint32_t)c << (16 * (i & 1));
+            uint16_t h;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(h) : "f"(lo), "f"(hi));
+            c[i] = h;
         }
     }
-    codes = make_uint2(w[0], w[1]);
+    if constexpr (kFp4)
+        codes = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410), 0u);
+    else
+        codes = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // The bf16 values (exact) that eight codes and their scale byte stand for.

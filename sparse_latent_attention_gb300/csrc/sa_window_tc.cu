@@ -932,11 +932,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // How many parts a task's blocks are cut into: more than one only where the tasks (about: a token's tile or the
-// rows' tiles, whichever are more) leave pairs of SMs without work, and at most one a tile.
+// rows' tiles, whichever are more) leave pairs of SMs without work, and at most one for two tiles (a part of one tile
+// saves its time, some 2 us, and costs the merge, which takes as long and is a launch more).
 int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, int sms) {
     const int64_t tiles = std::max<int64_t>(std::max<int64_t>((n * h + kM - 1) / kM, std::min(b, n)), 1);
     const int64_t keys = first + kBlock + window + kM / h + 2 * kBlock;
-    const int64_t most = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks);
+    const int64_t most = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks) / 2;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / 2 / tiles, most), 64));
 }
 
