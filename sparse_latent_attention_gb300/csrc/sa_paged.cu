@@ -426,6 +426,8 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
         WindowCall c;
         c.q = q;
         c.kv = kv;
+        c.kv_scale = kv_scale;
+        c.kv_format = kv_format;
         c.sink = sink;
         c.a = a;
         c.softmax_scale = softmax_scale;

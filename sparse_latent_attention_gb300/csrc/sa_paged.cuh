@@ -68,6 +68,8 @@ __device__ __forceinline__ int64_t row_of(const Batch& a, int64_t seq, uint32_t 
 struct WindowCall {
     const void* q;
     const void* kv;
+    const uint8_t* kv_scale;
+    int kv_format;
     const float* sink;
     paged::Batch a;
     float softmax_scale;
@@ -84,7 +86,7 @@ struct WindowCall {
     cudaStream_t stream;
 };
 
-// Pairs of SMs over whole blocks of positions (sa_window_tc.cu): d = 512, bf16, pages of a multiple of 32 rows.
+// Pairs of SMs over whole blocks of positions (sa_window_tc.cu): d = 512, pages of a multiple of 32 rows.
 bool window_tc_supports(int d, int kv_format, int page);
 size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int64_t first);
 cudaError_t window_tc_launch(const WindowCall& c);

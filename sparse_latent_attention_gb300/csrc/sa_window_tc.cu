@@ -1,4 +1,4 @@
-// Window attention over a paged bf16 cache, head_dim 512, on pairs of SMs (tcgen05 with cta_group::2).
+// Window attention over a paged cache, head_dim 512, on pairs of SMs (tcgen05 with cta_group::2).
 //
 // Formulation.  Every query row of a sequence (token x head) attends to rows that its neighbours attend to
 // too, so a task is 128 query rows: consecutive (token, head) rows of one sequence (two tokens of 64 heads,
@@ -22,9 +22,11 @@
 // product; a row that is not finite gives every query row such a logit.  Rows that see the row have a NaN there
 // anyway.
 //
-// Roles (each CTA of the pair, 704 threads): warps 0 and 21 issue the pair's logits and P.V (rank 0; rank 1's warp 21
+// Roles (each CTA of the pair, 22 warps): warps 0 and 21 issue the pair's logits and P.V (rank 0; rank 1's warp 21
 // passes on that its V has landed); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 20 V,
-// warp 3 Q; warps 4-7 and 8-11 softmax, every second tile each; warps 12-15 and 16-19 epilogue, half of d each.  Every wait is bounded; one that gives up raises the timeout bit
+// warp 3 Q; warps 4-7 and 8-11 softmax, every second tile each; warps 12-15 and 16-19 epilogue, half of d each.
+// Rows of codes (25 warps) come through registers instead: warp 2 describes the tiles and pulls their rows into L2,
+// warps 16-19 widen K and 20-23 V into the same stages, warps 12-15 are the epilogue and warp 24 issues P.V.  Every wait is bounded; one that gives up raises the timeout bit
 // and every role unwinds.
 
 #include <cuda.h>
@@ -34,6 +36,8 @@
 
 #include <algorithm>
 
+#include "sa_fp4.cuh"
+#include "sa_fp8.cuh"
 #include "sa_internal.cuh"
 #include "sa_paged.cuh"
 #include "sa_tc.cuh"
@@ -48,8 +52,15 @@ constexpr int kM = 128;            // query rows of a task
 constexpr int kBlock = 32;         // positions of a block
 constexpr int kTileBlocks = 4;     // blocks of a tile
 constexpr int kKStages = 4, kVStages = 4;  // of the two rings
-constexpr int kThreads = 704;
 constexpr int kInfos = 8, kTasks = 4;  // tiles and tasks described ahead
+// Warps: the first four, softmax and the first epilogue group are the same for every format
+constexpr bool codes_of(int fmt) { return fmt != SA_KV_BF16; }
+constexpr int epilogue_groups(int fmt) { return codes_of(fmt) ? 1 : 2; }
+constexpr int kWarpEpilogue = 12;
+constexpr int kWarpWiden = 16;                                            // codes: four warps of K, four of V
+constexpr int warp_v(int fmt) { return codes_of(fmt) ? -1 : 20; }         // bf16: V's loads
+constexpr int warp_pv(int fmt) { return codes_of(fmt) ? 24 : 21; }
+constexpr int warps_of(int fmt) { return warp_pv(fmt) + 1; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // TMEM columns: O, three S buffers, a row's running maximum after the last two tiles, and the softmax groups' final
@@ -83,23 +94,26 @@ struct Misc {
     uint64_t q_full[4], q_empty[4];          // (a quarter of Q)
     uint64_t s_full[3], s_empty[3];          // (s_empty, p_full, o_empty: rank 0's, both CTAs arrive)
     uint64_t p_full[2], p_empty[2], o_full, o_empty;
-    uint64_t info_full[kInfos];
+    uint64_t info_full[kInfos], info_empty[kInfos];  // (info_empty: codes)
     uint64_t task_full[kTasks], task_empty[kTasks];
     uint64_t stats_full, stats_empty;
-    uint64_t pair_bar[2][2], m_full[4], sum_full[2][2], sum_empty[2][2], done;
+    uint64_t pair_bar[2][2], m_full[4], sum_full[2], sum_empty[2], done;
     uint32_t tmem_base;
     int abort;
     int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
+    int rows[kInfos][kTileBlocks];    // codes: their first rows in the pool
     int whole[kInfos];                // every token of the task sees every position of the tile's blocks
     Task task[kTasks];
     float mx[2][128];
-    float sum[2][128];
+    float sum[128];
 };
 constexpr uint32_t kSmem = kOffMisc + sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory budget");
 
 struct Params {
     paged::Batch a;
+    const uint8_t* kv8;       // codes and their scales
+    const uint8_t* kv_scale;
     const float* sink;
     __nv_bfloat16* o;
     float* lse;
@@ -114,7 +128,6 @@ struct Params {
     int h;
     int window, first;
     int n_splits;
-    int n_units;         // below 2^31: at most 2^24 tiles and b, 64 splits only of few tiles
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -275,17 +288,47 @@ static __device__ __noinline__ uint32_t seen(int window, int first, int base, in
     return base < 0 ? 0u : bits(p1 - window + 1 - base, p0 - base) | bits(0, min(first - 1, p0) - base);
 }
 
-// Unit u -> its task (the whole warp calls); false: nothing there.  Sequence i's tiles of 128 rows are numbered
-// from q_start[i] h / 128 + i on: more numbers than tiles, but the same on every CTA without a list of them.
-__device__ __forceinline__ int first_tile(const Params& p, int64_t i) {
-    return (int)((uint32_t)(min(max(__ldg(p.a.q_start + i), 0), p.n) * p.h) / kM) + (int)i;  // (n h < 2^31)
-}
-__device__ __forceinline__ bool task_of(const Params& p, int u, Task& t) {
+// Walks the sequences, 32 at a time, to the one that a tile of 128 rows is in; the tiles asked for rise.  (The whole warp.)
+struct Walk {
+    int seq0 = -32, before = 0, total = 0;  // the sequences at hand, and the tiles before and in them
+    int q0 = 0, q1 = 0, upto = 0;           // lane l: sequence seq0 + l's tokens, and its and its forerunners' tiles
+
+    // Sequence and tile in it, or false: there are no more.
+    __device__ __forceinline__ bool find(const Params& p, int tile, int lane, int& seq, int& at, int& from, int& to) {
+        while (tile >= before + total) {
+            before += total;
+            seq0 += 32;
+            if (seq0 >= p.a.b) return false;
+            const int s = seq0 + lane;
+            q0 = q1 = 0;
+            if (s < p.a.b) {
+                q0 = min(max(__ldg(p.a.q_start + s), 0), p.n);
+                q1 = min(max(__ldg(p.a.q_start + s + 1), q0), p.n);
+            }
+            upto = ((q1 - q0) * p.h + kM - 1) / kM;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += o;
+            }
+            total = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        const int who = __ffs(__ballot_sync(0xffffffffu, upto > tile - before)) - 1;
+        const int prev = __shfl_sync(0xffffffffu, upto, who == 0 ? 0 : who - 1);
+        seq = seq0 + who;
+        at = tile - before - (who == 0 ? 0 : prev);
+        from = __shfl_sync(0xffffffffu, q0, who);
+        to = __shfl_sync(0xffffffffu, q1, who);
+        return true;
+    }
+};
+
+// Unit u -> its task (the whole warp calls, with rising u); false: there are no more.
+__device__ __forceinline__ bool task_of(const Params& p, int u, int lane, Walk& walk, Task& t) {
     const int tile = u / p.n_splits;
-    const int seq = (int)paged::last_at_most(p.a.b, tile, [&](int64_t i) { return first_tile(p, i); });
-    const int q0 = min(max(__ldg(p.a.q_start + seq), 0), p.n), q1 = min(max(__ldg(p.a.q_start + seq + 1), 0), p.n);
-    const int r0 = (tile - first_tile(p, seq)) * kM, rows = (q1 - q0) * p.h - r0;
-    if (r0 < 0 || rows <= 0) return false;
+    int seq, at, q0, q1;
+    if (!walk.find(p, tile, lane, seq, at, q0, q1)) return false;
+    const int r0 = at * kM, rows = (q1 - q0) * p.h - r0;
     t.seq = seq;
     t.split = u - tile * p.n_splits;
     t.rows = min(rows, kM);
@@ -312,10 +355,79 @@ __device__ __forceinline__ bool task_of(const Params& p, int u, Task& t) {
     return true;
 }
 
-template <bool kRope>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// Rows of codes widened into the stages: a warp's share of a stage is `kLoads` pieces of 16 bytes a lane, which wait in
+// registers while the stage before is written.
+template <int kFmt>
+struct Widen {
+    static constexpr int kLoads = kFmt == SA_KV_FP8_E4M3 ? 4 : 2;
+    static constexpr int kRowBytes = kFmt == SA_KV_FP8_E4M3 ? kD : kD / 2;
+    uint4 code[kLoads];
+    uint32_t scale[kLoads];
+
+    // Rows row + first + (32 / lanes) x + lane / lanes, each from byte `at` of its codes and scale `sc` on.
+    __device__ __forceinline__ void load(const Params& p, int64_t row, int first, int lanes, int at, int sc, int lane) {
+        const int ul = lane & (lanes - 1), step = 32 / lanes, r0 = first + lane / lanes;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const int64_t r = row + r0 + step * x;
+            code[x] = __ldg(reinterpret_cast<const uint4*>(p.kv8 + r * kRowBytes + at + 16 * ul));
+            scale[x] = __ldg(p.kv_scale + r * (kD / 32) + sc + (kFmt == SA_KV_FP8_E4M3 ? ul >> 1 : ul));
+        }
+    }
+    // Into a stage whose groups of eight rows are `group` bytes apart and whose blocks of 64 d `block`; the rows in the
+    // stage start at `first`.  (Lanes of a row that hold the same place of different blocks, which are the same
+    // banks, store their 16-byte units in different orders.)
+    __device__ __forceinline__ void store(uint32_t stage, int first, int lanes, int group, int block, int lane) const {
+        const int ul = lane & (lanes - 1), step = 32 / lanes, r0 = first + lane / lanes;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const int r = r0 + step * x;
+            const uint32_t row = stage + (uint32_t)((r >> 3) * group + (r & 7) * 128);
+            if constexpr (kFmt == SA_KV_FP8_E4M3) {
+                uint4 lo, hi;
+                fp8::dequant16(code[x], fp8::e8m0_to_f32(scale[x]), lo, hi);
+                const int u = 2 * ul, turn = (ul >> 2) & 1;
+                const uint32_t at = row + (uint32_t)((u >> 3) * block) + (uint32_t)((((u & 7) | turn) ^ (r & 7)) << 4);
+                const uint4 a = turn ? hi : lo, b = turn ? lo : hi;
+                st_shared_v4(at, a.x, a.y, a.z, a.w);
+                st_shared_v4(at ^ 16u, b.x, b.y, b.z, b.w);
+            } else {
+                const int u = 4 * ul, turn = lanes == 8 ? (ul >> 1) & 3 : ul & 2;
+                const uint32_t at = row + (uint32_t)((u >> 3) * block) + (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+                const float sc = fp4::scale_f32(scale[x]);
+                uint32_t w[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+                if (turn & 1) {
+                    uint32_t v = w[0];
+                    w[0] = w[1];
+                    w[1] = v;
+                    v = w[2];
+                    w[2] = w[3];
+                    w[3] = v;
+                }
+                if (turn & 2) {
+                    uint32_t v = w[0];
+                    w[0] = w[2];
+                    w[2] = v;
+                    v = w[1];
+                    w[1] = w[3];
+                    w[3] = v;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 v = fp4::dequant8(w[k], sc);
+                    st_shared_v4(at ^ (uint32_t)((k ^ turn) << 4), v.x, v.y, v.z, v.w);
+                }
+            }
+        }
+    }
+};
+
+template <int kFmt, bool kRope>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt), 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Params p) {
+    constexpr bool kCodes = codes_of(kFmt);
+    constexpr int kEpilogues = epilogue_groups(kFmt), kWarpV = warp_v(kFmt), kWarpPv = warp_pv(kFmt);
     extern __shared__ __align__(1024) uint8_t smem[];
     Misc& M = *reinterpret_cast<Misc*>(smem + kOffMisc);
     const uint32_t s_k = smem_addr(smem + kOffK), s_v = smem_addr(smem + kOffV), s_q = smem_addr(smem + kOffQ), s_p = smem_addr(smem + kOffP);
@@ -330,11 +442,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kKStages; ++s) {
-            mbar_init(smem_addr(&M.k_full[s]), 1);
+            mbar_init(smem_addr(&M.k_full[s]), kCodes ? 8 : 1);  // (codes: the widening warps of both CTAs)
             mbar_init(smem_addr(&M.k_empty[s]), 1);
         }
         for (int s = 0; s < kVStages; ++s) {
-            mbar_init(smem_addr(&M.v_full[s]), rank == 0 ? 2 : 1);
+            mbar_init(smem_addr(&M.v_full[s]), (kCodes ? 4 : 1) * (rank == 0 ? 2 : 1));
             mbar_init(smem_addr(&M.v_empty[s]), 1);
         }
         for (int i = 0; i < 4; ++i) {
@@ -343,10 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_addr(&M.info_full[i]), 1);
+            mbar_init(smem_addr(&M.info_empty[i]), 12);  // (codes: the widening warps and a softmax group)
         }
         for (int i = 0; i < kTasks; ++i) {
             mbar_init(smem_addr(&M.task_full[i]), 1);
-            mbar_init(smem_addr(&M.task_empty[i]), 21);  // all warps but the one that fills it
+            mbar_init(smem_addr(&M.task_empty[i]), warps_of(kFmt) - 1);  // all but the one that fills it
         }
         for (int b = 0; b < 3; ++b) {
             mbar_init(smem_addr(&M.s_full[b]), 1);
@@ -355,18 +468,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&M.pair_bar[b][0]), 2);
             mbar_init(smem_addr(&M.pair_bar[b][1]), 2);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_addr(&M.sum_full[b][i]), 2);
-                mbar_init(smem_addr(&M.sum_empty[b][i]), 2);
-            }
+            mbar_init(smem_addr(&M.sum_full[b]), 2 * kEpilogues);
+            mbar_init(smem_addr(&M.sum_empty[b]), 2 * kEpilogues);
             mbar_init(smem_addr(&M.p_full[b]), 8);
             mbar_init(smem_addr(&M.p_empty[b]), 1);
         }
         mbar_init(smem_addr(&M.o_full), 1);
-        mbar_init(smem_addr(&M.o_empty), 16);
+        mbar_init(smem_addr(&M.o_empty), 8 * kEpilogues);
         for (int w = 0; w < 4; ++w) mbar_init(smem_addr(&M.m_full[w]), 1);
         mbar_init(smem_addr(&M.stats_full), 8);
-        mbar_init(smem_addr(&M.stats_empty), 8);
+        mbar_init(smem_addr(&M.stats_empty), 4 * kEpilogues);
         mbar_init(smem_addr(&M.done), 2);
         M.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -376,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (warp == 2 && lane == 0) {
+    if (!kCodes && warp == 2 && lane == 0) {
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
     }
@@ -407,16 +518,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 1) {
         // ------------------------------------------------------------------ tasks
-        // In every round of `pairs` units a pair takes the place behind its last: the units that are nothing lie evenly
-        // among the others (every second one where a token is a tile), and would fall to the same pairs.
         const int pairs = gridDim.x >> 1;
-        int place = blockIdx.x >> 1;
-        for (int u0 = 0; ok; u0 += pairs) {
-            const int u = u0 + place;
-            if (++place == pairs) place = 0;
+        Walk walk;
+        for (int u = blockIdx.x >> 1; ok; u += pairs) {
             Task t = {};
-            const bool more = u0 < p.n_units;
-            if (more && (u >= p.n_units || !task_of(p, u, t))) continue;
+            const bool more = task_of(p, u, lane, walk, t);
             t.more = more;
             const uint32_t i = nth % kTasks;
             if (!(ok = wait(M.task_empty[i], (nth / kTasks) ^ 1u, abort))) break;
@@ -425,9 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++nth;
             if (!more) break;
         }
-    } else if (warp == 0 || warp == 21) {
+    } else if (warp == 0 || warp == kWarpPv) {
         // ------------------------------------------------------------------ the pair's products
-        // Warp 0 issues the logits, warp 21 P.V (rank 1: they pass on that K, and V, have landed).  One warp for both
+        // Warp 0 issues the logits, another one P.V (of bf16 rows, rank 1's passes on that its V has landed).  One warp for both
         // spent 600 cycles a stage of 256 cycles of products (a wait for a barrier that has long completed takes
         // 130, a commit 75, and the tensor pipe holds too few products to bridge them); of two, one's products run
         // behind the other's barriers.
@@ -489,6 +595,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 ++c;
             }
+        } else if (kCodes && !leader) {
+            while (fetch(t)) {
+            }
         } else {
             while (fetch(t)) {
                 if (t.nb == 0) continue;
@@ -501,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int nb = min(kTileBlocks, t.nb - kTileBlocks * i);
                     for (int j = 0; j < nb && ok; ++j) {
                         if (!stage_in(M.v_full)) break;
-                        if (!leader) warp_arrive_leader(M.v_full[st], lane);
+                        if (!kCodes && !leader) warp_arrive_leader(M.v_full[st], lane);
                         bool next = false;
                         if (leader) {
                             tc_fence_after();
@@ -531,9 +640,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // released (an abandoned one too)
         if (leader) commit_pair(M.done);
         wait(M.done, 0, abort);
-    } else if (warp == 2 || warp == 20) {
-        // ------------------------------------------------------------------ K (warp 2) and V (warp 20)
-        const bool is_v = warp == 20;
+    } else if (warp == 2 || warp == kWarpV) {
+        // ------------------------------------------------------------------ K (warp 2) and V
+        // (codes: warp 2 describes the tiles, up to eight ahead, and pulls their rows into L2)
+        const bool is_v = warp == kWarpV;
         const uint32_t stages = is_v ? kVStages : kKStages, ring = is_v ? s_v : s_k;
         uint64_t* const full = is_v ? M.v_full : M.k_full;
         uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
@@ -580,10 +690,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
+                if (kCodes && !(ok = wait(M.info_empty[g % kInfos], (g / kInfos) ^ 1u, abort))) break;
                 const bool all = lane < nb && seen(p.window, p.first, base, t.pos0, t.pmax) == 0xffffffffu;
                 const bool whole = __all_sync(0xffffffffu, lane >= kTileBlocks || all);
                 if (lane < kTileBlocks) M.base[g % kInfos][lane] = lane < nb ? base : -2;
                 if (lane == 0) M.whole[g % kInfos] = whole;
+                if constexpr (kCodes) {
+                    constexpr int kBytes = Widen<kFmt>::kRowBytes;
+                    if (lane < kTileBlocks) M.rows[g % kInfos][lane] = row;
+                    if (lane < nb && (lane & 1) == (int)rank) {
+                        prefetch_l2(p.kv8 + (int64_t)row * kBytes, kBlock * kBytes);
+                        prefetch_l2(p.kv_scale + (int64_t)row * (kD / 32), kBlock * (kD / 32));
+                    }
+                    warp_arrive(M.info_full[g % kInfos], lane);
+                    continue;
+                }
                 warp_arrive(M.info_full[g % kInfos], lane);
                 const int own = (nb - (int)rank + 1) / 2;  // this CTA's blocks: rank, rank + 2
                 const int g0 = __shfl_sync(0xffffffffu, row, (int)rank) >> 3,
@@ -597,9 +718,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // after a failed wait, the copies under way land before the CTA exits (K's: rank 0 sees those of both, and
         // rank 1 gives its own the time)
-        if (!ok && lane == 0 && !is_v && rank != 0)
+        if (!kCodes && !ok && lane == 0 && !is_v && rank != 0)
             for (int i = 0; i < 100; ++i) __nanosleep(1000);
-        if (!ok && lane == 0 && (is_v || rank == 0)) {
+        if (!kCodes && !ok && lane == 0 && (is_v || rank == 0)) {
             const uint32_t n = st_use * stages + st;
             for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
                 mbar_drain(smem_addr(&full[k % stages]), (k / stages) & 1);
@@ -623,7 +744,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0 && rank == 0)
             for (uint32_t k = sent > 4 ? sent - 4 : 0; k < sent; ++k) mbar_drain(smem_addr(&M.q_full[k % 4]), (k / 4) & 1);
-    } else if (warp >= 4 && warp < 12) {
+    } else if (kCodes && warp >= kWarpWiden && warp < kWarpWiden + 8) {
+        // ------------------------------------------------------------------ rows of codes: K (four warps) and V (four)
+        if constexpr (kCodes) {
+            constexpr bool k8 = kFmt == SA_KV_FP8_E4M3;
+            const bool is_v = warp >= kWarpWiden + 4;
+            const int w = warp & 3;
+            uint64_t* const full = is_v ? M.v_full : M.k_full;
+            uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
+            const uint32_t ring = is_v ? s_v : s_k;
+            // K: a stage is 64 rows x 128 d, warps 0 and 1 those of block `rank`, 2 and 3 of rank + 2; V: 32 rows x this
+            // CTA's 256 d
+            const int lanes = (is_v ? 16 : 8) / (k8 ? 1 : 2), first = is_v ? 8 * w : 16 * w;
+            const int group = is_v ? 1024 : 2048, block = is_v ? 4096 : 1024;
+            uint32_t st = 0, st_use = 0, g = 0;
+            Task t;
+            while (fetch(t)) {
+                const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks, stages = is_v ? t.nb : 4 * nt;
+                Widen<kFmt> x[2];
+                // stage n's codes (a tile's last stage lets its description go)
+                auto load = [&](int n, Widen<kFmt>& to) {
+                    const uint32_t gi = (g + (n >> 2)) % kInfos;
+                    if ((n & 3) == 0) ok = ok && wait(M.info_full[gi], (g + (n >> 2)) / kInfos, abort);
+                    if (!ok) return;
+                    const int j = is_v ? n & 3 : (int)rank + 2 * (w >> 1);
+                    if ((n & ~3) + j < t.nb || is_v) {
+                        const int64_t row = M.rows[gi][j];
+                        if (is_v) to.load(p, row, first, lanes, Widen<kFmt>::kRowBytes / 2 * (int)rank, 8 * (int)rank, lane);
+                        else to.load(p, row, first & 31, lanes, Widen<kFmt>::kRowBytes / 4 * (n & 3), 4 * (n & 3), lane);
+                    }
+                    if ((n & 3) == 3 || n == stages - 1) warp_arrive(M.info_empty[gi], lane);
+                };
+                if (stages) load(0, x[0]);
+                for (int n = 0; n < stages && ok; n += 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (n + h >= stages || !ok) break;
+                        if (n + h + 1 < stages) load(n + h + 1, x[h ^ 1]);
+                        if (!(ok = ok && wait(empty[st], st_use ^ 1u, abort))) break;
+                        const int j = is_v ? 0 : (int)rank + 2 * (w >> 1);
+                        if (is_v || ((n + h) & ~3) + j < t.nb)
+                            x[h].store(ring + st * kStageBytes, first, lanes, group, block, lane);
+                        fence_proxy_async_smem();
+                        if (is_v && rank != 0) warp_arrive(full[st], lane);
+                        warp_arrive_leader(full[st], lane);
+                        if (++st == (is_v ? kVStages : kKStages)) {
+                            st = 0;
+                            ++st_use;
+                        }
+                    }
+                }
+                g += nt;
+            }
+        }
+    } else if (warp >= 4 && warp < kWarpEpilogue) {
         // ------------------------------------------------------------------ softmax
         // A thread has one row of the CTA's 64 and half of a tile's columns (64: blocks `half` and half + 2); the
         // thread 64 further has the other half, and the two trade their maxima.  Two groups of four warps take the
@@ -706,6 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bad0 = base0 == -2 ? 0u : bad0 & ~seen(p.window, p.first, base0, t.pos0, t.pmax);
                     bad1 = base1 == -2 ? 0u : bad1 & ~seen(p.window, p.first, base1, t.pos0, t.pmax);
                 }
+                if constexpr (kCodes) warp_arrive(M.info_empty[gi], lane);
                 M.mx[b][me] = mt;
                 warp_arrive(M.pair_bar[grp][w & 1], lane);
                 if (!(ok = wait(M.pair_bar[grp][w & 1], g >> 1, abort))) break;
@@ -805,8 +980,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ epilogue
-        // A thread has one row and 128 of its d: of the half that its lane holds, those of its group of four warps.
-        const int w = warp & 3, grp = (warp - 12) >> 2, half = w >> 1, row = 32 * (w & 1) + lane;
+        // A thread has one row and 128 of its d (256, where there is one group of four warps): of the half that its
+        // lane holds, those of its group.
+        constexpr int kSteps = 8 / kEpilogues;  // of 32 d
+        const int w = warp & 3, grp = (warp - kWarpEpilogue) >> 2, half = w >> 1, row = 32 * (w & 1) + lane;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const bool split = p.n_splits > 1;
         uint32_t c = 0, c_o = 0;
@@ -836,12 +1013,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             warp_arrive(M.stats_empty, lane);
             const float top = fmaxf(m0, m1), mu = top == -INFINITY ? 0.f : top;
             const float mine_l = l0 * fast_exp2(m0 - mu) + l1 * fast_exp2(m1 - mu);
-            if (!(ok = wait(M.sum_empty[grp][w & 1], c ^ 1u, abort))) break;  // (the last task's have been read)
-            M.sum[grp][32 * w + lane] = mine_l;
-            warp_arrive(M.sum_full[grp][w & 1], lane);
-            if (!(ok = wait(M.sum_full[grp][w & 1], c, abort))) break;
-            const float l = mine_l + M.sum[grp][(32 * w + lane) ^ 64];
-            warp_arrive(M.sum_empty[grp][w & 1], lane);
+            if (!(ok = wait(M.sum_empty[w & 1], c ^ 1u, abort))) break;  // (the last task's have been read)
+            M.sum[32 * w + lane] = mine_l;  // (the same from either group)
+            warp_arrive(M.sum_full[w & 1], lane);
+            if (!(ok = wait(M.sum_full[w & 1], c, abort))) break;
+            const float l = mine_l + M.sum[(32 * w + lane) ^ 64];
+            warp_arrive(M.sum_empty[w & 1], lane);
             ++c;
             const int64_t flat = (int64_t)t.row0 + r;
             const int64_t part = ((int64_t)(t.tok0 + tok) * p.n_splits + t.split) * p.h + head;
@@ -859,14 +1036,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int at_row = mine ? (split ? (int)part : (int)flat) : -1;
             const int even_row = __shfl_sync(0xffffffffu, at_row, lane & 30), odd_row = __shfl_sync(0xffffffffu, at_row, lane | 1);
 #pragma unroll 1
-            for (int k = 4 * grp; k < 4 * grp + 4; ++k) {  // 32 d at a time
+            for (int k = kSteps * grp; k < kSteps * grp + kSteps; ++k) {  // 32 d at a time
                 const int d0 = 256 * half + 32 * k;
                 uint32_t o[32];
                 __syncwarp();
                 if (t.nb) {
                     tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * k, o);
                     tmem_wait_ld();
-                    if (k == 4 * grp + 3) {
+                    if (k == kSteps * grp + kSteps - 1) {
                         tc_fence_before();
                         warp_arrive_leader(M.o_empty, lane);
                     }
@@ -944,7 +1121,8 @@ int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, in
 }  // namespace
 
 bool window_tc_supports(int d, int kv_format, int page) {
-    return d == kD && kv_format == SA_KV_BF16 && page % kBlock == 0;
+    (void)kv_format;
+    return d == kD && page % kBlock == 0;
 }
 
 size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int64_t first) {
@@ -959,11 +1137,16 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     // two boxes, are 2 KB a step of eight in either block).
     CUtensorMap q_map, k_map, v_map;
     const int64_t rows = c.a.n_pages * c.a.page;
-    if (!encode_blocks_map(q_map, c.q, kD, c.n * c.h, 64, 2) || !encode_blocks_map(v_map, c.kv, kD, rows, kBlock, 4) ||
-        !encode_groups_map(k_map, c.kv, kD, rows, kBlock, 2))
+    const bool codes = c.kv_format != SA_KV_BF16;
+    if (!encode_blocks_map(q_map, c.q, kD, c.n * c.h, 64, 2)) return cudaErrorInvalidValue;
+    if (codes) {
+        k_map = v_map = q_map;  // (not looked at)
+    } else if (!encode_blocks_map(v_map, c.kv, kD, rows, kBlock, 4) || !encode_groups_map(k_map, c.kv, kD, rows, kBlock, 2))
         return cudaErrorInvalidValue;
     Params p = {};
     p.a = c.a;
+    p.kv8 = codes ? reinterpret_cast<const uint8_t*>(c.kv) : nullptr;
+    p.kv_scale = c.kv_scale;
     p.sink = c.sink;
     p.o = reinterpret_cast<__nv_bfloat16*>(c.o);
     p.lse = c.lse;
@@ -978,28 +1161,34 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     p.first = (int)c.first;
     p.n_splits = window_splits(c.n, c.a.b, c.h, c.window, c.first, sms);
     const int64_t units = (c.n * c.h / kM + c.a.b) * p.n_splits;
-    if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;
-    p.n_units = (int)units;
+    if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;  // (the kernel counts units in 32 bits)
     if (p.n_splits > 1) {
         p.part_ml = reinterpret_cast<float*>(c.scratch);
         p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(c.scratch) +
                                             align_up((size_t)c.n * p.n_splits * c.h * 2 * sizeof(float), 256));
     }
-    auto kernel = c.rope ? window_tc_kernel<true> : window_tc_kernel<false>;
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params);
+    static const Kernel kernels[3][2] = {
+        {window_tc_kernel<SA_KV_BF16, false>, window_tc_kernel<SA_KV_BF16, true>},
+        {window_tc_kernel<SA_KV_FP8_E4M3, false>, window_tc_kernel<SA_KV_FP8_E4M3, true>},
+        {window_tc_kernel<SA_KV_FP4_E2M1, false>, window_tc_kernel<SA_KV_FP4_E2M1, true>}};
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !configured[dev]) {
-        for (auto fn : {window_tc_kernel<true>, window_tc_kernel<false>}) {
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-            if (e != cudaSuccess) return e;
-        }
+        for (auto& by_rope : kernels)
+            for (auto fn : by_rope) {
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+                if (e != cudaSuccess) return e;
+            }
         if (dev < 64) configured[dev] = true;
     }
+    const Kernel kernel = kernels[c.kv_format][c.rope ? 1 : 0];
+    const int threads = 32 * (codes ? warps_of(SA_KV_FP8_E4M3) : warps_of(SA_KV_BF16));
     int64_t pairs = sms / 2;
     if (pairs > units) pairs = units;
-    e = launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, c.stream, q_map, k_map, v_map, p);
+    e = launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(threads), kSmem, c.stream, q_map, k_map, v_map, p);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     return attn_combine_launch(p.part_ml, p.part_o, c.sink, c.o, c.lse, c.n, c.h, kD, p.n_splits,
                                c.a.q_start + c.a.b, c.stream);
