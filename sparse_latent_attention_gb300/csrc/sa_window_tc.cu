@@ -153,7 +153,8 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
 // A wait by a converged warp, with a warp-uniform result.  The hardware suspends the warp until the phase completes or
 // a millisecond has passed (a poll that returns at once takes issue slots from the warps that work); bounded to
 // some two seconds, and left as soon as another role has given up.  (Out of line: see the note on code below.)
-static __device__ __noinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
     for (int i = 0; i < 2000; ++i) {
         uint32_t ok;
         asm volatile(
@@ -162,10 +163,13 @@ static __device__ __noinline__ bool wait_for(uint32_t bar, uint32_t parity, vola
             : "r"(bar), "r"(parity & 1), "r"(1000000u)
             : "memory");
         if (__all_sync(0xffffffffu, ok != 0)) return true;
-        if (*abort) return false;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
     }
     *abort = 1;
     return false;
+}
+static __device__ __noinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return wait_here(bar, parity, abort);
 }
 __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, wait_for(smem_addr(&bar), parity, abort));
@@ -781,7 +785,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                     for (int h = 0; h < 2; ++h) {
                         if (n + h >= stages || !ok) break;
                         if (n + h + 1 < stages) load(n + h + 1, x[h ^ 1]);
-                        if (!(ok = ok && wait(empty[st], st_use ^ 1u, abort))) break;
+                        // (in line: a call would wait for the loads under way)
+                        if (!(ok = ok && wait_here(smem_addr(&empty[st]), st_use ^ 1u, abort))) break;
                         const int j = is_v ? 0 : (int)rank + 2 * (w >> 1);
                         if (is_v || ((n + h) & ~3) + j < t.nb)
                             x[h].store(ring + st * kStageBytes, first, lanes, group, block, lane);
