@@ -11,7 +11,7 @@
  * position kv_len[i] - n_i + t.  A negative position (kv_len[i] < n_i) is no position: nothing is written for
  * it, and it attends to nothing.
  *
- * The cache is a pool of n_pages pages of `page` rows that the sequences share.  Position p of sequence i is
+ * The cache is a pool of n_pages (at least 1, where there are tokens) pages of `page` rows that the sequences share.  Position p of sequence i is
  * row p mod page of page page_table[i][p / page] (int32 [b][max_pages], rows table_stride entries apart).
  * Entries of positions that a call neither writes nor attends to are not looked at (pages that a window has
  * left behind may be given back, and their entries hold anything).  An entry outside [0, n_pages), or a

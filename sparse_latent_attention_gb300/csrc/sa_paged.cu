@@ -296,12 +296,13 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
     if (weight && !(eps >= 0.f)) return SA_ERR_INVALID_ARG;
     if (d > 1024 || n >= (int64_t(1) << 31) || n_pages * (int64_t)page >= (int64_t(1) << 40)) return SA_ERR_UNSUPPORTED;
     if (n == 0 || b == 0) return SA_OK;
+    if (n_pages < 1) return SA_ERR_INVALID_ARG;
     if (!x || !aligned(x, 2) || x_stride < d) return SA_ERR_INVALID_ARG;
     if (!q_start || !aligned(q_start, 4) || !kv_len || !aligned(kv_len, 4)) return SA_ERR_INVALID_ARG;
     if ((max_pages > 0 && !page_table) || !aligned(page_table, 4) || (b > 1 && table_stride < max_pages))
         return SA_ERR_INVALID_ARG;
     if (!aligned(weight, 4) || !aligned(rot, 8) || !aligned(status, 4)) return SA_ERR_INVALID_ARG;
-    const int64_t cw = quant == SA_KV_FP4_E2M1 ? d / 2 : d, sw = d / 32, r1 = page - 1, g1 = n_pages > 0 ? n_pages - 1 : 0;
+    const int64_t cw = quant == SA_KV_FP4_E2M1 ? d / 2 : d, sw = d / 32, r1 = page - 1, g1 = n_pages - 1;
     const int64_t p1 = r1 * pages_stride + d, c1 = r1 * codes_stride + cw, s1 = r1 * scales_stride + sw;  // a page's
     if (pages && (!aligned(pages, 2) || pages_stride < d || (n_pages > 1 && pages_page_stride < p1)))
         return SA_ERR_INVALID_ARG;
@@ -312,9 +313,9 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
         const void* at;
         int64_t bytes;
         bool written;
-    } t[] = {{n_pages ? pages : nullptr, 2 * (g1 * pages_page_stride + p1), true},
-             {n_pages ? codes : nullptr, g1 * codes_page_stride + c1, true},
-             {n_pages ? scales : nullptr, g1 * scales_page_stride + s1, true},
+    } t[] = {{pages, 2 * (g1 * pages_page_stride + p1), true},
+             {codes, g1 * codes_page_stride + c1, true},
+             {scales, g1 * scales_page_stride + s1, true},
              {status, 4, true},
              {x, 2 * ((n - 1) * x_stride + d), false},
              {weight, 4 * (int64_t)d, false},
@@ -325,9 +326,9 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
     for (int i = 0; i < 4; ++i)
         for (int j = i + 1; j < 10; ++j)
             if (j >= 3 && overlap(t[i].at, t[i].bytes, t[j].at, t[j].bytes)) return SA_ERR_INVALID_ARG;
-    const Pool pools[] = {{n_pages ? pages : nullptr, 2 * (int64_t)d, 2 * pages_stride, 2 * pages_page_stride},
-                          {n_pages ? codes : nullptr, cw, codes_stride, codes_page_stride},
-                          {n_pages ? scales : nullptr, sw, scales_stride, scales_page_stride}};
+    const Pool pools[] = {{pages, 2 * (int64_t)d, 2 * pages_stride, 2 * pages_page_stride},
+                          {codes, cw, codes_stride, codes_page_stride},
+                          {scales, sw, scales_stride, scales_page_stride}};
     if (pools_overlap(pools[0], pools[1], n_pages, page) || pools_overlap(pools[0], pools[2], n_pages, page) ||
         pools_overlap(pools[1], pools[2], n_pages, page))
         return SA_ERR_INVALID_ARG;
@@ -390,7 +391,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (n == 0 || b == 0) return SA_OK;
     const bool codes = kv_format != SA_KV_BF16;
     if (!q || !sink || !o || !q_start || !kv_len || (max_pages > 0 && !page_table)) return SA_ERR_INVALID_ARG;
-    if (n_pages > 0 && (!kv || (codes && !kv_scale))) return SA_ERR_INVALID_ARG;
+    if (n_pages < 1 || !kv || (codes && !kv_scale)) return SA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) || !aligned(lse, 4) ||
         !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
         !aligned(kv_scale, tc ? 16 : 4) || (b > 1 && table_stride < max_pages))

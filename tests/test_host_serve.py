@@ -57,7 +57,7 @@ def test_add_rms_norm_refuses(lib, change, code):
     (dict(n=0, x=None), OK), (dict(b=0, q_start=None), OK), (dict(n=-1), INVALID), (dict(d=40), INVALID),
     (dict(d=0), INVALID), (dict(d=1056, xs=1056, pgs=1056, pgp=1 << 20, cs=1056, ss=40), UNSUPPORTED),
     (dict(n=1 << 31), UNSUPPORTED), (dict(n_pages=1 << 38), UNSUPPORTED), (dict(b=-1), INVALID),
-    (dict(n_pages=-1), INVALID), (dict(page=0), INVALID), (dict(max_pages=-1), INVALID), (dict(quant=3), INVALID),
+    (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID), (dict(page=0), INVALID), (dict(max_pages=-1), INVALID), (dict(quant=3), INVALID),
     (dict(quant=0), INVALID), (dict(codes=None, scales=None, pages=None), INVALID), (dict(scales=None), INVALID),
     (dict(x=None), INVALID), (dict(x=at(1, 1)), INVALID), (dict(xs=63), INVALID), (dict(q_start=None), INVALID),
     (dict(kv_len=None), INVALID), (dict(table=None), INVALID), (dict(table=at(2, 2)), INVALID),
@@ -97,7 +97,7 @@ def test_page_write_takes_rows_between_one_another(lib):
     (dict(scale_ptr=at(9)), INVALID), (dict(fmt=1, scale_ptr=at(9, 4)), INVALID), (dict(fmt=1, scale_ptr=at(9)), WORKSPACE),
     (dict(n=-1), INVALID), (dict(h=0), INVALID), (dict(h=129), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
     (dict(d=576), UNSUPPORTED), (dict(window=0), INVALID), (dict(window=1 << 30), INVALID), (dict(first=-1), INVALID),
-    (dict(first=(1 << 30) - 128), INVALID), (dict(page=0), INVALID), (dict(n_pages=-1), INVALID),
+    (dict(first=(1 << 30) - 128), INVALID), (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID),
     (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED), (dict(max_pages=-1), INVALID),
     (dict(ts=3), INVALID), (dict(q=None), INVALID), (dict(q=at(1, 8)), INVALID), (dict(kv=None), INVALID),
     (dict(kv=at(2, 8)), INVALID), (dict(sink=None), INVALID), (dict(sink=at(3, 2)), INVALID), (dict(o=None), INVALID),
@@ -109,7 +109,7 @@ def test_page_write_takes_rows_between_one_another(lib):
     (dict(lse=at(1, 64)), INVALID), (dict(lse=at(2, 64)), INVALID), (dict(rot=at(10), lse=at(10)), INVALID),
     (dict(ws=at(11), ws_bytes=255), WORKSPACE), (dict(ws=at(11, 64), ws_bytes=1 << 30), INVALID),
     (dict(ws=at(7), ws_bytes=1 << 30), INVALID), (dict(ws=at(2), ws_bytes=1 << 30), INVALID),
-    (dict(lse=at(11, 1024), ws=at(11), ws_bytes=1 << 30), INVALID),
+    (dict(lse=at(11, 128), ws=at(11), ws_bytes=1 << 30), INVALID),
 ])
 def test_window_attn_refuses(lib, change, code):
     a = dict(q=at(1), kv=at(2), scale_ptr=None, fmt=0, sink=at(3), table=at(4), max_pages=4, ts=4, q_start=at(5),
