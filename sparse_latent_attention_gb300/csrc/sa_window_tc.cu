@@ -57,10 +57,11 @@ constexpr int kInfos = 8, kTasks = 4;  // tiles and tasks described ahead
 constexpr bool codes_of(int fmt) { return fmt != SA_KV_BF16; }
 constexpr int epilogue_groups(int fmt) { return codes_of(fmt) ? 1 : 2; }
 constexpr int kWarpEpilogue = 12;
-constexpr int kWarpWiden = 16;                                            // codes: four warps of K, four of V
+constexpr int kWarpWiden = 16;                                            // codes: eight warps of K, eight of V
 constexpr int warp_v(int fmt) { return codes_of(fmt) ? -1 : 20; }         // bf16: V's loads
-constexpr int warp_pv(int fmt) { return codes_of(fmt) ? 24 : 21; }
-constexpr int warps_of(int fmt) { return warp_pv(fmt) + 1; }
+constexpr int warp_q(int fmt) { return codes_of(fmt) ? 1 : 3; }           // (codes: the tasks' warp loads Q too)
+constexpr int warp_pv(int fmt) { return codes_of(fmt) ? 3 : 21; }
+constexpr int warps_of(int fmt) { return codes_of(fmt) ? 32 : 22; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // TMEM columns: O, three S buffers, a row's running maximum after the last two tiles, and the softmax groups' final
@@ -359,8 +360,16 @@ __device__ __forceinline__ bool task_of(const Params& p, int u, int lane, Walk& 
     return true;
 }
 
-// Rows of codes widened into the stages: a warp's share of a stage is `kLoads` pieces of 16 bytes a lane, which wait in
-// registers while the stage before is written.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Rows of codes widened into the stages, in place: a warp copies its share of a stage's codes, `kLoads` pieces of 16 bytes
+// a lane, and their scales into the part of the stage that its bf16 rows will fill, ahead of the one that it reads back
+// and writes widened.  (Through registers, a warp waited for its loads, and every scoreboard that they share.)
 template <int kFmt>
 struct Widen {
     static constexpr int kLoads = kFmt == SA_KV_FP8_E4M3 ? 4 : 2;
@@ -368,14 +377,24 @@ struct Widen {
     uint4 code[kLoads];
     uint32_t scale[kLoads];
 
-    // Rows row + first + (32 / lanes) x + lane / lanes, each from byte `at` of its codes and scale `sc` on.
-    __device__ __forceinline__ void load(const Params& p, int64_t row, int first, int lanes, int at, int sc, int lane) {
-        const int ul = lane & (lanes - 1), step = 32 / lanes, r0 = first + lane / lanes;
+    // `own` is the warp's part of the stage, which goes on every `hop` bytes; a lane's codes start at `src`, the pieces
+    // `step` rows apart, and a word of scales for every one of 16 lanes at `sc`.
+    static __device__ __forceinline__ void copy(uint32_t own, int hop, const uint8_t* src, int step, const uint8_t* sc,
+                                                int lane) {
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x)
+            copy16(own + (x >> 1) * hop + (x & 1) * 512 + 16 * lane, src + x * step * kRowBytes);
+        if (lane < 16) copy4(own + 2 * hop + 4 * lane, sc);
+    }
+    // Back: a lane's own pieces, and its rows' scales (`at`, and `by` bytes from piece to piece).
+    __device__ __forceinline__ void read(uint32_t own, int hop, int at, int by, int lane) {
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
-            const int64_t r = row + r0 + step * x;
-            code[x] = __ldg(reinterpret_cast<const uint4*>(p.kv8 + r * kRowBytes + at + 16 * ul));
-            scale[x] = __ldg(p.kv_scale + r * (kD / 32) + sc + (kFmt == SA_KV_FP8_E4M3 ? ul >> 1 : ul));
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(code[x].x), "=r"(code[x].y), "=r"(code[x].z), "=r"(code[x].w)
+                         : "r"(own + (x >> 1) * hop + (x & 1) * 512 + 16 * lane)
+                         : "memory");
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(scale[x]) : "r"(own + 2 * hop + at + x * by) : "memory");
         }
     }
     // Into a stage whose groups of eight rows are `group` bytes apart and whose blocks of 64 d `block`; the rows in the
@@ -459,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_addr(&M.info_full[i]), 1);
-            mbar_init(smem_addr(&M.info_empty[i]), 12);  // (codes: the widening warps and a softmax group)
+            mbar_init(smem_addr(&M.info_empty[i]), 20);  // (codes: the widening warps and a softmax group)
         }
         for (int i = 0; i < kTasks; ++i) {
             mbar_init(smem_addr(&M.task_full[i]), 1);
@@ -495,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
     }
-    if (warp == 3 && lane == 0) tma_prefetch_desc(&q_map);
+    if (warp == warp_q(kFmt) && lane == 0) tma_prefetch_desc(&q_map);
     tc_fence_before();
     __syncthreads();
     cluster_barrier();  // the other CTA's barriers and TMEM are there
@@ -520,6 +539,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         return __shfl_sync(0xffffffffu, t.more, 0) != 0;
     };
 
+    uint32_t q_tasks = 0, q_sent = 0;
+    auto load_q = [&](int row0) {
+        for (int q = 0; q < 4 && ok; ++q) {
+            if (!(ok = wait(M.q_empty[q], q_tasks ^ 1u, abort))) break;
+            if (lane == 0) {
+                const uint32_t bar = smem_addr(&M.q_full[q]);
+                if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 16384);
+                tma_load_3d_pair(s_q + q * 16384, &q_map, 0, row0 + 64 * (int)rank, 2 * q, at_leader(bar));
+            }
+            ++q_sent;
+        }
+        ++q_tasks;
+    };
+    auto drain_q = [&] {
+        if (!ok && lane == 0 && rank == 0)
+            for (uint32_t k = q_sent > 4 ? q_sent - 4 : 0; k < q_sent; ++k)
+                mbar_drain(smem_addr(&M.q_full[k % 4]), (k / 4) & 1);
+    };
+
     if (warp == 1) {
         // ------------------------------------------------------------------ tasks
         const int pairs = gridDim.x >> 1;
@@ -534,7 +572,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
             warp_arrive(M.task_full[i], lane);
             ++nth;
             if (!more) break;
+            if (kCodes && t.nb) load_q(t.row0);
         }
+        if (kCodes) drain_q();
     } else if (warp == 0 || warp == kWarpPv) {
         // ------------------------------------------------------------------ the pair's products
         // Warp 0 issues the logits, another one P.V (of bf16 rows, rank 1's passes on that its V has landed).  One warp for both
@@ -729,31 +769,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
             for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
                 mbar_drain(smem_addr(&full[k % stages]), (k / stages) & 1);
         }
-    } else if (warp == 3) {
+    } else if (!kCodes && warp == warp_q(kFmt)) {
         // ------------------------------------------------------------------ Q
-        uint32_t c = 0, sent = 0;
         Task t;
-        while (fetch(t)) {
-            if (t.nb == 0) continue;
-            for (int q = 0; q < 4 && ok; ++q) {
-                if (!(ok = wait(M.q_empty[q], c ^ 1u, abort))) break;
-                if (lane == 0) {
-                    const uint32_t bar = smem_addr(&M.q_full[q]);
-                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 16384);
-                    tma_load_3d_pair(s_q + q * 16384, &q_map, 0, t.row0 + 64 * (int)rank, 2 * q, at_leader(bar));
-                }
-                ++sent;
-            }
-            ++c;
-        }
-        if (!ok && lane == 0 && rank == 0)
-            for (uint32_t k = sent > 4 ? sent - 4 : 0; k < sent; ++k) mbar_drain(smem_addr(&M.q_full[k % 4]), (k / 4) & 1);
-    } else if (kCodes && warp >= kWarpWiden && warp < kWarpWiden + 8) {
-        // ------------------------------------------------------------------ rows of codes: K (four warps) and V (four)
+        while (fetch(t))
+            if (t.nb) load_q(t.row0);
+        drain_q();
+    } else if (kCodes && warp >= kWarpWiden && warp < kWarpWiden + 16) {
+        // ------------------------------------------------------------------ rows of codes: K (eight warps) and V (eight)
+        // Four warps of either take the even stages of a task, four the odd.
         if constexpr (kCodes) {
             constexpr bool k8 = kFmt == SA_KV_FP8_E4M3;
-            const bool is_v = warp >= kWarpWiden + 4;
-            const int w = warp & 3;
+            const bool is_v = warp >= kWarpWiden + 8;
+            const int w = warp & 3, turn = (warp >> 2) & 1;
             uint64_t* const full = is_v ? M.v_full : M.k_full;
             uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
             const uint32_t ring = is_v ? s_v : s_k;
@@ -761,46 +789,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
             // CTA's 256 d
             const int lanes = (is_v ? 16 : 8) / (k8 ? 1 : 2), first = is_v ? 8 * w : 16 * w;
             const int group = is_v ? 1024 : 2048, block = is_v ? 4096 : 1024;
-            uint32_t st = 0, st_use = 0, g = 0;
+            // (the warp's part of a stage, and a lane's place in its rows' codes and scales: see Widen)
+            using W = Widen<kFmt>;
+            constexpr uint32_t kRing = 4;
+            static_assert(kKStages == kRing && kVStages == kRing, "one ring's arithmetic for both");
+            const uint32_t own = ring + (is_v ? 1024 : 4096) * w;
+            const int hop = is_v ? 4096 : 1024, ul = lane & (lanes - 1), rl = lane / lanes, step = 32 / lanes;
+            const uint8_t* const src = p.kv8 + ((first & 31) + rl) * W::kRowBytes + 16 * ul +
+                                       (is_v ? W::kRowBytes / 2 * (int)rank : 0);
+            const uint8_t* const sc = p.kv_scale + (is_v ? (first + (lane >> 1)) * (kD / 32) + 8 * (int)rank + 4 * (lane & 1)
+                                                         : ((first & 31) + lane) * (kD / 32));
+            const int sc_by = (is_v ? 8 : 4) * step, sc_at = (is_v ? 8 : 4) * rl + (k8 ? ul >> 1 : ul);
+            uint32_t seq = 0, g = 0;  // stages before the task's, tiles before them
             Task t;
             while (fetch(t)) {
                 const int nt = (t.nb + kTileBlocks - 1) / kTileBlocks, stages = is_v ? t.nb : 4 * nt;
-                Widen<kFmt> x[2];
-                // stage n's codes (a tile's last stage lets its description go)
-                auto load = [&](int n, Widen<kFmt>& to) {
-                    const uint32_t gi = (g + (n >> 2)) % kInfos;
-                    if ((n & 3) == 0) ok = ok && wait(M.info_full[gi], (g + (n >> 2)) / kInfos, abort);
-                    if (!ok) return;
-                    const int j = is_v ? n & 3 : (int)rank + 2 * (w >> 1);
-                    if ((n & ~3) + j < t.nb || is_v) {
-                        const int64_t row = M.rows[gi][j];
-                        if (is_v) to.load(p, row, first, lanes, Widen<kFmt>::kRowBytes / 2 * (int)rank, 8 * (int)rank, lane);
-                        else to.load(p, row, first & 31, lanes, Widen<kFmt>::kRowBytes / 4 * (n & 3), 4 * (n & 3), lane);
-                    }
-                    if ((n & 3) == 3 || n == stages - 1) warp_arrive(M.info_empty[gi], lane);
-                };
-                if (stages) load(0, x[0]);
-                for (int n = 0; n < stages && ok; n += 2) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (n + h >= stages || !ok) break;
-                        if (n + h + 1 < stages) load(n + h + 1, x[h ^ 1]);
-                        // (in line: a call would wait for the loads under way)
-                        if (!(ok = ok && wait_here(smem_addr(&empty[st]), st_use ^ 1u, abort))) break;
-                        const int j = is_v ? 0 : (int)rank + 2 * (w >> 1);
-                        if (is_v || ((n + h) & ~3) + j < t.nb)
-                            x[h].store(ring + st * kStageBytes, first, lanes, group, block, lane);
-                        fence_proxy_async_smem();
-                        if (is_v && rank != 0) warp_arrive(full[st], lane);
-                        warp_arrive_leader(full[st], lane);
-                        if (++st == (is_v ? kVStages : kKStages)) {
-                            st = 0;
-                            ++st_use;
+                const int j_k = (int)rank + 2 * (w >> 1);
+                // Stage `put`'s copies go out before `n`, the last but one, is widened, but with a stage to be widened
+                // they do not wait for their place: the product that frees it may need that stage (where rows of V
+                // are cleared, all of a tile's before its first is used).
+                int put = turn;
+#pragma unroll 1
+                for (int n = turn; n < stages; n += 2) {
+                    while (put < stages && put <= n + 2) {
+                        const uint32_t gi = (g + (put >> 2)) % kInfos, m = seq + put, e = smem_addr(&empty[m % kRing]);
+                        if (put > n && !__all_sync(0xffffffffu, mbar_test_wait(e, ((m / kRing) ^ 1u) & 1u))) break;
+                        if ((put & 2) == 0) ok = ok && wait_here(smem_addr(&M.info_full[gi]), (g + (put >> 2)) / kInfos, abort);
+                        ok = ok && wait_here(e, (m / kRing) ^ 1u, abort);
+                        if (!ok) break;
+                        if (is_v || (put & ~3) + j_k < t.nb) {
+                            const int64_t row = M.rows[gi][is_v ? put & 3 : j_k];
+                            W::copy(own + (m % kRing) * kStageBytes, hop,
+                                    src + row * W::kRowBytes + (is_v ? 0 : W::kRowBytes / 4 * (put & 3)), step,
+                                    sc + row * (kD / 32) + (is_v ? 0 : 4 * (put & 3)), lane);
                         }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        // (the last of a tile's stages of this warp lets its description go)
+                        if ((put & 2) || put + 2 >= stages) warp_arrive(M.info_empty[gi], lane);
+                        put += 2;
                     }
+                    if (!ok) break;
+                    const uint32_t st = (seq + n) % kRing;
+                    if (put > n + 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();
+                    if (is_v || (n & ~3) + j_k < t.nb) {
+                        W x;
+                        x.read(own + st * kStageBytes, hop, sc_at, sc_by, lane);
+                        __syncwarp();
+                        x.store(ring + st * kStageBytes, first, lanes, group, block, lane);
+                    }
+                    fence_proxy_async_smem();
+                    if (is_v && rank != 0) warp_arrive(full[st], lane);
+                    warp_arrive_leader(full[st], lane);
                 }
+                if (is_v && turn && (stages & 3) == 1 && ok) {  // (a last tile of one block has no odd stage)
+                    const uint32_t last = g + nt - 1, gi = last % kInfos;
+                    ok = wait_here(smem_addr(&M.info_full[gi]), last / kInfos, abort);
+                    warp_arrive(M.info_empty[gi], lane);
+                }
+                seq += stages;
                 g += nt;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp >= 4 && warp < kWarpEpilogue) {
         // ------------------------------------------------------------------ softmax
