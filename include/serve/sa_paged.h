@@ -11,8 +11,9 @@
  * position kv_len[i] - n_i + t.  A negative position (kv_len[i] < n_i) is no position: nothing is written for
  * it, and it attends to nothing.
  *
- * The cache is a pool of n_pages (at least 1, where there are tokens) pages of `page` rows that the sequences share.  Position p of sequence i is
- * row p mod page of page page_table[i][p / page] (int32 [b][max_pages], rows table_stride entries apart).
+ * The cache is a pool of n_pages pages of `page` rows that the sequences share (one page at least, where there
+ * are tokens).  Position p of sequence i is row p mod page of page page_table[i][p / page] (int32
+ * [b][max_pages], rows table_stride entries apart).
  * Entries of positions that a call neither writes nor attends to are not looked at (pages that a window has
  * left behind may be given back, and their entries hold anything).  An entry outside [0, n_pages), or a
  * position past the table's last page, that a call does meet sets SA_ERR_INDEX in its status word; the row is
@@ -91,7 +92,9 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  *   kv, kv_scale, kv_format   the pool [n_pages][page][.] in one of the formats of sa_sparse_attn, dense;
  *              kv_scale aligned to 16 bytes at d = 512, else to 4
  *   window     >= 1, first >= 0 (first + window < 2^30)
- *   o          bf16 [n][h][d], written; lse  f32 [n][h] or NULL: the log of each softmax's denominator
+ *   o          bf16 [n][h][d], written; aligned to 32 bytes at d = 512 with pages of a multiple of 32 rows, else
+ *              to 16
+ *   lse        f32 [n][h] or NULL: the log of each softmax's denominator
  *   rot        f32 [npos][rope_dim / 2][2], or NULL; d = 512 only (else SA_ERR_UNSUPPORTED)
  *   workspace  at least sa_window_attn_workspace_size(...) bytes, aligned to 256, as sa_sparse_attn's: its
  *              first SA_STATUS_BYTES zeroed once by the caller, calls sharing one stream-ordered

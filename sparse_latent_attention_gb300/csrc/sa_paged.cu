@@ -394,7 +394,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (n_pages < 1 || !kv || (codes && !kv_scale)) return SA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) || !aligned(lse, 4) ||
         !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
-        !aligned(kv_scale, tc ? 16 : 4) || (b > 1 && table_stride < max_pages))
+        !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) || (b > 1 && table_stride < max_pages))
         return SA_ERR_INVALID_ARG;
     const Parts parts = parts_of(n, b, h, d, window, first, page, kv_format);
     const int64_t ob = 2 * n * h * d, rows = n_pages * page;

@@ -101,7 +101,9 @@ def test_page_write_takes_rows_between_one_another(lib):
     (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED), (dict(max_pages=-1), INVALID),
     (dict(ts=3), INVALID), (dict(q=None), INVALID), (dict(q=at(1, 8)), INVALID), (dict(kv=None), INVALID),
     (dict(kv=at(2, 8)), INVALID), (dict(sink=None), INVALID), (dict(sink=at(3, 2)), INVALID), (dict(o=None), INVALID),
-    (dict(o=at(7, 8)), INVALID), (dict(table=None), INVALID), (dict(q_start=None), INVALID), (dict(kv_len=None), INVALID),
+    (dict(o=at(7, 8)), INVALID), (dict(o=at(7, 16)), INVALID), (dict(o=at(7, 32)), WORKSPACE),
+    (dict(o=at(7, 16), page=48), WORKSPACE), (dict(o=at(7, 16), d=256), WORKSPACE), (dict(o=at(7, 8), d=256), INVALID),
+    (dict(table=None), INVALID), (dict(q_start=None), INVALID), (dict(kv_len=None), INVALID),
     (dict(q_start=at(5, 2)), INVALID), (dict(lse=at(8, 2)), INVALID), (dict(rot=at(10)), WORKSPACE),
     (dict(rot=at(10, 4)), INVALID), (dict(rot=at(10), rope=63), INVALID), (dict(rot=at(10), npos=0), INVALID),
     (dict(rot=at(10), d=256), UNSUPPORTED), (dict(o=at(1)), INVALID), (dict(o=at(2, 64)), INVALID), (dict(o=at(4)), INVALID),
