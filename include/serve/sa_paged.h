@@ -63,7 +63,8 @@ extern "C" {
  *              (their rows are not written).
  * Rows of one call have to be distinct: two tokens at one row write it in any order.
  * Requires d % 32 == 0, 32 <= d <= 1024 (else SA_ERR_UNSUPPORTED), strides at least the row's length, page
- * strides that keep pages apart, rope_dim even, 2 <= rope_dim <= d, page >= 1, n < 2^31.  No output may overlap
+ * strides that keep pages apart, rope_dim even, 2 <= rope_dim <= d, page >= 1; n, b, n_pages and
+ * max_pages < 2^31.  No output may overlap
  * another, x, weight, rot, q_start, kv_len or page_table.
  */
 sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const int32_t* page_table,
@@ -99,7 +100,7 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  *   workspace  at least sa_window_attn_workspace_size(...) bytes, aligned to 256, as sa_sparse_attn's: its
  *              first SA_STATUS_BYTES zeroed once by the caller, calls sharing one stream-ordered
  * o and lse must not overlap an input, the workspace or each other.
- * Supported: d a multiple of 64 in [64, 512]; 1 <= h <= 128; n * h < 2^31; n_pages * page < 2^31.
+ * Supported: d a multiple of 64 in [64, 512]; 1 <= h <= 128; n * h, b, max_pages and n_pages * page < 2^31.
  */
 size_t sa_window_attn_workspace_size(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page,
                                      int kv_format);

@@ -247,13 +247,18 @@ bool pools_overlap(const Pool& a, const Pool& b, int64_t n_pages, int64_t rows) 
              apart(a.at, a.width, b.at, b.width, a.row));
 }
 
+constexpr int64_t k31 = int64_t(1) << 31;
+
+// What count * stride elements span has to be an address's distance.
+bool spans(int64_t count, int64_t stride) { return (double)count * (double)stride < 72057594037927936.0; }
+
 bool window_shape(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page) {
     return n >= 0 && b >= 0 && h >= 1 && d >= 1 && window >= 1 && first >= 0 && page >= 1 &&
            window < (int64_t(1) << 30) && first < (int64_t(1) << 30) && first + window < (int64_t(1) << 30);
 }
 
 bool window_supported(int64_t n, int h, int d) {
-    return h <= 128 && d >= 64 && d <= 512 && d % 64 == 0 && n * (int64_t)h < (int64_t(1) << 31);
+    return h <= 128 && d >= 64 && d <= 512 && d % 64 == 0 && n < k31 && n * (int64_t)h < k31;
 }
 
 // The workspace: the status word and the scratch of the kernels that the call is routed to, then, of those that
@@ -294,7 +299,9 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
     if (codes && quant == SA_KV_BF16) return SA_ERR_INVALID_ARG;
     if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 0)) return SA_ERR_INVALID_ARG;
     if (weight && !(eps >= 0.f)) return SA_ERR_INVALID_ARG;
-    if (d > 1024 || n >= (int64_t(1) << 31) || n_pages * (int64_t)page >= (int64_t(1) << 40)) return SA_ERR_UNSUPPORTED;
+    if (d > 1024 || n >= k31 || n_pages >= k31 || n_pages * (int64_t)page >= (int64_t(1) << 40) || max_pages >= k31 ||
+        b >= k31)
+        return SA_ERR_UNSUPPORTED;
     if (n == 0 || b == 0) return SA_OK;
     if (n_pages < 1) return SA_ERR_INVALID_ARG;
     if (!x || !aligned(x, 2) || x_stride < d) return SA_ERR_INVALID_ARG;
@@ -302,6 +309,11 @@ extern "C" sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_st
     if ((max_pages > 0 && !page_table) || !aligned(page_table, 4) || (b > 1 && table_stride < max_pages))
         return SA_ERR_INVALID_ARG;
     if (!aligned(weight, 4) || !aligned(rot, 8) || !aligned(status, 4)) return SA_ERR_INVALID_ARG;
+    if (!spans(n, x_stride) || !spans(b, table_stride) || !spans(npos, rot ? rope_dim : 0) ||
+        (pages && (!spans(page, pages_stride) || !spans(n_pages, pages_page_stride))) ||
+        (codes && (!spans(page, codes_stride) || !spans(n_pages, codes_page_stride) || !spans(page, scales_stride) ||
+                   !spans(n_pages, scales_page_stride))))
+        return SA_ERR_INVALID_ARG;
     const int64_t cw = quant == SA_KV_FP4_E2M1 ? d / 2 : d, sw = d / 32, r1 = page - 1, g1 = n_pages - 1;
     const int64_t p1 = r1 * pages_stride + d, c1 = r1 * codes_stride + cw, s1 = r1 * scales_stride + sw;  // a page's
     if (pages && (!aligned(pages, 2) || pages_stride < d || (n_pages > 1 && pages_page_stride < p1)))
@@ -382,7 +394,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     using namespace sa;
     if (!kv_format_known(kv_format) || !window_shape(n, b, h, d, window, first, page) || n_pages < 0 || max_pages < 0)
         return SA_ERR_INVALID_ARG;
-    if (!window_supported(n, h, d) || n_pages >= (int64_t(1) << 31) || n_pages * page >= (int64_t(1) << 31))
+    if (!window_supported(n, h, d) || n_pages >= k31 || n_pages * page >= k31 || max_pages >= k31 || b >= k31)
         return SA_ERR_UNSUPPORTED;
     if (kv_format == SA_KV_BF16 && kv_scale) return SA_ERR_INVALID_ARG;
     if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 1)) return SA_ERR_INVALID_ARG;
@@ -394,7 +406,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (n_pages < 1 || !kv || (codes && !kv_scale)) return SA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) || !aligned(lse, 4) ||
         !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
-        !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) || (b > 1 && table_stride < max_pages))
+        !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) || (b > 1 && table_stride < max_pages) || !spans(b, table_stride) || !spans(npos, rot ? rope_dim : 0))
         return SA_ERR_INVALID_ARG;
     const Parts parts = parts_of(n, b, h, d, window, first, page, kv_format);
     const int64_t ob = 2 * n * h * d, rows = n_pages * page;

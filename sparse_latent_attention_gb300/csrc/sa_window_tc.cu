@@ -129,6 +129,7 @@ struct Params {
     int h;
     int window, first;
     int n_splits;
+    int units;           // no more than these
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -295,33 +296,35 @@ static __device__ __noinline__ uint32_t seen(int window, int first, int base, in
 
 // Walks the sequences, 32 at a time, to the one that a tile of 128 rows is in; the tiles asked for rise.  (The whole warp.)
 struct Walk {
-    int seq0 = -32, before = 0, total = 0;  // the sequences at hand, and the tiles before and in them
-    int q0 = 0, q1 = 0, upto = 0;           // lane l: sequence seq0 + l's tokens, and its and its forerunners' tiles
+    int seq0 = -32;
+    uint32_t before = 0, total = 0;         // the sequences at hand are from seq0 on, with the tiles before and in them
+    int q0 = 0, q1 = 0;
+    uint32_t upto = 0;                      // lane l: sequence seq0 + l's tokens, and its and its forerunners' tiles
 
     // Sequence and tile in it, or false: there are no more.
-    __device__ __forceinline__ bool find(const Params& p, int tile, int lane, int& seq, int& at, int& from, int& to) {
+    __device__ __forceinline__ bool find(const Params& p, uint32_t tile, int lane, int& seq, int& at, int& from, int& to) {
         while (tile >= before + total) {
             before += total;
             seq0 += 32;
-            if (seq0 >= p.a.b) return false;
-            const int s = seq0 + lane;
+            if (seq0 < 0 || seq0 >= p.a.b) return false;  // (2^31 - 1 sequences: seq0 wraps)
+            const int64_t s = (int64_t)seq0 + lane;
             q0 = q1 = 0;
             if (s < p.a.b) {
                 q0 = min(max(__ldg(p.a.q_start + s), 0), p.n);
                 q1 = min(max(__ldg(p.a.q_start + s + 1), q0), p.n);
             }
-            upto = ((q1 - q0) * p.h + kM - 1) / kM;
+            upto = ((uint32_t)(q1 - q0) * (uint32_t)p.h + kM - 1) / kM;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, upto, d);
+                const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
                 if (lane >= d) upto += o;
             }
             total = __shfl_sync(0xffffffffu, upto, 31);
         }
         const int who = __ffs(__ballot_sync(0xffffffffu, upto > tile - before)) - 1;
-        const int prev = __shfl_sync(0xffffffffu, upto, who == 0 ? 0 : who - 1);
+        const uint32_t prev = __shfl_sync(0xffffffffu, upto, who == 0 ? 0 : who - 1);
         seq = seq0 + who;
-        at = tile - before - (who == 0 ? 0 : prev);
+        at = (int)(tile - before - (who == 0 ? 0 : prev));
         from = __shfl_sync(0xffffffffu, q0, who);
         to = __shfl_sync(0xffffffffu, q1, who);
         return true;
@@ -564,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         Walk walk;
         for (int u = blockIdx.x >> 1; ok; u += pairs) {
             Task t = {};
-            const bool more = task_of(p, u, lane, walk, t);
+            const bool more = u < p.units && task_of(p, u, lane, walk, t);
             t.more = more;
             const uint32_t i = nth % kTasks;
             if (!(ok = wait(M.task_empty[i], (nth / kTasks) ^ 1u, abort))) break;
@@ -1218,6 +1221,7 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     p.n_splits = window_splits(c.n, c.a.b, c.h, c.window, c.first, sms);
     const int64_t units = (c.n * c.h / kM + c.a.b) * p.n_splits;
     if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;  // (the kernel counts units in 32 bits)
+    p.units = (int)units;
     if (p.n_splits > 1) {
         p.part_ml = reinterpret_cast<float*>(c.scratch);
         p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(c.scratch) +

@@ -56,7 +56,11 @@ def test_add_rms_norm_refuses(lib, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(n=0, x=None), OK), (dict(b=0, q_start=None), OK), (dict(n=-1), INVALID), (dict(d=40), INVALID),
     (dict(d=0), INVALID), (dict(d=1056, xs=1056, pgs=1056, pgp=1 << 20, cs=1056, ss=40), UNSUPPORTED),
-    (dict(n=1 << 31), UNSUPPORTED), (dict(n_pages=1 << 38), UNSUPPORTED), (dict(b=-1), INVALID),
+    (dict(n=1 << 31), UNSUPPORTED), (dict(n_pages=1 << 38), UNSUPPORTED),
+    (dict(n_pages=1 << 31, page=1), UNSUPPORTED), (dict(n_pages=1 << 62), UNSUPPORTED), (dict(max_pages=1 << 31), UNSUPPORTED),
+    (dict(b=1 << 31), UNSUPPORTED), (dict(xs=1 << 62), INVALID), (dict(ts=1 << 62), INVALID), (dict(pgp=1 << 60), INVALID),
+    (dict(pgs=1 << 60), INVALID), (dict(cp=1 << 60), INVALID), (dict(ss=1 << 62), INVALID),
+    (dict(b=-1), INVALID),
     (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID), (dict(page=0), INVALID), (dict(max_pages=-1), INVALID), (dict(quant=3), INVALID),
     (dict(quant=0), INVALID), (dict(codes=None, scales=None, pages=None), INVALID), (dict(scales=None), INVALID),
     (dict(x=None), INVALID), (dict(x=at(1, 1)), INVALID), (dict(xs=63), INVALID), (dict(q_start=None), INVALID),
@@ -98,7 +102,10 @@ def test_page_write_takes_rows_between_one_another(lib):
     (dict(n=-1), INVALID), (dict(h=0), INVALID), (dict(h=129), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
     (dict(d=576), UNSUPPORTED), (dict(window=0), INVALID), (dict(window=1 << 30), INVALID), (dict(first=-1), INVALID),
     (dict(first=(1 << 30) - 128), INVALID), (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID),
-    (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED), (dict(max_pages=-1), INVALID),
+    (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED),
+    (dict(n=1 << 58), UNSUPPORTED), (dict(b=1 << 31), UNSUPPORTED), (dict(max_pages=1 << 31), UNSUPPORTED),
+    (dict(n_pages=1 << 62), UNSUPPORTED), (dict(ts=1 << 62), INVALID), (dict(rot=at(10), npos=1 << 60), INVALID),
+    (dict(max_pages=-1), INVALID),
     (dict(ts=3), INVALID), (dict(q=None), INVALID), (dict(q=at(1, 8)), INVALID), (dict(kv=None), INVALID),
     (dict(kv=at(2, 8)), INVALID), (dict(sink=None), INVALID), (dict(sink=at(3, 2)), INVALID), (dict(o=None), INVALID),
     (dict(o=at(7, 8)), INVALID), (dict(o=at(7, 16)), INVALID), (dict(o=at(7, 32)), WORKSPACE),
@@ -128,7 +135,8 @@ def test_window_attn_workspace_size(lib):
         assert f(8192, 3, 64, 512, 128, 4, 64, fmt) >= _lib.SA_STATUS_BYTES
     for bad in ((-1, 1, 64, 512, 128, 4, 64, 0), (1, 1, 0, 512, 128, 4, 64, 0), (1, 1, 64, 500, 128, 4, 64, 0),
                 (1, 1, 64, 512, 0, 4, 64, 0), (1, 1, 64, 512, 128, -1, 64, 0), (1, 1, 64, 512, 128, 4, 0, 0),
-                (1, 1, 64, 512, 128, 4, 64, 3), (1 << 25, 1, 64, 512, 128, 4, 64, 0)):
+                (1, 1, 64, 512, 128, 4, 64, 3), (1 << 25, 1, 64, 512, 128, 4, 64, 0),
+                (1 << 58, 1, 64, 512, 128, 4, 64, 0)):
         assert f(*bad) == 0
     with pytest.raises(sa.SparseAttnError):
         sa.window_workspace_size(1, 1, 64, 500, 128, 4, 64)
