@@ -454,7 +454,7 @@ Geometry geometry(int64_t n_tokens, int h, int topk, int sms) {
     const int64_t base = n_tokens * g.hblocks;
     const int64_t kTargetCtas = 2 * (int64_t)sms;
     int splits = 1;
-    if (g.n_tiles > 1 && base < kTargetCtas) {
+    if (g.n_tiles > 1 && base > 0 && base < kTargetCtas) {
         splits = (int)((kTargetCtas + base - 1) / base);
         if (splits > g.n_tiles) splits = g.n_tiles;
     }

@@ -1329,7 +1329,7 @@ TcGeometry tc_geometry(int64_t n_tokens, int h, int topk, int sms) {
     const int pairs = (g.n_tiles + 1) / 2;
     const int64_t base = n_tokens * g.hblocks;
     int splits = 1;
-    if (pairs > 1 && base < sms) {
+    if (pairs > 1 && base > 0 && base < sms) {
         splits = (int)(sms / base);
         if (splits > pairs) splits = pairs;
         if (splits < 1) splits = 1;

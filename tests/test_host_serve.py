@@ -142,6 +142,13 @@ def test_window_attn_workspace_size(lib):
         sa.window_workspace_size(1, 1, 64, 500, 128, 4, 64)
 
 
+def test_workspace_size_without_tokens(lib):
+    """A batch of no tokens, or of no sequences, over a long table: the status word and no more."""
+    for b, s in ((0, 4), (4, 0), (0, 0)):
+        for d, fmt in ((512, 0), (512, 1), (512, 2), (128, 0)):
+            assert lib.sa_sparse_attn_workspace_size(b, s, 64, d, 4096, 2048, fmt) == _lib.SA_STATUS_BYTES
+
+
 def test_host_tensors_are_refused():
     """Tensors that are not on a GPU, or of another type, are refused before the library is called."""
     i = dict(dtype=torch.int32)
