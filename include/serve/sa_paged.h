@@ -87,6 +87,8 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  * as sa_sparse_attn_rope turns them; a position that rot does not hold sets SA_ERR_INDEX and counts as its last
  * one.
  * Rows of the cache outside J may hold anything, a NaN or an infinity too, and change nothing.
+ * A row of J with a NaN makes o NaN; one with an infinity does, or, where that makes its logit -infinity, may count
+ * as a weight of zero.
  *
  * Arguments
  *   q          bf16 [n][h][d]

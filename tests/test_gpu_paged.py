@@ -407,3 +407,208 @@ def test_nothing_to_do(dev):  # noqa: F811
     sa.window_attn(torch.zeros_like(out), pool, sink, torch.zeros(0, 2, **z), torch.zeros(1, **z), torch.zeros(0, **z),
                    1.0, 8, out=out)
     assert (out == 5.0).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# calls that the cases above do not make
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("b,h", [(33, 64), (1100, 16), (400, 128)])
+def test_window_attn_many_sequences(dev, b, h, fmt):  # noqa: F811
+    """A task's sequence among many, a run of them without tokens, some with more than a tile."""
+    new = [0 if i % 5 == 3 or 60 <= i < 200 else 9 if i % 50 == 7 else 1 for i in range(b)]
+    bt = _paged.Batch(new, [(37 * i) % 150 for i in range(b)], 32, b, spare=2)
+    q, sink, pool, sc = _attn_inputs(dev, bt, h, 512, fmt, 40, 3, b + 1)
+    _check_attn(bt, q, pool, sc, sink, 40, 3)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("new,held", [([1], [0]), ([1, 1, 2], [0, 40, 200]), ([1], [700])])
+@pytest.mark.parametrize("rope", [0, 64])
+def test_window_attn_parts_without_positions(dev, new, held, rope, fmt):  # noqa: F811
+    """A window far longer than the caches: most of the parts that a token's positions are cut into have none."""
+    bt = _paged.Batch(new, held, 64, 80)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 1 << 16, 100, 81, peak=2.0)
+    _check_attn(bt, q, pool, sc, sink, 1 << 16, 100, rot=_paged.rotations(800, rope).to(dev) if rope else None)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_tokens_without_positions(dev, fmt):  # noqa: F811
+    """Hundreds of sequences one behind the other whose caches are shorter than their new tokens, a few that are not."""
+    b = 900
+    bt = _paged.Batch([1] * b, [50] * b, 64, 82)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 30, 2, 83)
+    want, lse_w = _attend(bt, q, pool, sc, sink, 0.05, 30, 2)
+    want, lse_w = want.clone(), lse_w.clone()
+    none = torch.ones(b, dtype=torch.bool, device=dev)
+    none[[0, 300, 301, 777, 899]] = False
+    bt.kv_len[none] = 0
+    bt.kv_len[5] = -(1 << 31)
+    got, lse = _attend(bt, q, pool, sc, sink, 0.05, 30, 2)
+    assert torch.equal(got[~none], want[~none]) and torch.equal(lse[~none], lse_w[~none])
+    assert (got[none] == 0).all() and torch.allclose(lse[none], sink.expand(int(none.sum()), -1))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("new", [90, 1])
+@pytest.mark.parametrize("page", [64, 16])
+def test_window_attn_far_past_the_table(dev, new, page, fmt):  # noqa: F811
+    """The largest length there is: noted, nothing read past the table, and the other sequences are right."""
+    bt = _paged.Batch([new, 3], [400, 70], page, 84)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 85)
+    want, _ = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+    ws = sa.new_window_workspace(bt.n, 2, 64, 512, 128, 4, page, sa.SA_KV_FP8_E4M3 if sc is not None else 0)
+    for length in (2 ** 31 - 1, (bt.max_pages + 5) * page):
+        bt.kv_len[0] = length
+        got = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 128, first=4, kv_scale=sc, workspace=ws)
+        assert sa.read_status(ws, clear=True) == SA_ERR_INDEX
+        assert torch.equal(got[new:], want[new:])
+        # what is left of it are the first rows, which are in the table
+        kv = _cache.rows_f64(pool.view(-1, pool.shape[2])[[bt.row(0, p) for p in range(4)]][None] if sc is None else
+                             pool.view(-1, 512)[[bt.row(0, p) for p in range(4)]][None],
+                             None if sc is None else sc.view(-1, 16)[[bt.row(0, p) for p in range(4)]][None], 512)
+        idx = torch.arange(4, dtype=torch.int32, device=dev).expand(1, new, 4).contiguous()
+        if length == 2 ** 31 - 1:
+            o, _, tol, _ = _cache.attention(q[None, :new], kv, sink, idx, 0.05)
+            assert ((got[:new].double() - o[0]).abs() <= tol[0]).all()
+
+
+def test_window_attn_rotation_past_its_table(dev):  # noqa: F811
+    """A position that the rotations do not hold counts as their last one, and is noted."""
+    bt = _paged.Batch([4], [96], 64, 86)
+    q, sink, pool, _ = _attn_inputs(dev, bt, 64, 512, "bf16", 64, 0, 87)
+    rot = _paged.rotations(100, 64).to(dev)
+    call = lambda r, **kw: sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 64, rope=r, **kw)
+    ws = sa.new_window_workspace(4, 1, 64, 512, 64, 0, 64)
+    got = call(rot[:98].contiguous(), workspace=ws)
+    assert sa.read_status(ws, clear=True) == SA_ERR_INDEX
+    held = rot.clone()
+    held[98:] = rot[97]
+    assert torch.equal(got, call(held, workspace=ws)) and sa.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("page", [64, 16])
+def test_window_attn_nan_rows(dev, fmt, page):  # noqa: F811
+    """A row that is NaN: NaN for the tokens that see it, nothing to the others of the same tile."""
+    bt = _paged.Batch([120], [30], page, 88)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 16, 3, 89)
+    want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 16, 3)
+    for p in (60, 77, 130, 149):
+        flat = pool.view(-1, 512)
+        if sc is None:
+            flat[bt.row(0, p)] = float("nan")
+        else:
+            flat[bt.row(0, p)] = 0x7F
+    got, lse = _attend(bt, q, pool, sc, sink, 0.05, 16, 3)
+    at = bt.positions()
+    sees = torch.zeros(bt.n, dtype=torch.bool)
+    for p in (60, 77, 130, 149):
+        sees |= (at >= p) & (at < p + 16)
+    sees = sees.to(dev)
+    assert got[sees].isnan().all() and lse[sees].isnan().all()
+    assert ((got[~sees].double() - want[~sees]).abs() <= tol[~sees]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_window_attn_takes_a_strided_table(dev, fmt):  # noqa: F811
+    """The page table as columns of a wider one; another table is the same rows elsewhere."""
+    bt = _paged.Batch([5, 1, 70], [100, 300, 0], 64, 90)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 128, 4, 91)
+    want, _ = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+    wide = torch.full((bt.b, bt.max_pages + 9), 1 << 30, dtype=torch.int32, device=dev)
+    wide[:, 4:4 + bt.max_pages] = bt.table
+    plain, bt.table = bt.table, wide[:, 4:4 + bt.max_pages]
+    got, _ = _attend(bt, q, pool, sc, sink, 0.05, 128, 4)
+    assert torch.equal(got, want)
+    x = _rows(dev, bt.n, 512, 92)
+    a, b = torch.zeros_like(pool), torch.zeros_like(pool)
+    if fmt == "bf16":
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=a)
+        sa.page_write(x, plain, bt.q_start, bt.kv_len, pages=b)
+    else:
+        sa.page_write(x, bt.table, bt.q_start, bt.kv_len, codes=a, scales=torch.zeros_like(sc))
+        sa.page_write(x, plain, bt.q_start, bt.kv_len, codes=b, scales=torch.zeros_like(sc))
+    assert torch.equal(a, b) and (a != 0).any()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_page_write_scales_behind_a_pages_codes(dev, fmt):  # noqa: F811
+    """Pages that hold their codes and behind them their scales, in one buffer."""
+    bt = _paged.Batch([40, 1], [0, 100], 64, 93)
+    d, w = 512, 512 if fmt == "fp8" else 256
+    x = _rows(dev, bt.n, d, 94)
+    both = torch.full((bt.n_pages, 64 * (w + 16)), 0x55, dtype=torch.uint8, device=dev)
+    codes, scales = both[:, :64 * w].unflatten(1, (64, w)), both[:, 64 * w:].unflatten(1, (64, 16))
+    before = (None, codes.clone(), scales.clone())
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, codes=codes, scales=scales)
+    _check_rows(bt, x.double(), None, codes, scales, fmt, before, 0.0)
+
+
+def test_graphs_that_share_a_workspace(dev):  # noqa: F811
+    """Two captured calls whose parts go through one workspace, replayed in turn on a stream."""
+    ins = []
+    ws = None
+    for k, (window, fmt) in enumerate([(2000, "bf16"), (3000, "fp8")]):
+        bt = _paged.Batch([1, 2], [1500 + 300 * k, 2500], 64, 95 + k)
+        ins.append((bt, window, *_attn_inputs(dev, bt, 64, 512, fmt, window, 8, 97 + k)))
+    size = max(sa.window_workspace_size(3, 2, 64, 512, w, 8, 64, f) for w, f in ((2000, 0), (3000, sa.SA_KV_FP8_E4M3)))
+    assert size > SA_STATUS_BYTES + 256  # (parts there are)
+    ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+    graphs, outs = [], []
+    for bt, window, q, sink, pool, sc in ins:
+        out = torch.empty_like(q)
+        call = lambda: sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, window, first=8,
+                                      kv_scale=sc, workspace=ws, out=out)
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(10):
+        for g, out in zip(graphs, outs):
+            out.fill_(9.0)
+            g.replay()
+    assert sa.read_status(ws) == 0
+    for (bt, window, q, sink, pool, sc), out in zip(ins, outs):
+        want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, window, 8)
+        assert ((out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_past_32_bits(dev, fmt):  # noqa: F811
+    """q and o of more than 2^31 elements and a pool of more than 2^32 bytes, the last sequence at the end of all three."""
+    tail, long, h = _paged.Batch([40], [60], 64, 99), 33100, 128
+    q, sink, small, sc_small = _attn_inputs(dev, tail, h, 512, fmt, 32, 5, 100)
+    n_pages = 72000 if fmt == "bf16" else 140000
+    assert long * h * 512 > 1 << 31 and n_pages * 64 * small.shape[2] * small.element_size() > 1 << 32
+    pool = torch.zeros(n_pages, *small.shape[1:], dtype=small.dtype, device=dev)
+    sc = None if sc_small is None else torch.zeros(n_pages, *sc_small.shape[1:], dtype=torch.uint8, device=dev)
+    pool[-tail.n_pages:] = small
+    if sc is not None:
+        sc[-tail.n_pages:] = sc_small
+    table = torch.full((2, -(-long // 64)), -1, dtype=torch.int32, device=dev)
+    table[0] = torch.arange(table.shape[1], device=dev)
+    table[1, :tail.max_pages] = torch.where(tail.table >= 0, tail.table + n_pages - tail.n_pages, -1)
+    qs = torch.zeros(long + 40, h, 512, dtype=torch.bfloat16, device=dev)
+    qs[long:] = q
+    out = torch.full_like(qs, 3.0)
+    q_start = torch.tensor([0, long, long + 40], dtype=torch.int32, device=dev)
+    kv_len = torch.tensor([long, 100], dtype=torch.int32, device=dev)
+    sa.window_attn(qs, pool, sink, table, q_start, kv_len, 0.05, 32, first=5, kv_scale=sc, out=out)
+    want, _, tol, _ = _paged.attention(tail, q, small, sc_small, sink, 0.05, 32, 5)
+    assert ((out[long:].double() - want).abs() <= tol).all()
+    assert (out[:long:997] == 0).all() and (out[long - 1] == 0).all()   # (zero rows)
+    # and the write
+    x = _rows(dev, 40, 512, 101)
+    x_all = torch.zeros(long + 40, 512, dtype=torch.bfloat16, device=dev)
+    x_all[long:] = x
+    before = [None if t is None else t[-tail.n_pages:].clone() for t in (pool, sc)]
+    if fmt == "bf16":
+        sa.page_write(x_all, table, q_start, kv_len, pages=pool)
+        _check_rows(tail, x.double(), pool[-tail.n_pages:], None, None, None, (before[0], None, None), 0.0)
+    else:
+        sa.page_write(x_all, table, q_start, kv_len, codes=pool, scales=sc)
+        _check_rows(tail, x.double(), None, pool[-tail.n_pages:], sc[-tail.n_pages:], "fp8", (None, *before), 0.0)
