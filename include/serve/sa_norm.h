@@ -39,8 +39,8 @@ typedef enum {
  *            of 32 along d, s = the smallest power of two with max |y| (at least 1e-4) <= 448 s, codes e4m3
  *            of y / s, scales the e8m0 byte of s.  Infinities saturate; a NaN stays one and does not count
  *            for its block's scale.
- * Squares are summed in f32 within a thread and with the rounding kept from there on; y is rounded to f32
- * once before it is rounded to its type, so that a value next to the border of two codes falls on its side.
+ * The sums, the factor and y are f32 with what f32 drops carried along beside them, and y is rounded once, to
+ * its type, so that a value next to the border of two codes falls on its side.
  *
  * Arguments
  *   x        bf16, row i at x + i * x_stride elements

@@ -48,8 +48,8 @@ extern "C" {
  *            sa_act_quant_fp8 and sa_act_quant_fp4 quantise: blocks of 32 along d, each with the smallest power
  *            of two s that takes max |y| (at least 1e-4) to 448 s (6 s), codes to the nearest, ties to even.
  *            Infinities saturate; a NaN does not count for the scale, and stays one in 8 bits and is a 0 in 4.
- * y is formed with what f32 loses carried along and is rounded to f32 once, then to its type, so that a value
- * next to the border of two codes falls on its side.
+ * y is formed with what f32 loses carried along and is rounded once, to its type, so that a value next to the
+ * border of two codes falls on its side.
  *
  * Arguments
  *   x          bf16, token t's row at x + t * x_stride elements

@@ -35,7 +35,7 @@ struct Norm {
 };
 
 // The sum over a block's warps of the pairs that they hold (every thread gets it).
-__device__ __forceinline__ Two block_sum(float x, Two* part) {
+__device__ __forceinline__ Two block_sum(Two x, Two* part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const Two v = warp_sum(x);
     if (lane == 0) part[warp] = v;
@@ -55,8 +55,7 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
     const int64_t row = kWarpRow ? blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (kWarpRow && row >= p.n) return;
     const int chunks = p.d >> 3;
-    float h[kPer][8];
-    float sum = 0.f;
+    float h[kPer][8], top = 0.f;
     {
         uint4 in[kPer];
         const __nv_bfloat16* x = p.x + row * p.xs;
@@ -114,20 +113,20 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
             }
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            float s[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = fmaf(h[i][2 * k], h[i][2 * k], h[i][2 * k + 1] * h[i][2 * k + 1]);
-            sum += (s[0] + s[1]) + (s[2] + s[3]);
-        }
+        for (int i = 0; i < kPer; ++i) top = fmaxf(top, largest8(h[i]));
     }
-    const Two r = inverse_rms(kWarpRow ? warp_sum(sum) : block_sum(sum, part), p.of);
+    Squares<4 * kPer> sum(top);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.add(tc::f2(h[i][2 * k], h[i][2 * k + 1]));
+    const Two r = inverse_rms(kWarpRow ? warp_sum(sum.total()) : block_sum(sum.total(), part), p.of);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int c = me + i * width;
         const bool in = c < chunks;
         if (!kWarpRow && i > 0 && me - (me & 31) + i * width >= chunks) break;  // (the whole warp)
-        float w[8], y[8];
+        float w[8], a[8], b[8], y[8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float4 v = in ? __ldg(reinterpret_cast<const float4*>(p.weight + 8 * c + 4 * k))
@@ -138,12 +137,18 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
             w[4 * k + 3] = v.w;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = rounded(mul(mul(h[i][k], r), w[k]));
+        for (int k = 0; k < 8; ++k) {
+            const Two v = mul(mul(h[i][k], r), w[k]);
+            a[k] = v.h;
+            b[k] = v.l;
+            y[k] = v.h + v.l;
+        }
+        top = settle8(a, b, y, [] {});
         if (p.out && in) store8<true>(p.out + row * p.os + 8 * c, packed8(y));
         if (p.codes) {
             uint2 codes;
             uint32_t se;
-            quantise8<false>(y, codes, se);
+            quantise8<false>(y, top, codes, se);
             if (in) {
                 store_codes8<true, false>(p.codes + row * p.cs + 8 * c, codes);
                 if ((c & 3) == 0) p.scales[row * p.ss + (c >> 2)] = (uint8_t)se;
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
     const __nv_bfloat16* x = p.x + row * p.xs;
     __nv_bfloat16* res16 = reinterpret_cast<__nv_bfloat16*>(p.res) + (kRes == SA_RESIDUAL_BF16 ? row * p.rs : 0);
     float* res32 = reinterpret_cast<float*>(p.res) + (kRes == SA_RESIDUAL_F32 ? row * p.rs : 0);
-    float sum = 0.f;
+    Two sum = {0.f, 0.f};
     for (int k = threadIdx.x; k < p.d; k += blockDim.x) {
         float h = __bfloat162float(x[k]);
         if constexpr (kRes == SA_RESIDUAL_BF16) {
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
             h = __bfloat162float(v);
         }
         if constexpr (kRes == SA_RESIDUAL_F32) res32[k] = h = h + res32[k];
-        sum = fmaf(h, h, sum);
+        sum = add(sum, mul(h, Two{h, 0.f}));
     }
     const Two r = inverse_rms(block_sum(sum, part), p.of);
     for (int k0 = threadIdx.x & ~31; k0 < p.d; k0 += blockDim.x) {  // (a warp's 32 elements)
@@ -182,7 +187,11 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
             const float h = kRes == SA_RESIDUAL_BF16  ? __bfloat162float(res16[k])
                             : kRes == SA_RESIDUAL_F32 ? res32[k]
                                                       : __bfloat162float(x[k]);
-            y = rounded(mul(mul(h, r), p.weight[k]));
+            const Two v = mul(mul(h, r), p.weight[k]);
+            const float a[8] = {v.h}, b[8] = {v.l};
+            float c[8] = {v.h + v.l};
+            settle8(a, b, c, [] {});
+            y = c[0];
             if (p.out) p.out[row * p.os + k] = __float2bfloat16_rn(y);
         }
         if (p.codes) {  // d % 32 == 0

@@ -41,11 +41,12 @@ struct Write {
 
 // A warp a token, eight consecutive elements a lane and chunk (kPer chunks of 256).  kRun tokens one behind the
 // other a warp: their rows are under way before the first one's sequence and page are known, and the sequence is
-// looked for once.  Bound by instructions, some 550 a row of 512 with norm, rotation and 4-bit codes (a third of them the
-// norm's products and what they lose, a third the codes and their round trip): 65536 such rows take 60 us with two
-// tokens a warp and six blocks a SM, 64 with four tokens or four blocks, 65 with one token.
+// looked for once.  Bound by instructions, some 650 a row of 512 with norm, rotation and 4-bit codes: a third are the
+// norm's products and what they lose, a third the codes and their round trip, and a sixth what makes the codes exact
+// (the sum's lost parts, the look for values on a border).  65536 such rows take 73 us with two tokens a warp and
+// five or six blocks a SM, 74 with seven (registers spill), 61 where codes next to a border may fall to its other side.
 template <int kQuant, int kPer, int kRun, bool kVec>
-__global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(const __grid_constant__ Write p) {
+__global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(const __grid_constant__ Write p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, chunks = p.d >> 3;
@@ -87,7 +88,14 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
             continue;
         }
         uint64_t v[kPer][4];  // elements 2 j and 2 j + 1
-        uint64_t sum = 0ull;
+        uint32_t large = 0u;
+        if (p.weight) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                large = largest_pair(largest_pair(large, largest_pair(in[r][i].x, in[r][i].y)), largest_pair(in[r][i].z, in[r][i].w));
+            large = largest_pair(large, large << 16);
+        }
+        Squares<4 * kPer> sum(__uint_as_float(large));
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             float e[8];
@@ -95,15 +103,11 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 v[i][j] = tc::f2(e[2 * j], e[2 * j + 1]);
-                sum = fma2(v[i][j], v[i][j], sum);
+                if (p.weight) sum.add(v[i][j]);
             }
         }
         Two f = {1.f, 0.f};
-        if (p.weight) {
-            float s0, s1;
-            tc::f2_split(sum, s0, s1);
-            f = inverse_rms(warp_sum(s0 + s1), p.of);
-        }
+        if (p.weight) f = inverse_rms(warp_sum(sum.total()), p.of);
         const uint64_t fh = tc::f2(f.h, f.h), fn = tc::f2(-f.h, -f.h), fl = tc::f2(f.l, f.l);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -133,7 +137,8 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
                 }
             }
             const int first = p.d - p.rope_dim;
-            if (p.rot && mine && 8 * c + 8 > first) {
+            const bool turned = p.rot && mine && 8 * c + 8 > first;
+            if (turned) {
                 const float2* turn = reinterpret_cast<const float2*>(p.rot) + k.pos * (p.rope_dim >> 1);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -142,8 +147,8 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
                     // a c - b s: b s rounded to u, what that lost, a c - u in one rounding, and the parts' own
                     const float2 cs = __ldg(turn + (e >> 1));
                     const float a = h[2 * j], b = h[2 * j + 1], al = l[2 * j], bl = l[2 * j + 1];
-                    const float u = b * cs.y, ul = fmaf(bl, cs.y, fmaf(b, cs.y, -u));
-                    const float z = b * cs.x, zl = fmaf(bl, cs.x, fmaf(b, cs.x, -z));
+                    const float u = __fmul_rn(b, cs.y), ul = fmaf(bl, cs.y, fmaf(b, cs.y, -u));
+                    const float z = __fmul_rn(b, cs.x), zl = fmaf(bl, cs.x, fmaf(b, cs.x, -z));
                     h[2 * j] = fmaf(a, cs.x, -u);
                     l[2 * j] = fmaf(al, cs.x, -ul);
                     h[2 * j + 1] = fmaf(a, cs.y, z);
@@ -152,10 +157,32 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
                     out[2 * j + 1] = h[2 * j + 1] + l[2 * j + 1];
                 }
             }
-            if (!(largest8(out) < INFINITY)) {  // (an infinity has no second part)
+            // (for a value on a border, which is seldom: what that one rounding lost, from the row read again)
+            auto whole = [&] {
+                if (!turned) return;
+                const float2* turn = reinterpret_cast<const float2*>(p.rot) + k.pos * (p.rope_dim >> 1);
+                float x[8];
+                unpacked8(load8<kVec>(p.x + t * p.xs + 8 * c), x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) out[j] = rounded({h[j], l[j]});
-            }
+                for (int j = 0; j < 4; ++j) {
+                    const int e = 8 * c + 2 * j - first;
+                    if (e < 0) continue;
+                    float a = x[2 * j], b = x[2 * j + 1];
+                    if (p.weight) {
+                        a = __fmul_rn(__fmul_rn(a, f.h), __ldg(p.weight + 8 * c + 2 * j));
+                        b = __fmul_rn(__fmul_rn(b, f.h), __ldg(p.weight + 8 * c + 2 * j + 1));
+                    }
+                    auto lost = [&](float m, float y, float sum) {  // a m + y - sum
+                        const float q = __fmul_rn(a, m);
+                        const Two s = two_sum(q, y);
+                        return ((s.h - sum) + s.l) + fmaf(a, m, -q);
+                    };
+                    const float2 cs = __ldg(turn + (e >> 1));
+                    l[2 * j] += lost(cs.x, -__fmul_rn(b, cs.y), h[2 * j]);
+                    l[2 * j + 1] += lost(cs.y, __fmul_rn(b, cs.x), h[2 * j + 1]);
+                }
+            };
+            const float top = p.weight || p.rot ? settle8(h, l, out, whole) : largest8(out);
             uint4 values;
             if constexpr (kQuant == SA_KV_BF16) {
                 values = packed8(out);
@@ -163,7 +190,7 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
                 constexpr bool kFp4 = kQuant == SA_KV_FP4_E2M1;
                 uint2 codes;
                 uint32_t se;
-                quantise8<kFp4>(out, codes, se);
+                quantise8<kFp4>(out, top, codes, se);
                 values = values8<kFp4>(codes, se);
                 if (p.codes && mine) {
                     store_codes8<kVec, kFp4>(p.codes + page * p.cp + off * p.cs + (kFp4 ? 4 : 8) * c, codes);
@@ -177,8 +204,8 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 6) page_write_kernel(cons
 
 template <int kQuant, int kPer, bool kVec>
 cudaError_t write_run(const Write& p, cudaStream_t st) {
-    // a wave of blocks holds 24 tokens a SM: below that, a token a warp; beyond, two
-    const bool few = p.n <= 24 * (int64_t)device_sm_count();
+    // a wave of blocks holds 20 tokens a SM: below that, a token a warp; beyond, two
+    const bool few = p.n <= 20 * (int64_t)device_sm_count();
     const int64_t per = few ? 4 : 8, grid = (p.n + per - 1) / per;
     return few ? launch_pdl(page_write_kernel<kQuant, kPer, 1, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p)
                : launch_pdl(page_write_kernel<kQuant, kPer, 2, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p);

@@ -3,8 +3,9 @@
 //
 // A code is chosen from the value that the formula gives, so a value next to the border between two codes
 // has to fall on its own side: what a row's factor and its rotation lose to f32 is carried along as a second
-// f32 (p = a b rounded, e = fma(a, b, -p) what the rounding dropped), and a value is rounded to f32 once, from
-// both.  It costs a handful of FMAs an element in kernels that wait for memory.
+// f32 (p = a b rounded, e = fma(a, b, -p) what the rounding dropped), and a value that f32 rounds onto a border is
+// moved to the side that it came from: of 33 million codes some 15 fell to the wrong side without that, and none
+// does now.  It costs a handful of FMAs an element.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -20,7 +21,8 @@
 namespace sa {
 namespace rows {
 
-// A value as the unevaluated sum h + l, |l| at most half a unit of h's last place.
+// A value as the unevaluated sum h + l, |l| at most half a unit of h's last place.  (A product whose rounding is carried
+// along is __fmul_rn: the compiler would put a plain one into the addition behind it, unrounded.)
 struct Two {
     float h, l;
 };
@@ -40,16 +42,13 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 
 // (x) times a pair, and a pair times w
 __device__ __forceinline__ Two mul(float x, Two r) {
-    const float p = x * r.h;
+    const float p = __fmul_rn(x, r.h);
     return {p, fmaf(x, r.l, fmaf(x, r.h, -p))};
 }
 __device__ __forceinline__ Two mul(Two x, float w) {
-    const float p = x.h * w;
+    const float p = __fmul_rn(x.h, w);
     return {p, fmaf(x.l, w, fmaf(x.h, w, -p))};
 }
-// (an infinity has no second part)
-__device__ __forceinline__ float rounded(Two v) { return fabsf(v.h) < INFINITY ? v.h + v.l : v.h; }
-
 // Two elements an instruction: the packed products and sums.
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -59,21 +58,63 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) { return tc::fadd2(a, b); }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) { return tc::ffma2(a, b, c); }
 
-// The sum of one f32 a lane over a warp: of the additions of a tree, the last two, whose rounding the whole sum shares,
-// keep what they lose (that of the ones before, of 4 sums and more, averages out: some 2^-26).
-__device__ __forceinline__ Two warp_sum(float v) {
-#pragma unroll
-    for (int m = 16; m > 2; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    Two s = two_sum(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    s = add(s, {__shfl_xor_sync(0xffffffffu, s.h, 1), __shfl_xor_sync(0xffffffffu, s.l, 1)});
-    return s;
+// The larger magnitude in either half of two pairs of bf16 (its sign is neither's).
+__device__ __forceinline__ uint32_t largest_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-// The same of pairs, every addition's rounding kept.
+
+// A running sum of squares, of even and of odd elements, with what its additions drop: h + x^2 rounded to n dropped
+// x^2 - (n - h), and n - h is exact because h starts at a power of two that no sum of the thread's reaches.
+template <int kCount>  // of either
+struct Squares {
+    float from;
+    uint64_t h, l = 0;
+
+    // largest: of the elements' magnitudes (a NaN or less gives some sum that is one).
+    __device__ __forceinline__ explicit Squares(float largest) {
+        constexpr int kLog = kCount <= 4 ? 2 : kCount <= 8 ? 3 : 4;
+        static_assert(kCount <= 16, "the sum's bound");
+        // x < 2^(e - 126), and kCount squares < 2^(2 (e - 126) + log2 kCount)
+        const int e = (int)(__float_as_uint(largest) >> 23 & 255u);
+        from = __uint_as_float((uint32_t)min(max(2 * e - 125 + kLog, 1), 254) << 23);
+        h = tc::f2(from, from);
+    }
+    __device__ __forceinline__ void add(uint64_t x) {
+        const uint64_t n = fma2(x, x, h);
+        l = add2(l, fma2(x, x, fma2(n, tc::f2(-1.f, -1.f), h)));
+        h = n;
+    }
+    __device__ __forceinline__ Two total() const {
+        Two a, b;
+        tc::f2_split(h, a.h, b.h);
+        tc::f2_split(l, a.l, b.l);
+        a.h -= from;
+        b.h -= from;
+        return rows::add(a, b);
+    }
+};
+
+// The sum over a warp of pairs that are not negative.  Their first parts are cut at one place, 18 bits below the largest's
+// exponent, so that 32 of them add up without a rounding; what is cut off, and the second parts, are added up beside
+// them.  (A tree that keeps every addition's rounding takes more than twice the instructions.  Sums of 2^121 and more are
+// added up plainly.)
 __device__ __forceinline__ Two warp_sum(Two v) {
+    const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(v.h) & 0x7FFFFFFFu) >> 23;
+    const float cut = __uint_as_float((e + 6u) << 23);
+    float h = v.h, l = 0.f;
+    if (e < 248u) {
+        h = __fadd_rn(__fadd_rn(v.h, cut), -cut);
+        l = (v.h - h) + v.l;
+    }
 #pragma unroll
-    for (int m = 16; m; m >>= 1)
-        v = add(v, {__shfl_xor_sync(0xffffffffu, v.h, m), __shfl_xor_sync(0xffffffffu, v.l, m)});
-    return v;
+    for (int m = 16; m; m >>= 1) {
+        h += __shfl_xor_sync(0xffffffffu, h, m);
+        l += __shfl_xor_sync(0xffffffffu, l, m);
+    }
+    const float s = h + l;
+    return {s, e < 248u ? l - (s - h) : 0.f};
 }
 
 // What a norm over d elements needs of d and eps: (sum / d + eps)^(-1/2) = d^(1/2) (sum + d eps)^(-1/2).
@@ -95,8 +136,8 @@ __device__ __forceinline__ Two inverse_rms(Two sum, const RmsOf& of) {
     const Two v = add(sum, of.shift);
     const float r0 = rsqrtf(v.h);
     if (!(r0 > 0.f && r0 < INFINITY)) return {r0, 0.f};
-    const float t = r0 * r0, tl = fmaf(r0, r0, -t);
-    const float p = v.h * t, pl = fmaf(v.h, t, -p);
+    const float t = __fmul_rn(r0, r0), tl = fmaf(r0, r0, -t);
+    const float p = __fmul_rn(v.h, t), pl = fmaf(v.h, t, -p);
     const float e = ((1.f - p) - pl) - fmaf(v.h, tl, v.l * t);
     const Two r = mul(Two{r0, 0.5f * r0 * e}, of.root.h);
     return {r.h, fmaf(r0, of.root.l, r.l)};
@@ -129,16 +170,40 @@ __device__ __forceinline__ float largest8(const float (&v)[8]) {
     return top(top(top(v[0], v[1]), top(v[2], v[3])), top(top(v[4], v[5]), top(v[6], v[7])));
 }
 
+// Settles out = h + l, rounded to f32, for a further rounding, to bf16 or to a code of fewer bits: a value that comes to
+// lie on a border of any of those (its last 15 bits are zero) without being on it moves one place back to its own
+// side.  |l| is at most half a unit of h's last place; an infinity has no second part.  Returns largest8(out).
+// `whole` is called before any is moved, and adds to l what it may leave out till then.
+template <class Whole>
+__device__ __forceinline__ float settle8(const float (&h)[8], const float (&l)[8], float (&out)[8], Whole whole) {
+    uint32_t z = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z = min(z, __float_as_uint(out[j]) << 17);
+    float top = largest8(out);
+    if (z == 0 || !(top < INFINITY)) {
+        whole();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = __float_as_uint(out[j]);
+            const float lost = l[j] - (out[j] - h[j]);
+            if (!(fabsf(h[j]) < INFINITY)) out[j] = h[j];
+            else if ((b << 17) == 0 && lost != 0.f) out[j] = __uint_as_float((lost > 0.f) == (out[j] > 0.f) ? b + 1 : b - 1);
+        }
+        top = largest8(out);
+    }
+    return top;
+}
+
 // Eight elements of a block of 32, the other 24 with the warp's three neighbouring lanes (lanes 4 k .. 4 k
-// + 3; the whole warp calls).  codes: eight e4m3 bytes, or eight e2m1 codes in the first word; se: the
+// + 3; the whole warp calls); top is largest8(v).  codes: eight e4m3 bytes, or eight e2m1 codes in the first word; se: the
 // scale byte.  A block with an infinity or a NaN, whose bits exceed every finite value's, is looked at again.
 template <bool kFp4>
-__device__ __forceinline__ void quantise8(float (&v)[8], uint2& codes, uint32_t& se) {
+__device__ __forceinline__ void quantise8(float (&v)[8], float top, uint2& codes, uint32_t& se) {
     auto block_max = [](uint32_t m) {
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     };
-    uint32_t m = block_max(__float_as_uint(largest8(v)));
+    uint32_t m = block_max(__float_as_uint(top));
     if (__any_sync(0xffffffffu, m > 0x7F7FFFFFu)) {
         m = 0;
 #pragma unroll

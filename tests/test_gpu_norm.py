@@ -60,6 +60,23 @@ def test_norm(dev, kind, n, d, pad):  # noqa: F811
         _check(x, w, r, res, out, codes, scales)
 
 
+@pytest.mark.parametrize("kind,d", [("bf16", 4096), ("f32", 4096), ("none", 512), ("f32", 1024)])
+def test_rounds_once(dev, kind, d):  # noqa: F811
+    """Millions of codes, to within 2^-36 of a border on their own side: of as many rounded to f32 on the way some
+    would not be."""
+    n, eps = (1 << 22) // d, float(torch.tensor(EPS))
+    x, w, r = _inputs(dev, n, d, kind, d)
+    codes = torch.empty(n, d, dtype=torch.uint8, device=dev)
+    scales = torch.empty(n, d // 32, dtype=torch.uint8, device=dev)
+    out = torch.empty(n, d, dtype=torch.bfloat16, device=dev)
+    sa.add_rms_norm(x, w, residual=r, eps=EPS, out=out, codes=codes, scales=scales)
+    y = _paged.norm((x if r is None else r).double(), w, eps)
+    _paged.check_codes(codes.view(torch.float8_e4m3fn).double(), scales, y, "fp8", 2.0 ** -36)
+    got = out.double()
+    step = _paged.pow2(torch.frexp(torch.maximum(got.abs(), y.abs())).exponent.long() - 9)   # half a step
+    assert ((got - y).abs() <= step + 2.0 ** -36 * y.abs()).all()
+
+
 def test_both_outputs_and_in_place(dev):  # noqa: F811
     x, w, r = _inputs(dev, 37, 1536, "bf16", 5)
     want, res = sa.add_rms_norm(x, w, residual=r.clone()), r.clone()

@@ -143,6 +143,34 @@ def test_page_write_bad_pages(dev):  # noqa: F811
     assert sa.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4", "bf16"])
+def test_page_write_rounds_once(dev, fmt):  # noqa: F811
+    """Millions of normed and turned values, to within 2^-36 of a border on its own side: of as many rounded to f32 on
+    the way some would not be."""
+    eps = float(torch.tensor(EPS))
+    bt = _paged.Batch([8192], [0], 64, 8)
+    x = _rows(dev, bt.n, 512, 9)
+    w = 1 + 0.3 * torch.randn(512, device=dev, generator=torch.Generator(device=dev).manual_seed(10))
+    rot = _paged.rotations(bt.n, 64).to(dev)
+    y = _paged.turned(_paged.norm(x, w, eps), rot, bt.positions().to(dev))
+    pages, codes, scales = _pools(dev, bt, 512, None if fmt == "bf16" else fmt, 11)
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, codes=codes, scales=scales, weight=w, eps=EPS, rope=rot)
+    rows = bt.rows().to(dev)
+    if fmt == "bf16":
+        got = pages.flatten(0, 1)[rows].double()
+        # half a step of the larger neighbour's
+        step = _paged.pow2(torch.frexp(torch.maximum(got.abs(), y.abs())).exponent.long() - 9)
+        assert ((got - y).abs() <= step + 2.0 ** -36 * y.abs()).all()
+    else:
+        c = codes.flatten(0, 1)[rows]
+        v = c.view(torch.float8_e4m3fn).double() if fmt == "fp8" else _paged.fp4_values(c)
+        # (a pair that cancels in the rotation keeps its error, which is relative to its length)
+        keep = torch.ones_like(y, dtype=torch.bool)
+        keep[:, -64:] = (y[:, -64:].unflatten(1, (32, 2)).square().sum(-1, keepdim=True).sqrt().expand(-1, -1, 2).flatten(1)
+                         < 256 * y[:, -64:].abs())
+        _paged.check_codes(torch.where(keep, v, 0.0), scales.flatten(0, 1)[rows], torch.where(keep, y, 0.0), fmt, 2.0 ** -36)
+
+
 def test_page_write_nan_and_inf(dev):  # noqa: F811
     bt = _paged.Batch([3], [0], 16, 5)
     x = _rows(dev, 3, 64, 6)
