@@ -1040,8 +1040,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
     } else {
         // ------------------------------------------------------------------ epilogue
         // A thread has one row and 128 of its d (256, where there is one group of four warps): of the half that its
-        // lane holds, those of its group.
-        constexpr int kSteps = 8 / kEpilogues;  // of 32 d
+        // lane holds, every second 32, so that the groups share the turned ones (all of them in one group's half
+        // made it 40 us of a prompt's 175: O is free for the next task when the last warp has read it).
         const int w = warp & 3, grp = (warp - kWarpEpilogue) >> 2, half = w >> 1, row = 32 * (w & 1) + lane;
         const uint32_t lane_base = (uint32_t)(32 * w) << 16;
         const bool split = p.n_splits > 1;
@@ -1095,14 +1095,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
             const int at_row = mine ? (split ? (int)part : (int)flat) : -1;
             const int even_row = __shfl_sync(0xffffffffu, at_row, lane & 30), odd_row = __shfl_sync(0xffffffffu, at_row, lane | 1);
 #pragma unroll 1
-            for (int k = kSteps * grp; k < kSteps * grp + kSteps; ++k) {  // 32 d at a time
+            for (int k = grp; k < 8; k += kEpilogues) {  // 32 d at a time
                 const int d0 = 256 * half + 32 * k;
                 uint32_t o[32];
                 __syncwarp();
                 if (t.nb) {
                     tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * k, o);
                     tmem_wait_ld();
-                    if (k == kSteps * grp + kSteps - 1) {
+                    if (k + kEpilogues >= 8) {
                         tc_fence_before();
                         warp_arrive_leader(M.o_empty, lane);
                     }
