@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(cons
 
 template <int kQuant, int kPer, bool kVec>
 cudaError_t write_run(const Write& p, cudaStream_t st) {
-    // a wave of blocks holds 20 tokens a SM: below that, a token a warp; beyond, two
-    const bool few = p.n <= 20 * (int64_t)device_sm_count();
+    // two waves of a token a warp hold 40 a SM; beyond, two tokens a warp (one / two: 64 rows 4.3 / 5.0 us, 4096 rows 7.6 /
+    // 8.5, 8192 rows 12.1 / 11.9, 65536 rows 72.0 / 64.5)
+    const bool few = p.n <= 40 * (int64_t)device_sm_count();
     const int64_t per = few ? 4 : 8, grid = (p.n + per - 1) / per;
     return few ? launch_pdl(page_write_kernel<kQuant, kPer, 1, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p)
                : launch_pdl(page_write_kernel<kQuant, kPer, 2, kVec>, dim3((unsigned)grid), dim3(128), 0, st, p);
@@ -225,7 +226,7 @@ cudaError_t write_launch(const Write& p, bool vec, cudaStream_t st) {
 
 // The pool's row of each position that a token may see: entry c < first of a token's row is position c,
 // entry first + c position p - window + 1 + c where that is not below first; -1 where there is none.  pos: each
-// token's position in the rotation's table.  A warp per 128 entries, four a lane.
+// token's position in the rotation's table.  A block a token and 128 entries at a time.
 __global__ void __launch_bounds__(128) window_rows_kernel(Batch a, int64_t n, int window, int first, int topk,
                                                           int32_t* idx, int32_t* pos, int64_t npos,
                                                           uint32_t* status) {

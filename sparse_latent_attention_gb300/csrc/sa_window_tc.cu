@@ -10,11 +10,12 @@
 // Both are M = 128 products of the pair: an SM's 64 rows fill its 128 TMEM lanes, lanes 0-63 with the first
 // half of the columns and 64-127 with the second.  One SM alone would have O of 128 rows x 512 in all of its
 // TMEM, and M = 64 products run at half the rate (64 rows x N 256 x K 16 take 64 cycles a SM here, measured).
-// TMEM: O in 256 columns, two S buffers of 64.
+// TMEM: O in 256 columns, three S buffers of 64, and the softmax's running maxima and sums.
 //
 // Blocks, not rows, are loaded: 32 positions lie in one page (a page is a multiple of 32 rows), so a block is a TMA
 // box and there is no gather.  K (stages of 64 rows x 128 of d, 16 KB) and V (of a block x 256 of d) go through a ring
-// each, five and four stages, and a tile's softmax runs behind the next tile's logits.
+// of four stages each, a tile's worth: the two rows of one position that a SM needs for K and for V are other halves,
+// and are fetched from L2 separately.  The softmax of a tile runs behind the next two tiles' logits.
 //
 // Masked positions.  A block is loaded whole, so rows that some or all of the task's tokens do not see come
 // with it, and they may hold anything.  Their p is set to zero, but 0 x NaN is NaN: a logit that is not finite in
@@ -25,9 +26,16 @@
 // Roles (each CTA of the pair, 22 warps): warps 0 and 21 issue the pair's logits and P.V (rank 0; rank 1's warp 21
 // passes on that its V has landed); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 20 V,
 // warp 3 Q; warps 4-7 and 8-11 softmax, every second tile each; warps 12-15 and 16-19 epilogue, half of d each.
-// Rows of codes (25 warps) come through registers instead: warp 2 describes the tiles and pulls their rows into L2,
-// warps 16-19 widen K and 20-23 V into the same stages, warps 12-15 are the epilogue and warp 24 issues P.V.  Every wait is bounded; one that gives up raises the timeout bit
-// and every role unwinds.
+// Rows of codes (32 warps) are widened to bf16 in the same stages: warp 2 describes the tiles and pulls their rows
+// into L2, warps 16-23 widen K and 24-31 V, warps 12-15 are the epilogue, warp 1 loads Q too and warp 3 issues P.V.
+// Every wait is bounded; one that gives up raises the timeout bit and every role unwinds.
+//
+// What it measured (a call among others, b sequences of one token but for the prompts): 128 heads, window 4096 + 128 first,
+// b = 256: 254 us, 4.7 TB/s of cache; 64 heads, window 128, a prompt of 4095 with the rotation: 135 us, 4 TB/s of q
+// and o; 128 heads, window 2048, prompts of 4096 tokens in all: 1.59 ms, 1.4 PFLOP/s; e4m3 rows, 64 heads, window
+// 1024, b = 64: 40 us; e2m1 rows, 16 heads, window 512, 240 tokens of 48 sequences: 23 us.  Long windows of bf16 rows are
+// bound by memory and the products in turn, prompts of short windows by a task's chain (Q, logits, softmax, P.V, O out:
+// O has one buffer), codes by the widening's instructions.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1168,12 +1176,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
 }
 
 // How many parts a task's blocks are cut into: more than one only where the tasks (about: a token's tile or the
-// rows' tiles, whichever are more) leave pairs of SMs without work, and at most one for two tiles (a part of one tile
-// saves its time, some 2 us, and costs the merge, which takes as long and is a launch more).
+// rows' tiles, whichever are more) leave pairs of SMs without work, and only of four tiles and more: a part a tile.  (One
+// token of 64 heads, whole / in parts of two tiles / of one, the merge's launch among them: window 256, 3 tiles, 12.8 / - /
+// 13.1 us; 384, 4 tiles, 14.6 / 14.4 / 13.2; 1024, 9 tiles, 21.7 / 15.7 / 13.9.  30 such tokens of window 4096: 61 whole, 44
+// in two parts.)
 int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, int sms) {
     const int64_t tiles = std::max<int64_t>(std::max<int64_t>((n * h + kM - 1) / kM, std::min(b, n)), 1);
     const int64_t keys = first + kBlock + window + kM / h + 2 * kBlock;
-    const int64_t most = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks) / 2;
+    const int64_t key_tiles = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks), most = key_tiles > 3 ? key_tiles : 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / 2 / tiles, most), 64));
 }
 
