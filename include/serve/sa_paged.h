@@ -102,7 +102,8 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  *   workspace  at least sa_window_attn_workspace_size(...) bytes, aligned to 256, as sa_sparse_attn's: its
  *              first SA_STATUS_BYTES zeroed once by the caller, calls sharing one stream-ordered
  * o and lse must not overlap an input, the workspace or each other.
- * Supported: d a multiple of 64 in [64, 512]; 1 <= h <= 128; n * h, b, max_pages and n_pages * page < 2^31.
+ * Supported: d a multiple of 64 in [64, 512]; 1 <= h <= 128; n * h, b, max_pages and n_pages * page < 2^31; at
+ * d = 512 with pages of a multiple of 32 rows first + window or max_pages * page at most 2^24.
  */
 size_t sa_window_attn_workspace_size(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page,
                                      int kv_format);

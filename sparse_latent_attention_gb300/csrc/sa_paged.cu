@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "sa_internal.cuh"
 #include "sa_paged.cuh"
 #include "sa_rows.cuh"
@@ -428,6 +430,10 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 1)) return SA_ERR_INVALID_ARG;
     const bool tc = attn_tc_supports(h, d, kv_format, 1, 0);
     if (rot && !tc) return SA_ERR_UNSUPPORTED;
+    // (the pair kernel's roles wait at most some two seconds for one another, a task's positions among it: 2^24 take half of
+    // one)
+    if (window_tc_supports(d, kv_format, page) && std::min(first + window, max_pages * page) > (int64_t(1) << 24))
+        return SA_ERR_UNSUPPORTED;
     if (n == 0 || b == 0) return SA_OK;
     const bool codes = kv_format != SA_KV_BF16;
     if (!q || !sink || !o || !q_start || !kv_len || (max_pages > 0 && !page_table)) return SA_ERR_INVALID_ARG;

@@ -502,6 +502,18 @@ def test_window_attn_far_past_the_table(dev, new, page, fmt):  # noqa: F811
             assert ((got[:new].double() - o[0]).abs() <= tol[0]).all()
 
 
+@pytest.mark.parametrize("page", [64, 16])
+def test_window_attn_without_a_table(dev, page):  # noqa: F811
+    """A table of no pages: every position is past it, nothing is attended to, and that is noted."""
+    q = torch.randn(3, 64, 512, device=dev).to(torch.bfloat16)
+    pool, sink = torch.full((2, page, 512), float("nan"), dtype=torch.bfloat16, device=dev), torch.randn(64, device=dev)
+    i = dict(dtype=torch.int32, device=dev)
+    ws, lse = sa.new_window_workspace(3, 2, 64, 512, 128, 4, page), torch.zeros(3, 64, device=dev)
+    o = sa.window_attn(q, pool, sink, torch.zeros(2, 0, **i), torch.tensor([0, 1, 3], **i), torch.tensor([9, 70], **i), 0.05,
+                       128, first=4, lse=lse, workspace=ws)
+    assert sa.read_status(ws) == SA_ERR_INDEX and (o == 0).all() and torch.allclose(lse, sink.expand(3, -1))
+
+
 def test_window_attn_rotation_past_its_table(dev):  # noqa: F811
     """A position that the rotations do not hold counts as their last one, and is noted."""
     bt = _paged.Batch([4], [96], 64, 86)

@@ -101,7 +101,10 @@ def test_page_write_takes_rows_between_one_another(lib):
     (dict(scale_ptr=at(9)), INVALID), (dict(fmt=1, scale_ptr=at(9, 4)), INVALID), (dict(fmt=1, scale_ptr=at(9)), WORKSPACE),
     (dict(n=-1), INVALID), (dict(h=0), INVALID), (dict(h=129), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
     (dict(d=576), UNSUPPORTED), (dict(window=0), INVALID), (dict(window=1 << 30), INVALID), (dict(first=-1), INVALID),
-    (dict(first=(1 << 30) - 128), INVALID), (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID),
+    (dict(first=(1 << 30) - 128), INVALID), (dict(window=1 << 24, max_pages=1 << 18, ts=1 << 18), WORKSPACE),
+    (dict(window=1 << 24, max_pages=(1 << 18) + 1, ts=1 << 19), UNSUPPORTED), (dict(window=1 << 29), WORKSPACE),
+    (dict(window=(1 << 24) - 4, max_pages=1 << 20, ts=1 << 20), WORKSPACE),
+    (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(n_pages=0), INVALID),
     (dict(n_pages=1 << 25), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED),
     (dict(n=1 << 58), UNSUPPORTED), (dict(b=1 << 31), UNSUPPORTED), (dict(max_pages=1 << 31), UNSUPPORTED),
     (dict(n_pages=1 << 62), UNSUPPORTED), (dict(ts=1 << 62), INVALID), (dict(rot=at(10), npos=1 << 60), INVALID),
@@ -162,3 +165,50 @@ def test_host_tensors_are_refused():
                        torch.zeros(2, **i), torch.zeros(1, **i), 1.0, 8)
     with pytest.raises(TypeError):
         sa.add_rms_norm(None, w)
+
+
+from tests.test_host_calls import DEV, bf16, calls, i32, on_device, u8  # noqa: E402, F401 (calls: a fixture)
+
+
+def _batch():
+    return on_device(2, 3, dtype=i32), on_device(3, dtype=i32), on_device(2, dtype=i32)
+
+
+SERVE = {
+    "sa_add_rms_norm": lambda **kw: sa.add_rms_norm(on_device(4, 64, dtype=bf16), on_device(64),
+                                                    **{"out": on_device(4, 64, dtype=bf16), **kw}),
+    "sa_page_write": lambda **kw: sa.page_write(on_device(4, 64, dtype=bf16), *_batch(),
+                                                **{"pages": on_device(5, 8, 64, dtype=bf16), **kw}),
+    "sa_window_attn": lambda **kw: sa.window_attn(
+        on_device(4, 2, 64, dtype=bf16), on_device(5, 8, 64, dtype=bf16), on_device(2), *_batch(), 0.1, 8,
+        **{"out": on_device(4, 2, 64, dtype=bf16), "workspace": on_device(1024, dtype=u8), **kw}),
+}
+
+
+@pytest.mark.parametrize("name", SERVE)
+def test_calls_run_on_their_tensors_device(calls, monkeypatch, name):  # noqa: F811
+    """With another device current: that of the tensors is current for the call, on its own stream or the given one."""
+    monkeypatch.setattr(sa, "_current_device", lambda: 0)
+    SERVE[name]()
+    stream = type("Stream", (), {"cuda_stream": 77})()
+    SERVE[name](stream=stream)
+    assert calls["calls"] == [(name, DEV, 1000 + DEV), (name, DEV, 77)]
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("sa_add_rms_norm", dict(out=torch.zeros(4, 64, dtype=torch.bfloat16))),
+    ("sa_add_rms_norm", dict(residual=torch.zeros(4, 64))),
+    ("sa_add_rms_norm", dict(codes=torch.zeros(4, 64, dtype=torch.uint8), scales=torch.zeros(4, 2, dtype=torch.uint8))),
+    ("sa_page_write", dict(pages=torch.zeros(5, 8, 64, dtype=torch.bfloat16))),
+    ("sa_page_write", dict(weight=torch.zeros(64))), ("sa_page_write", dict(rope=torch.zeros(9, 4, 2))),
+    ("sa_page_write", dict(workspace=torch.zeros(256, dtype=torch.uint8))),
+    ("sa_window_attn", dict(out=torch.zeros(4, 2, 64, dtype=torch.bfloat16))),
+    ("sa_window_attn", dict(lse=torch.zeros(4, 2))), ("sa_window_attn", dict(rope=torch.zeros(9, 4, 2))),
+    ("sa_window_attn", dict(workspace=torch.zeros(256, dtype=torch.uint8))),
+])
+def test_tensors_elsewhere_are_refused(calls, monkeypatch, name, kw):  # noqa: F811
+    """A host tensor among those of a device: its address never reaches the library."""
+    monkeypatch.setattr(sa, "_current_device", lambda: DEV)
+    with pytest.raises((TypeError, ValueError)):
+        SERVE[name](**kw)
+    assert not calls["calls"]
