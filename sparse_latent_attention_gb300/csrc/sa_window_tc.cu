@@ -306,18 +306,19 @@ static __device__ __noinline__ uint32_t seen(int window, int first, int base, in
 struct Walk {
     int seq0 = -32;
     uint32_t before = 0, total = 0;         // the sequences at hand are from seq0 on, with the tiles before and in them
-    int q0 = 0, q1 = 0;
-    uint32_t upto = 0;                      // lane l: sequence seq0 + l's tokens, and its and its forerunners' tiles
+    int q0 = 0, q1 = 0, len = 0;            // lane l: sequence seq0 + l's tokens and length
+    uint32_t upto = 0;                      // and its and its forerunners' tiles
 
     // Sequence and tile in it, or false: there are no more.
-    __device__ __forceinline__ bool find(const Params& p, uint32_t tile, int lane, int& seq, int& at, int& from, int& to) {
+    __device__ __forceinline__ bool find(const Params& p, uint32_t tile, int lane, int& seq, int& at, int& from, int& to, int& length) {
         while (tile >= before + total) {
             before += total;
             seq0 += 32;
             if (seq0 < 0 || seq0 >= p.a.b) return false;  // (2^31 - 1 sequences: seq0 wraps)
             const int64_t s = (int64_t)seq0 + lane;
-            q0 = q1 = 0;
+            q0 = q1 = len = 0;
             if (s < p.a.b) {
+                len = __ldg(p.a.kv_len + s);
                 q0 = min(max(__ldg(p.a.q_start + s), 0), p.n);
                 q1 = min(max(__ldg(p.a.q_start + s + 1), q0), p.n);
             }
@@ -335,6 +336,7 @@ struct Walk {
         at = (int)(tile - before - (who == 0 ? 0 : prev));
         from = __shfl_sync(0xffffffffu, q0, who);
         to = __shfl_sync(0xffffffffu, q1, who);
+        length = __shfl_sync(0xffffffffu, len, who);
         return true;
     }
 };
@@ -342,8 +344,8 @@ struct Walk {
 // Unit u -> its task (the whole warp calls, with rising u); false: there are no more.
 __device__ __forceinline__ bool task_of(const Params& p, int u, int lane, Walk& walk, Task& t) {
     const int tile = u / p.n_splits;
-    int seq, at, q0, q1;
-    if (!walk.find(p, tile, lane, seq, at, q0, q1)) return false;
+    int seq, at, q0, q1, len;
+    if (!walk.find(p, tile, lane, seq, at, q0, q1, len)) return false;
     const int r0 = at * kM, rows = (q1 - q0) * p.h - r0;
     t.seq = seq;
     t.split = u - tile * p.n_splits;
@@ -353,7 +355,7 @@ __device__ __forceinline__ bool task_of(const Params& p, int u, int lane, Walk& 
     t.tok0 = q0 + tok;
     t.row0 = q0 * p.h + r0;
     // (lengths far outside the table's range, which are errors, are held where 32 bits do)
-    const int64_t pos = (int64_t)__ldg(p.a.kv_len + seq) - (q1 - q0) + tok;
+    const int64_t pos = (int64_t)len - (q1 - q0) + tok;
     t.pos0 = (int)min(max(pos, -(int64_t(1) << 30)), (int64_t(1) << 31) - 1 - kM);
     t.pmax = t.pos0 + (t.off0 + t.rows - 1) / p.h;
     // blocks: the first positions' and the window's, those of both once; none past the table's last page
@@ -1067,6 +1069,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                     pos = p.npos - 1;
                 }
                 turn = reinterpret_cast<const float2*>(p.rope) + max(pos, (int64_t)0) * (p.rope_dim >> 1);
+                // (on its way while the products run: one token's epilogue would wait a microsecond for it)
+                if (half)
+                    for (int x = 0; x < p.rope_dim >> 1; x += 16)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(turn + x));
             }
             const float sink = __ldg(p.sink + head);
             ok = wait(M.stats_full, c, abort);
