@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(cons
         if (p.weight) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                large = largest_pair(largest_pair(large, largest_pair(in[r][i].x, in[r][i].y)), largest_pair(in[r][i].z, in[r][i].w));
+                large = largest_pair(largest_pair(large, largest_pair(in[r][i].x, in[r][i].y)),
+                                     largest_pair(in[r][i].z, in[r][i].w));
             large = largest_pair(large, large << 16);
         }
         Squares<4 * kPer> sum(__uint_as_float(large));
@@ -430,8 +431,8 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (rot && (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > d || npos < 1)) return SA_ERR_INVALID_ARG;
     const bool tc = attn_tc_supports(h, d, kv_format, 1, 0);
     if (rot && !tc) return SA_ERR_UNSUPPORTED;
-    // (the pair kernel's roles wait at most some two seconds for one another, a task's positions among it: 2^24 take half of
-    // one)
+    // (the pair kernel's roles wait at most some two seconds for one another, for a task's positions too: 2^24 of them
+    // take half of one)
     if (window_tc_supports(d, kv_format, page) && std::min(first + window, max_pages * page) > (int64_t(1) << 24))
         return SA_ERR_UNSUPPORTED;
     if (n == 0 || b == 0) return SA_OK;
@@ -440,7 +441,8 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     if (n_pages < 1 || !kv || (codes && !kv_scale)) return SA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(sink, 4) || !aligned(lse, 4) ||
         !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(rot, 8) ||
-        !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) || (b > 1 && table_stride < max_pages) || !spans(b, table_stride) || !spans(npos, rot ? rope_dim : 0))
+        !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) ||
+        (b > 1 && table_stride < max_pages) || !spans(b, table_stride) || !spans(npos, rot ? rope_dim : 0))
         return SA_ERR_INVALID_ARG;
     const Parts parts = parts_of(n, b, h, d, window, first, page, kv_format);
     const int64_t ob = 2 * n * h * d, rows = n_pages * page;

@@ -187,7 +187,8 @@ __device__ __forceinline__ float settle8(const float (&h)[8], const float (&l)[8
             const uint32_t b = __float_as_uint(out[j]);
             const float lost = l[j] - (out[j] - h[j]);
             if (!(fabsf(h[j]) < INFINITY)) out[j] = h[j];
-            else if ((b << 17) == 0 && lost != 0.f) out[j] = __uint_as_float((lost > 0.f) == (out[j] > 0.f) ? b + 1 : b - 1);
+            else if ((b << 17) == 0 && lost != 0.f)
+                out[j] = __uint_as_float((lost > 0.f) == (out[j] > 0.f) ? b + 1 : b - 1);
         }
         top = largest8(out);
     }

@@ -310,7 +310,8 @@ struct Walk {
     uint32_t upto = 0;                      // and its and its forerunners' tiles
 
     // Sequence and tile in it, or false: there are no more.
-    __device__ __forceinline__ bool find(const Params& p, uint32_t tile, int lane, int& seq, int& at, int& from, int& to, int& length) {
+    __device__ __forceinline__ bool find(const Params& p, uint32_t tile, int lane, int& seq, int& at, int& from, int& to,
+                                         int& length) {
         while (tile >= before + total) {
             before += total;
             seq0 += 32;
@@ -466,7 +467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
     constexpr int kEpilogues = epilogue_groups(kFmt), kWarpV = warp_v(kFmt), kWarpPv = warp_pv(kFmt);
     extern __shared__ __align__(1024) uint8_t smem[];
     Misc& M = *reinterpret_cast<Misc*>(smem + kOffMisc);
-    const uint32_t s_k = smem_addr(smem + kOffK), s_v = smem_addr(smem + kOffV), s_q = smem_addr(smem + kOffQ), s_p = smem_addr(smem + kOffP);
+    const uint32_t s_k = smem_addr(smem + kOffK), s_v = smem_addr(smem + kOffV), s_q = smem_addr(smem + kOffQ),
+                   s_p = smem_addr(smem + kOffP);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = __shfl_sync(0xffffffffu, cta_rank(), 0);  // (warp-uniform for the compiler too)
     volatile int* abort = &M.abort;
@@ -590,8 +592,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         if (kCodes) drain_q();
     } else if (warp == 0 || warp == kWarpPv) {
         // ------------------------------------------------------------------ the pair's products
-        // Warp 0 issues the logits, another one P.V (of bf16 rows, rank 1's passes on that its V has landed).  One warp for both
-        // spent 600 cycles a stage of 256 cycles of products (a wait for a barrier that has long completed takes
+        // Warp 0 issues the logits, another one P.V (of bf16 rows, rank 1's passes on that its V has landed).  One warp for
+        // both spent 600 cycles a stage of 256 cycles of products (a wait for a barrier that has long completed takes
         // 130, a commit 75, and the tensor pipe holds too few products to bridge them); of two, one's products run
         // behind the other's barriers.
         constexpr uint32_t id_s = idesc_bf16_f32(kM, 128, false, false);
@@ -827,7 +829,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                     while (put < stages && put <= n + 2) {
                         const uint32_t gi = (g + (put >> 2)) % kInfos, m = seq + put, e = smem_addr(&empty[m % kRing]);
                         if (put > n && !__all_sync(0xffffffffu, mbar_test_wait(e, ((m / kRing) ^ 1u) & 1u))) break;
-                        if ((put & 2) == 0) ok = ok && wait_here(smem_addr(&M.info_full[gi]), (g + (put >> 2)) / kInfos, abort);
+                        if ((put & 2) == 0)
+                            ok = ok && wait_here(smem_addr(&M.info_full[gi]), (g + (put >> 2)) / kInfos, abort);
                         ok = ok && wait_here(e, (m / kRing) ^ 1u, abort);
                         if (!ok) break;
                         if (is_v || (put & ~3) + j_k < t.nb) {
@@ -933,7 +936,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float x0, x1;
-                            f2_split(fmul2(f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(sc, sc)), x0, x1);
+                            const uint64_t s2 = f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            f2_split(fmul2(s2, f2(sc, sc)), x0, x1);
                             r[2 * j] = __float_as_uint(x0);
                             r[2 * j + 1] = __float_as_uint(x1);
                         }
@@ -988,7 +992,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                         for (int j = 0; j < 4; ++j) {
                             const int at = 8 * u + 2 * j;
                             float x0, x1;
-                            f2_split(ffma2(f2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f2(sc, sc), f2(-mu, -mu)), x0, x1);
+                            const uint64_t s2 = f2(__uint_as_float(r[at]), __uint_as_float(r[at + 1]));
+                            f2_split(ffma2(s2, f2(sc, sc), f2(-mu, -mu)), x0, x1);
                             if (!whole) {
                                 x0 = v & (1u << at) ? x0 : -INFINITY;
                                 x1 = v & (2u << at) ? x1 : -INFINITY;
@@ -1107,7 +1112,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
             // of 32, a lane's own, take twice the time: a store's time is its pieces')
             const bool odd = lane & 1;
             const int at_row = mine ? (split ? (int)part : (int)flat) : -1;
-            const int even_row = __shfl_sync(0xffffffffu, at_row, lane & 30), odd_row = __shfl_sync(0xffffffffu, at_row, lane | 1);
+            const int even_row = __shfl_sync(0xffffffffu, at_row, lane & 30);
+            const int odd_row = __shfl_sync(0xffffffffu, at_row, lane | 1);
 #pragma unroll 1
             for (int k = grp; k < 8; k += kEpilogues) {  // 32 d at a time
                 const int d0 = 256 * half + 32 * k;
@@ -1189,7 +1195,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
 int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, int sms) {
     const int64_t tiles = std::max<int64_t>(std::max<int64_t>((n * h + kM - 1) / kM, std::min(b, n)), 1);
     const int64_t keys = first + kBlock + window + kM / h + 2 * kBlock;
-    const int64_t key_tiles = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks), most = key_tiles > 3 ? key_tiles : 1;
+    const int64_t key_tiles = (keys + kBlock * kTileBlocks - 1) / (kBlock * kTileBlocks);
+    const int64_t most = key_tiles > 3 ? key_tiles : 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / 2 / tiles, most), 64));
 }
 
