@@ -514,6 +514,23 @@ def test_window_attn_without_a_table(dev, page):  # noqa: F811
     assert sa.read_status(ws) == SA_ERR_INDEX and (o == 0).all() and torch.allclose(lse, sink.expand(3, -1))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("d,page,window,first", [(512, 16, 5000, 10), (512, 1, 90, 600), (256, 64, 5000, 10), (64, 64, 60, 600),
+                                                 (64, 5, 1, 100), (448, 32, 1 << 20, 0)])
+def test_window_attn_longer_than_the_table(dev, d, page, window, first, fmt):  # noqa: F811
+    """A table of fewer positions than a token may see, in the kernels that gather by row: all of them are looked at, and
+    a position past them is still an error."""
+    bt = _paged.Batch([40, 0, 1], [100, 9, 300], page, 102, 2)
+    rot = _paged.rotations(400, 64).to(dev) if d == 512 else None
+    q, sink, pool, sc = _attn_inputs(dev, bt, 40, d, fmt, window, first, 103, peak=2.0)
+    _check_attn(bt, q, pool, sc, sink, window, first, rot=rot)
+    bt.kv_len[2] = bt.max_pages * page + 1
+    ws = sa.new_window_workspace(bt.n, bt.b, 40, d, window, first, page,
+                                 {"bf16": sa.SA_KV_BF16, "fp8": sa.SA_KV_FP8_E4M3, "fp4": sa.SA_KV_FP4_E2M1}[fmt])
+    sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, window, first=first, kv_scale=sc, workspace=ws)
+    assert sa.read_status(ws) == SA_ERR_INDEX
+
+
 def test_window_attn_rotation_past_its_table(dev):  # noqa: F811
     """A position that the rotations do not hold counts as their last one, and is noted."""
     bt = _paged.Batch([4], [96], 64, 86)
