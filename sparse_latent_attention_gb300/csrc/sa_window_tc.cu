@@ -31,10 +31,10 @@
 // Every wait is bounded; one that gives up raises the timeout bit and every role unwinds.
 //
 // What it measured (a call among others, b sequences of one token but for the prompts): 128 heads, window 4096 + 128 first,
-// b = 256: 254 us, 4.7 TB/s of cache; 64 heads, window 128, a prompt of 4095 with the rotation: 135 us, 4 TB/s of q
+// b = 256: 252 us, 4.7 TB/s of cache; 64 heads, window 128, a prompt of 4095 with the rotation: 132 us, 4 TB/s of q
 // and o; 128 heads, window 2048, prompts of 4096 tokens in all: 1.59 ms, 1.4 PFLOP/s; e4m3 rows, 64 heads, window
-// 1024, b = 64: 40 us; e2m1 rows, 16 heads, window 512, 240 tokens of 48 sequences: 23 us.  Long windows of bf16 rows are
-// bound by memory and the products in turn, prompts of short windows by a task's chain (Q, logits, softmax, P.V, O out:
+// 1024, b = 64: 39 us; e2m1 rows, 16 heads, window 512, 240 tokens of 48 sequences: 23 us.  Long windows of bf16 rows are
+// bound by L2, out of which each row comes twice (pulled into L2 ahead they take longer), prompts of short windows by a task's chain (Q, logits, softmax, P.V, O out:
 // O has one buffer), codes by the widening's instructions.
 
 #include <cuda.h>
@@ -1241,7 +1241,9 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     p.h = c.h;
     p.window = (int)c.window;
     p.first = (int)c.first;
-    p.n_splits = window_splits(c.n, c.a.b, c.h, c.window, c.first, sms);
+    // (no more parts than the table's positions make: the scratch is sized without it, for as many or more)
+    const int64_t held = std::max<int64_t>(c.a.max_pages * c.a.page, 1);
+    p.n_splits = window_splits(c.n, c.a.b, c.h, std::min(c.window, held), std::min(c.first, held), sms);
     const int64_t units = (c.n * c.h / kM + c.a.b) * p.n_splits;
     if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;  // (the kernel counts units in 32 bits)
     p.units = (int)units;
