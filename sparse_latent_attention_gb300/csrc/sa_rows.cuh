@@ -78,7 +78,8 @@ struct Squares {
         static_assert(kCount <= 16, "the sum's bound");
         // x < 2^(e - 126), and kCount squares < 2^(2 (e - 126) + log2 kCount)
         const int e = (int)(__float_as_uint(largest) >> 23 & 255u);
-        from = __uint_as_float((uint32_t)min(max(2 * e - 125 + kLog, 1), 254) << 23);
+        const int at = 2 * e - 125 + kLog;
+        from = at > 253 ? 0.f : __uint_as_float((uint32_t)max(at, 1) << 23);  // (no such power: from 0, plainly)
         h = tc::f2(from, from);
     }
     __device__ __forceinline__ void add(uint64_t x) {

@@ -2,6 +2,8 @@
 
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -126,6 +128,22 @@ def test_extremes(dev):  # noqa: F811
     sa.add_rms_norm(x[5:], w2, codes=codes[5:], scales=scales[5:])
     v = codes[5].view(torch.float8_e4m3fn).float()
     assert (v[:32].abs() == 448).all() and (v[32:64] == 0).all() and (scales[5] < 255).all()
+
+
+@pytest.mark.parametrize("d", [64, 512, 4096])
+def test_squares_at_the_edges_of_f32(dev, d):  # noqa: F811
+    """One element whose square is all but the largest that f32 holds, rows of few or of many magnitudes, and squares
+    below the smallest normal."""
+    x = torch.zeros(5, d, device=dev)
+    x[0, 3] = 1.7e19
+    x[1, 3], x[1, 40] = 1e19, -1.2e19
+    x[2] = 2.0 ** torch.linspace(-30, 62 - 0.5 * math.log2(d), d, device=dev)
+    x[3] = 2.0 ** torch.linspace(-60, 0, d, device=dev).flip(0)
+    x[4] = 3e-23                                     # (eps is all of the mean)
+    x = x.to(torch.bfloat16)
+    w = torch.linspace(0.5, 1.5, d, device=dev)
+    _check(x, w, None, None, sa.add_rms_norm(x, w), None, None)
+    _check(x[:4], w, None, None, sa.add_rms_norm(x[:4], w, eps=0.0), None, None, eps=0.0)
 
 
 def test_rows_of_nothing(dev):  # noqa: F811
