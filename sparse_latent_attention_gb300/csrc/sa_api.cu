@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kVersion = 300;  // 0.3.0: 4-bit kv, the log-sum-exp output, row weights and eviction
+constexpr int kVersion = 400;  // 0.4.0: the paged cache, its window attention and the residual norm
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
