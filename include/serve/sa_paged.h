@@ -89,6 +89,8 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  * Rows of the cache outside J may hold anything, a NaN or an infinity too, and change nothing.
  * A row of J with a NaN makes o NaN; one with an infinity does, or, where that makes its logit -infinity, may count
  * as a weight of zero.
+ * A row of q (a token's head) that is not finite, or whose logits are not, changes its own o and lse and no
+ * others: a NaN in it makes both NaN where J is not empty.  q of the tokens from q_start[b] on may hold anything.
  *
  * Arguments
  *   q          bf16 [n][h][d]

@@ -19,9 +19,10 @@
 //
 // Masked positions.  A block is loaded whole, so rows that some or all of the task's tokens do not see come
 // with it, and they may hold anything.  Their p is set to zero, but 0 x NaN is NaN: a logit that is not finite in
-// a column that not every token sees makes the softmax warps clear that row of V (in their half of d) before the
-// product; a row that is not finite gives every query row such a logit.  Rows that see the row have a NaN there
-// anyway.
+// a column that not every token sees makes the softmax warps look at that row of V (in their half of d) before the
+// product, and clear what is not finite in it.  A row that is not finite gives every query row such a logit, those behind
+// the task's last among them (they find it where a CTA has none of the task's own); a query row that is not finite
+// gives one to every position, whose rows are not touched then.  Rows that see a bad row have a NaN there anyway.
 //
 // Roles (each CTA of the pair, 22 warps): warps 0 and 21 issue the pair's logits and P.V (rank 0; rank 1's warp 21
 // passes on that its V has landed); warp 1 turns units into tasks, up to four ahead; warp 2 loads K, warp 20 V,
@@ -283,6 +284,19 @@ __device__ __forceinline__ void tmem_st_x2(uint32_t at, float a, float b) {
                  "r"(__float_as_uint(b))
                  : "memory");
     tmem_wait_st();
+}
+// Whether one of eight bf16 in shared memory is an infinity or a NaN.
+__device__ __forceinline__ bool any_not_finite(uint32_t at) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        any |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
+    return any;
 }
 // 32 bytes at a 32-byte aligned address
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
@@ -1035,9 +1049,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                         if (!rows) continue;
                         const uint32_t vs = v_at + half + 2 * k;
                         if (!(ok = wait(M.v_full[vs % kVStages], vs / kVStages, abort))) break;
-                        // (4 pieces of 128 bytes: a lane 16 of them)
+                        // (4 pieces of 128 bytes: a lane 16 of them.  The logit may be a bad q's, and other rows of the
+                        // task see this one of V: only what is not finite itself is cleared, 0 times the rest is 0)
                         const uint32_t at = s_v + (vs % kVStages) * kStageBytes + (lane >> 3) * 4096 + (lane & 7) * 16;
-                        for (; rows; rows &= rows - 1) st_shared_v4(at + (__ffs(rows) - 1) * 128, 0u, 0u, 0u, 0u);
+                        for (; rows; rows &= rows - 1) {
+                            const uint32_t to = at + (__ffs(rows) - 1) * 128;
+                            if (any_not_finite(to)) st_shared_v4(to, 0u, 0u, 0u, 0u);
+                        }
                     }
                     if (!ok) break;
                 }

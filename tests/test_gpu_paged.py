@@ -669,3 +669,48 @@ def test_window_attn_past_32_bits(dev, fmt):  # noqa: F811
     else:
         sa.page_write(x_all, table, q_start, kv_len, codes=pool, scales=sc)
         _check_rows(tail, x.double(), None, pool[-tail.n_pages:], sc[-tail.n_pages:], "fp8", (None, *before), 0.0)
+
+
+NOT_FINITE = (float("nan"), float("inf"), -float("inf"), 3.3e38)  # (the last: finite, but for its logits)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("h", [1, 16, 40, 64, 128])
+@pytest.mark.parametrize("page,d", [(64, 512), (16, 512), (64, 256)])
+@pytest.mark.parametrize("value", NOT_FINITE)
+def test_window_attn_q_that_is_not_finite(dev, value, page, d, h, fmt):  # noqa: F811
+    """A row of q that is not finite changes its own o and no other: not that of its token's other heads, of tokens in
+    the same tile, of the sequence before, nor of the last one where it belongs to no sequence."""
+    bt = _paged.Batch([40, 3, 9, 21], [70, 200, 0, 31], page, 104, spare=12)
+    q, sink, pool, sc = _attn_inputs(dev, bt, h, d, fmt, 16, 3, 105)
+    want, lse_w = _attend(bt, q, pool, sc, sink, 0.05, 16, 3)
+    want, lse_w = want.clone(), lse_w.clone()
+    bad = torch.zeros(bt.n, h, dtype=torch.bool, device=dev)
+    bad[7, h // 2] = bad[20, 0] = bad[20, h - 1] = True     # inside a sequence
+    bad[43, 0] = bad[52, h // 3] = True                     # the first token of the next one
+    bad[bt.live:] = True                                    # behind the last
+    odd = q.clone()
+    odd[..., 200] = torch.where(bad, value, q[..., 200].float()).to(torch.bfloat16)
+    odd[bt.live:] = value
+    got, lse = _attend(bt, odd, pool, sc, sink, 0.05, 16, 3)
+    ok = ~bad[:bt.live]
+    assert torch.equal(got[ok], want[ok]) and torch.equal(lse[ok], lse_w[ok])
+    if value != value:
+        assert got[~ok].isnan().all() and lse[~ok].isnan().all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_q_and_rows_that_are_not_finite(dev, fmt):  # noqa: F811
+    """Both at once: tokens that see a NaN row are NaN, a NaN row of q is, and the rest are as without either."""
+    bt = _paged.Batch([90, 5], [30, 0], 64, 106, spare=7)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 64, 512, fmt, 16, 3, 107)
+    want, _ = _attend(bt, q, pool, sc, sink, 0.05, 16, 3)
+    want = want.clone()
+    pool.view(-1, pool.shape[2])[bt.row(0, 60)] = float("nan") if sc is None else 0x7F
+    q[[33, 80, 91], 11], q[bt.live:] = float("nan"), float("nan")
+    got, _ = _attend(bt, q, pool, sc, sink, 0.05, 16, 3)
+    at = bt.positions().to(dev)
+    nan = torch.zeros(bt.live, 64, dtype=torch.bool, device=dev)
+    nan[:90][(at[:90] >= 60) & (at[:90] < 76)] = True
+    nan[[33, 80, 91], 11] = True
+    assert got[nan].isnan().all() and torch.equal(got[~nan], want[~nan])
