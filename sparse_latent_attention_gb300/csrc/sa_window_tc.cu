@@ -806,7 +806,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         drain_q();
     } else if (kCodes && warp >= kWarpWiden && warp < kWarpWiden + 16) {
         // ------------------------------------------------------------------ rows of codes: K (eight warps) and V (eight)
-        // Four warps of either take the even stages of a task, four the odd.
+        // Four warps of either take the even stages of the ring, four the odd, whichever task they belong to: a warp has a
+        // stage's every use, so that the use before has been let go when it waits for this one's turn.  (By stages of a
+        // task, the odd four had none of a task of one block, ran up to four tasks ahead, and took a stage whose last
+        // use but one was still to come for free: a wait tells a phase from the next, not from the one after.)
         if constexpr (kCodes) {
             constexpr bool k8 = kFmt == SA_KV_FP8_E4M3;
             const bool is_v = warp >= kWarpWiden + 8;
@@ -837,9 +840,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                 // Stage `put`'s copies go out before `n`, the last but one, is widened, but with a stage to be widened
                 // they do not wait for their place: the product that frees it may need that stage (where rows of V
                 // are cleared, all of a tile's before its first is used).
-                int put = turn;
+                const int n0 = (turn ^ (int)seq) & 1;
+                int put = n0;
 #pragma unroll 1
-                for (int n = turn; n < stages; n += 2) {
+                for (int n = n0; n < stages; n += 2) {
                     while (put < stages && put <= n + 2) {
                         const uint32_t gi = (g + (put >> 2)) % kInfos, m = seq + put, e = smem_addr(&empty[m % kRing]);
                         if (put > n && !__all_sync(0xffffffffu, mbar_test_wait(e, ((m / kRing) ^ 1u) & 1u))) break;
@@ -873,7 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                     if (is_v && rank != 0) warp_arrive(full[st], lane);
                     warp_arrive_leader(full[st], lane);
                 }
-                if (is_v && turn && (stages & 3) == 1 && ok) {  // (a last tile of one block has no odd stage)
+                if (is_v && n0 && (stages & 3) == 1 && ok) {  // (a last tile of one block has no second stage)
                     const uint32_t last = g + nt - 1, gi = last % kInfos;
                     ok = wait_here(smem_addr(&M.info_full[gi]), last / kInfos, abort);
                     warp_arrive(M.info_empty[gi], lane);

@@ -714,3 +714,18 @@ def test_window_attn_q_and_rows_that_are_not_finite(dev, fmt):  # noqa: F811
     nan[:90][(at[:90] >= 60) & (at[:90] < 76)] = True
     nan[[33, 80, 91], 11] = True
     assert got[nan].isnan().all() and torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("h", [16, 64, 128])
+@pytest.mark.parametrize("held", [(10, 0, 40, 130), (200, 31, 5, 0, 100, 9), (600, 20, 20, 20, 20, 700)])
+def test_window_attn_tasks_of_few_blocks(dev, held, h, fmt):  # noqa: F811
+    """Tasks of one block between others of two and more, many for each pair of SMs: the roles run ahead of one another
+    by as many tasks as they may."""
+    rng = torch.Generator().manual_seed(108)
+    at = torch.randint(0, len(held), (900,), generator=rng).tolist()
+    bt = _paged.Batch([1] * len(at), [held[i] for i in at], 32, 109)
+    q, sink, pool, sc = _attn_inputs(dev, bt, h, 512, fmt, 100, 3, 110)
+    first = _check_attn(bt, q, pool, sc, sink, 100, 3).clone()
+    for _ in range(10):
+        assert torch.equal(_attend(bt, q, pool, sc, sink, 512 ** -0.5, 100, 3)[0], first)

@@ -4,6 +4,9 @@ and every refusal before anything is enqueued."""
 from __future__ import annotations
 
 import ctypes
+import os
+import random
+import re
 
 import pytest
 import torch
@@ -212,3 +215,24 @@ def test_tensors_elsewhere_are_refused(calls, monkeypatch, name, kw):  # noqa: F
     with pytest.raises((TypeError, ValueError)):
         SERVE[name](**kw)
     assert not calls["calls"]
+
+
+def test_the_widening_warps_stages():
+    """window_attn over codes: a warp that widens waits by a phase's parity for a stage of the ring of four, which is
+    safe only where it knows that the stage's use before the last has ended: where it had that use itself, and waited for
+    its turn then.  So whatever blocks the tasks have, a stage's uses are all of one set of warps.  (Which stages of a task
+    a set has is the source's expression.)"""
+    with open(os.path.join(build.CSRC, "sa_window_tc.cu")) as f:
+        source = f.read()
+    start = re.search(r"const int n0 = ([^;]+);\s*int put = n0;.*?for \(int n = n0; n < stages; n \+= 2\)", source, re.S)
+    assert start
+    start = compile(start[1].replace("(int)", ""), "n0", "eval")
+    rng = random.Random(1)
+    for _ in range(50):
+        seq, owner = 0, {}
+        for _ in range(100):
+            stages = rng.choice([0, 1, 1, 2, 3, 4, 5, 9])
+            for turn in (0, 1):
+                for n in range(eval(start, {"turn": turn, "seq": seq}), stages, 2):
+                    assert owner.setdefault((seq + n) % 4, turn) == turn, (seq, n)
+            seq += stages
