@@ -107,7 +107,7 @@ struct Misc {
     uint64_t info_full[kInfos], info_empty[kInfos];  // (info_empty: codes)
     uint64_t task_full[kTasks], task_empty[kTasks];
     uint64_t stats_full, stats_empty;
-    uint64_t pair_bar[2][2], m_full[4], sum_full[2], sum_empty[2], done;
+    uint64_t pair_bar[2][2], mx_empty[2][2], m_full[4], sum_full[2], sum_empty[2], done;
     uint32_t tmem_base;
     int abort;
     int base[kInfos][kTileBlocks];    // first position of a tile's blocks: -1 no page, -2 no block
@@ -184,6 +184,10 @@ static __device__ __noinline__ bool wait_for(uint32_t bar, uint32_t parity, vola
 }
 __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, wait_for(smem_addr(&bar), parity, abort));
+}
+// The same for a phase that has most likely completed long ago: looked at in line first.
+__device__ __forceinline__ bool wait_done(uint64_t& bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_test_wait(smem_addr(&bar), parity & 1)) || wait(bar, parity, abort);
 }
 // One arrival for a converged warp, after what every lane did.
 __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane) {
@@ -520,6 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&M.pair_bar[b][0]), 2);
             mbar_init(smem_addr(&M.pair_bar[b][1]), 2);
+            mbar_init(smem_addr(&M.mx_empty[b][0]), 2);
+            mbar_init(smem_addr(&M.mx_empty[b][1]), 2);
             mbar_init(smem_addr(&M.sum_full[b]), 2 * kEpilogues);
             mbar_init(smem_addr(&M.sum_empty[b]), 2 * kEpilogues);
             mbar_init(smem_addr(&M.p_full[b]), 8);
@@ -972,10 +978,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
                     bad1 = base1 == -2 ? 0u : bad1 & ~seen(p.window, p.first, base1, t.pos0, t.pmax);
                 }
                 if constexpr (kCodes) warp_arrive(M.info_empty[gi], lane);
+                // (the partner may be a tile behind, and still has to read this warp's last maxima)
+                if (!(ok = wait_done(M.mx_empty[grp][w & 1], (g >> 1) ^ 1u, abort))) break;
                 M.mx[b][me] = mt;
                 warp_arrive(M.pair_bar[grp][w & 1], lane);
                 if (!(ok = wait(M.pair_bar[grp][w & 1], g >> 1, abort))) break;
                 mt = fmaxf(mt, M.mx[b][me ^ 64]);
+                warp_arrive(M.mx_empty[grp][w & 1], lane);
                 // P's buffer is free once the P.V two tiles back has completed
                 if (!(ok = wait(M.p_empty[b], (g >> 1) ^ 1u, abort))) break;
                 // the running maximum before this tile, and after it: raised only where a logit exceeds it by more

@@ -236,3 +236,60 @@ def test_the_widening_warps_stages():
                 for n in range(eval(start, {"turn": turn, "seq": seq}), stages, 2):
                     assert owner.setdefault((seq + n) % 4, turn) == turn, (seq, n)
             seq += stages
+
+
+def _interleavings(program, tiles, count):
+    """Whether two warps that run `program` for each of some tiles always read the other's value of the same tile: every
+    order of their steps is tried.  A step: ("write",), ("read",), ("arrive", barrier) or ("wait", barrier, flip), a wait
+    for the phase with the parity of the tile's number, flipped or not; a barrier's phase has `count` arrivals."""
+    bars = sorted({s[1] for s in program if len(s) > 1})
+    seen, todo = set(), [((0, 0), (-1, -1), (0,) * len(bars))]
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        at, slot, arrived = state
+        moved = False
+        for me in (0, 1):
+            if at[me] == tiles * len(program):
+                continue
+            tile, step = divmod(at[me], len(program))
+            step, slots, counts = program[step], list(slot), list(arrived)
+            if step[0] == "write":
+                slots[me] = tile
+            elif step[0] == "read":
+                if slot[1 - me] != tile:
+                    return False
+            elif step[0] == "arrive":
+                counts[bars.index(step[1])] += 1
+            elif (arrived[bars.index(step[1])] // count) % 2 == (tile + step[2]) % 2:
+                continue                              # (the phase at hand has the parity that is waited for)
+            moved = True
+            todo.append((tuple(a + (i == me) for i, a in enumerate(at)), tuple(slots), tuple(counts)))
+        assert moved or at == (tiles * len(program),) * 2, f"both warps wait: {at}"
+    return True
+
+
+def test_the_maxima_that_two_warps_trade():
+    """window_attn's softmax: a row's two halves, in two warps, trade their maxima through shared memory tile by tile.
+    The steps are those of the source, in its order; neither warp may overwrite a maximum that the other has yet to
+    read, however far it is ahead."""
+    with open(os.path.join(build.CSRC, "sa_window_tc.cu")) as f:
+        source = f.read()
+    part = source[source.index("- softmax\n"):source.index("- epilogue\n")]
+    step = re.compile(r"M\.mx\[b\]\[(me|me \^ 64)\]( = )?"
+                      r"|(arrive|wait\w*)\(M\.(\w+)\[grp\]\[w & 1\], (lane|g >> 1|\(g >> 1\) \^ 1u)[,)]")
+    program = []
+    for m in step.finditer(part):
+        if m[1]:
+            assert (m[1] == "me") == bool(m[2])
+            program.append(("write",) if m[2] else ("read",))
+        else:
+            program.append(("arrive", m[4]) if m[3] == "arrive" else ("wait", m[4], int("^" in m[5])))
+    for bar in {s[1] for s in program if len(s) > 1}:
+        assert re.findall(rf"mbar_init\(smem_addr\(&M\.{bar}\[b\]\[\d\]\), (\d+)\)", source) == ["2", "2"], bar
+    assert program.count(("write",)) == program.count(("read",)) == 1
+    assert _interleavings(program, 5, 2)
+    # (without the wait for the reader, one warp's next maximum may come first)
+    assert not _interleavings([("write",), ("arrive", "a"), ("wait", "a", 0), ("read",)], 5, 2)
