@@ -41,6 +41,7 @@ typedef enum {
  *            for its block's scale.
  * The sums, the factor and y are f32 with what f32 drops carried along beside them, and y is rounded once, to
  * its type, so that a value next to the border of two codes falls on its side.
+ * Rows whose squares are below or beyond f32 are normed like any other; a row of zeros with eps = 0 gives NaN.
  *
  * Arguments
  *   x        bf16, row i at x + i * x_stride elements

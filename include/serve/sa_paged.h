@@ -50,6 +50,7 @@ extern "C" {
  *            Infinities saturate; a NaN does not count for the scale, and stays one in 8 bits and is a 0 in 4.
  * y is formed with what f32 loses carried along and is rounded once, to its type, so that a value next to the
  * border of two codes falls on its side.
+ * Rows whose squares are below or beyond f32 are normed like any other; a row of zeros with eps = 0 gives NaN.
  *
  * Arguments
  *   x          bf16, token t's row at x + t * x_stride elements

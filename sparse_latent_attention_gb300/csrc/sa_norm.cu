@@ -116,12 +116,24 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < kPer; ++i) top = fmaxf(top, largest8(h[i]));
     }
-    Squares<4 * kPer> sum(top);
+    Two r;
+    float scale = 1.f;
+    for (;;) {  // (a second time where the row's squares leave f32's range)
+        Squares<4 * kPer> sum(top);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum.add(tc::f2(h[i][2 * k], h[i][2 * k + 1]));
-    const Two r = inverse_rms(kWarpRow ? warp_sum(sum.total()) : block_sum(sum.total(), part), p.of);
+            for (int k = 0; k < 4; ++k) sum.add(tc::f2(h[i][2 * k], h[i][2 * k + 1]));
+        r = add_scaled(kWarpRow ? warp_sum(sum.total()) : block_sum(sum.total(), part), p.of.shift, scale);
+        if (scale != 1.f || (scale = rescaling(r)) == 1.f) break;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[i][k] *= scale;
+        top *= scale;
+        if (!kWarpRow) __syncthreads();  // (every warp has read the parts)
+    }
+    r = inverse_rms(r, p.of);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int c = me + i * width;
@@ -180,14 +192,27 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
         if constexpr (kRes == SA_RESIDUAL_F32) res32[k] = h = h + res32[k];
         sum = add(sum, mul(h, Two{h, 0.f}));
     }
-    const Two r = inverse_rms(block_sum(sum, part), p.of);
+    auto held = [&](int k) {
+        return kRes == SA_RESIDUAL_BF16 ? __bfloat162float(res16[k]) : kRes == SA_RESIDUAL_F32 ? res32[k] : __bfloat162float(x[k]);
+    };
+    Two r = add(block_sum(sum, part), p.of.shift);
+    float scale = 1.f;
+    if (leaves_range(r)) {  // (the whole row)
+        scale = rescaling(r);
+        sum = {0.f, 0.f};
+        for (int k = threadIdx.x; k < p.d; k += blockDim.x) {
+            const float h = held(k) * scale;
+            sum = add(sum, mul(h, Two{h, 0.f}));
+        }
+        __syncthreads();  // (every warp has read the parts)
+        r = add_scaled(block_sum(sum, part), p.of.shift, scale);
+    }
+    r = inverse_rms(r, p.of);
     for (int k0 = threadIdx.x & ~31; k0 < p.d; k0 += blockDim.x) {  // (a warp's 32 elements)
         const int lane = threadIdx.x & 31, k = k0 + lane;
         float y = 0.f;
         if (k < p.d) {
-            const float h = kRes == SA_RESIDUAL_BF16  ? __bfloat162float(res16[k])
-                            : kRes == SA_RESIDUAL_F32 ? res32[k]
-                                                      : __bfloat162float(x[k]);
+            const float h = held(k) * scale;
             const Two v = mul(mul(h, r), p.weight[k]);
             const float a[8] = {v.h}, b[8] = {v.l};
             float c[8] = {v.h + v.l};

@@ -98,19 +98,35 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(cons
                                      largest_pair(in[r][i].z, in[r][i].w));
             large = largest_pair(large, large << 16);
         }
-        Squares<4 * kPer> sum(__uint_as_float(large));
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             float e[8];
             unpacked8(in[r][i], e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[i][j] = tc::f2(e[2 * j], e[2 * j + 1]);
-                if (p.weight) sum.add(v[i][j]);
-            }
+            for (int j = 0; j < 4; ++j) v[i][j] = tc::f2(e[2 * j], e[2 * j + 1]);
         }
         Two f = {1.f, 0.f};
-        if (p.weight) f = inverse_rms(warp_sum(sum.total()), p.of);
+        float scale = 1.f;
+        if (p.weight) {
+            auto squares = [&](float largest) {
+                Squares<4 * kPer> sum(largest);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sum.add(v[i][j]);
+                return warp_sum(sum.total());
+            };
+            f = add(squares(__uint_as_float(large)), p.of.shift);
+            if (leaves_range(f)) {
+                scale = rescaling(f);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], tc::f2(scale, scale));
+                f = add_scaled(squares(__uint_as_float(large & 0x7FFFFFFFu) * scale), p.of.shift, scale);
+            }
+            f = inverse_rms(f, p.of);
+        }
         const uint64_t fh = tc::f2(f.h, f.h), fn = tc::f2(-f.h, -f.h), fl = tc::f2(f.l, f.l);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -172,8 +188,8 @@ __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(cons
                     if (e < 0) continue;
                     float a = x[2 * j], b = x[2 * j + 1];
                     if (p.weight) {
-                        a = __fmul_rn(__fmul_rn(a, f.h), __ldg(p.weight + 8 * c + 2 * j));
-                        b = __fmul_rn(__fmul_rn(b, f.h), __ldg(p.weight + 8 * c + 2 * j + 1));
+                        a = __fmul_rn(__fmul_rn(a * scale, f.h), __ldg(p.weight + 8 * c + 2 * j));
+                        b = __fmul_rn(__fmul_rn(b * scale, f.h), __ldg(p.weight + 8 * c + 2 * j + 1));
                     }
                     auto lost = [&](float m, float y, float sum) {  // a m + y - sum
                         const float q = __fmul_rn(a, m);

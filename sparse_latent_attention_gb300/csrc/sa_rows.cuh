@@ -130,11 +130,26 @@ inline RmsOf rms_of(int d, float eps) {
     return {two((double)d * (double)eps), two(sqrt((double)d))};
 }
 
-// The factor of a row with this sum of squares: the hardware's estimate r0 of v^(-1/2) and one step of Newton's
-// iteration, whose correction r0 (1 - v r0^2) / 2 is formed from exact products and kept as the second part.  A sum
-// that overflowed or is a NaN gives what the estimate gives (0, NaN).
-__device__ __forceinline__ Two inverse_rms(Two sum, const RmsOf& of) {
-    const Two v = add(sum, of.shift);
+// The power of two to scale a row by, and to sum its squares again, where they leave what f32 holds, from their sum with
+// d eps (1: they do not): below 2^-80 what f32 drops of a square may be more than its second part, and from some 2^128 on
+// there is an infinity in place of the sum.  Scaled by 2^96, rows of sums below 2^-80 have squares of 2^-106 to 2^112;
+// by 2^-72, the largest of 32768 elements up to 2^127, and what the smallest of them lose is below what y holds.
+// (In range, or a NaN: one comparison of the bits.)
+__device__ __forceinline__ bool leaves_range(Two v) {
+    return __float_as_uint(v.h) - __float_as_uint(0x1p-80f) >= __float_as_uint(INFINITY) - __float_as_uint(0x1p-80f);
+}
+__device__ __forceinline__ float rescaling(Two v) {
+    return v.h < 0x1p-80f ? 0x1p96f : v.h == INFINITY ? 0x1p-72f : 1.f;
+}
+// sum + d eps of a row that was scaled.
+__device__ __forceinline__ Two add_scaled(Two sum, Two shift, float scale) {
+    return add(sum, {shift.h * scale * scale, shift.l * scale * scale});
+}
+
+// The factor of a row with this mean square (times d): the hardware's estimate r0 of v^(-1/2) and one step of Newton's
+// iteration, whose correction r0 (1 - v r0^2) / 2 is formed from exact products and kept as the second part.  A row of
+// zeros without an eps, of infinities or NaN gives what the estimate gives (infinity, 0, NaN).
+__device__ __forceinline__ Two inverse_rms(Two v, const RmsOf& of) {
     const float r0 = rsqrtf(v.h);
     if (!(r0 > 0.f && r0 < INFINITY)) return {r0, 0.f};
     const float t = __fmul_rn(r0, r0), tl = fmaf(r0, r0, -t);

@@ -169,3 +169,44 @@ def test_graph_and_stream(dev):  # noqa: F811
         res.copy_(r2)
         graph.replay()
         _check(x, w, r2, res, out, None, None)
+
+
+def _far_rows(dev, d):  # noqa: F811
+    """f32 rows whose squares, or the sum of them, are below or beyond what f32 holds."""
+    g = torch.Generator(device=dev).manual_seed(d)
+    z = torch.randn(12, d, device=dev, generator=g)
+    for i, m in enumerate((1e-12, 1e-18, 1e-21, 3e-23, 1e-30, 1e-37, 2e-38, 1e20, 1e25, 6e37)):
+        z[i] *= m
+    z[9].clamp_(-3e38, 3e38)
+    z[10] *= torch.where(torch.arange(d, device=dev) % 3 == 0, 1e22, 1.0)   # large ones, and others beside them
+    z[11] = 0.0
+    z[11, d // 2] = 4e-39                                                   # one element, below the smallest normal
+    return z
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-30, EPS])
+@pytest.mark.parametrize("kind", ["none", "bf16", "f32"])
+@pytest.mark.parametrize("d,pad", [(64, 0), (512, 0), (1024, 0), (4096, 0), (8192, 0), (32768, 0), (512, 1), (33, 0)])
+def test_squares_outside_f32(dev, d, pad, kind, eps):  # noqa: F811
+    """Rows of any magnitude, with an eps that is none, or less than they are: y is the formula's."""
+    z = _far_rows(dev, d)
+    eps = float(torch.tensor(eps))
+    w = torch.linspace(0.5, 1.5, d, device=dev)
+    wide = torch.zeros(12, d + pad, dtype=torch.bfloat16, device=dev)[:, :d]
+    r = None
+    if kind == "none":
+        wide.copy_(z)
+    else:
+        r = z.to(torch.bfloat16) if kind == "bf16" else z
+    res = None if r is None else r.clone()
+    out = sa.add_rms_norm(wide, w, residual=res, eps=eps)
+    _check(wide, w, r, res, None, None, None)
+    y = _paged.norm(wide if r is None else res, w, eps)
+    # (bf16's smallest number is 2^-133: below the normal ones a rounding is off by up to 2^-134)
+    assert ((out.double() - y).abs() <= (2.0 ** -8 + _paged.NORM_REL) * y.abs() + 2.0 ** -134).all()
+    if d % 32 == 0:
+        codes = torch.empty(12, d, dtype=torch.uint8, device=dev)
+        scales = torch.empty(12, d // 32, dtype=torch.uint8, device=dev)
+        res = None if r is None else r.clone()
+        sa.add_rms_norm(wide, w, residual=res, eps=eps, codes=codes, scales=scales)
+        _check(wide, w, r, res, None, codes, scales, eps=eps)

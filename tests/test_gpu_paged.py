@@ -9,6 +9,7 @@ import sparse_latent_attention_gb300 as sa
 from sparse_latent_attention_gb300._lib import SA_ERR_INDEX, SA_STATUS_BYTES
 from tests import _cache, _paged
 from tests.test_gpu_cache import dev  # noqa: F401 (a fixture)
+from tests.test_gpu_norm import _far_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -729,3 +730,27 @@ def test_window_attn_tasks_of_few_blocks(dev, held, h, fmt):  # noqa: F811
     first = _check_attn(bt, q, pool, sc, sink, 100, 3).clone()
     for _ in range(10):
         assert torch.equal(_attend(bt, q, pool, sc, sink, 512 ** -0.5, 100, 3)[0], first)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-44, EPS])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("d,pad", [(64, 0), (512, 0), (1024, 0), (512, 1)])
+def test_page_write_squares_outside_f32(dev, d, pad, fmt, eps):  # noqa: F811
+    """Rows whose squares are below or beyond what f32 holds, and an eps that is none, or less than they are."""
+    eps = float(torch.tensor(eps))
+    bt = _paged.Batch([12], [5], 16, 111)
+    x = torch.zeros(12, d + pad, dtype=torch.bfloat16, device=dev)[:, :d].copy_(_far_rows(dev, d))
+    w, rot = torch.linspace(0.5, 1.5, d, device=dev), _paged.rotations(17, 64).to(dev)
+    pages, codes, scales = _pools(dev, bt, d, None if fmt == "bf16" else fmt, 112)
+    before = [None if t is None else t.clone() for t in (pages, codes, scales)]
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, codes=codes, scales=scales, weight=w, eps=eps)
+    y = _paged.norm(x, w, eps)
+    _check_rows(bt, y, pages, codes, scales, None if fmt == "bf16" else fmt, before, _paged.NORM_REL)
+    # (turned: a pair that cancels keeps an error relative to its length)
+    sa.page_write(x, bt.table, bt.q_start, bt.kv_len, pages=pages, weight=w, eps=eps, rope=rot)
+    turned = _paged.turned(y, rot, bt.positions().to(dev))
+    size = y.clone()
+    size[:, -64:] = y[:, -64:].unflatten(1, (32, 2)).norm(dim=-1, keepdim=True).expand(-1, -1, 2).flatten(1)
+    got = pages.flatten(0, 1)[bt.rows().to(dev)].double()
+    # (and below bf16's normal numbers a rounding is off by up to 2^-134)
+    assert ((got - turned).abs() <= 2.0 ** -8 * turned.abs() + _paged.NORM_REL * size.abs() + 2.0 ** -134).all()
