@@ -805,7 +805,7 @@ def _rotation(rope, dev, like):
 
 
 def window_workspace_size(n, b, h, d, window, first, page, kv_format=SA_KV_BF16) -> int:
-    """Bytes of workspace that window_attn needs for n tokens of b sequences."""
+    """Bytes of workspace that window_attn needs for any batch of at most n tokens of b sequences."""
     size = int(load().sa_window_attn_workspace_size(n, b, h, d, window, first, page, kv_format))
     if size == 0:
         raise SparseAttnError(_lib.SA_ERR_UNSUPPORTED, "sa_window_attn_workspace_size")

@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "sa_fp4.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.cuh"
@@ -442,6 +444,7 @@ __global__ void lse_of_sinks_kernel(float* lse, const float* sink, int64_t n, in
 
 struct Geometry {
     int n_tiles, n_splits, tiles_per_split, hblocks;
+    int most;  // n_splits, and those of any fewer entries, are no more
 };
 
 // The idx columns of a token are split over several CTAs when the tokens alone would not give
@@ -458,6 +461,7 @@ Geometry geometry(int64_t n_tokens, int h, int topk, int sms) {
         splits = (int)((kTargetCtas + base - 1) / base);
         if (splits > g.n_tiles) splits = g.n_tiles;
     }
+    g.most = splits;
     g.tiles_per_split = splits > 1 ? (g.n_tiles + splits - 1) / splits : (g.n_tiles > 0 ? g.n_tiles : 1);
     g.n_splits = splits > 1 ? (g.n_tiles + g.tiles_per_split - 1) / g.tiles_per_split : 1;
     return g;
@@ -507,6 +511,15 @@ size_t attn_mma_scratch_bytes(int64_t b, int64_t s, int h, int d, int topk) {
     const size_t ml = align_up(ntok * g.n_splits * h * 2 * sizeof(float), 256);
     const size_t po = ntok * g.n_splits * h * (size_t)d * sizeof(float);
     return ml + po;
+}
+
+size_t attn_mma_scratch_bound(int64_t n, int h, int d, int topk) {
+    size_t rows = 0;  // of partials: of some entries fewer the splits may come out as many as were asked for
+    for (int64_t k = 1; k <= n && k < 2 * kMaxSmCount; ++k) {  // (of more tokens there is one)
+        const Geometry g = geometry(k, h, topk, kMaxSmCount);
+        if (g.most > 1) rows = std::max(rows, (size_t)k * g.most * h);
+    }
+    return align_up(rows * 2 * sizeof(float), 256) + rows * (size_t)d * sizeof(float);
 }
 
 cudaError_t attn_mma_launch(const AttnCall& c) {

@@ -56,6 +56,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "sa_fp4.cuh"
@@ -1317,6 +1318,7 @@ void (*const kKernels[3][2][2])(const CUtensorMap, Params) = {
 
 struct TcGeometry {
     int n_tiles, hblocks, n_splits, tiles_per_split;
+    int most;  // n_splits, and those of any fewer entries, are no more
 };
 
 // Split the idx columns of a token over several tasks only when the tokens alone cannot fill
@@ -1334,6 +1336,7 @@ TcGeometry tc_geometry(int64_t n_tokens, int h, int topk, int sms) {
         if (splits > pairs) splits = pairs;
         if (splits < 1) splits = 1;
     }
+    g.most = splits;
     if (splits > 1) {
         g.tiles_per_split = 2 * ((pairs + splits - 1) / splits);
         g.n_splits = (g.n_tiles + g.tiles_per_split - 1) / g.tiles_per_split;
@@ -1410,6 +1413,15 @@ size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk) {
     const size_t ntok = (size_t)(b * s);
     const size_t ml = align_up(ntok * g.n_splits * h * 2 * sizeof(float), 256);
     return ml + ntok * g.n_splits * h * (size_t)kD * sizeof(float);
+}
+
+size_t attn_tc_scratch_bound(int64_t n, int h, int topk) {
+    size_t rows = 0;  // of partials: of some entries fewer the splits may come out as many as were asked for
+    for (int64_t k = 1; k <= n && k < kMaxSmCount; ++k) {  // (of more tokens there is one)
+        const TcGeometry g = tc_geometry(k, h, topk, kMaxSmCount);
+        if (g.most > 1) rows = std::max(rows, (size_t)k * g.most * h);
+    }
+    return align_up(rows * 2 * sizeof(float), 256) + rows * (size_t)kD * sizeof(float);
 }
 
 cudaError_t attn_tc_launch(const AttnCall& c) {

@@ -73,6 +73,8 @@ cudaError_t lse_of_sinks_launch(float* lse, const float* sink, int64_t n_tokens,
 
 // mma.sync family (sa_attn_mma.cu)
 size_t attn_mma_scratch_bytes(int64_t b, int64_t s, int h, int d, int topk);
+// no call of 1 to n tokens and at most topk entries takes more (fewer of either may be cut into more splits)
+size_t attn_mma_scratch_bound(int64_t n, int h, int d, int topk);
 cudaError_t attn_mma_launch(const AttnCall& c);
 // merge of split partials: part_ml [tokens][splits][h][2] (max in log2 units, sum),
 // part_o [tokens][splits][h][d] f32 -> o bf16, and lse unless it is nullptr; n_live as AttnCall's
@@ -85,6 +87,7 @@ cudaError_t attn_combine_launch(const float* part_ml, const float* part_o, const
 // d = 512, every kv format
 bool attn_tc_supports(int h, int d, int kv_format, int64_t b, int64_t rows);
 size_t attn_tc_scratch_bytes(int64_t b, int64_t s, int h, int topk);
+size_t attn_tc_scratch_bound(int64_t n, int h, int topk);
 cudaError_t attn_tc_launch(const AttnCall& c);
 
 // The TMA map of n bf16 rows of d, in boxes of [box_rows x 64] with the 128-byte swizzle; false when the

@@ -309,7 +309,7 @@ bool window_supported(int64_t n, int h, int d) {
     return h <= 128 && d >= 64 && d <= 512 && d % 64 == 0 && n < k31 && n * (int64_t)h < k31;
 }
 
-// The workspace: the status word and the scratch of the kernels that the call is routed to, then, of those that
+// The workspace of a call: the status word and the scratch of the kernels that the call is routed to, then, of those that
 // gather by row, the index table and positions.
 struct Parts {
     size_t idx, pos, all;
@@ -429,7 +429,15 @@ extern "C" size_t sa_window_attn_workspace_size(int64_t n, int64_t b, int h, int
     using namespace sa;
     if (!kv_format_known(kv_format) || !window_shape(n, b, h, d, window, first, page) || !window_supported(n, h, d))
         return 0;
-    return parts_of(n, b, h, d, window, first, page, kv_format).all;
+    if (n < 1) n = 1;
+    if (window_tc_supports(d, kv_format, page))
+        return SA_STATUS_BYTES + align_up(window_tc_scratch_bound(n, h, window, first), 256);
+    const int topk = (int)(first + window);
+    const size_t scratch = routed_family(SA_FAMILY_AUTO, h, d, kv_format, 1, 0) == SA_FAMILY_TCGEN05
+                               ? attn_tc_scratch_bound(n, h, topk)
+                               : attn_mma_scratch_bound(n, h, d, topk);
+    return align_up(SA_STATUS_BYTES + align_up(scratch, 256), 256) + align_up((size_t)n * topk * sizeof(int32_t), 256) +
+           align_up((size_t)n * sizeof(int32_t), 256);
 }
 
 extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t* kv_scale, int kv_format,

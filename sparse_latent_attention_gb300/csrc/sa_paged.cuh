@@ -89,6 +89,8 @@ struct WindowCall {
 // Pairs of SMs over whole blocks of positions (sa_window_tc.cu): d = 512, pages of a multiple of 32 rows.
 bool window_tc_supports(int d, int kv_format, int page);
 size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int64_t first);
+// no call of 1 to n tokens, and of a smaller window and first, takes more
+size_t window_tc_scratch_bound(int64_t n, int h, int64_t window, int64_t first);
 cudaError_t window_tc_launch(const WindowCall& c);
 
 }  // namespace sa

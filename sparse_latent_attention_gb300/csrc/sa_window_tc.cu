@@ -1243,6 +1243,14 @@ size_t window_tc_scratch_bytes(int64_t n, int64_t b, int h, int64_t window, int6
     return s == 1 ? 0 : align_up((size_t)n * s * h * 2 * sizeof(float), 256) + (size_t)n * s * h * kD * sizeof(float);
 }
 
+size_t window_tc_scratch_bound(int64_t n, int h, int64_t window, int64_t first) {
+    // (of one sequence, which has the fewest tiles: as many parts only from as few tiles, and of those the most tokens)
+    size_t most = 0;
+    for (int s = 2; s <= 64 && 2 * s <= kMaxSmCount; ++s)
+        most = std::max(most, window_tc_scratch_bytes(std::min<int64_t>(n, kMaxSmCount / 2 / s * kM / h), 1, h, window, first));
+    return most;
+}
+
 cudaError_t window_tc_launch(const WindowCall& c) {
     const int sms = device_sm_count();
     // Q: 64 rows x two blocks of 64 d, block by block.  V: 32 rows x four blocks of 64 d, block by block.  K: 32

@@ -754,3 +754,17 @@ def test_page_write_squares_outside_f32(dev, d, pad, fmt, eps):  # noqa: F811
     got = pages.flatten(0, 1)[bt.rows().to(dev)].double()
     # (and below bf16's normal numbers a rounding is off by up to 2^-134)
     assert ((got - turned).abs() <= 2.0 ** -8 * turned.abs() + _paged.NORM_REL * size.abs() + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("d,page", [(512, 64), (512, 16), (128, 64)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_window_attn_one_workspace_for_all_batches(dev, fmt, d, page):  # noqa: F811
+    """A workspace made for the largest batch serves the smaller ones, whose positions are cut into parts."""
+    kind = sa.SA_KV_BF16 if fmt == "bf16" else sa.SA_KV_FP8_E4M3
+    ws = sa.new_window_workspace(150, 150, 64, d, 2000, 8, page, kind)
+    for n in (150, 1, 40, 2, 9, 150):
+        bt = _paged.Batch([1] * n, [(977 * i + 2500) % 4000 for i in range(n)], page, 113 + n)
+        q, sink, pool, sc = _attn_inputs(dev, bt, 64, d, fmt, 2000, 8, 114)
+        o = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 2000, first=8, kv_scale=sc, workspace=ws)
+        want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 2000, 8)
+        assert sa.read_status(ws) == 0 and ((o.double() - want).abs() <= tol).all()

@@ -293,3 +293,25 @@ def test_the_maxima_that_two_warps_trade():
     assert _interleavings(program, 5, 2)
     # (without the wait for the reader, one warp's next maximum may come first)
     assert not _interleavings([("write",), ("arrive", "a"), ("wait", "a", 0), ("read",)], 5, 2)
+
+
+@pytest.mark.parametrize("fmt,d,page", [(0, 512, 64), (1, 512, 64), (2, 512, 32), (0, 512, 16), (1, 512, 1), (0, 256, 64),
+                                        (2, 64, 64)])
+@pytest.mark.parametrize("h", [1, 16, 64, 100, 128])
+def test_window_attn_workspace_of_the_largest_batch(lib, fmt, d, page, h):
+    """A workspace of the size for n tokens, b sequences, window and first is taken by every call of no more.  (The calls
+    stop at its misaligned address, which is looked at after its size.)"""
+    a = dict(q=at(1), kv=at(2), scale_ptr=at(9) if fmt else None, fmt=fmt, sink=at(3), table=at(4), max_pages=400, ts=400,
+             q_start=at(5), kv_len=at(6), scale=0.1, n=3, b=2, h=h, d=d, n_pages=1000, page=page, window=128, first=4, o=at(7),
+             lse=None, rot=None, npos=0, rope=0, ws=at(11, 64), ws_bytes=0)
+    for n, b, window, first in ((200, 200, 1024, 64), (400, 3, 333, 0), (7, 7, 4096, 128), (1, 1, 5000, 9)):
+        size = lib.sa_window_attn_workspace_size(n, b, h, d, window, first, page, fmt)
+        for m in {k for k in (1, 2, 3, n // 9, n // 5, n // 3, n // 2, n - 1, n) if 0 < k <= n}:
+            for seqs in {1, min(2, b), min(m, b)}:
+                for w, f in ((window, first), (window // 2 + 1, first), (window // 7 + 1, first // 2), (1, 0), (64, 0)):
+                    assert lib.sa_window_attn_workspace_size(m, seqs, h, d, w, f, page, fmt) <= size
+                    for pages in (400, 9, 1):
+                        a.update(n=m, b=seqs, window=w, first=f, max_pages=pages, ts=pages, ws_bytes=size)
+                        assert lib.sa_window_attn(*a.values(), None) == INVALID, (n, m, seqs, w, f, pages)
+    a.update(ws_bytes=size, ws=None)
+    assert lib.sa_window_attn(*a.values(), None) == WORKSPACE
