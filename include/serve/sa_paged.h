@@ -106,7 +106,10 @@ sa_status sa_page_write(const void* x, int64_t n, int d, int64_t x_stride, const
  *              first SA_STATUS_BYTES zeroed once by the caller, calls sharing one stream-ordered.  The size for n
  *              tokens and b sequences is enough for every batch of at most as many of either, and of a smaller
  *              window and first, at the same h, d, page and kv_format (a few tokens' positions are cut into parts
- *              over the GPU, so that the smaller batch may take more than the larger).
+ *              over the GPU, so that the smaller batch may take more than the larger).  A window that reaches
+ *              beyond the table's max_pages * page positions takes as much as one of so many with first = 0:
+ *              where d != 512 or pages are no multiple of 32 rows there are 4 bytes a token and position that
+ *              it may see.
  * o and lse must not overlap an input, the workspace or each other.
  * Supported: d a multiple of 64 in [64, 512]; 1 <= h <= 128; n * h, b, max_pages and n_pages * page < 2^31; at
  * d = 512 with pages of a multiple of 32 rows first + window or max_pages * page at most 2^24.

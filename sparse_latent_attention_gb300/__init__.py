@@ -805,7 +805,8 @@ def _rotation(rope, dev, like):
 
 
 def window_workspace_size(n, b, h, d, window, first, page, kv_format=SA_KV_BF16) -> int:
-    """Bytes of workspace that window_attn needs for any batch of at most n tokens of b sequences."""
+    """Bytes of workspace that window_attn needs for any batch of at most n tokens of b sequences.  (A window may
+    be given as the positions that the page table holds, with first 0, where it reaches beyond them.)"""
     size = int(load().sa_window_attn_workspace_size(n, b, h, d, window, first, page, kv_format))
     if size == 0:
         raise SparseAttnError(_lib.SA_ERR_UNSUPPORTED, "sa_window_attn_workspace_size")
@@ -865,7 +866,9 @@ def window_attn(q, pages, sink, page_table, q_start, kv_len, softmax_scale, wind
         lp = lse.data_ptr()
     turn, npos, rope_dim = _NO_POOL if rope is None else _rotation(rope, dev, q)
     if workspace is None:
-        workspace = _new(stream, lambda: new_window_workspace(n, b, h, d, window, first, page, fmt, q.device))
+        held = max(max_pages * page, 1)  # (positions beyond them need no room)
+        seen = min(window, held)
+        workspace = _new(stream, lambda: new_window_workspace(n, b, h, d, seen, min(first, held - seen), page, fmt, q.device))
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and workspace.get_device() == dev
               and workspace.is_contiguous()):
         _need(workspace, "workspace", _U8, q.device)

@@ -312,18 +312,19 @@ bool window_supported(int64_t n, int h, int d) {
 // The workspace of a call: the status word and the scratch of the kernels that the call is routed to, then, of those that
 // gather by row, the index table and positions.
 struct Parts {
+    int topk;  // entries of the index table
     size_t idx, pos, all;
 };
 
-Parts parts_of(int64_t n, int64_t b, int h, int d, int64_t window, int64_t first, int page, int kv_format) {
-    if (n < 1) n = 1;
+Parts parts_of(int64_t n, int64_t b, int h, int d, Reach seen, int page, int kv_format) {
     if (window_tc_supports(d, kv_format, page)) {
-        const size_t all = SA_STATUS_BYTES + align_up(window_tc_scratch_bytes(n, b, h, window, first), 256);
-        return {all, all, all};
+        const size_t all = SA_STATUS_BYTES + align_up(window_tc_scratch_bytes(n, b, h, seen.window, seen.first), 256);
+        return {0, all, all, all};
     }
-    const int topk = (int)(first + window);
+    const int topk = (int)(seen.first + seen.window);
     const int fam = routed_family(SA_FAMILY_AUTO, h, d, kv_format, 1, 0);
     Parts s;
+    s.topk = topk;
     s.idx = align_up(routed_workspace_bytes(fam, 1, n, h, d, 0, topk), 256);
     s.pos = s.idx + align_up((size_t)n * topk * sizeof(int32_t), 256);
     s.all = s.pos + align_up((size_t)n * sizeof(int32_t), 256);
@@ -469,7 +470,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
         !aligned(kv_scale, tc ? 16 : 4) || (window_tc_supports(d, kv_format, page) && !aligned(o, 32)) ||
         (b > 1 && table_stride < max_pages) || !spans(b, table_stride) || !spans(npos, rot ? rope_dim : 0))
         return SA_ERR_INVALID_ARG;
-    const Parts parts = parts_of(n, b, h, d, window, first, page, kv_format);
+    const Parts parts = parts_of(n, b, h, d, reach_of(window, first, max_pages, page), page, kv_format);
     const int64_t ob = 2 * n * h * d, rows = n_pages * page;
     const struct {
         const void* at;
@@ -521,14 +522,9 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     }
     int32_t* idx = reinterpret_cast<int32_t*>(ws + parts.idx);
     int32_t* pos = rot ? reinterpret_cast<int32_t*>(ws + parts.pos) : nullptr;
-    // no more entries than the table has positions, where the scratch of so many is not more (fewer entries may be cut into
-    // more parts): 116 tokens of 100 heads over some 60 e4m3 rows of 256 take 38 us, 158 with all entries of a window of 1133
-    const int64_t held = std::max<int64_t>(max_pages * page, 1);
-    const size_t scratch = parts.idx - SA_STATUS_BYTES;
-    int lead = (int)first, topk = (int)(first + window);
-    if (held < topk && (tc ? attn_tc_scratch_bytes(1, n, h, (int)held)
-                           : attn_mma_scratch_bytes(1, n, h, d, (int)held)) <= scratch)
-        lead = topk = (int)held;
+    // no more entries than the table has positions: 116 tokens of 100 heads over some 60 e4m3 rows of 256 take 38 us, 158 with
+    // all entries of a window of 1133
+    const int topk = parts.topk, lead = topk < first + window ? topk : (int)first;
     const int cols = (topk + 511) / 512 < 64 ? (topk + 511) / 512 : 64;
     cudaError_t e = launch_pdl(window_rows_kernel, dim3((unsigned)n, cols), dim3(128), 0, st, a, n, (int)window,
                                (int)first, lead, topk, idx, pos, npos, reinterpret_cast<uint32_t*>(ws));
@@ -550,7 +546,7 @@ extern "C" sa_status sa_window_attn(const void* q, const void* kv, const uint8_t
     c.o = o;
     c.status = reinterpret_cast<uint32_t*>(ws);
     c.scratch = ws + SA_STATUS_BYTES;
-    c.scratch_bytes = scratch;
+    c.scratch_bytes = parts.idx - SA_STATUS_BYTES;
     c.stream = st;
     c.rope = rot;
     c.rope_dim = rot ? rope_dim : 0;

@@ -64,6 +64,15 @@ __device__ __forceinline__ int64_t row_of(const Batch& a, int64_t seq, uint32_t 
 
 }  // namespace paged
 
+// What of a window and of first positions a table can hold: no more positions together than its own.
+struct Reach {
+    int64_t window, first;
+};
+inline Reach reach_of(int64_t window, int64_t first, int64_t max_pages, int page) {
+    const int64_t held = max_pages > 0 ? max_pages * page : 1, w = window < held ? window : held;
+    return {w, first < held - w ? first : held - w};
+}
+
 // A window_attn call, already validated.
 struct WindowCall {
     const void* q;

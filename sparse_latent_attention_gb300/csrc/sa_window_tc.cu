@@ -1280,9 +1280,9 @@ cudaError_t window_tc_launch(const WindowCall& c) {
     p.h = c.h;
     p.window = (int)c.window;
     p.first = (int)c.first;
-    // (no more parts than the table's positions make: the scratch is sized without it, for as many or more)
-    const int64_t held = std::max<int64_t>(c.a.max_pages * c.a.page, 1);
-    p.n_splits = window_splits(c.n, c.a.b, c.h, std::min(c.window, held), std::min(c.first, held), sms);
+    // (no more parts than the table's positions make)
+    const Reach seen = reach_of(c.window, c.first, c.a.max_pages, c.a.page);
+    p.n_splits = window_splits(c.n, c.a.b, c.h, seen.window, seen.first, sms);
     const int64_t units = (c.n * c.h / kM + c.a.b) * p.n_splits;
     if (units > INT32_MAX - kMaxSmCount) return cudaErrorInvalidConfiguration;  // (the kernel counts units in 32 bits)
     p.units = (int)units;

@@ -768,3 +768,14 @@ def test_window_attn_one_workspace_for_all_batches(dev, fmt, d, page):  # noqa: 
         o = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 2000, first=8, kv_scale=sc, workspace=ws)
         want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 2000, 8)
         assert sa.read_status(ws) == 0 and ((o.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("d,page", [(512, 64), (512, 16), (64, 64)])
+def test_window_attn_of_everything(dev, d, page, fmt):  # noqa: F811
+    """The largest window, its workspace made for the call: as large as the table's positions need."""
+    bt = _paged.Batch([300, 1], [0, 500], page, 115, 2)
+    q, sink, pool, sc = _attn_inputs(dev, bt, 16, d, fmt, 1000, 0, 116)
+    o = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, (1 << 30) - 9, first=8, kv_scale=sc)
+    want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 1000, 0)
+    assert ((o[:bt.live].double() - want).abs() <= tol).all()

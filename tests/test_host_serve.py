@@ -315,3 +315,18 @@ def test_window_attn_workspace_of_the_largest_batch(lib, fmt, d, page, h):
                         assert lib.sa_window_attn(*a.values(), None) == INVALID, (n, m, seqs, w, f, pages)
     a.update(ws_bytes=size, ws=None)
     assert lib.sa_window_attn(*a.values(), None) == WORKSPACE
+
+
+@pytest.mark.parametrize("fmt,d,page", [(0, 512, 64), (1, 512, 16), (0, 256, 64), (2, 64, 5)])
+@pytest.mark.parametrize("n,pages", [(3, 4), (4096, 8), (1, 400), (65536, 1), (7, 0)])
+def test_window_attn_workspace_of_the_tables_positions(lib, fmt, d, page, n, pages):
+    """A window beyond the page table's positions asks for no more than one of as many."""
+    a = dict(q=at(1), kv=at(2), scale_ptr=at(9) if fmt else None, fmt=fmt, sink=at(3), table=at(4), max_pages=pages, ts=pages,
+             q_start=at(5), kv_len=at(6), scale=0.1, n=n, b=1, h=16, d=d, n_pages=1000, page=page, window=1, first=0, o=at(7),
+             lse=None, rot=None, npos=0, rope=0, ws=at(11, 64), ws_bytes=0)
+    held = max(pages * page, 1)
+    a.update(ws_bytes=lib.sa_window_attn_workspace_size(n, 1, 16, d, held, 0, page, fmt))
+    for window, first in ((held, 5), (2 * held + 77, 0), (1 << 20, 1 << 20), ((1 << 30) - 9, 8), (1, 1 << 29)):
+        a.update(window=window, first=first)
+        assert lib.sa_window_attn(*a.values(), None) == INVALID, (window, first)   # (the workspace's address)
+    assert a["ws_bytes"] < 256 + (24 << 20) + n * (4 * held + 4) + 1024
