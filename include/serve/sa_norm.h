@@ -51,8 +51,9 @@ typedef enum {
  *   out      row i at out + i * out_stride elements; may equal x with the same stride (in place)
  *   codes, scales   row i at codes + i * codes_stride, scales + i * scales_stride bytes; both or neither
  * At least one of out and codes is given.  No output may overlap another, the residual, the weight or x (apart
- * from out == x).  1 <= d <= SA_NORM_MAX_DIM, else SA_ERR_UNSUPPORTED; d % 32 == 0 with codes; strides at
- * least the row's length; 0 <= eps.  n == 0 is a no-op.
+ * from out == x); rows equally far apart in bytes may lie between one another's (codes and scales side by side in a
+ * row, x and out as columns of one buffer).  1 <= d <= SA_NORM_MAX_DIM, else SA_ERR_UNSUPPORTED; d % 32 == 0 with
+ * codes; strides at least the row's length; 0 <= eps.  n == 0 is a no-op.
  */
 sa_status sa_add_rms_norm(const void* x, int64_t n, int d, int64_t x_stride, const float* weight, float eps,
                           void* residual, int residual_type, int64_t r_stride, void* out, int64_t out_stride,

@@ -276,18 +276,20 @@ extern "C" sa_status sa_add_rms_norm(const void* x, int64_t n, int d, int64_t x_
     if (out && (!aligned(out, 2) || out_stride < d)) return SA_ERR_INVALID_ARG;
     if (codes && (codes_stride < d || scales_stride < d / 32)) return SA_ERR_INVALID_ARG;
     if (out == x && out_stride != x_stride) return SA_ERR_INVALID_ARG;
-    const int64_t xb = ((n - 1) * x_stride + d) * 2, wb = (int64_t)d * 4, resb = ((n - 1) * r_stride + d) * rb,
-                  ob = ((n - 1) * out_stride + d) * 2, cb = (n - 1) * codes_stride + d,
-                  sb = (n - 1) * scales_stride + d / 32;
     const struct {
         const void* at;
-        int64_t bytes;
+        int64_t width, row, span;  // a row's bytes, their distance, all rows'
         bool written;
-    } t[] = {{out == x ? nullptr : x, xb, false}, {weight, wb, false}, {residual, resb, true},
-             {out, ob, true},                     {codes, cb, true},   {scales, sb, true}};
+    } t[] = {{out == x ? nullptr : x, 2 * (int64_t)d, 2 * x_stride, 2 * ((n - 1) * x_stride + d), false},
+             {weight, 4 * (int64_t)d, 0, 4 * (int64_t)d, false},
+             {residual, rb * d, rb * r_stride, rb * ((n - 1) * r_stride + d), true},
+             {out, 2 * (int64_t)d, 2 * out_stride, 2 * ((n - 1) * out_stride + d), true},
+             {codes, d, codes_stride, (n - 1) * codes_stride + d, true},
+             {scales, d / 32, scales_stride, (n - 1) * scales_stride + d / 32, true}};
     for (int i = 0; i < 6; ++i)
         for (int j = i + 1; j < 6; ++j)
-            if ((t[i].written || t[j].written) && overlap(t[i].at, t[i].bytes, t[j].at, t[j].bytes))
+            if ((t[i].written || t[j].written) && overlap(t[i].at, t[i].span, t[j].at, t[j].span) &&
+                !(n > 1 && t[i].row == t[j].row && apart(t[i].at, t[i].width, t[j].at, t[j].width, t[i].row)))
                 return SA_ERR_INVALID_ARG;
     Norm p = {};
     p.x = reinterpret_cast<const __nv_bfloat16*>(x);

@@ -277,13 +277,6 @@ struct Pool {
     int64_t width, row, page;
 };
 
-// Whether pieces of aw and bw bytes, each repeated every s bytes, never share one.
-bool apart(const void* a, int64_t aw, const void* b, int64_t bw, int64_t s) {
-    if (aw > s || bw > s) return false;
-    const uintptr_t u = (uintptr_t)s, at = (reinterpret_cast<uintptr_t>(b) % u + u - reinterpret_cast<uintptr_t>(a) % u) % u;
-    return at >= (uintptr_t)aw && at + (uintptr_t)bw <= u;
-}
-
 // Whether two pools share a byte.  Pages, or rows, equally far apart may lie between one another (codes and
 // scales side by side in a row, or in a page); of others the whole spans count.
 bool pools_overlap(const Pool& a, const Pool& b, int64_t n_pages, int64_t rows) {

@@ -325,5 +325,12 @@ inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
     return a0 < b0 + (uintptr_t)bn && b0 < a0 + (uintptr_t)an;
 }
 
+// Whether pieces of aw and bw bytes, each repeated every s bytes, never share one.
+inline bool apart(const void* a, int64_t aw, const void* b, int64_t bw, int64_t s) {
+    if (aw > s || bw > s) return false;
+    const uintptr_t u = (uintptr_t)s, at = (reinterpret_cast<uintptr_t>(b) % u + u - reinterpret_cast<uintptr_t>(a) % u) % u;
+    return at >= (uintptr_t)aw && at + (uintptr_t)bw <= u;
+}
+
 }  // namespace rows
 }  // namespace sa

@@ -210,3 +210,21 @@ def test_squares_outside_f32(dev, d, pad, kind, eps):  # noqa: F811
         res = None if r is None else r.clone()
         sa.add_rms_norm(wide, w, residual=res, eps=eps, codes=codes, scales=scales)
         _check(wide, w, r, res, None, codes, scales, eps=eps)
+
+
+@pytest.mark.parametrize("d", [512, 4096, 96])
+def test_rows_between_one_another(dev, d):  # noqa: F811
+    """Codes and scales side by side in a row; x, the residual and out as columns of one buffer: no byte is another's."""
+    x, w, r = _inputs(dev, 9, d, "bf16", d)
+    both = torch.full((9, d + d // 32), 0x55, dtype=torch.uint8, device=dev)
+    codes, scales = both[:, :d], both[:, d:]
+    wide = torch.cat([x, r, torch.full_like(x, 5.0), torch.full((9, 8), 7.0, dtype=x.dtype, device=dev)], 1)
+    sa.add_rms_norm(wide[:, :d], w, residual=wide[:, d:2 * d], out=wide[:, 2 * d:3 * d], codes=codes, scales=scales)
+    assert torch.equal(wide[:, :d], x) and (wide[:, 3 * d:] == 7.0).all()
+    _check(x, w, r, wide[:, d:2 * d], wide[:, 2 * d:3 * d], codes, scales)
+    with pytest.raises(sa.SparseAttnError):   # (a column further: the residual's last)
+        sa.add_rms_norm(wide[:, :d], w, residual=wide[:, d:2 * d], out=wide[:, 2 * d - 1:3 * d - 1])
+    with pytest.raises(sa.SparseAttnError):
+        sa.add_rms_norm(x, w, codes=codes, scales=both[:, d - 1:d - 1 + d // 32])
+    with pytest.raises(sa.SparseAttnError):   # (rows of another distance)
+        sa.add_rms_norm(wide[:, :d], w, out=wide.view(-1)[d:].as_strided((9, d), (wide.stride(0) - 8, 1)))

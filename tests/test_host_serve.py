@@ -330,3 +330,16 @@ def test_window_attn_workspace_of_the_tables_positions(lib, fmt, d, page, n, pag
         a.update(window=window, first=first)
         assert lib.sa_window_attn(*a.values(), None) == INVALID, (window, first)   # (the workspace's address)
     assert a["ws_bytes"] < 256 + (24 << 20) + n * (4 * held + 4) + 1024
+
+
+@pytest.mark.parametrize("change", [
+    dict(scales=at(5, 63)), dict(scales=at(5, 65)),                     # the last code; the next row's first
+    dict(out=at(1, 126)), dict(out=at(1, 134)), dict(res=at(1, 126)),   # x's last column; the next row's first
+    dict(n=4, ss=67),                                                   # rows of another distance
+    dict(cs=64, ss=64),                                                 # a row that leaves no room
+])
+def test_add_rms_norm_refuses_rows_that_share_a_byte(lib, change):
+    a = dict(x=at(1), n=3, d=64, xs=130, w=at(2), eps=1e-6, res=at(3), kind=1, rs=130, out=at(4), os=130, codes=at(5),
+             cs=66, scales=at(5, 64), ss=66)
+    a.update(change)
+    assert lib.sa_add_rms_norm(*a.values(), None) == INVALID
