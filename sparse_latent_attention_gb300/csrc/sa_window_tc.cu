@@ -498,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
 
     if (tid == 0) {
         for (int s = 0; s < kKStages; ++s) {
-            mbar_init(smem_addr(&M.k_full[s]), kCodes ? 8 : 1);  // (codes: the widening warps of both CTAs)
+            mbar_init(smem_addr(&M.k_full[s]), kCodes ? 8 : 2);  // (both CTAs' loading warp, or widening warps)
             mbar_init(smem_addr(&M.k_empty[s]), 1);
         }
         for (int s = 0; s < kVStages; ++s) {
@@ -727,13 +727,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * warps_of(kFmt),
         uint64_t* const full = is_v ? M.v_full : M.k_full;
         uint64_t* const empty = is_v ? M.v_empty : M.k_empty;
         uint32_t st = 0, st_use = 0, g = 0;
-        // (V's copies complete at this CTA's barrier, K's of both CTAs at rank 0's, which expects them all)
+        // (V's copies complete at this CTA's barrier, K's of both CTAs at rank 0's, which expects them all.  Rank 1's warp
+        // arrives there as well, also for a tile of one block, of which it copies nothing: else the products would go
+        // on without it, and its wait for a stage would come more than a phase too late to tell that it is free.)
         auto load = [&](uint32_t bytes, auto issue) {
             if (!(ok = ok && wait(empty[st], st_use ^ 1u, abort))) return;
             if (lane == 0) {
                 const uint32_t bar = smem_addr(&full[st]);
                 if (is_v || rank == 0) mbar_arrive_expect_tx(bar, bytes);
                 issue(ring + st * kStageBytes, is_v ? bar : at_leader(bar));
+                if (!is_v && rank != 0) arrive_at(at_leader(bar));
             }
             if (++st == stages) {
                 st = 0;

@@ -779,3 +779,23 @@ def test_window_attn_of_everything(dev, d, page, fmt):  # noqa: F811
     o = sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, (1 << 30) - 9, first=8, kv_scale=sc)
     want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 1000, 0)
     assert ((o[:bt.live].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("h,held", [(1, (0, 10, 31)), (8, (0, 20, 200)), (1, (31, 32, 33, 64, 100))])
+def test_window_attn_many_small_tasks(dev, held, h, fmt):  # noqa: F811
+    """Two thousand sequences of no, one or two tokens and few rows, again and again: the same result every time."""
+    g = torch.Generator().manual_seed(117)
+    new, at = torch.randint(0, 3, (2000,), generator=g).tolist(), torch.randint(0, len(held), (2000,), generator=g).tolist()
+    bt = _paged.Batch(new, [held[i] for i in at], 64, 118)
+    q, sink, pool, sc = _attn_inputs(dev, bt, h, 512, fmt, 40, 3, 119)
+    ws = sa.new_window_workspace(bt.n, bt.b, h, 512, 40, 3, 64, {"bf16": sa.SA_KV_BF16, "fp8": sa.SA_KV_FP8_E4M3,
+                                                                  "fp4": sa.SA_KV_FP4_E2M1}[fmt])
+    call = lambda: sa.window_attn(q, pool, sink, bt.table, bt.q_start, bt.kv_len, 0.05, 40, first=3, kv_scale=sc, workspace=ws)
+    want, _, tol, _ = _paged.attention(bt, q, pool, sc, sink, 0.05, 40, 3)
+    first = call()
+    assert ((first.double() - want).abs() <= tol).all()
+    same = torch.ones((), dtype=torch.bool, device=dev)
+    for _ in range(200):
+        same &= (call() == first).all()
+    assert same and sa.read_status(ws) == 0
