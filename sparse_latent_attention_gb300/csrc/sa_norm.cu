@@ -171,7 +171,9 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : 1024) norm_kernel(const __gri
 }
 
 // Any alignment and length: a block a row, an element a thread and step.  The residual, once written, is read
-// back by the thread that wrote it; a warp's 32 elements are a block of the quantiser's.
+// back by the thread that wrote it; a warp's 32 elements are a block of the quantiser's.  8191 rows of 4096 at odd
+// places, bf16 residual and out: 168 us, 47 where they are aligned (loads of two bytes, each row twice, and the look
+// for a border at every element).
 template <int kRes>
 __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ Norm p) {
     __shared__ Two part[32];

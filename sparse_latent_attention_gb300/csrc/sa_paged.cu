@@ -43,10 +43,12 @@ struct Write {
 
 // A warp a token, eight consecutive elements a lane and chunk (kPer chunks of 256).  kRun tokens one behind the
 // other a warp: their rows are under way before the first one's sequence and page are known, and the sequence is
-// looked for once.  Bound by instructions, some 650 a row of 512 with norm, rotation and 4-bit codes: a third are the
-// norm's products and what they lose, a third the codes and their round trip, and a sixth what makes the codes exact
-// (the sum's lost parts, the look for values on a border).  65536 such rows take 73 us with two tokens a warp and
-// five or six blocks a SM, 74 with seven (registers spill), 61 where codes next to a border may fall to its other side.
+// looked for once.  Bound by arithmetic whose steps wait for one another, at few warps: some 650 instructions a row of
+// 512 with norm, rotation and 4-bit codes (a third are the norm's products and what they lose, a third the codes and
+// their round trip, a sixth what makes the codes exact), 96 registers, so that 29 % of the warps are there; 59 % of
+// the issue slots are used, and the first stall is the wait for the instruction before.  65536 such rows take 74 us with
+// two tokens a warp and five blocks a SM (seven, whose registers spill, take 1 us more), 61 where codes next to a border
+// may fall to its other side.
 template <int kQuant, int kPer, int kRun, bool kVec>
 __global__ void __launch_bounds__(128, kPer == 4 ? 3 : 5) page_write_kernel(const __grid_constant__ Write p) {
     pdl_wait();

@@ -31,12 +31,13 @@
 // into L2, warps 16-23 widen K and 24-31 V, warps 12-15 are the epilogue, warp 1 loads Q too and warp 3 issues P.V.
 // Every wait is bounded; one that gives up raises the timeout bit and every role unwinds.
 //
-// What it measured (a call among others, b sequences of one token but for the prompts): 128 heads, window 4096 + 128 first,
-// b = 256: 252 us, 4.7 TB/s of cache; 64 heads, window 128, a prompt of 4095 with the rotation: 132 us, 4 TB/s of q
-// and o; 128 heads, window 2048, prompts of 4096 tokens in all: 1.59 ms, 1.4 PFLOP/s; e4m3 rows, 64 heads, window
-// 1024, b = 64: 39 us; e2m1 rows, 16 heads, window 512, 240 tokens of 48 sequences: 23 us.  Long windows of bf16 rows are
-// bound by L2, out of which each row comes twice (pulled into L2 ahead they take longer), prompts of short windows by a task's chain (Q, logits, softmax, P.V, O out:
-// O has one buffer), codes by the widening's instructions.
+// What it measured (a call among others, the range over several GPUs; b sequences of one token but for the prompts): 128
+// heads, window 4096 + 128 first, b = 256: 258-272 us, 4.3-4.6 TB/s of cache; 64 heads, window 128, a prompt of 4095
+// with the rotation: 139-143 us, 3.8 TB/s of q and o (over e4m3 rows 204, e2m1 202); 128 heads, window 2048, prompts of
+// 4096 tokens in all: 1.62-1.67 ms, 1.4 PFLOP/s; e4m3 rows, 64 heads, window 1024, b = 64: 39 us; e2m1 rows, 16 heads,
+// window 512, 240 tokens of 48 sequences: 23 us.  Long windows of bf16 rows are bound by L2, out of which each row comes
+// twice (pulled into L2 ahead they take longer), prompts of short windows by a task's chain (Q, logits, softmax, P.V, O
+// out: O has one buffer), codes by the widening's instructions.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1236,6 +1237,8 @@ int window_splits(int64_t n, int64_t b, int h, int64_t window, int64_t first, in
 
 }  // namespace
 
+// (Other pages, and other d, go by index table through the families that gather by row: pages of 16 rows take 509 us where
+// pages of 64 take 258-272 (256 tokens of 128 heads, window 4096), and 197 where they take 139-143 (a prompt of 4095).)
 bool window_tc_supports(int d, int kv_format, int page) {
     (void)kv_format;
     return d == kD && page % kBlock == 0;
